@@ -495,6 +495,176 @@ strata_status strata_tier_read(strata_tier* tier, float* counters, int32_t* resi
 /* Free a tier (detach it from its handle first).  NULL is accepted. */
 strata_status strata_tier_destroy(strata_tier* tier);
 
+/* ---------------------------------------------------------------------------
+ * The attention half of a decoder layer as calls of its own: the norms of each
+ * query and key head with the rotation by position, and KV caches of the slots
+ * held in 8 bits (written from a call's rows, read back, attended over).
+ *
+ * The stack above fuses a layer's attention over fp16 caches into its one
+ * launch for windows of at most 8 rows.  These calls serve the same slots with
+ * half the cache bytes, for windows and for prompts, and beside
+ * strata_moe_window_forward they are the other half of a layer that a caller
+ * runs by its parts.  The Strata pages describe no counterpart.
+ *
+ * All of them are asynchronous on cuda_stream, allocate nothing, copy nothing
+ * to the host and may be captured into a CUDA graph; the device arrays that
+ * describe the rows are read when the work runs, so a replay follows their
+ * contents.  The handle's device is made current for the call and the caller's
+ * restored.  Values are f32, f16 or bf16 (strata_dtype), every row's heads back
+ * to back ([heads][head_dim]); *_stride is the distance between rows in
+ * elements.  Value pointers are 16-byte aligned and strides a multiple of 16
+ * bytes (EINVAL otherwise).  Offsets are 64-bit throughout.
+ * ------------------------------------------------------------------------- */
+typedef enum { STRATA_F32 = 0, STRATA_F16 = 1, STRATA_BF16 = 2 } strata_dtype;
+
+/* Norms of the query and key heads with the rotation by position.
+ *   n = x / sqrt(mean(x^2) + eps) * gain         per head, fp32 (norm = 1)
+ *   pairs (a, b) = (n_i, n_{i + rotary_dim/2}), or (n_2i, n_{2i+1}) when
+ *   interleaved, i < rotary_dim/2, turn by t = position * freq_i:
+ *   (a cos t - b sin t, a sin t + b cos t); the other dims pass.
+ * t is reduced exactly: freq_i / 2 pi is kept as a 64-bit fraction of a turn,
+ * whose product with the position wraps by itself, so that far positions lose
+ * nothing. */
+typedef struct strata_qknorm strata_qknorm;
+
+typedef struct {
+  int32_t heads;        /* query heads: 1..1024 */
+  int32_t kv_heads;     /* key heads: 0..1024 (0: q only) */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t rotary_dim;   /* dims of a head that turn: 0..head_dim, a multiple of head_dim/16 */
+  int32_t interleaved;  /* 0: pairs half a rotary_dim apart; 1: neighbours */
+  int32_t norm;         /* 1: normalise first; 0: rotate only */
+  float eps;            /* >= 0, finite */
+} strata_qknorm_desc;
+
+/* Create on the current device.  q_gain, k_gain: device fp32 [head_dim], or
+ * NULL for unit gain (copied on cuda_stream; create waits); freqs: host double
+ * [rotary_dim/2], radians per position, finite.  Returns EINVAL, EUNSUPPORTED,
+ * ENOMEM, ECUDA. */
+strata_status strata_qknorm_create(const strata_qknorm_desc* desc, const float* q_gain, const float* k_gain,
+                                   const double* freqs, void* cuda_stream, strata_qknorm** out);
+
+/* T rows: q [T][heads][head_dim] to q_out, k [T][kv_heads][head_dim] to k_out
+ * (k and k_out may be NULL when kv_heads is 0).  position: device int32 [T],
+ * any value.  An output may be its own input (same pointer and stride); any
+ * other overlap is not allowed.  T = 0 does nothing.  A row's bits do not
+ * depend on the other rows.  Returns EINVAL, ECUDA.  One handle may run on
+ * several streams at once. */
+strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, int32_t dtype,
+                                    const int32_t* position, int32_t T, void* cuda_stream);
+
+/* Free it (its launches must have finished).  NULL is accepted. */
+strata_status strata_qknorm_destroy(strata_qknorm* h);
+
+/* KV caches of the slots in 8 bits.  For each layer, slot and kv head, the
+ * positions are cut into blocks of `block`; a block of keys (and of values) has
+ * one exponent e and its values are code * 2^e, where a code is an e4m3 number
+ * (qmax 448) or an int8 (qmax 127, -128 unused).  The exponent is held as the
+ * byte e + 127, e in -48..47 (other bytes are read as the nearest of these). */
+typedef struct strata_kv8 strata_kv8;
+
+typedef enum { STRATA_KV8_E4M3 = 0, STRATA_KV8_INT8 = 1 } strata_kv8_format;
+
+typedef struct {
+  int32_t n_layers;   /* 1.. */
+  int32_t n_slots;    /* 1.. */
+  int32_t heads;      /* query heads, a multiple of kv_heads, at most 1024 */
+  int32_t kv_heads;   /* 1.. */
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t max_ctx;    /* positions a slot holds: 1.. */
+  int32_t block;      /* positions per exponent: 16, 32, 64 or 128 */
+  int32_t format;     /* strata_kv8_format */
+} strata_kv8_desc;
+
+/* Caller-owned device arrays; they must outlive the handle's use.  Codes are
+ * 128-byte aligned.  Contents need no initialisation: a slot's positions are
+ * written before they are read. */
+typedef struct {
+  uint8_t* k;      /* codes [n_layers][n_slots][kv_heads][max_ctx][head_dim] */
+  uint8_t* v;
+  uint8_t* k_exp;  /* exponent bytes [n_layers][n_slots][kv_heads][ceil(max_ctx / block)] */
+  uint8_t* v_exp;
+} strata_kv8_cache;
+
+/* The rows of a call: n_seq sequences, sequence i the rows row_start[i] to
+ * row_start[i+1] - 1 (possibly none) of slot slot[i], which holds length[i]
+ * positions with them; they are its last ones, so row r is at position
+ * length[i] - (row_start[i+1] - r).  Rows from row_start[n_seq] on belong to
+ * no sequence (a padded batch): outputs there are left as they were.
+ * A sequence with row_start out of order or outside 0..n_rows, or with more
+ * than max_rows rows, is skipped; one with a slot or length out of range is
+ * left out (nothing is written to the caches; zeros are written to its rows of
+ * an output).  Both make the next strata_kv8_sync report EDEVICE. */
+typedef struct {
+  int32_t n_seq;             /* 0..4096 (0: nothing is done) */
+  int32_t n_rows;            /* rows of the value arrays (0: nothing is done) */
+  int32_t max_rows;          /* no sequence has more rows than this */
+  const int32_t* row_start;  /* device [n_seq + 1] */
+  const int32_t* slot;       /* device [n_seq] */
+  const int32_t* length;     /* device [n_seq] */
+} strata_kv8_rows;
+
+/* Create on the current device (the workspace of strata_kv8_attend is
+ * allocated here).  Returns EINVAL (bad pointer or field), EUNSUPPORTED,
+ * ENOMEM, ECUDA. */
+strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_cache* cache, strata_kv8** out);
+
+/* Write the rows' keys and values (each [n_rows][kv_heads][head_dim]) to their
+ * positions.  For each block that a sequence's rows touch, and each kv head:
+ *   a = max |x| over its new rows' (finite) elements
+ *   e = the least integer with a <= qmax * 2^e, clamped to -48..47
+ *   where the block holds earlier positions of the sequence (those before its
+ *   first row): e = max(e, e_held), and when that exceeds e_held the held codes
+ *   become rne(code * 2^(e_held - e))
+ *   codes = rne(x * 2^-e), saturated at qmax
+ * (rne: to nearest, ties to even).  Every step but the roundings is exact.  A
+ * power-of-two step means a held block is rewritten at most once each time its
+ * largest value doubles.  A row sequence that starts inside earlier positions
+ * (rejected proposals written over) keeps the block's exponent.
+ * A NaN is held as 0 and an infinity as the largest code; either makes the
+ * next sync report EDEVICE.  Sequences of one call name different slots: of
+ * sequences with rows that name the same slot the first is written, the others
+ * are left out (EDEVICE); so is a sequence with length[i] below its rows. */
+strata_status strata_kv8_append(strata_kv8* h, int32_t layer, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream);
+
+/* Read the rows' positions back: code * 2^e, rounded once to dtype (exact in
+ * f32; f16 overflows to infinity as any rounding to it).  A sequence with
+ * length[i] below its rows is left out. */
+strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                              int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream);
+
+/* Attention of the rows over their slots' caches: for query head a, kv head
+ * a / (heads / kv_heads), a row at position p gets
+ *   sum_j softmax_j(scale * q . K_j) V_j   over j = 0..p
+ * with K_j, V_j the values the cache holds.  A row whose position is negative
+ * (length below the rows) attends to nothing: zeros.  Sums and softmax
+ * statistics are fp32; products take 16-bit parts of q and of the softmax
+ * weights, one for f16 and bf16 rows and two (22 bits) for f32 rows.  Cache
+ * contents at positions a row does not see never reach its output.  Sequences
+ * may share a slot.  q and out are [n_rows][heads][head_dim] of the same dtype
+ * and must not overlap.  scale is finite.
+ * The rows written by an earlier strata_kv8_append on the same stream are
+ * seen.  The handle's workspace joins the parts of long rows, so calls of
+ * strata_kv8_attend on one handle, replays of captured ones among them, must
+ * not overlap on the GPU (append and read use none).  The same call gives the
+ * same bits; a row's bits may depend on the other sequences' lengths. */
+strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int64_t q_stride, void* out,
+                                int64_t out_stride, int32_t dtype, float scale, const strata_kv8_rows* rows,
+                                void* cuda_stream);
+
+/* Wait for the handle's device; report (and clear) any error the GPU recorded:
+ * EDEVICE in that case.  Not during a capture. */
+strata_status strata_kv8_sync(strata_kv8* h);
+
+/* Cache bytes of the desc (codes and exponents of all layers) and the
+ * handle's workspace bytes; either pointer may be NULL. */
+strata_status strata_kv8_query(const strata_kv8* h, int64_t* cache_bytes, int64_t* workspace_bytes);
+
+/* Free the handle (the caches are the caller's).  NULL is accepted. */
+strata_status strata_kv8_destroy(strata_kv8* h);
+
 /* Free the handle and everything it owns.  NULL is accepted (returns OK). */
 strata_status strata_window_destroy(strata_window* h);
 

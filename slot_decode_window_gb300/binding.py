@@ -27,7 +27,11 @@ EXPORTED = ("strata_window_create", "strata_moe_window_forward", "strata_window_
             "strata_window_plan", "strata_tier_create", "strata_window_set_tier", "strata_tier_read",
             "strata_tier_destroy", "strata_head_create", "strata_head_forward", "strata_head_sync",
             "strata_head_query", "strata_head_set_profiling", "strata_head_timings", "strata_head_destroy",
-            "strata_window_slots", "strata_stack_set_kv", "strata_stack_forward_kv")
+            "strata_window_slots", "strata_stack_set_kv", "strata_stack_forward_kv", "strata_qknorm_create",
+            "strata_qknorm_forward", "strata_qknorm_destroy", "strata_kv8_create", "strata_kv8_append",
+            "strata_kv8_read", "strata_kv8_attend", "strata_kv8_sync", "strata_kv8_query", "strata_kv8_destroy")
+STRATA_F32, STRATA_F16, STRATA_BF16 = range(3)
+STRATA_KV8_E4M3, STRATA_KV8_INT8 = range(2)
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -106,6 +110,25 @@ class strata_draw_in(ctypes.Structure):
 
 class strata_draw_out(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("tokens", "n_emit", "logits")]
+
+
+class strata_qknorm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "kv_heads", "head_dim", "rotary_dim", "interleaved", "norm")] + \
+        [("eps", ctypes.c_float)]
+
+
+class strata_kv8_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "n_slots", "heads", "kv_heads", "head_dim", "max_ctx",
+                                              "block", "format")]
+
+
+class strata_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")]
+
+
+class strata_kv8_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seq", "n_rows", "max_rows")] + \
+        [(n, ctypes.c_void_p) for n in ("row_start", "slot", "length")]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -194,6 +217,26 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.strata_stack_forward_kv.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                             ctypes.c_void_p, ctypes.c_void_p, P(strata_stack_out), ctypes.c_void_p]
     lib.strata_stack_forward_kv.restype = ctypes.c_int
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    lib.strata_qknorm_create.argtypes = [P(strata_qknorm_desc), vp, vp, vp, vp, P(vp)]
+    lib.strata_qknorm_create.restype = ctypes.c_int
+    lib.strata_qknorm_forward.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, vp]
+    lib.strata_qknorm_forward.restype = ctypes.c_int
+    lib.strata_qknorm_destroy.argtypes = [vp]
+    lib.strata_qknorm_destroy.restype = ctypes.c_int
+    lib.strata_kv8_create.argtypes = [P(strata_kv8_desc), P(strata_kv8_cache), P(vp)]
+    lib.strata_kv8_create.restype = ctypes.c_int
+    for fn in (lib.strata_kv8_append, lib.strata_kv8_read):
+        fn.argtypes = [vp, i32, vp, i64, vp, i64, i32, P(strata_kv8_rows), vp]
+        fn.restype = ctypes.c_int
+    lib.strata_kv8_attend.argtypes = [vp, i32, vp, i64, vp, i64, i32, ctypes.c_float, P(strata_kv8_rows), vp]
+    lib.strata_kv8_attend.restype = ctypes.c_int
+    lib.strata_kv8_sync.argtypes = [vp]
+    lib.strata_kv8_sync.restype = ctypes.c_int
+    lib.strata_kv8_query.argtypes = [vp, P(i64), P(i64)]
+    lib.strata_kv8_query.restype = ctypes.c_int
+    lib.strata_kv8_destroy.argtypes = [vp]
+    lib.strata_kv8_destroy.restype = ctypes.c_int
     lib.strata_status_str.argtypes = [ctypes.c_int]
     lib.strata_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -391,6 +434,61 @@ def strata_stack_forward_kv(handle, x_ptr: int, T: int, y_ptr: int, slot_ptr: in
     return load().strata_stack_forward_kv(ctypes.c_void_p(handle), ctypes.c_void_p(x_ptr), T, ctypes.c_void_p(y_ptr),
                                           ctypes.c_void_p(slot_ptr), ctypes.c_void_p(pos_ptr),
                                           ctypes.byref(out) if out is not None else None, ctypes.c_void_p(stream))
+
+
+def strata_qknorm_create(desc: strata_qknorm_desc, q_gain_ptr=None, k_gain_ptr=None, freqs=None, stream: int = 0):
+    """freqs: a sequence of rotary_dim/2 radians per position.  Returns (status, handle or None)."""
+    h = ctypes.c_void_p()
+    arr = (ctypes.c_double * len(freqs))(*[float(f) for f in freqs]) if freqs else None
+    st = load().strata_qknorm_create(ctypes.byref(desc), q_gain_ptr, k_gain_ptr, arr, stream, ctypes.byref(h))
+    return st, (h.value if st == STRATA_OK else None)
+
+
+def strata_qknorm_forward(handle, q_ptr, q_stride, k_ptr, k_stride, q_out_ptr, q_out_stride, k_out_ptr, k_out_stride,
+                          dtype: int, position_ptr, T: int, stream: int = 0) -> int:
+    return load().strata_qknorm_forward(handle, q_ptr, q_stride, k_ptr, k_stride, q_out_ptr, q_out_stride, k_out_ptr,
+                                        k_out_stride, dtype, position_ptr, T, stream)
+
+
+def strata_qknorm_destroy(handle) -> int:
+    return load().strata_qknorm_destroy(handle)
+
+
+def strata_kv8_create(desc: strata_kv8_desc, cache: strata_kv8_cache):
+    """Returns (status, handle or None)."""
+    h = ctypes.c_void_p()
+    st = load().strata_kv8_create(ctypes.byref(desc), ctypes.byref(cache), ctypes.byref(h))
+    return st, (h.value if st == STRATA_OK else None)
+
+
+def strata_kv8_append(handle, layer: int, k_ptr, k_stride: int, v_ptr, v_stride: int, dtype: int,
+                      rows: strata_kv8_rows, stream: int = 0) -> int:
+    return load().strata_kv8_append(handle, layer, k_ptr, k_stride, v_ptr, v_stride, dtype, rows, stream)
+
+
+def strata_kv8_read(handle, layer: int, k_ptr, k_stride: int, v_ptr, v_stride: int, dtype: int,
+                    rows: strata_kv8_rows, stream: int = 0) -> int:
+    return load().strata_kv8_read(handle, layer, k_ptr, k_stride, v_ptr, v_stride, dtype, rows, stream)
+
+
+def strata_kv8_attend(handle, layer: int, q_ptr, q_stride: int, out_ptr, out_stride: int, dtype: int, scale: float,
+                      rows: strata_kv8_rows, stream: int = 0) -> int:
+    return load().strata_kv8_attend(handle, layer, q_ptr, q_stride, out_ptr, out_stride, dtype, scale, rows, stream)
+
+
+def strata_kv8_sync(handle) -> int:
+    return load().strata_kv8_sync(handle)
+
+
+def strata_kv8_query(handle):
+    """Returns (status, cache bytes, workspace bytes)."""
+    cb, wb = ctypes.c_int64(), ctypes.c_int64()
+    st = load().strata_kv8_query(handle, ctypes.byref(cb), ctypes.byref(wb))
+    return st, cb.value, wb.value
+
+
+def strata_kv8_destroy(handle) -> int:
+    return load().strata_kv8_destroy(handle)
 
 
 def check(status: int, what: str) -> None:
@@ -639,6 +737,221 @@ class Head:
     def close(self) -> None:
         if getattr(self, "handle", None):
             strata_head_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _values(t, heads: int, head_dim: int, what: str, like=None):
+    """(pointer, row stride in elements, strata_dtype) of a CUDA tensor [T][heads][head_dim] whose rows may be
+    strided; raises for any other layout."""
+    import torch
+    code = {torch.float32: STRATA_F32, torch.float16: STRATA_F16, torch.bfloat16: STRATA_BF16}.get(t.dtype)
+    st = t.stride()
+    if code is None or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or \
+            st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [rows][{heads}][{head_dim}] of float32, float16 "
+                                         "or bfloat16 whose rows are contiguous")
+    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.device != like.device):
+        raise StrataError(STRATA_EINVAL, f"{what}: rows, type or device differ")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * head_dim), code
+
+
+def _int32(t, n: int, what: str):
+    import torch
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise StrataError(STRATA_EINVAL, f"{what}: want a contiguous CUDA int32 tensor [{n}]")
+    return t.data_ptr()
+
+
+def _stream_of(t, stream):
+    import torch
+    return (stream or torch.cuda.current_stream(t.device)).cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class QkNorm:
+    """Norms of the query and key heads with the rotation by position.
+
+    q_gain, k_gain: CUDA float32 [head_dim] or None (unit gain).  freqs:
+    rotary_dim/2 radians per position; None forms theta ** (-2 i / rotary_dim).
+    """
+
+    def __init__(self, heads: int, kv_heads: int, head_dim: int, rotary_dim: Optional[int] = None, freqs=None,
+                 theta: float = 10000.0, interleaved: bool = False, norm: bool = True, eps: float = 1e-6,
+                 q_gain=None, k_gain=None, device=None, stream=None):
+        import torch
+        rd = head_dim if rotary_dim is None else rotary_dim
+        if freqs is None:
+            freqs = [theta ** (-2.0 * i / rd) for i in range(rd // 2)] if rd > 0 else []
+        if len(freqs) != max(rd, 0) // 2:
+            raise StrataError(STRATA_EINVAL, "QkNorm: freqs has rotary_dim/2 entries")
+        for g in (q_gain, k_gain):
+            if g is not None:
+                if not g.is_cuda or g.dtype != torch.float32 or tuple(g.shape) != (head_dim,) or \
+                        not g.is_contiguous():
+                    raise StrataError(STRATA_EINVAL, "QkNorm: a gain is a contiguous CUDA float32 [head_dim]")
+                device = device or g.device
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        with torch.cuda.device(device):
+            s = (stream or torch.cuda.current_stream()).cuda_stream
+            st, h = strata_qknorm_create(
+                strata_qknorm_desc(heads, kv_heads, head_dim, rd, int(interleaved), int(norm), eps),
+                q_gain.data_ptr() if q_gain is not None else None, k_gain.data_ptr() if k_gain is not None else None,
+                freqs, s)
+        check(st, "strata_qknorm_create")
+        self.handle = h
+
+    def forward(self, q, k, position, q_out=None, k_out=None, stream=None):
+        """Enqueue q [T][heads][head_dim] and k [T][kv_heads][head_dim] at position (CUDA int32 [T]); returns
+        (q_out, k_out), new tensors unless given (an output may be its own input)."""
+        qp, qs, dt = _values(q, self.heads, self.head_dim, "q")
+        if q_out is None:
+            q_out = _empty(q.shape, q.dtype, q.device, stream)
+        qop, qos, _ = _values(q_out, self.heads, self.head_dim, "q_out", q)
+        kp = ks = kop = kos = 0
+        if self.kv_heads > 0:
+            kp, ks, _ = _values(k, self.kv_heads, self.head_dim, "k", q)
+            if k_out is None:
+                k_out = _empty(k.shape, k.dtype, k.device, stream)
+            kop, kos, _ = _values(k_out, self.kv_heads, self.head_dim, "k_out", q)
+        T = q.shape[0]
+        st = load().strata_qknorm_forward(self.handle, qp, qs, kp, ks, qop, qos, kop, kos, dt,
+                                          _int32(position, T, "position"), T, _stream_of(q, stream))
+        if st != STRATA_OK:
+            check(st, "strata_qknorm_forward")
+        return q_out, k_out
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            strata_qknorm_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KvRows:
+    """The rows of a KvCache8 call: sequence i has rows row_start[i] to row_start[i+1] - 1, the last ones of the
+    length[i] positions that slot[i] holds with them.  row_start [n_seq + 1], slot and length [n_seq] are CUDA int32
+    tensors that the calls read on the device; n_rows is the rows of the value tensors (those behind the last
+    sequence are left as they were), max_rows the most rows of one sequence."""
+
+    def __init__(self, row_start, slot, length, n_rows: int, max_rows: int):
+        n = slot.shape[0]
+        self.keep = (row_start, slot, length)
+        self.n_rows, self.device = n_rows, slot.device
+        self.c = strata_kv8_rows(n, n_rows, max_rows, _int32(row_start, n + 1, "row_start"), _int32(slot, n, "slot"),
+                                 _int32(length, n, "length"))
+
+
+class KvCache8:
+    """8-bit KV caches of the slots, one exponent per block of positions and kv head.
+
+    The codes (k, v: uint8 [n_layers][n_slots][kv_heads][max_ctx][head_dim]) and exponent bytes (k_exp, v_exp:
+    uint8 [...][ceil(max_ctx / block)]) are torch tensors, made here or given as ``buffers`` (contiguous, of these
+    sizes).  format: "e4m3" or "int8".  Calls are asynchronous; sync() raises what the GPU recorded.
+    """
+
+    def __init__(self, n_layers: int, n_slots: int, heads: int, kv_heads: int, head_dim: int, max_ctx: int,
+                 block: int = 64, format: str = "e4m3", buffers=None, device=None):
+        import torch
+        fmt = {"e4m3": STRATA_KV8_E4M3, "int8": STRATA_KV8_INT8}.get(format)
+        if fmt is None:
+            raise StrataError(STRATA_EINVAL, "KvCache8: format is e4m3 or int8")
+        desc = strata_kv8_desc(n_layers, n_slots, heads, kv_heads, head_dim, max_ctx, block, fmt)
+        if min(n_layers, n_slots, heads, kv_heads, head_dim, max_ctx, block) < 1:
+            raise StrataError(STRATA_EINVAL, "KvCache8: sizes are positive")
+        shape = (n_layers, n_slots, kv_heads, max_ctx, head_dim)
+        eshape = shape[:3] + ((max_ctx + block - 1) // block,)
+        if buffers is None:
+            buffers = tuple(torch.empty(x, dtype=torch.uint8, device=device or "cuda")
+                            for x in (shape, shape, eshape, eshape))
+        for t, x in zip(buffers, (shape, shape, eshape, eshape)):
+            n = 1
+            for d in x:
+                n *= d
+            if not t.is_cuda or t.element_size() != 1 or t.numel() != n or not t.is_contiguous() or \
+                    t.device != buffers[0].device:
+                raise StrataError(STRATA_EINVAL, f"KvCache8: want contiguous 8-bit CUDA buffers of {shape}, {eshape}")
+        self.heads, self.kv_heads, self.head_dim, self.n_layers = heads, kv_heads, head_dim, n_layers
+        self.k, self.v, self.k_exp, self.v_exp = buffers
+        self.scale = head_dim ** -0.5
+        with torch.cuda.device(self.k.device):
+            st, h = strata_kv8_create(desc, strata_kv8_cache(*(t.data_ptr() for t in buffers)))
+        check(st, "strata_kv8_create")
+        self.handle = h
+
+    def _rows(self, rows, t, what):
+        if t.shape[0] != rows.n_rows or t.device != self.k.device or rows.device != t.device:
+            raise StrataError(STRATA_EINVAL, f"{what}: rows or device differ")
+        return rows.c
+
+    def append(self, layer: int, k, v, rows: KvRows, stream=None) -> None:
+        """Enqueue the rows' keys and values [n_rows][kv_heads][head_dim] into the layer's caches."""
+        kp, ks, dt = _values(k, self.kv_heads, self.head_dim, "k")
+        vp, vs, _ = _values(v, self.kv_heads, self.head_dim, "v", k)
+        st = load().strata_kv8_append(self.handle, layer, kp, ks, vp, vs, dt, self._rows(rows, k, "append"),
+                                      _stream_of(k, stream))
+        if st != STRATA_OK:
+            check(st, "strata_kv8_append")
+
+    def read(self, layer: int, rows: KvRows, dtype=None, k=None, v=None, stream=None):
+        """Enqueue the rows' positions as values; returns (k, v), [n_rows][kv_heads][head_dim] of dtype (float32),
+        new tensors unless given; rows of no sequence are not written."""
+        import torch
+        shape = (rows.n_rows, self.kv_heads, self.head_dim)
+        if k is None:
+            k = _empty(shape, dtype or torch.float32, self.k.device, stream)
+        if v is None:
+            v = _empty(shape, k.dtype, self.k.device, stream)
+        kp, ks, dt = _values(k, self.kv_heads, self.head_dim, "k")
+        vp, vs, _ = _values(v, self.kv_heads, self.head_dim, "v", k)
+        st = load().strata_kv8_read(self.handle, layer, kp, ks, vp, vs, dt, self._rows(rows, k, "read"),
+                                    _stream_of(k, stream))
+        if st != STRATA_OK:
+            check(st, "strata_kv8_read")
+        return k, v
+
+    def attend(self, layer: int, q, rows: KvRows, out=None, scale: Optional[float] = None, stream=None):
+        """Enqueue the attention of q [n_rows][heads][head_dim] over the layer's caches; returns out, a new tensor
+        unless given; rows of no sequence are not written.  scale: 1 / sqrt(head_dim) unless given."""
+        qp, qs, dt = _values(q, self.heads, self.head_dim, "q")
+        if out is None:
+            out = _empty(q.shape, q.dtype, q.device, stream)
+        op, os_, _ = _values(out, self.heads, self.head_dim, "out", q)
+        st = load().strata_kv8_attend(self.handle, layer, qp, qs, op, os_, dt, self.scale if scale is None else scale,
+                                      self._rows(rows, q, "attend"), _stream_of(q, stream))
+        if st != STRATA_OK:
+            check(st, "strata_kv8_attend")
+        return out
+
+    def sync(self) -> None:
+        check(strata_kv8_sync(self.handle), "strata_kv8_sync")
+
+    def cache_bytes(self) -> int:
+        st, cb, _ = strata_kv8_query(self.handle)
+        check(st, "strata_kv8_query")
+        return cb
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            strata_kv8_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

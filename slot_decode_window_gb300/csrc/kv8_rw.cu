@@ -1,0 +1,254 @@
+// Writing a call's keys and values into the 8-bit caches, and reading them
+// back.
+#include "kv8.cuh"
+
+namespace strata {
+namespace {
+
+constexpr int kThreads = 256;
+
+// --- append -------------------------------------------------------------------
+//
+// One CTA owns one block of one head, of the keys or of the values: it finds
+// the largest new magnitude, fixes the exponent, requantises what the block
+// holds if the exponent grew, and writes the new codes.  Its new values stay in
+// registers between the two passes (NP 16-byte loads a thread, all in flight),
+// so they are read once; HBM bound (values in, codes out).
+template <typename T, int NP>
+__global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, const T* __restrict__ kin,
+                                                          long long k_stride, const T* __restrict__ vin,
+                                                          long long v_stride, int nb) {
+  constexpr int kPer = Val<T>::kPer;
+  __shared__ unsigned red[kThreads / 32];
+  __shared__ int bad;
+  int id = blockIdx.x;
+  const int b_at = id % nb;
+  id /= nb;
+  const int head = id % C.kv_heads;
+  id /= C.kv_heads;
+  const bool is_v = id & 1;
+  const int i = id >> 1;
+  const Kv8Seq q = kv8_seq(R, C, i);
+  const bool lead = threadIdx.x == 0 && b_at == 0 && head == 0 && !is_v;
+  if (!q.held_ok || q.length < q.n) {
+    if (lead) atomicOr(C.err, kErrIndex);
+    return;
+  }
+  if (q.n == 0) return;
+  const int p0 = q.length - q.n;  // first new position
+  const int B = 1 << C.block_log2;
+  const int blk = (p0 >> C.block_log2) + b_at;
+  const int lo = max(p0, blk << C.block_log2), hi = min(q.length, (blk + 1) << C.block_log2);
+  if (lo >= hi) return;
+  // an earlier sequence with rows that names the same slot owns it
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int j = threadIdx.x; j < i; j += kThreads)
+    if (R.slot[j] == q.slot && R.row_start[j + 1] > R.row_start[j]) bad = 1;
+  __syncthreads();
+  if (bad) {
+    if (lead) atomicOr(C.err, kErrIndex);
+    return;
+  }
+
+  const int hd = C.head_dim;
+  const int tpt_log2 = (hd == 128 ? 7 : 6) - (kPer == 4 ? 2 : 3);  // threads per token
+  const int per_pass = kThreads >> tpt_log2;
+  const int t0 = threadIdx.x >> tpt_log2, d = (threadIdx.x & ((1 << tpt_log2) - 1)) * kPer;
+  const T* src = is_v ? vin : kin;
+  const long long stride = is_v ? v_stride : k_stride;
+  const T* base = src + (long long)(q.row0 + lo - p0) * stride + (long long)head * hd + d;
+  const int n = hi - lo;
+  uint4 raw[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int t = t0 + p * per_pass;
+    raw[p] = t < n ? *reinterpret_cast<const uint4*>(base + (long long)t * stride) : make_uint4(0, 0, 0, 0);
+  }
+  unsigned a = 0;
+  bool odd = false;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    float f[kPer];
+    Val<T>::unpack(raw[p], f);
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const unsigned m = __float_as_uint(f[x]) & 0x7FFFFFFFu;
+      if (m < 0x7F800000u)
+        a = max(a, m);
+      else
+        odd = true;
+    }
+  }
+  a = __reduce_max_sync(0xFFFFFFFFu, a);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  if (odd) atomicOr(C.err, kErrNonFinite);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) a = max(a, red[w]);
+
+  const long long line = (long long)q.slot * C.kv_heads + head;
+  uint8_t* codes = (is_v ? C.v : C.k) + (line * C.max_ctx + (blk << C.block_log2)) * hd;
+  uint8_t* ep = (is_v ? C.v_exp : C.k_exp) + line * C.n_blocks + blk;
+  int e = kv8_least_exp(__uint_as_float(a), C.format);
+  const int held = lo - (blk << C.block_log2);
+  if (held > 0) {
+    const int e_held = kv8_exp(*ep);
+    if (e > e_held) {
+      const float f = pow2i(e_held - e);
+      uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+      for (int j = threadIdx.x; j < held * hd / 4; j += kThreads) {
+        float x[4];
+        kv8_decode4(w[j], C.format, x);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) x[y] = x[y] == x[y] ? x[y] * f : 0.f;
+        w[j] = kv8_encode4(x, C.format);
+      }
+    } else {
+      e = e_held;
+    }
+  }
+  __syncthreads();  // every thread has read the held exponent
+  if (threadIdx.x == 0) *ep = (uint8_t)(e + kKv8Bias);
+  const float f = pow2i(-e);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int t = t0 + p * per_pass;
+    if (t >= n) break;
+    float x[kPer];
+    Val<T>::unpack(raw[p], x);
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) x[y] = x[y] == x[y] ? x[y] * f : 0.f;
+    uint8_t* to = codes + (held + t) * hd + d;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint32_t*>(to) = kv8_encode4(x, C.format);
+    else
+      *reinterpret_cast<uint2*>(to) = make_uint2(kv8_encode4(x, C.format), kv8_encode4(x + 4, C.format));
+  }
+}
+
+template <typename T>
+cudaError_t append_typed(const Kv8Dev& C, const Kv8Rows& R, const void* k, long long k_stride, const void* v,
+                         long long v_stride, cudaStream_t s) {
+  // blocks that max_rows consecutive positions can touch
+  const int B = 1 << C.block_log2;
+  const int nb = (min(R.max_rows, C.max_ctx) + B - 2) / B + 1;
+  const long long grid = 2LL * R.n_seq * C.kv_heads * nb;
+  if (grid > 0x7FFFFFFFLL) return cudaErrorNotSupported;
+  const T *kk = static_cast<const T*>(k), *vv = static_cast<const T*>(v);
+  // passes of the CTA over the tokens that a block can gain in this call
+  const int most = min(B, R.max_rows);
+  const int per_pass = kThreads * Val<T>::kPer / C.head_dim;
+  const int np = (most + per_pass - 1) / per_pass;
+#define STRATA_APPEND(NP) \
+  append_kernel<T, NP><<<(unsigned)grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nb)
+  if (np <= 1)
+    STRATA_APPEND(1);
+  else if (np <= 2)
+    STRATA_APPEND(2);
+  else if (np <= 4)
+    STRATA_APPEND(4);
+  else if (np <= 8)
+    STRATA_APPEND(8);
+  else
+    STRATA_APPEND(16);
+#undef STRATA_APPEND
+  return cudaGetLastError();
+}
+
+// --- read -----------------------------------------------------------------------
+//
+// A CTA turns up to kReadPasses passes of tokens of one head into values: a
+// thread reads as many codes as fill a 16-byte store, so that both sides are
+// contiguous across a warp.  HBM bound (codes in, values out).
+constexpr int kReadPasses = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read_kernel(Kv8Dev C, Kv8Rows R, T* __restrict__ kout, long long k_stride,
+                                                        T* __restrict__ vout, long long v_stride, int nchunk) {
+  constexpr int kPer = Val<T>::kPer;
+  int id = blockIdx.x;
+  const int chunk = id % nchunk;
+  id /= nchunk;
+  const int head = id % C.kv_heads;
+  id /= C.kv_heads;
+  const bool is_v = id & 1;
+  const int i = id >> 1;
+  const Kv8Seq q = kv8_seq(R, C, i);
+  const bool ok = q.held_ok && q.length >= q.n;
+  if (!ok && threadIdx.x == 0 && chunk == 0 && head == 0 && !is_v) atomicOr(C.err, kErrIndex);
+  if (!q.rows_ok) return;
+  const int hd = C.head_dim;
+  const int tpt_log2 = (hd == 128 ? 7 : 6) - (kPer == 4 ? 2 : 3);
+  const int per_pass = kThreads >> tpt_log2;
+  const int d = (threadIdx.x & ((1 << tpt_log2) - 1)) * kPer;
+  const int t0 = chunk * (per_pass * kReadPasses) + (threadIdx.x >> tpt_log2);
+  const long long line = (long long)q.slot * C.kv_heads + head;
+  const int p0 = q.length - q.n;
+  const uint8_t* codes = (is_v ? C.v : C.k);
+  const uint8_t* eb = (is_v ? C.v_exp : C.k_exp);
+  if (ok) {
+    codes += (line * C.max_ctx + p0) * hd + d;
+    eb += line * C.n_blocks;
+  }
+  T* dst = is_v ? vout : kout;
+  const long long stride = is_v ? v_stride : k_stride;
+  dst += (long long)q.row0 * stride + (long long)head * hd + d;
+  uint2 raw[kReadPasses];
+  uint8_t ex[kReadPasses];
+#pragma unroll
+  for (int p = 0; p < kReadPasses; ++p) {
+    const int t = t0 + p * per_pass;
+    raw[p] = make_uint2(0, 0);
+    ex[p] = 0;
+    if (ok && t < q.n) {
+      if constexpr (kPer == 4)
+        raw[p].x = *reinterpret_cast<const uint32_t*>(codes + (long long)t * hd);
+      else
+        raw[p] = *reinterpret_cast<const uint2*>(codes + (long long)t * hd);
+      ex[p] = eb[(p0 + t) >> C.block_log2];
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kReadPasses; ++p) {
+    const int t = t0 + p * per_pass;
+    if (t >= q.n) break;
+    const float f = pow2i(kv8_exp(ex[p]));
+    float x[8];
+    kv8_decode4(raw[p].x, C.format, x);
+    if constexpr (kPer == 8) kv8_decode4(raw[p].y, C.format, x + 4);
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) x[y] = ok ? x[y] * f : 0.f;
+    *reinterpret_cast<uint4*>(dst + (long long)t * stride) = Val<T>::pack(x);
+  }
+}
+
+template <typename T>
+cudaError_t read_typed(const Kv8Dev& C, const Kv8Rows& R, void* k, long long k_stride, void* v, long long v_stride,
+                       cudaStream_t s) {
+  const int per_cta = kThreads * Val<T>::kPer / C.head_dim * kReadPasses;
+  const int nchunk = (R.max_rows + per_cta - 1) / per_cta;
+  const long long grid = 2LL * R.n_seq * C.kv_heads * nchunk;
+  if (grid > 0x7FFFFFFFLL) return cudaErrorNotSupported;
+  read_kernel<T><<<(unsigned)grid, kThreads, 0, s>>>(C, R, static_cast<T*>(k), k_stride, static_cast<T*>(v), v_stride,
+                                                     nchunk);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8Dev& C, const Kv8Rows& R, const void* k, long long k_stride, const void* v,
+                              long long v_stride, int dtype, cudaStream_t s) {
+  if (dtype == 0) return append_typed<float>(C, R, k, k_stride, v, v_stride, s);
+  if (dtype == 1) return append_typed<__half>(C, R, k, k_stride, v, v_stride, s);
+  return append_typed<__nv_bfloat16>(C, R, k, k_stride, v, v_stride, s);
+}
+
+cudaError_t launch_kv8_read(const Kv8Dev& C, const Kv8Rows& R, void* k, long long k_stride, void* v,
+                            long long v_stride, int dtype, cudaStream_t s) {
+  if (dtype == 0) return read_typed<float>(C, R, k, k_stride, v, v_stride, s);
+  if (dtype == 1) return read_typed<__half>(C, R, k, k_stride, v, v_stride, s);
+  return read_typed<__nv_bfloat16>(C, R, k, k_stride, v, v_stride, s);
+}
+
+}  // namespace strata

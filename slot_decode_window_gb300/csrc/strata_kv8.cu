@@ -1,0 +1,211 @@
+// C ABI of the slots' 8-bit KV caches: argument checks, the handle's error word
+// and the launches of kv8_rw.cu and kv8_attend.cu.
+#include <cmath>
+#include <new>
+
+#include "handle.h"
+#include "kv8.cuh"
+#include "strata_window.h"
+
+using namespace strata;
+
+struct strata_kv8 {
+  strata_kv8_desc desc;
+  strata_kv8_cache cache;
+  int device = 0, nsm = 0;
+  Kv8Dev C{};  // layer 0
+  void* ws = nullptr;
+  long long ws_bytes = 0;
+};
+
+namespace {
+
+void free_kv8(strata_kv8* h) {
+  if (!h) return;
+  if (h->ws) {
+    DeviceScope on(h->device);
+    cudaFree(h->ws);
+  }
+  delete h;
+}
+
+strata_status check_desc(const strata_kv8_desc* d) {
+  if (!d) return STRATA_EINVAL;
+  if (d->n_layers < 1 || d->n_slots < 1 || d->heads < 1 || d->kv_heads < 1 || d->max_ctx < 1) return STRATA_EINVAL;
+  if (d->heads % d->kv_heads != 0) return STRATA_EINVAL;
+  if (d->format != STRATA_KV8_E4M3 && d->format != STRATA_KV8_INT8) return STRATA_EINVAL;
+  if (d->head_dim != 64 && d->head_dim != 128) return STRATA_EUNSUPPORTED;
+  if (d->block != 16 && d->block != 32 && d->block != 64 && d->block != 128) return STRATA_EUNSUPPORTED;
+  if (d->heads > 1024 || d->max_ctx > (1 << 24)) return STRATA_EUNSUPPORTED;
+  // rows of the code arrays are addressed by 31 bits in the attention's copies
+  if ((long long)d->n_slots * d->kv_heads > 0x7FFFFFFFLL / d->max_ctx) return STRATA_EUNSUPPORTED;
+  return STRATA_OK;
+}
+
+long long lines(const strata_kv8_desc& d) { return (long long)d.n_slots * d.kv_heads; }
+long long n_blocks(const strata_kv8_desc& d) { return ((long long)d.max_ctx + d.block - 1) / d.block; }
+
+// The part of a call's checks that the three calls share.  *skip: nothing to do.
+strata_status check_call(const strata_kv8* h, int32_t layer, int32_t dtype, const strata_kv8_rows* r, bool* skip) {
+  *skip = false;
+  if (!h || !r || layer < 0 || layer >= h->desc.n_layers) return STRATA_EINVAL;
+  if (dtype < STRATA_F32 || dtype > STRATA_BF16) return STRATA_EINVAL;
+  if (r->n_seq < 0 || r->n_rows < 0 || r->max_rows < 0) return STRATA_EINVAL;
+  if (r->n_seq > kKv8MaxSeq || r->n_rows > (1 << 28)) return STRATA_EUNSUPPORTED;
+  if (r->n_seq == 0 || r->n_rows == 0 || r->max_rows == 0) {
+    *skip = true;
+    return STRATA_OK;
+  }
+  return r->row_start && r->slot && r->length ? STRATA_OK : STRATA_EINVAL;
+}
+
+strata_status check_values(const void* p, long long stride, int width, int dtype) {
+  const int size = dtype == STRATA_F32 ? 4 : 2;
+  if (!p || reinterpret_cast<uintptr_t>(p) % 16 != 0 || stride < width || stride > (1LL << 40) ||
+      (stride * size) % 16 != 0)
+    return STRATA_EINVAL;
+  return STRATA_OK;
+}
+
+Kv8Dev layer_dev(const strata_kv8* h, int layer) {
+  Kv8Dev C = h->C;
+  const long long codes = lines(h->desc) * h->desc.max_ctx * h->desc.head_dim * layer;
+  const long long exps = lines(h->desc) * C.n_blocks * layer;
+  C.k += codes, C.v += codes, C.k_exp += exps, C.v_exp += exps;
+  return C;
+}
+
+Kv8Rows rows_dev(const strata_kv8_rows* r) {
+  return {r->n_seq, r->n_rows, r->max_rows < r->n_rows ? r->max_rows : r->n_rows, r->row_start, r->slot, r->length};
+}
+
+strata_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return STRATA_OK;
+  cudaGetLastError();
+  return e == cudaErrorNotSupported ? STRATA_EUNSUPPORTED : STRATA_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_cache* cache, strata_kv8** out) {
+  if (!out) return STRATA_EINVAL;
+  *out = nullptr;
+  const strata_status st = check_desc(desc);
+  if (st != STRATA_OK) return st;
+  if (!cache || !cache->k || !cache->v || !cache->k_exp || !cache->v_exp) return STRATA_EINVAL;
+  if (reinterpret_cast<uintptr_t>(cache->k) % 128 != 0 || reinterpret_cast<uintptr_t>(cache->v) % 128 != 0)
+    return STRATA_EINVAL;
+  if (fault_is("alloc")) return STRATA_ENOMEM;
+  strata_kv8* h = new (std::nothrow) strata_kv8();
+  if (!h) return STRATA_ENOMEM;
+  h->desc = *desc;
+  h->cache = *cache;
+  if (cudaGetDevice(&h->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&h->nsm, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
+    cudaGetLastError();
+    free_kv8(h);
+    return STRATA_ECUDA;
+  }
+  h->ws_bytes = 256;
+  if (cudaMalloc(&h->ws, (size_t)h->ws_bytes) != cudaSuccess) {
+    cudaGetLastError();
+    free_kv8(h);
+    return STRATA_ENOMEM;
+  }
+  if (cudaMemset(h->ws, 0, (size_t)h->ws_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    free_kv8(h);
+    return STRATA_ECUDA;
+  }
+  Kv8Dev& C = h->C;
+  C.k = cache->k, C.v = cache->v, C.k_exp = cache->k_exp, C.v_exp = cache->v_exp;
+  C.n_slots = desc->n_slots, C.heads = desc->heads, C.kv_heads = desc->kv_heads;
+  C.head_dim = desc->head_dim, C.max_ctx = desc->max_ctx, C.format = desc->format;
+  C.n_blocks = (int)n_blocks(*desc);
+  C.block_log2 = desc->block == 16 ? 4 : desc->block == 32 ? 5 : desc->block == 64 ? 6 : 7;
+  C.err = static_cast<unsigned*>(h->ws);
+  *out = h;
+  return STRATA_OK;
+}
+
+strata_status strata_kv8_append(strata_kv8* h, int32_t layer, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream) {
+  bool skip;
+  strata_status st = check_call(h, layer, dtype, rows, &skip);
+  if (st != STRATA_OK || skip) return st;
+  const int width = h->desc.kv_heads * h->desc.head_dim;
+  if ((st = check_values(k, k_stride, width, dtype)) != STRATA_OK) return st;
+  if ((st = check_values(v, v_stride, width, dtype)) != STRATA_OK) return st;
+  if (fault_is("launch")) return STRATA_ECUDA;
+  DeviceScope on(h->device);
+  if (!on.ok) return launched(cudaErrorInvalidDevice);
+  return launched(launch_kv8_append(layer_dev(h, layer), rows_dev(rows), k, k_stride, v, v_stride, dtype,
+                                    static_cast<cudaStream_t>(cuda_stream)));
+}
+
+strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                              int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream) {
+  bool skip;
+  strata_status st = check_call(h, layer, dtype, rows, &skip);
+  if (st != STRATA_OK || skip) return st;
+  const int width = h->desc.kv_heads * h->desc.head_dim;
+  if ((st = check_values(k, k_stride, width, dtype)) != STRATA_OK) return st;
+  if ((st = check_values(v, v_stride, width, dtype)) != STRATA_OK) return st;
+  if (fault_is("launch")) return STRATA_ECUDA;
+  DeviceScope on(h->device);
+  if (!on.ok) return launched(cudaErrorInvalidDevice);
+  return launched(launch_kv8_read(layer_dev(h, layer), rows_dev(rows), k, k_stride, v, v_stride, dtype,
+                                  static_cast<cudaStream_t>(cuda_stream)));
+}
+
+strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int64_t q_stride, void* out,
+                                int64_t out_stride, int32_t dtype, float scale, const strata_kv8_rows* rows,
+                                void* cuda_stream) {
+  bool skip;
+  strata_status st = check_call(h, layer, dtype, rows, &skip);
+  if (st != STRATA_OK || skip) return st;
+  const int width = h->desc.heads * h->desc.head_dim;
+  if ((st = check_values(q, q_stride, width, dtype)) != STRATA_OK) return st;
+  if ((st = check_values(out, out_stride, width, dtype)) != STRATA_OK) return st;
+  if (!std::isfinite(scale)) return STRATA_EINVAL;
+  if (fault_is("launch")) return STRATA_ECUDA;
+  DeviceScope on(h->device);
+  if (!on.ok) return launched(cudaErrorInvalidDevice);
+  return launched(launch_kv8_attend(layer_dev(h, layer), rows_dev(rows), q, q_stride, out, out_stride, dtype, scale,
+                                    static_cast<cudaStream_t>(cuda_stream)));
+}
+
+strata_status strata_kv8_sync(strata_kv8* h) {
+  if (!h) return STRATA_EINVAL;
+  DeviceScope on(h->device);
+  unsigned err = 0;
+  if (!on.ok || cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(&err, h->C.err, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    cudaGetLastError();
+    return STRATA_ECUDA;
+  }
+  if (err == 0) return STRATA_OK;
+  if (cudaMemset(h->ws, 0, (size_t)h->ws_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    return STRATA_ECUDA;
+  }
+  return STRATA_EDEVICE;
+}
+
+strata_status strata_kv8_query(const strata_kv8* h, int64_t* cache_bytes, int64_t* workspace_bytes) {
+  if (!h) return STRATA_EINVAL;
+  const strata_kv8_desc& d = h->desc;
+  if (cache_bytes)
+    *cache_bytes = 2LL * d.n_layers * lines(d) * ((long long)d.max_ctx * d.head_dim + n_blocks(d));
+  if (workspace_bytes) *workspace_bytes = h->ws_bytes;
+  return STRATA_OK;
+}
+
+strata_status strata_kv8_destroy(strata_kv8* h) {
+  free_kv8(h);
+  return STRATA_OK;
+}
+
+}  // extern "C"
