@@ -597,7 +597,7 @@ typedef struct {
  * left out (nothing is written to the caches; zeros are written to its rows of
  * an output).  Both make the next strata_kv8_sync report EDEVICE. */
 typedef struct {
-  int32_t n_seq;             /* 0..4096 (0: nothing is done) */
+  int32_t n_seq;             /* 0..1024 (0: nothing is done) */
   int32_t n_rows;            /* rows of the value arrays (0: nothing is done) */
   int32_t max_rows;          /* no sequence has more rows than this */
   const int32_t* row_start;  /* device [n_seq + 1] */
@@ -642,7 +642,8 @@ strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_s
  * (length below the rows) attends to nothing: zeros.  Sums and softmax
  * statistics are fp32; products take 16-bit parts of q and of the softmax
  * weights, one for f16 and bf16 rows and two (22 bits) for f32 rows.  Cache
- * contents at positions a row does not see never reach its output.  Sequences
+ * contents at positions from length[i] on never reach an output, whatever
+ * their bits; below it codes are numbers (append writes no other).  Sequences
  * may share a slot.  q and out are [n_rows][heads][head_dim] of the same dtype
  * and must not overlap.  scale is finite.
  * The rows written by an earlier strata_kv8_append on the same stream are

@@ -2,6 +2,7 @@
 // the append, read and attention kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -13,7 +14,7 @@
 namespace strata {
 
 constexpr int kKv8EMin = -48, kKv8EMax = 47, kKv8Bias = 127;
-constexpr int kKv8MaxSeq = 4096;
+constexpr int kKv8MaxSeq = 1024;
 
 // One layer's caches as a launch sees them.
 struct Kv8Dev {
@@ -183,7 +184,14 @@ cudaError_t launch_kv8_append(const Kv8Dev& C, const Kv8Rows& R, const void* k, 
                               long long v_stride, int dtype, cudaStream_t s);
 cudaError_t launch_kv8_read(const Kv8Dev& C, const Kv8Rows& R, void* k, long long k_stride, void* v,
                             long long v_stride, int dtype, cudaStream_t s);
-cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const void* q, long long q_stride, void* out,
-                              long long out_stride, int dtype, float scale, cudaStream_t s);
+// The attention's copy descriptors: codes as [layers][rows][head_dim], boxes of 64 rows, swizzled.
+struct Kv8Maps {
+  CUtensorMap k, v;
+};
+// Workspace: 256 bytes that begin with the error word, then the attention's.
+long long kv8_attend_workspace(int nsm, int head_dim);
+cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& M, int layer, void* workspace, int nsm,
+                              const void* q, long long q_stride, void* out, long long out_stride, int dtype,
+                              float scale, cudaStream_t s);
 
 }  // namespace strata

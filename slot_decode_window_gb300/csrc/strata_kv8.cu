@@ -14,6 +14,7 @@ struct strata_kv8 {
   strata_kv8_cache cache;
   int device = 0, nsm = 0;
   Kv8Dev C{};  // layer 0
+  Kv8Maps maps{};
   void* ws = nullptr;
   long long ws_bytes = 0;
 };
@@ -44,6 +45,29 @@ strata_status check_desc(const strata_kv8_desc* d) {
 
 long long lines(const strata_kv8_desc& d) { return (long long)d.n_slots * d.kv_heads; }
 long long n_blocks(const strata_kv8_desc& d) { return ((long long)d.max_ctx + d.block - 1) / d.block; }
+
+// Codes as [layers][n_slots kv_heads max_ctx][head_dim] bytes in boxes of 64
+// rows; a row is one swizzle span.  The encoder is the driver's, found at run
+// time so that the library loads where there is no driver.
+bool make_map(CUtensorMap* map, uint8_t* base, const strata_kv8_desc& d) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return false;
+  const cuuint64_t rows = (cuuint64_t)lines(d) * d.max_ctx;
+  const cuuint64_t dims[3] = {(cuuint64_t)d.head_dim, rows, (cuuint64_t)d.n_layers};
+  const cuuint64_t strides[2] = {(cuuint64_t)d.head_dim, rows * d.head_dim};
+  const cuuint32_t box[3] = {(cuuint32_t)d.head_dim, 64, 1}, step[3] = {1, 1, 1};
+  return reinterpret_cast<Encode>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, step,
+                                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                      d.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
 
 // The part of a call's checks that the three calls share.  *skip: nothing to do.
 strata_status check_call(const strata_kv8* h, int32_t layer, int32_t dtype, const strata_kv8_rows* r, bool* skip) {
@@ -108,7 +132,12 @@ strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_ca
     free_kv8(h);
     return STRATA_ECUDA;
   }
-  h->ws_bytes = 256;
+  if (!make_map(&h->maps.k, cache->k, *desc) || !make_map(&h->maps.v, cache->v, *desc)) {
+    cudaGetLastError();
+    free_kv8(h);
+    return STRATA_ECUDA;
+  }
+  h->ws_bytes = kv8_attend_workspace(h->nsm, desc->head_dim);
   if (cudaMalloc(&h->ws, (size_t)h->ws_bytes) != cudaSuccess) {
     cudaGetLastError();
     free_kv8(h);
@@ -173,8 +202,8 @@ strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int
   if (fault_is("launch")) return STRATA_ECUDA;
   DeviceScope on(h->device);
   if (!on.ok) return launched(cudaErrorInvalidDevice);
-  return launched(launch_kv8_attend(layer_dev(h, layer), rows_dev(rows), q, q_stride, out, out_stride, dtype, scale,
-                                    static_cast<cudaStream_t>(cuda_stream)));
+  return launched(launch_kv8_attend(layer_dev(h, layer), rows_dev(rows), h->maps, layer, h->ws, h->nsm, q, q_stride,
+                                    out, out_stride, dtype, scale, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 strata_status strata_kv8_sync(strata_kv8* h) {

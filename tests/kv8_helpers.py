@@ -7,7 +7,8 @@ Attention.  For a row and head with weights p, values V and scores s:
   scaling each lose at most 2^-23 of c = scale sum |q||K|: under 18 * 2^-23 c; two 11-bit parts of q leave 2^-22 of
   the row's largest element: d = 2^-18 c + 2^-22 scale max|q| sum |K|.
 * a weight is off by 2 d (its score's and the maximum's), by 2^-20 (exp2) and by its 16-bit parts: one part 2^-11,
-  two 2^-22.
+  two 2^-22.  Below 2^-14 an f16 loses relative precision: weights are held relative to W = max p 2^ev and times 2^14,
+  so half of f16's least step, 2^-25, is 2^-39 W, and every position may add that times its code: 2^-39 W sum |code|.
 * the sums over n positions lose at most 2^-23 in each of n/16 + 24 steps (the splits' joins among them), in numerator
   and in denominator.
 The numerator's error is relative to A = sum p |V|; the result's rounding adds u |out|.
@@ -85,7 +86,10 @@ def attend_bound(q, kc, ke, vc, ve, seqs, block, scale, dtype, want):
                 d = 2.0 ** -18 * c + 2.0 ** -22 * scale * np.abs(x).max() * np.abs(kk).sum(-1)
                 w = 2 * d.max() + 2.0 ** -20 + part + (seen / 16 + 24) * 2.0 ** -23
                 a = p @ np.abs(v[h // group, :seen])
-                b[row0 + r, h] = 2 * w * a + half_step(dtype) * (np.abs(want[row0 + r, h]) + 2 * w * a)
+                step = np.exp2(ve[slot, h // group][np.arange(seen) // block].astype(np.float64))
+                floor = 2.0 ** -39 * (p * step).max() * (np.abs(v[h // group, :seen]) / step[:, None]).sum(0)
+                off = 2 * w * a + 2 * floor
+                b[row0 + r, h] = off + half_step(dtype) * (np.abs(want[row0 + r, h]) + off)
     tiny = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -149}[dtype]
     return b + tiny
 

@@ -386,7 +386,7 @@ def test_refusals(B):
         a = dict(layer=0, q=p, s=s, dtype=0, scale=1.0)
         a.update(kw)
         assert B.strata_kv8_attend(h, a["layer"], a["q"], a["s"], p, s, a["dtype"], a["scale"], rows.c) == EI, kw
-    for field, val, st in (("n_seq", -1, EI), ("n_rows", -1, EI), ("max_rows", -1, EI), ("n_seq", 4097, EU),
+    for field, val, st in (("n_seq", -1, EI), ("n_rows", -1, EI), ("max_rows", -1, EI), ("n_seq", 1025, EU),
                            ("row_start", None, EI), ("slot", None, EI), ("length", None, EI)):
         c = B.strata_kv8_rows(*(getattr(rows.c, n) for n, _ in rows.c._fields_))
         setattr(c, field, val)
