@@ -569,7 +569,7 @@ typedef enum { STRATA_KV8_E4M3 = 0, STRATA_KV8_INT8 = 1 } strata_kv8_format;
 typedef struct {
   int32_t n_layers;   /* 1.. */
   int32_t n_slots;    /* 1.. */
-  int32_t heads;      /* query heads, a multiple of kv_heads, at most 1024 */
+  int32_t heads;      /* query heads, at most 1024: a multiple of kv_heads, at most 128 of them to each */
   int32_t kv_heads;   /* 1.. */
   int32_t head_dim;   /* 64 or 128 */
   int32_t max_ctx;    /* positions a slot holds: 1.. */

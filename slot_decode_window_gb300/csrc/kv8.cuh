@@ -188,10 +188,19 @@ cudaError_t launch_kv8_read(const Kv8Dev& C, const Kv8Rows& R, void* k, long lon
 struct Kv8Maps {
   CUtensorMap k, v;
 };
+// Shared-memory limits of the attention kernels for a shape, on the current device (once per handle).
+cudaError_t setup_kv8_attend(int head_dim, int format);
 // Workspace: 256 bytes that begin with the error word, then the attention's.
 long long kv8_attend_workspace(int nsm, int head_dim);
 cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& M, int layer, void* workspace, int nsm,
                               const void* q, long long q_stride, void* out, long long out_stride, int dtype,
                               float scale, cudaStream_t s);
+
+// The many-row path of the same call (kv8_prompt.cu).
+int kv8_prompt_part_floats(int head_dim);
+cudaError_t setup_kv8_prompt(int head_dim, int format);
+cudaError_t launch_kv8_prompt(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& M, int layer, unsigned* count,
+                              float* parts, int nsm, const void* q, long long q_stride, void* out,
+                              long long out_stride, int dtype, float scale, cudaStream_t s);
 
 }  // namespace strata

@@ -37,7 +37,7 @@ strata_status check_desc(const strata_kv8_desc* d) {
   if (d->format != STRATA_KV8_E4M3 && d->format != STRATA_KV8_INT8) return STRATA_EINVAL;
   if (d->head_dim != 64 && d->head_dim != 128) return STRATA_EUNSUPPORTED;
   if (d->block != 16 && d->block != 32 && d->block != 64 && d->block != 128) return STRATA_EUNSUPPORTED;
-  if (d->heads > 1024 || d->max_ctx > (1 << 24)) return STRATA_EUNSUPPORTED;
+  if (d->heads > 1024 || d->heads / d->kv_heads > 128 || d->max_ctx > (1 << 24)) return STRATA_EUNSUPPORTED;
   // rows of the code arrays are addressed by 31 bits in the attention's copies
   if ((long long)d->n_slots * d->kv_heads > 0x7FFFFFFFLL / d->max_ctx) return STRATA_EUNSUPPORTED;
   return STRATA_OK;
@@ -132,7 +132,8 @@ strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_ca
     free_kv8(h);
     return STRATA_ECUDA;
   }
-  if (!make_map(&h->maps.k, cache->k, *desc) || !make_map(&h->maps.v, cache->v, *desc)) {
+  if (setup_kv8_attend(desc->head_dim, desc->format) != cudaSuccess || !make_map(&h->maps.k, cache->k, *desc) ||
+      !make_map(&h->maps.v, cache->v, *desc)) {
     cudaGetLastError();
     free_kv8(h);
     return STRATA_ECUDA;

@@ -26,6 +26,7 @@ def _desc(**kw):
     (dict(format=2), B.STRATA_EINVAL), (dict(format=-1), B.STRATA_EINVAL), (dict(head_dim=96), B.STRATA_EUNSUPPORTED),
     (dict(head_dim=0), B.STRATA_EUNSUPPORTED), (dict(block=48), B.STRATA_EUNSUPPORTED),
     (dict(block=8), B.STRATA_EUNSUPPORTED), (dict(heads=2048, kv_heads=2), B.STRATA_EUNSUPPORTED),
+    (dict(heads=129, kv_heads=1), B.STRATA_EUNSUPPORTED),
     (dict(max_ctx=(1 << 24) + 1), B.STRATA_EUNSUPPORTED),
     (dict(n_slots=1 << 20, max_ctx=1 << 11), B.STRATA_EUNSUPPORTED),
 ])
