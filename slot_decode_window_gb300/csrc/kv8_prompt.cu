@@ -20,11 +20,15 @@
 //
 // Roles (20 warps): two warpgroups of softmax (even and odd units, a row a
 // thread), one of correction (a row's output a thread), one of conversion, and
-// a warp each for TMA and MMA.
+// a warp each for MMA, TMA and the list of the CTA's segments.
 // A role sees what another wrote through the chain of barriers between them;
-// what a reader does not free by a barrier of its own (the units' factors and
-// statistics, the rows' powers of two) has four slots, of which the chain keeps
-// at most three in use.
+// what a reader does not free by a barrier of its own has slots enough that the
+// chain keeps them apart.  S(u) is issued after U(u - 3), so when S(u) can be
+// read the softmax of u - 3 is done, and the correction of u - 4 (U has one
+// place): 4 slots of statistics, written for u and read for u - 4; 4 of the
+// rows' powers of two, written for an item once S of the unit before it is
+// done; 8 of the units' factors, written once S(u - 2) is done, that is, after
+// the softmax of u - 5.
 //   TMA -> raw codes -> conversion -> f16 K, V -> MMA -> S -> softmax -> P (in
 //   S's place) -> MMA -> U -> correction
 #include "kv8.cuh"
@@ -36,27 +40,41 @@ constexpr int kPUnit = 128;      // positions per unit
 constexpr int kPRows = 128;      // rows per tile
 constexpr int kPThreads = 640;
 constexpr int kRegs = 96;        // registers per thread at launch; the roles' shares below sum to 5 x 96
-constexpr int kRegSoftmax = 112, kRegCorrect = 168, kRegConvert = 48, kRegIssue = 40;
-static_assert(2 * kRegSoftmax + kRegCorrect + kRegConvert + kRegIssue <= 5 * kRegs, "register split");
+constexpr int kSegs = 8;         // slots of the segment list
 constexpr float kPWeightTop = 14.f;
 constexpr int kRawStages = 3;
+constexpr int kScores = 3;         // places of S (and then P) in tensor memory
 
 template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kTile = kPRows * HD * 2;      // a 128-row f16 tile: panels of 64 halves (one swizzle span)
   static constexpr int kRaw = kPUnit * HD;           // a unit's codes of K or V
   static constexpr int kVStages = TWO ? 1 : 2;
-  static constexpr int kParts = TWO ? 2 : 1;
   static constexpr int kQ = 0;                       // byte offsets from a 1024-byte boundary
-  static constexpr int kK = kQ + kParts * kTile;
+  static constexpr int kK = kQ + (TWO ? 2 : 1) * kTile;
   static constexpr int kV = kK + 2 * kTile;
   static constexpr int kRawOff = kV + kVStages * kTile;
   static constexpr int kStats = kRawOff + kRawStages * kRaw;  // [4][128] float2: a unit's maxima and sums
   static constexpr int kRf = kStats + 4 * kPRows * 8;         // [4][128] the rows' powers of two, by item
-  static constexpr int kExp = kRf + 4 * kPRows * 4;           // [4][8] float4: a unit's factors per 16 positions
-  static constexpr int kBars = kExp + 4 * 8 * 16;
-  static constexpr int kMisc = kBars + 256;                   // tensor memory address, flags, scan sums
-  static constexpr int kPre = kMisc + 256;
+  static constexpr int kExp = kRf + 4 * kPRows * 4;           // [8][8] float4: a unit's factors per 16 positions
+  static constexpr int kBars = kExp + 8 * 8 * 16;
+  static constexpr int kMisc = kBars + 512;                   // tensor memory address, flags, scan sums
+  static constexpr int kSegOff = kMisc + 256;                 // [kSegs] Seg
+  static constexpr int kPre = kSegOff + 64 * kSegs;
+  // registers per thread by role (softmax keeps the launch's)
+  static constexpr int kRegCorrect = 176, kRegConvert = TWO ? 72 : 80, kRegIssue = TWO ? 40 : 32;
+  static_assert(2 * kRegs + kRegCorrect + kRegConvert + kRegIssue <= 5 * kRegs, "register split");
 };
+
+// What a CTA does of one item: units u0 to u1 of `units`.  Written once by the
+// list's warp, read by every role; a slot is free again when all have passed it.
+struct alignas(64) Seg {
+  int row0, n, length, slot;   // the sequence
+  int head, tile;
+  int u0, u1, units;
+  int end;                     // the CTA's units up to this segment's end
+  long long first;             // the item's first unit in the whole list
+};
+constexpr int kSegReaders = 8 + 4 + 4 + 1 + 1;  // warps (softmax, correction, conversion, MMA, TMA)
 
 struct PromptArgs {
   Kv8Dev C;
@@ -75,6 +93,12 @@ struct PromptArgs {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -132,6 +156,7 @@ constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
+#pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
     if (*dead) return false;
     if (clock64() - t0 > (1LL << 31)) {
@@ -148,11 +173,28 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, dead, err));
 }
 
+// Barrier of the 128 correction threads: whether all of them say yes.
+__device__ __forceinline__ bool all_of_128(bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.and.pred q, 1, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)yes)
+      : "memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ void p_tma_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ float p_ex2(float x) {
@@ -161,18 +203,26 @@ __device__ __forceinline__ float p_ex2(float x) {
   return r;
 }
 
-// Four neighbouring values of a row.
-__device__ __forceinline__ float4 p_load4(const void* p, int dtype, long long i) {
-  if (dtype == 0) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
-  if (dtype == 1) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+// A lane's E neighbouring values of a row of q, as they are in memory (TWO: f32, else f16 or bf16).
+template <int E, bool TWO> struct alignas(TWO ? 4 * E : 2 * E) Raw {
+  uint32_t w[TWO ? E : E / 2];
+  __device__ __forceinline__ void get(float* f, int dtype) const {
+    if constexpr (TWO) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        if (dtype == 1) {
+          const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          f[2 * i] = t.x, f[2 * i + 1] = t.y;
+        } else {
+          f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+    }
   }
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
-}
+};
 __device__ __forceinline__ void p_store4(void* p, int dtype, long long i, float4 v) {
   if (dtype == 0) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
@@ -187,16 +237,17 @@ __device__ __forceinline__ void p_store4(void* p, int dtype, long long i, float4
 
 // --- the list of units ----------------------------------------------------------
 
-// sum of floor((a i + b) / m) over i = 0..n-1, a, b >= 0 (Euclid's steps)
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum of floor((a i + b) / m) over i = 0..n-1 (Euclid's steps); a n + b stays below 2^32: a and m are at most 128,
+// n at most 2^24 row tiles and b about a cache's length.
+__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long sum = 0;
   while (n > 0) {
-    sum += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    sum += (long long)(n - 1) * n / 2 * (a / m) + (long long)n * (b / m);
     a %= m, b %= m;
-    const long long y = a * n + b;
+    const unsigned y = a * n + b;
     if (y < m) break;
     n = y / m, b = y % m;
-    const long long t = m;
+    const unsigned t = m;
     m = a, a = t;
   }
   return sum;
@@ -217,19 +268,32 @@ __device__ inline long long p_units_before(const Kv8Seq& s, int tokens, int tile
   const int base = s.length - s.n;
   int t0 = 0;
   if (base + tokens <= 0) t0 = min(tiles, -base / tokens);
-  if (tiles > t0) sum += floor_sum(tiles - t0, kPUnit, tokens, base + (long long)tokens * (t0 + 1) + kPUnit - 1);
+  if (tiles > t0) sum += floor_sum(tiles - t0, kPUnit, tokens, base + tokens * (t0 + 1) + kPUnit - 1);
   return sum;
 }
 __device__ __forceinline__ long long p_head_units(const Kv8Seq& s, int tokens) {
   return s.held_ok && s.n > 0 ? p_units_before(s, tokens, p_tiles(s, tokens)) : 0;
 }
 
-// The items of a CTA in turn; begin() finds the first, next() steps.
+// A sequence's row tiles are taken from both ends inwards (first, last, second,
+// ...): a tile's units grow with its position, and so every stretch of the list
+// has about the same number of items, whose starts cost a CTA time too.
+__device__ __forceinline__ int p_tile_at(const Kv8Seq& s, int tokens, int i) {
+  return i & 1 ? p_tiles(s, tokens) - 1 - (i >> 1) : i >> 1;
+}
+// Units of the first k tiles in that order.
+__device__ inline long long p_ordered_before(const Kv8Seq& s, int tokens, int k) {
+  const int tiles = p_tiles(s, tokens);
+  return p_units_before(s, tokens, (k + 1) >> 1) + p_units_before(s, tokens, tiles) -
+         p_units_before(s, tokens, tiles - (k >> 1));
+}
+
+// The items of a CTA's part of the list in turn; begin() finds the first, next() steps.
 struct PItem {
   Kv8Seq s;
-  int seq, head, tile, units;  // units of the whole item
-  int u0, u1;                  // the CTA's part of them
-  long long first;             // the item's first unit in the whole list
+  int seq, head, i, tile, units;  // i: the tile's place in the order
+  int u0, u1;
+  long long first;
 };
 
 __device__ inline void p_begin(PItem& it, const PromptArgs& A, const long long* pre, long long lo, long long hi) {
@@ -241,7 +305,6 @@ __device__ inline void p_begin(PItem& it, const PromptArgs& A, const long long* 
     else
       b = m;
   }
-  while (pre[a + 1] <= lo) ++a;
   it.seq = a;
   it.s = kv8_seq(A.R, A.C, a);
   long long r = lo - pre[a];
@@ -251,14 +314,15 @@ __device__ inline void p_begin(PItem& it, const PromptArgs& A, const long long* 
   int t0 = 0, t1 = p_tiles(it.s, A.tokens);  // before(t0) <= r < before(t1)
   while (t1 - t0 > 1) {
     const int m = (t0 + t1) >> 1;
-    if (p_units_before(it.s, A.tokens, m) <= r)
+    if (p_ordered_before(it.s, A.tokens, m) <= r)
       t0 = m;
     else
       t1 = m;
   }
-  it.tile = t0;
-  it.units = p_units(it.s, A.tokens, t0);
-  it.u0 = (int)(r - p_units_before(it.s, A.tokens, t0));
+  it.i = t0;
+  it.tile = p_tile_at(it.s, A.tokens, t0);
+  it.units = p_units(it.s, A.tokens, it.tile);
+  it.u0 = (int)(r - p_ordered_before(it.s, A.tokens, t0));
   it.u1 = (int)min((long long)it.units, it.u0 + (hi - lo));
   it.first = lo - it.u0;
 }
@@ -266,8 +330,8 @@ __device__ inline void p_begin(PItem& it, const PromptArgs& A, const long long* 
 // After a part that ended at unit u of the list (u < hi).
 __device__ inline void p_next(PItem& it, const PromptArgs& A, const long long* pre, long long u, long long hi) {
   do {
-    if (++it.tile >= p_tiles(it.s, A.tokens)) {
-      it.tile = 0;
+    if (++it.i >= p_tiles(it.s, A.tokens)) {
+      it.i = 0;
       if (++it.head >= A.C.kv_heads) {
         it.head = 0;
         do {
@@ -276,11 +340,113 @@ __device__ inline void p_next(PItem& it, const PromptArgs& A, const long long* p
         it.s = kv8_seq(A.R, A.C, it.seq);
       }
     }
+    it.tile = p_tile_at(it.s, A.tokens, it.i);
     it.units = p_units(it.s, A.tokens, it.tile);
   } while (it.units == 0);
   it.u0 = 0;
   it.u1 = (int)min((long long)it.units, hi - u);
   it.first = u;
+}
+
+// A stage of a ring of N and the parity of its current round.
+template <int N> struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++st == N) st = 0, ph ^= 1;
+  }
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A row's softmax over one unit: the 128 scores at s_addr become weights (16-bit
+// parts) relative to the unit's maximum m; l is their sum over 2^ev.  The
+// chunks are a rolled loop: the roles' straight-line code together has to stay
+// within the instruction cache (unrolled, instruction fetch was the largest
+// stall and a unit took 9400 cycles).
+template <bool TWO, bool MASKED>
+__device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac, float f_row, int left, float& m, float& l) {
+  m = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t r[32];
+    tc_ld32(s_addr + ch * 32, r);
+    tc_wait_ld();
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (ch * 32 + i >= left) r[i] = 0xFF800000u;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t* v = r + 16 * h;
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        a = max3(a, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        b = max3(b, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+      }
+      const float4 f = fac[ch * 2 + h];
+      a = fmaxf(a, b);
+      m = fmaxf(m, a == -INFINITY ? a : fmaf(a, f.x * f_row, f.y));
+    }
+  }
+  const float z = m == -INFINITY ? 0.f : kPWeightTop - m;
+  l = 0.f;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t r[32];
+    tc_ld32(s_addr + ch * 32, r);
+    tc_wait_ld();
+    uint32_t hi16[16], lo16[TWO ? 16 : 1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 f = fac[ch * 2 + h];
+      const float k = f.x * f_row, c = f.y + z;
+      const uint64_t k2 = pack2(k, k), c2 = pack2(c, c);
+      uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float w0, w1;
+        unpack2(fma2(pack2(__uint_as_float(r[16 * h + i]), __uint_as_float(r[16 * h + i + 1])), k2, c2), w0, w1);
+        w0 = p_ex2(w0), w1 = p_ex2(w1);
+        if constexpr (MASKED) {
+          if (ch * 32 + 16 * h + i >= left) w0 = 0.f;
+          if (ch * 32 + 16 * h + i + 1 >= left) w1 = 0.f;
+        }
+        sum = add2(sum, pack2(w0, w1));
+        const __half2 hh = __floats2half2_rn(w0, w1);
+        hi16[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+        if constexpr (TWO) {
+          const float2 back = __half22float2(hh);
+          lo16[8 * h + i / 2] = pack_half2(w0 - back.x, w1 - back.y);
+        }
+      }
+      float s0, s1;
+      unpack2(sum, s0, s1);
+      l = fmaf(s0 + s1, f.z, l);
+    }
+    // P takes the place of the 32 scores it came from: 16 columns of first parts, 16 of second ones
+    tc_st16(s_addr + ch * 32, hi16);
+    if constexpr (TWO) tc_st16(s_addr + ch * 32 + 16, lo16);
+  }
 }
 
 template <int HD, int FMT, bool TWO>
@@ -295,12 +461,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float4* factors = reinterpret_cast<float4*>(smem + P::kExp);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
   uint64_t *raw_full = bars, *raw_empty = bars + 3, *k_full = bars + 6, *k_empty = bars + 8, *v_full = bars + 10,
-           *v_empty = bars + 12, *q_full = bars + 14, *q_empty = bars + 15, *s_full = bars + 16, *p_full = bars + 18,
-           *u_full = bars + 20, *u_empty = bars + 22, *last = bars + 24;
+           *v_empty = bars + 12, *q_full = bars + 14, *q_empty = bars + 15, *s_full = bars + 16, *p_full = bars + 19,
+           *u_full = bars + 22, *u_empty = bars + 23, *last = bars + 24, *seg_full = bars + 32, *seg_empty = bars + 40;
+  const Seg* segs = reinterpret_cast<const Seg*>(smem + P::kSegOff);
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
   int* flag = reinterpret_cast<int*>(smem + P::kMisc + 12);
   long long* warp_sums = reinterpret_cast<long long*>(smem + P::kMisc + 16);
+  long long* span = reinterpret_cast<long long*>(smem + P::kMisc + 192);  // all units; this CTA's first, and end
   long long* pre = reinterpret_cast<long long*>(smem + P::kPre);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned* err = A.C.err;
@@ -310,10 +478,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4), mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
-      mbar_init(&u_full[i], 1), mbar_init(&u_empty[i], 4);
     }
+    for (int i = 0; i < kScores; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    mbar_init(u_full, 1), mbar_init(u_empty, 4);
     mbar_init(q_full, 4), mbar_init(q_empty, 1), mbar_init(last, 1);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], kSegReaders);
     *dead = 0;
     fence_mbar_init();
   }
@@ -356,13 +525,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (long long j = tid; j < (long long)blind * w4; j += kPThreads)
       p_store4(A.out, A.dtype, (s.row0 + j / w4) * A.out_stride + j % w4 * 4, make_float4(0, 0, 0, 0));
   }
-  const long long total = pre[n_seq];
-  const int G = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= G) return;
-  const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
-  const int n_units = (int)(hi - lo);
+  int n_units;
+  {
+    const long long total = pre[n_seq], G = min((long long)gridDim.x, total);
+    if (blockIdx.x >= G) return;
+    const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
+    n_units = (int)(hi - lo);
+    if (tid == 0) span[0] = total, span[1] = lo, span[2] = hi;  // for the roles that need them, now and then
+  }
 
-  if (warp == 16) {  // all of tensor memory: S0 S1 (128 columns each), U0 U1
+  if (warp == 16) {  // all of tensor memory: S in three places (128 columns each), U
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_word)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
@@ -373,138 +545,68 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp < 8) {
     // ---- softmax: warpgroup `odd` takes units odd, odd + 2, ...; a row a thread ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
     const int odd = warp >> 2, row = tid & 127;
-    const uint32_t s_addr = tmem + odd * 128 + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
-    PItem it;
-    p_begin(it, A, pre, lo, hi);
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
+    Ring<kScores> place;
+    if (odd) place.step();
+    const int row_tok = row < A.tokens * A.group ? row / A.group : 1 << 28;
+    Ring<kSegs> seg;
     bool ok = true;
     int n = 0;
-    for (int item = 0; n < n_units && ok; ++item) {
-      const int tok = it.tile * A.tokens + row / A.group;
-      const bool on = row < A.tokens * A.group && tok < it.s.n;
-      const int base = it.s.length - it.s.n;
-      const int lim = on ? max(0, base + tok + 1) : 0;          // positions the row sees
-      const int all = max(0, base + it.tile * A.tokens + 1);    // positions every row of the tile sees
+    for (int item = 0; n < n_units; ++item) {
+      if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
+      const Seg* it = segs + seg.st;
+      const int tok = it->tile * A.tokens + row_tok, base = it->length - it->n, u0 = it->u0, u1 = it->u1;
+      const int lim = tok < it->n ? max(0, base + tok + 1) : 0;  // positions the row sees
+      const int all = max(0, base + it->tile * A.tokens + 1);    // positions every row of the tile sees
       float f_row = 1.f;
       bool have = false;
-      for (int x = it.u0 + ((n ^ odd) & 1); x < it.u1; x += 2) {
-        const int at = n + x - it.u0;
-        if (!(ok = wait_warp(&s_full[odd], (at >> 1) & 1, dead, err))) break;
+      for (int x = u0 + ((n ^ odd) & 1); x < u1; x += 2) {
+        const int at = n + x - u0;
+        if (!(ok = wait_warp(&s_full[place.st], place.ph, dead, err))) break;
         tc_fence_after();
         if (!have) f_row = rf[(item & 3) * kPRows + row], have = true;
-        const float4* fac = factors + (at & 3) * 8;  // per 16 positions: scale 2^ek, ev, 2^-ev
-        const int p0 = x * kPUnit;
-        const bool masked = p0 + kPUnit > all;
-        uint32_t r[32];
-        float m = -INFINITY;
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tc_ld32(s_addr + ch * 32, r);
-          tc_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (p0 + ch * 32 + i >= lim) r[i] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              a = fmaxf(a, __uint_as_float(r[16 * h + i]));
-              b = fmaxf(b, __uint_as_float(r[16 * h + i + 1]));
-            }
-            const float4 f = fac[ch * 2 + h];
-            a = fmaxf(a, b);
-            m = fmaxf(m, a == -INFINITY ? a : fmaf(a, f.x * f_row, f.y));
-          }
-        }
-        const float z = m == -INFINITY ? 0.f : kPWeightTop - m;
-        float l = 0.f;
-        uint32_t rest[TWO ? 32 : 1];
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tc_ld32(s_addr + ch * 32, r);
-          tc_wait_ld();
-          uint32_t hi16[16], lo16[TWO ? 16 : 1];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 f = fac[ch * 2 + h];
-            const float k = f.x * f_row, c = f.y + z;
-            float sum = 0.f, sum2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float w0 = p_ex2(fmaf(__uint_as_float(r[16 * h + i]), k, c));
-              float w1 = p_ex2(fmaf(__uint_as_float(r[16 * h + i + 1]), k, c));
-              if (masked) {
-                const int p = p0 + ch * 32 + 16 * h + i;
-                if (p >= lim) w0 = 0.f;
-                if (p + 1 >= lim) w1 = 0.f;
-              }
-              sum += w0, sum2 += w1;
-              const __half2 hh = __floats2half2_rn(w0, w1);
-              hi16[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-              if constexpr (TWO) {
-                const float2 back = __half22float2(hh);
-                lo16[8 * h + i / 2] = pack_half2(w0 - back.x, w1 - back.y);
-              }
-            }
-            l = fmaf(sum + sum2, f.z, l);
-          }
-          // P's first parts go to columns 0..63 and the second ones to 64..127 of S's 128, each when those have been read
-          tc_st16(s_addr + ch * 16, hi16);
-          if constexpr (TWO) {
-            if (ch < 2) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) rest[16 * ch + i] = lo16[i];
-            } else {
-              if (ch == 2) {
-                uint32_t t[16];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) t[i] = rest[16 * y + i];
-                  tc_st16(s_addr + 64 + 16 * y, t);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) rest[i] = lo16[i];
-              } else {
-                uint32_t t[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) t[i] = rest[i];
-                tc_st16(s_addr + 96, t);
-                tc_st16(s_addr + 112, lo16);
-              }
-            }
-          }
-        }
+        const float4* fac = factors + (at & 7) * 8;  // per 16 positions: scale 2^ek, ev, 2^-ev
+        const int left = lim - x * kPUnit;  // positions of the unit that the row sees
+        const bool masked = (x + 1) * kPUnit > all;
+        float m, l;
+        if (masked)
+          unit_softmax<TWO, true>(lanes + place.st * 128, fac, f_row, left, m, l);
+        else
+          unit_softmax<TWO, false>(lanes + place.st * 128, fac, f_row, left, m, l);
         stats[(at & 3) * kPRows + row] = make_float2(m, l);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[odd]);
+        if (lane == 0) mbar_arrive(&p_full[place.st]);
+        place.step(), place.step();
       }
-      n += it.u1 - it.u0;
-      if (n < n_units) p_next(it, A, pre, lo + n, hi);
+      if (!ok) break;
+      n += u1 - u0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
+      seg.step();
     }
   } else if (warp < 12) {
     // ---- correction: a row's output in registers ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegCorrect));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kRegCorrect));
     const int row = tid & 127;
-    const uint32_t u_addr = tmem + 256 + ((uint32_t)(warp & 3) << 21);
-    PItem it;
-    p_begin(it, A, pre, lo, hi);
+    const uint32_t u_addr = tmem + kScores * 128 + ((uint32_t)(warp & 3) << 21);
+    const int row_tok = row < A.tokens * A.group ? row / A.group : 1 << 28, row_head = row % A.group;
+    Ring<kSegs> seg;
     bool ok = true;
     int n = 0;
     while (n < n_units) {
+      // all four warps go on or stop together: the barriers below count them all
+      if (!all_of_128(wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
+      const Seg* it = segs + seg.st;
       float o[HD];
 #pragma unroll
       for (int i = 0; i < HD; ++i) o[i] = 0.f;
       float m = -INFINITY, l = 0.f;
-      for (int x = it.u0; x < it.u1; ++x) {
-        const int at = n + x - it.u0;
-        if (ok) ok = wait_warp(&u_full[at & 1], (at >> 1) & 1, dead, err);
+      for (int x = it->u0; x < it->u1; ++x) {
+        const int at = n + x - it->u0;
+        if (ok) ok = wait_warp(u_full, at & 1, dead, err);
         if (!ok) break;
         tc_fence_after();
         const float2 st = stats[(at & 3) * kPRows + row];
@@ -517,33 +619,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int ch = 0; ch < HD / 32; ++ch) {
           uint32_t r[32];
-          tc_ld32(u_addr + (at & 1) * 128 + ch * 32, r);
+          tc_ld32(u_addr + ch * 32, r);
           if (grew) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[ch * 32 + i] *= a;
           }
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[ch * 32 + i] = fmaf(__uint_as_float(r[i]), b, o[ch * 32 + i]);
+          for (int i = 0; i < 32; i += 2)
+            unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pack2(b, b),
+                         pack2(o[ch * 32 + i], o[ch * 32 + i + 1])),
+                    o[ch * 32 + i], o[ch * 32 + i + 1]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&u_empty[at & 1]);
+        if (lane == 0) mbar_arrive(u_empty);
       }
-      n += it.u1 - it.u0;
-      const int tok = it.tile * A.tokens + row / A.group;
-      const bool on = row < A.tokens * A.group && tok < it.s.n;
-      const long long to = (long long)(it.s.row0 + tok) * A.out_stride + (long long)(it.head * A.group + row % A.group) * HD;
+      n += it->u1 - it->u0;
+      const int tok = it->tile * A.tokens + row_tok;
+      const bool on = tok < it->n;
+      const long long to = (long long)(it->row0 + tok) * A.out_stride + (long long)(it->head * A.group + row_head) * HD;
       bool write = on && ok;
-      if (it.u0 != 0 || it.u1 != it.units) {
+      if (it->u0 != 0 || it->u1 != it->units) {
         constexpr int kPart = (HD + 2) * kPRows;
-        float* part = A.parts + (long long)(2 * blockIdx.x + (it.first + it.u0 == lo ? 0 : 1)) * kPart + row;
+        const long long total = span[0], lo = span[1], G = min((long long)gridDim.x, total);
+        float* part = A.parts + (long long)(2 * blockIdx.x + (it->first + it->u0 == lo ? 0 : 1)) * kPart + row;
 #pragma unroll
         for (int i = 0; i < HD; ++i) part[i * kPRows] = o[i];
         part[HD * kPRows] = m, part[(HD + 1) * kPRows] = l;
         __threadfence();
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        const int c0 = (int)(((it.first + 1) * G - 1) / total), c1 = (int)(((it.first + it.units) * G - 1) / total);
+        const int c0 = (int)(((it->first + 1) * G - 1) / total), c1 = (int)(((it->first + it->units) * G - 1) / total);
         if (row == 0) {
           __threadfence();
           *flag = atomicInc(&A.count[c0], (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
@@ -552,7 +658,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         asm volatile("bar.sync 1, 128;" ::: "memory");
         write = write && *flag;
         if (write) {
-          const int s0 = 2 * c0 + (total * c0 / G == it.first ? 0 : 1);
+          const int s0 = 2 * c0 + (total * c0 / G == it->first ? 0 : 1);
           m = -INFINITY, l = 0.f;
           for (int y = c0; y <= c1; ++y)
             m = fmaxf(m, __ldcg(A.parts + (long long)(y == c0 ? s0 : 2 * y) * kPart + HD * kPRows + row));
@@ -575,242 +681,315 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int i = 0; i < HD; i += 4)
           p_store4(A.out, A.dtype, to + i, make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
       }
-      if (n < n_units) p_next(it, A, pre, lo + n, hi);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
+      seg.step();
     }
   } else if (warp < 16) {
     // ---- conversion: q of each item, then K and V of its units, to f16 tiles ----
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConvert));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegConvert));
     const int t = tid & 127;
-    PItem kt;  // the K side runs one unit ahead of the V side
-    p_begin(kt, A, pre, lo, hi);
-    int k_item = 0, k_at = 0, k_end = kt.u1 - kt.u0;  // units of the list before the K side's item ends
-    int k_x = kt.u0, v_x = kt.u0, v_end = k_end;
-    int v_len = kt.s.length, k_len = kt.s.length, v_len_next = 0, v_x_next = 0, v_end_next = 0;
-    bool ok = true, k_new = true;
-    int raw = 0;
-    // one tile of codes to f16; positions from `length` on become 0
-    auto tile = [&](uint8_t* dst, int p0, int length) {
-      const uint8_t* src = smem + P::kRawOff + (raw % kRawStages) * P::kRaw;
+    Ring<kRawStages> raw;
+    bool ok = true;
+    // one tile of codes to f16, 4 chunks of 16 codes in flight; rows from `valid` on become 0
+    auto tile = [&](uint8_t* dst, int valid) {
+      const uint8_t* src = smem + P::kRawOff + raw.st * P::kRaw;
       constexpr int kChunks = HD / 16;  // 16-code chunks per row
-#pragma unroll 2
-      for (int j = 0; j < kChunks; ++j) {
-        const int id = j * 128 + t, r = id / kChunks, ch = id % kChunks;
-        const uint8_t* from = HD == 128 ? src + r * 128 + ((ch ^ (r & 7)) << 4) : src + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-        uint4 cw = *reinterpret_cast<const uint4*>(from);
-        if (p0 + r >= length) cw = make_uint4(0, 0, 0, 0);
-        uint4 h0, h1;
-        if constexpr (FMT == 0) {
-          h0.x = e4m3x2_to_f16x2(cw.x & 0xFFFFu), h0.y = e4m3x2_to_f16x2(cw.x >> 16);
-          h0.z = e4m3x2_to_f16x2(cw.y & 0xFFFFu), h0.w = e4m3x2_to_f16x2(cw.y >> 16);
-          h1.x = e4m3x2_to_f16x2(cw.z & 0xFFFFu), h1.y = e4m3x2_to_f16x2(cw.z >> 16);
-          h1.z = e4m3x2_to_f16x2(cw.w & 0xFFFFu), h1.w = e4m3x2_to_f16x2(cw.w >> 16);
-        } else {
-          const uint32_t in[4] = {cw.x ^ 0x80808080u, cw.y ^ 0x80808080u, cw.z ^ 0x80808080u, cw.w ^ 0x80808080u};
-          uint32_t out[8];
+      const int ch = t % kChunks, r0 = t / kChunks;
+      constexpr int kStep = 128 / kChunks;  // rows from one chunk of a thread to the next: a multiple of 8 (16)
+      // so the swizzles do not change
+      const int from = HD == 128 ? r0 * 128 + ((ch ^ (r0 & 7)) << 4) : r0 * 64 + ((ch ^ ((r0 >> 1) & 3)) << 4);
+      const int flip = ch >> 2;  // the two halves' stores alternate so that 8 lanes of a row meet 8 different chunks
+      const int to = (ch >> 2) * (kPRows * 128) + r0 * 128;
+      const int c0 = (((ch & 3) * 2 + flip) ^ (r0 & 7)) << 4, c1 = (((ch & 3) * 2 + 1 - flip) ^ (r0 & 7)) << 4;
+#pragma unroll(TWO ? 1 : 2)
+      for (int j = 0; j < kChunks; j += 4) {
+        uint4 cw[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            out[2 * i] = hsub2_u32(__byte_perm(in[i], 0x64646464u, 0x4140), 0x64806480u);
-            out[2 * i + 1] = hsub2_u32(__byte_perm(in[i], 0x64646464u, 0x4342), 0x64806480u);
-          }
-          h0 = make_uint4(out[0], out[1], out[2], out[3]);
-          h1 = make_uint4(out[4], out[5], out[6], out[7]);
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = *reinterpret_cast<const uint4*>(src + from + (j + i) * (kStep * HD));
         }
-        // the two halves' stores alternate so that 8 lanes of a row meet 8 different chunks
-        uint8_t* to = dst + (ch >> 2) * (kPRows * 128) + r * 128;
-        const int c0 = (ch & 3) * 2, flip = ch >> 2;
-        const uint4 first = flip ? h1 : h0, second = flip ? h0 : h1;
-        *reinterpret_cast<uint4*>(to + (((c0 + flip) ^ (r & 7)) << 4)) = first;
-        *reinterpret_cast<uint4*>(to + (((c0 + 1 - flip) ^ (r & 7)) << 4)) = second;
+        if (valid < kPUnit) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r0 + (j + i) * kStep >= valid) cw[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 h0, h1;
+          if constexpr (FMT == 0) {
+            h0.x = e4m3x2_to_f16x2(cw[i].x & 0xFFFFu), h0.y = e4m3x2_to_f16x2(cw[i].x >> 16);
+            h0.z = e4m3x2_to_f16x2(cw[i].y & 0xFFFFu), h0.w = e4m3x2_to_f16x2(cw[i].y >> 16);
+            h1.x = e4m3x2_to_f16x2(cw[i].z & 0xFFFFu), h1.y = e4m3x2_to_f16x2(cw[i].z >> 16);
+            h1.z = e4m3x2_to_f16x2(cw[i].w & 0xFFFFu), h1.w = e4m3x2_to_f16x2(cw[i].w >> 16);
+          } else {
+            const uint32_t in[4] = {cw[i].x ^ 0x80808080u, cw[i].y ^ 0x80808080u, cw[i].z ^ 0x80808080u, cw[i].w ^ 0x80808080u};
+            uint32_t out[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              out[2 * y] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4140), 0x64806480u);
+              out[2 * y + 1] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4342), 0x64806480u);
+            }
+            h0 = make_uint4(out[0], out[1], out[2], out[3]);
+            h1 = make_uint4(out[4], out[5], out[6], out[7]);
+          }
+          uint8_t* at = dst + to + (j + i) * (kStep * 128);
+          *reinterpret_cast<uint4*>(at + c0) = flip ? h1 : h0;
+          *reinterpret_cast<uint4*>(at + c1) = flip ? h0 : h1;
+        }
       }
     };
-    auto done = [&](uint64_t* bar) {
+    // q of a segment: a warp brings in its 32 rows, a row at a time, lane l the dims l E .. l E + E - 1
+    auto load_q = [&](const Seg* it, float* powers) {
+      constexpr int E = HD / 32, kBatch = 8;
+      const int r_first = (warp & 3) * 32;
+      int tok = it->tile * A.tokens + r_first / A.group, h = r_first % A.group;
+      const int tok_end = min(it->n, (it->tile + 1) * A.tokens);
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += kBatch) {
+        Raw<E, TWO> raw_q[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          raw_q[b] = Raw<E, TWO>{};
+          if (tok < tok_end)
+            raw_q[b] = reinterpret_cast<const Raw<E, TWO>*>(static_cast<const char*>(A.q) +
+                ((long long)(it->row0 + tok) * A.q_stride + (long long)(it->head * A.group + h) * HD) * (TWO ? 4 : 2))[lane];
+          if (++h == A.group) h = 0, ++tok;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int row = r_first + r0 + b;
+          float f[E];
+          raw_q[b].get(f, A.dtype);
+          unsigned top = 0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
+          const float down = pow2i(-e) * A.sign;
+          if (lane == 0) powers[row] = pow2i(e);
+          uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+          for (int y = 0; y < E / 2; ++y) {
+            const float x0 = f[2 * y] * down, x1 = f[2 * y + 1] * down;
+            const __half2 hh = __floats2half2_rn(x0, x1);
+            hi[y] = *reinterpret_cast<const uint32_t*>(&hh);
+            const float2 back = __half22float2(hh);
+            lo[y] = pack_half2(x0 - back.x, x1 - back.y);
+          }
+          const int byte = lane * E * 2;  // within the row's halves
+          uint8_t* to = smem + P::kQ + (byte >> 7) * (kPRows * 128) + row * 128 + ((((byte & 127) >> 4) ^ (row & 7)) << 4) + (byte & 15);
+          if constexpr (E == 4) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            if constexpr (TWO) *reinterpret_cast<uint2*>(to + P::kTile) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint32_t*>(to) = hi[0];
+            if constexpr (TWO) *reinterpret_cast<uint32_t*>(to + P::kTile) = lo[0];
+          }
+        }
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+    // jobs K0, K1, K2, V0, K3, V1, ..., V(n-1): the K side runs two units ahead of the V side
+    Ring<kSegs> kseg, vseg;
+    Ring<2> kst;
+    Ring<P::kVStages> vst;
+    int k_at = 0, k_end = 0, k_x = 0, k_len = 0, v_at = 0, v_end = 0, v_x = 0, v_len = 0, items = 0;
+    // factors per 16 positions of the next K unit, fetched one unit ahead by 8 threads
+    int e_next = 0;
+    auto fetch = [&](const Seg* it, int x) {
+      const int p = x * kPUnit + t * 16;
+      if (t < 8 && p < it->length) {
+        const long long at = ((long long)it->slot * A.C.kv_heads + it->head) * A.C.n_blocks + (p >> A.C.block_log2);
+        e_next = A.C.k_exp[at] | A.C.v_exp[at] << 8;
+      }
+    };
+    while (v_at < n_units) {
+      const bool is_k = k_at < n_units && k_at <= v_at + kScores - 1;
+      uint8_t* dst;
+      uint64_t* full;
+      int valid;
+      if (is_k) {
+        if (k_at == k_end) {
+          if (k_at > 0) kseg.step();
+          if (!(ok = wait_warp(&seg_full[kseg.st], kseg.ph, dead, err))) break;
+          const Seg* it = segs + kseg.st;
+          k_end = it->end, k_x = it->u0, k_len = it->length;
+          fetch(it, k_x);
+          // once the last product with the old q is done
+          if (items > 0 && !(ok = wait_warp(q_empty, (items - 1) & 1, dead, err))) break;
+          load_q(it, rf + (items & 3) * kPRows);
+          ++items;
+        }
+        if (k_at >= 2 && !(ok = wait_warp(&k_empty[kst.st], kst.ph ^ 1, dead, err))) break;
+        if (t < 8)
+          factors[(k_at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(kv8_exp((uint8_t)e_next)), (float)kv8_exp((uint8_t)(e_next >> 8)),
+                                                    pow2i(-kv8_exp((uint8_t)(e_next >> 8))), 0.f);
+        dst = smem + P::kK + kst.st * P::kTile, full = &k_full[kst.st], valid = k_len - k_x * kPUnit;
+        kst.step();
+        ++k_at, ++k_x;
+        if (k_at < k_end) fetch(segs + kseg.st, k_x);
+      } else {
+        if (v_at == v_end) {
+          if (v_at > 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[vseg.st]);
+            vseg.step();
+          }
+          v_end = segs[vseg.st].end, v_x = segs[vseg.st].u0, v_len = segs[vseg.st].length;
+        }
+        if (v_at >= P::kVStages && !(ok = wait_warp(&v_empty[vst.st], vst.ph ^ 1, dead, err))) break;
+        dst = smem + P::kV + vst.st * P::kTile, full = &v_full[vst.st], valid = v_len - v_x * kPUnit;
+        vst.step();
+        ++v_at, ++v_x;
+      }
+      if (!(ok = wait_warp(&raw_full[raw.st], raw.ph, dead, err))) break;
+      tile(dst, valid);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar);
-        mbar_arrive(&raw_empty[raw % kRawStages]);
+        mbar_arrive(full);
+        mbar_arrive(&raw_empty[raw.st]);
       }
-      ++raw;
-    };
-    for (int v_at = -1; v_at < n_units && ok; ++v_at) {
-      if (k_at < n_units) {
-        if (k_new) {  // q of the item, once the last product with the old one is done
-          if (k_item > 0 && !(ok = wait_warp(q_empty, (k_item - 1) & 1, dead, err))) break;
-          const int tok = kt.tile * A.tokens + t / A.group;
-          const bool on = t < A.tokens * A.group && tok < kt.s.n;
-          const long long from = (long long)(kt.s.row0 + tok) * A.q_stride + (long long)(kt.head * A.group + t % A.group) * HD;
-          unsigned top = 0;
-          if (on) {
-#pragma unroll 8
-            for (int i = 0; i < HD; i += 4) {
-              const float4 f = p_load4(A.q, A.dtype, from + i);
-              top = max(max(top, __float_as_uint(f.x) & 0x7FFFFFFFu), __float_as_uint(f.y) & 0x7FFFFFFFu);
-              top = max(max(top, __float_as_uint(f.z) & 0x7FFFFFFFu), __float_as_uint(f.w) & 0x7FFFFFFFu);
-            }
-          }
-          const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
-          const float down = pow2i(-e) * A.sign;
-          rf[(k_item & 3) * kPRows + t] = pow2i(e);
-#pragma unroll 2
-          for (int i = 0; i < HD; i += 8) {
-            float f[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) f[y] = 0.f;
-            if (on) {
-              const float4 a = p_load4(A.q, A.dtype, from + i), b = p_load4(A.q, A.dtype, from + i + 4);
-              f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-            }
-            uint32_t h[4], g[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float x0 = f[2 * y] * down, x1 = f[2 * y + 1] * down;
-              const __half2 hh = __floats2half2_rn(x0, x1);
-              h[y] = *reinterpret_cast<const uint32_t*>(&hh);
-              if constexpr (TWO) {
-                const float2 back = __half22float2(hh);
-                g[y] = pack_half2(x0 - back.x, x1 - back.y);
-              }
-            }
-            uint8_t* to = smem + P::kQ + (i >> 6) * (kPRows * 128) + t * 128 + ((((i & 63) >> 3) ^ (t & 7)) << 4);
-            *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-            if constexpr (TWO) *reinterpret_cast<uint4*>(to + P::kTile) = make_uint4(g[0], g[1], g[2], g[3]);
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
-          k_new = false;
-        }
-        const int st = k_at & 1;
-        if (k_at >= 2 && !(ok = wait_warp(&k_empty[st], ((k_at >> 1) - 1) & 1, dead, err))) break;
-        if (t < 8) {  // factors per 16 positions
-          const int p = k_x * kPUnit + t * 16;
-          int ek = 0, ev = 0;
-          if (p < k_len) {
-            const long long line = (long long)kt.s.slot * A.C.kv_heads + kt.head;
-            ek = kv8_exp(A.C.k_exp[line * A.C.n_blocks + (p >> A.C.block_log2)]);
-            ev = kv8_exp(A.C.v_exp[line * A.C.n_blocks + (p >> A.C.block_log2)]);
-          }
-          factors[(k_at & 3) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
-        }
-        if (!(ok = wait_warp(&raw_full[raw % kRawStages], (raw / kRawStages) & 1, dead, err))) break;
-        tile(smem + P::kK + st * P::kTile, k_x * kPUnit, k_len);
-        done(&k_full[st]);
-        ++k_at, ++k_x;
-      }
-      if (v_at >= 0) {
-        const int st = v_at % P::kVStages;
-        if (v_at >= P::kVStages && !(ok = wait_warp(&v_empty[st], (v_at / P::kVStages - 1) & 1, dead, err))) break;
-        if (!(ok = wait_warp(&raw_full[raw % kRawStages], (raw / kRawStages) & 1, dead, err))) break;
-        tile(smem + P::kV + st * P::kTile, v_x * kPUnit, v_len);
-        done(&v_full[st]);
-        ++v_x;
-        if (v_at + 1 == v_end && v_at + 1 < n_units) v_x = v_x_next, v_len = v_len_next, v_end = v_end_next;
-      }
-      if (k_at == k_end && k_at < n_units) {
-        p_next(kt, A, pre, lo + k_at, hi);
-        k_end += kt.u1 - kt.u0;
-        k_x = kt.u0, k_len = kt.s.length, k_new = true, ++k_item;
-        v_x_next = k_x, v_len_next = k_len, v_end_next = k_end;  // the V side changes over one step later
-      }
+      raw.step();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegIssue));
-    if (warp == 16 && lane == 0) {
-      // ---- MMA ----
-      PItem it;
-      p_begin(it, A, pre, lo, hi);
-      int item = 0, q_end = it.u1 - it.u0;
-      bool ok = true, fresh = true;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegIssue));
+    if (warp == 16) {
+      // ---- MMA: the whole warp keeps step (so that descriptors stay in uniform registers), one lane issues ----
+      Ring<kSegs> seg;
+      int item = 0, q_end = 0, at_s = 0;
+      bool ok = true;
       const uint64_t q_desc = tc_desc(smem + P::kQ, 1024, 16), k_desc = tc_desc(smem + P::kK, 1024, 16),
                      v_desc = tc_desc(smem + P::kV, 1024, kPRows * 128);
       constexpr uint32_t s_id = tc_idesc(kPUnit, false), u_id = tc_idesc(HD, true);
-      auto scores = [&](int at) {  // S(at) = Q K(at)^T
-        if (fresh) {
-          if (!(ok = wait_for(q_full, item & 1, dead, err))) return;
-          fresh = false;
-        }
-        if (!(ok = wait_for(&k_full[at & 1], (at >> 1) & 1, dead, err))) return;
-        tc_fence_after();
-        const uint32_t d = tmem + (at & 1) * 128;
-#pragma unroll
-        for (int part = 0; part < P::kParts; ++part)
-#pragma unroll
-          for (int y = 0; y < HD / 16; ++y) {
-            const uint64_t step = ((y >> 2) * (kPRows * 128) + (y & 3) * 32) >> 4;
-            tc_mma_ss(d, q_desc + step + ((part * P::kTile) >> 4), k_desc + step + (((at & 1) * P::kTile) >> 4), s_id,
-                      part > 0 || y > 0);
+      // products in the order S0, S1, S2, U0, S3, U1, S4, ...: U(at) frees S's place for S(at + 3), so the softmax
+      // warps always have scores waiting
+      Ring<kScores> p_at, s_at;
+      for (int at = -kScores; at < n_units; ++at) {
+        if (at >= 0) {  // U(at) = P(at) V(at)
+          const int st = P::kVStages == 2 ? at & 1 : 0;
+          if (!(ok = wait_warp(&p_full[p_at.st], p_at.ph, dead, err))) break;
+          if (!(ok = wait_warp(&v_full[st], (P::kVStages == 2 ? at >> 1 : at) & 1, dead, err))) break;
+          if (at >= 1 && !(ok = wait_warp(u_empty, (at - 1) & 1, dead, err))) break;
+          tc_fence_after();
+          const uint32_t a = tmem + p_at.st * 128, d = tmem + kScores * 128;
+          const uint64_t b = v_desc + ((st * P::kTile) >> 4);
+          if (elect_one()) {
+#pragma unroll(TWO ? 2 : 8)
+            for (int y = 0; y < kPUnit / 16; ++y) {
+              tc_mma_ts(d, a + (y >> 1) * 32 + (y & 1) * 8, b + ((y * 16 * 128) >> 4), u_id, y > 0);
+              if constexpr (TWO) tc_mma_ts(d, a + (y >> 1) * 32 + (y & 1) * 8 + 16, b + ((y * 16 * 128) >> 4), u_id, 1);
+            }
+            tc_commit(u_full);
+            tc_commit(&v_empty[st]);
           }
-        tc_commit(&s_full[at & 1]);
-        tc_commit(&k_empty[at & 1]);
-        if (at + 1 == q_end) {
-          tc_commit(q_empty);
-          if (at + 1 < n_units) {
-            p_next(it, A, pre, lo + at + 1, hi);
-            q_end += it.u1 - it.u0;
-            ++item, fresh = true;
-          }
+          __syncwarp();
+          p_at.step();
         }
-      };
-      scores(0);
-      if (ok && n_units > 1) scores(1);
-      for (int at = 0; at < n_units && ok; ++at) {
-        if (!(ok = wait_for(&p_full[at & 1], (at >> 1) & 1, dead, err))) break;
-        if (!(ok = wait_for(&v_full[at % P::kVStages], (at / P::kVStages) & 1, dead, err))) break;
-        if (at >= 2 && !(ok = wait_for(&u_empty[at & 1], ((at >> 1) - 1) & 1, dead, err))) break;
-        tc_fence_after();
-        const uint32_t a = tmem + (at & 1) * 128, d = tmem + 256 + (at & 1) * 128;
-#pragma unroll
-        for (int part = 0; part < P::kParts; ++part)
-#pragma unroll
-          for (int y = 0; y < kPUnit / 16; ++y)
-            tc_mma_ts(d, a + part * 64 + y * 8,
-                      v_desc + ((y * 16 * 128) >> 4) + (((at % P::kVStages) * P::kTile) >> 4), u_id, part > 0 || y > 0);
-        tc_commit(&u_full[at & 1]);
-        tc_commit(&v_empty[at % P::kVStages]);
-        if (at + 2 < n_units) scores(at + 2);
+        if (at_s < n_units) {  // S = Q K^T
+          if (at_s == q_end) {
+            if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
+            q_end = segs[seg.st].end;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
+            seg.step();
+            if (!(ok = wait_warp(q_full, item & 1, dead, err))) break;
+            ++item;
+          }
+          if (!(ok = wait_warp(&k_full[at_s & 1], (at_s >> 1) & 1, dead, err))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + s_at.st * 128;
+          const uint64_t b = k_desc + (((at_s & 1) * P::kTile) >> 4);
+          if (elect_one()) {
+#pragma unroll(TWO ? 2 : 8)
+            for (int y = 0; y < HD / 16; ++y) {
+              const uint32_t step = ((y >> 2) * (kPRows * 128) + (y & 3) * 32) >> 4;
+              tc_mma_ss(d, q_desc + step, b + step, s_id, y > 0);
+              if constexpr (TWO) tc_mma_ss(d, q_desc + (P::kTile >> 4) + step, b + step, s_id, 1);
+            }
+            tc_commit(&s_full[s_at.st]);
+            tc_commit(&k_empty[at_s & 1]);
+            if (at_s + 1 == q_end) tc_commit(q_empty);
+          }
+          __syncwarp();
+          s_at.step();
+          ++at_s;
+        }
       }
       // every product is done before tensor memory is given back
-      tc_commit(last);
+      if (elect_one()) tc_commit(last);
+      __syncwarp();
       mbar_wait(last, 0, err);
     } else if (warp == 17 && lane == 0) {
-      // ---- TMA: K0, K1, V0, K2, V1, ..., two boxes of 64 positions each ----
-      PItem kt, vt;
-      p_begin(kt, A, pre, lo, hi);
-      vt = kt;
-      int k_at = 0, k_end = kt.u1 - kt.u0, v_end = k_end, k_x = kt.u0, v_x = kt.u0, raw = 0;
+      // ---- TMA: K0, K1, K2, V0, K3, V1, ..., two boxes of 64 positions each ----
+      Ring<kSegs> kseg, vseg;
+      Ring<kRawStages> raw;
+      int copies = 0, k_at = 0, k_end = 0, k_x = 0, k_y = 0, k_len = 0, v_end = 0, v_x = 0, v_y = 0, v_len = 0;
       bool ok = true;
-      auto copy = [&](const CUtensorMap* map, const PItem& it, int x) {
-        const int st = raw % kRawStages;
-        if (raw >= kRawStages && !(ok = wait_for(&raw_empty[st], (raw / kRawStages - 1) & 1, dead, err))) return;
-        uint8_t* dst = smem + P::kRawOff + st * P::kRaw;
-        const int y = (int)(((long long)it.s.slot * A.C.kv_heads + it.head) * A.C.max_ctx + (long long)x * kPUnit);
-        // the second box only where it holds positions of the sequence: the rows of the next head or past the end
-        // of the array are never needed (their codes become 0)
-        const bool both = x * kPUnit + 64 < it.s.length;
-        mbar_arrive_expect_tx(&raw_full[st], both ? P::kRaw : P::kRaw / 2);
-        p_tma_3d(dst, map, 0, y, A.layer, &raw_full[st]);
-        if (both) p_tma_3d(dst + P::kRaw / 2, map, 0, y + 64, A.layer, &raw_full[st]);
-        ++raw;
+      auto copy = [&](const CUtensorMap* map, int y, int left) {
+        if (copies >= kRawStages && !wait_for(&raw_empty[raw.st], raw.ph ^ 1, dead, err)) return false;
+        uint8_t* dst = smem + P::kRawOff + raw.st * P::kRaw;
+        // the second box only where it holds positions of the sequence: rows of the next head or past the end
+        // of the array are not needed (their codes become 0)
+        const bool both = left > 64;
+        mbar_arrive_expect_tx(&raw_full[raw.st], both ? P::kRaw : P::kRaw / 2);
+        p_tma_3d(dst, map, 0, y, A.layer, &raw_full[raw.st]);
+        if (both) p_tma_3d(dst + P::kRaw / 2, map, 0, y + 64, A.layer, &raw_full[raw.st]);
+        raw.step();
+        ++copies;
+        return true;
       };
-      for (int v_at = -1; v_at < n_units && ok; ++v_at) {
+      for (int v_at = 1 - kScores; v_at < n_units && ok; ++v_at) {
         if (k_at < n_units) {
           if (k_at == k_end) {
-            p_next(kt, A, pre, lo + k_at, hi);
-            k_end += kt.u1 - kt.u0, k_x = kt.u0;
+            if (k_at > 0) kseg.step();
+            if (!(ok = wait_for(&seg_full[kseg.st], kseg.ph, dead, err))) break;
+            const Seg* it = segs + kseg.st;
+            k_end = it->end, k_x = it->u0, k_len = it->length;
+            k_y = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
           }
-          copy(&kmap, kt, k_x++);
-          ++k_at;
+          if (!(ok = copy(&kmap, k_y + k_x * kPUnit, k_len - k_x * kPUnit))) break;
+          ++k_x, ++k_at;
         }
-        if (v_at >= 0 && ok) {
+        if (v_at >= 0) {
           if (v_at == v_end) {
-            p_next(vt, A, pre, lo + v_at, hi);
-            v_end += vt.u1 - vt.u0, v_x = vt.u0;
+            if (v_at > 0) {
+              mbar_arrive(&seg_empty[vseg.st]);
+              vseg.step();
+            }
+            const Seg* it = segs + vseg.st;
+            v_end = it->end, v_x = it->u0, v_len = it->length;
+            v_y = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
           }
-          copy(&vmap, vt, v_x++);
+          if (!(ok = copy(&vmap, v_y + v_x * kPUnit, v_len - v_x * kPUnit))) break;
+          ++v_x;
         }
       }
-      for (int i = max(0, raw - kRawStages); i < raw; ++i)  // the copies have landed before the CTA ends
+      for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
         mbar_wait(&raw_full[i % kRawStages], (i / kRawStages) & 1, err);
+    } else if (warp == 18 && lane == 0) {
+      // ---- the CTA's segments ----
+      PItem it;
+      const long long lo = span[1], hi = span[2];
+      p_begin(it, A, pre, lo, hi);
+      Ring<kSegs> seg;
+      int n = 0;
+      for (int i = 0;; ++i) {
+        if (i >= kSegs && !wait_for(&seg_empty[seg.st], seg.ph ^ 1, dead, err)) break;
+        Seg* to = const_cast<Seg*>(segs) + seg.st;
+        n += it.u1 - it.u0;
+        to->row0 = it.s.row0, to->n = it.s.n, to->length = it.s.length, to->slot = it.s.slot;
+        to->head = it.head, to->tile = it.tile;
+        to->u0 = it.u0, to->u1 = it.u1, to->units = it.units, to->end = n;
+        to->first = it.first;
+        mbar_arrive(&seg_full[seg.st]);
+        seg.step();
+        if (n >= n_units) break;
+        p_next(it, A, pre, lo + n, hi);
+      }
     }
     __syncwarp();
   }
