@@ -18,9 +18,10 @@
 // and no accumulator lives longer than one unit: the tensor core's truncating
 // adds do not pile up over a long cache.
 //
-// Roles (20 warps): two warpgroups of softmax (even and odd units, a row a
-// thread), one of correction (a row's output a thread), one of conversion, and
-// a warp each for MMA, TMA and the list of the CTA's segments.
+// Roles (24 warps): two warpgroups of softmax (even and odd units, a row a
+// thread), one of correction (a row's output a thread), one of conversion for q
+// and K and one for V, and a warp each for MMA, TMA of K, TMA of V and the list
+// of the CTA's segments.
 // A role sees what another wrote through the chain of barriers between them;
 // what a reader does not free by a barrier of its own has slots enough that the
 // chain keeps them apart.  S(u) is issued after U(u - 3), so when S(u) can be
@@ -38,22 +39,24 @@ namespace {
 
 constexpr int kPUnit = 128;      // positions per unit
 constexpr int kPRows = 128;      // rows per tile
-constexpr int kPThreads = 640;
-constexpr int kRegs = 96;        // registers per thread at launch; the roles' shares below sum to 5 x 96
+constexpr int kPThreads = 768;
+constexpr int kRegs = 80;        // registers per thread at launch; the roles' shares below sum to 6 x 80
 constexpr int kSegs = 8;         // slots of the segment list
+constexpr int kMmaWarp = 20, kTmaWarp = 21, kListWarp = 23;  // TMA: 21 for K, 22 for V
 constexpr float kPWeightTop = 14.f;
-constexpr int kRawStages = 3;
+constexpr float kLeastFactor = 1e-37f;
+constexpr int kRawStages = 3;      // of half a unit's codes, for K and for V
 constexpr int kScores = 3;         // places of S (and then P) in tensor memory
 
 template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kTile = kPRows * HD * 2;      // a 128-row f16 tile: panels of 64 halves (one swizzle span)
-  static constexpr int kRaw = kPUnit * HD;           // a unit's codes of K or V
+  static constexpr int kRaw = 64 * HD;               // half a unit's codes of K or V
   static constexpr int kVStages = TWO ? 1 : 2;
   static constexpr int kQ = 0;                       // byte offsets from a 1024-byte boundary
   static constexpr int kK = kQ + (TWO ? 2 : 1) * kTile;
   static constexpr int kV = kK + 2 * kTile;
   static constexpr int kRawOff = kV + kVStages * kTile;
-  static constexpr int kStats = kRawOff + kRawStages * kRaw;  // [4][128] float2: a unit's maxima and sums
+  static constexpr int kStats = kRawOff + 2 * kRawStages * kRaw;  // [4][128] float2: a unit's maxima and sums
   static constexpr int kRf = kStats + 4 * kPRows * 8;         // [4][128] the rows' powers of two, by item
   static constexpr int kExp = kRf + 4 * kPRows * 4;           // [8][8] float4: a unit's factors per 16 positions
   static constexpr int kBars = kExp + 8 * 8 * 16;
@@ -61,8 +64,8 @@ template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kSegOff = kMisc + 256;                 // [kSegs] Seg
   static constexpr int kPre = kSegOff + 64 * kSegs;
   // registers per thread by role (softmax keeps the launch's)
-  static constexpr int kRegCorrect = 176, kRegConvert = TWO ? 72 : 80, kRegIssue = TWO ? 40 : 32;
-  static_assert(2 * kRegs + kRegCorrect + kRegConvert + kRegIssue <= 5 * kRegs, "register split");
+  static constexpr int kRegCorrect = 176, kRegConvert = 56, kRegIssue = 32;
+  static_assert(2 * kRegs + kRegCorrect + 2 * kRegConvert + kRegIssue <= 6 * kRegs, "register split");
 };
 
 // What a CTA does of one item: units u0 to u1 of `units`.  Written once by the
@@ -74,7 +77,7 @@ struct alignas(64) Seg {
   int end;                     // the CTA's units up to this segment's end
   long long first;             // the item's first unit in the whole list
 };
-constexpr int kSegReaders = 8 + 4 + 4 + 1 + 1;  // warps (softmax, correction, conversion, MMA, TMA)
+constexpr int kSegReaders = 8 + 4 + 8 + 1 + 2;  // warps (softmax, correction, conversion, MMA, TMA)
 
 struct PromptArgs {
   Kv8Dev C;
@@ -129,6 +132,18 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -370,82 +385,89 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
+// The scores of positions that the row does not see become -inf.
+__device__ __forceinline__ void unit_mask(uint32_t s_addr, int left) {
+#pragma unroll 1
+  for (int ch = 0; ch < 8; ++ch) {
+    uint32_t r[16];
+    tc_ld16(s_addr + ch * 16, r);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (ch * 16 + i >= left) r[i] = 0xFF800000u;
+    tc_st16(s_addr + ch * 16, r);
+  }
+  tc_wait_st();
+}
+
 // A row's softmax over one unit: the 128 scores at s_addr become weights (16-bit
 // parts) relative to the unit's maximum m; l is their sum over 2^ev.  The
-// chunks are a rolled loop: the roles' straight-line code together has to stay
-// within the instruction cache (unrolled, instruction fetch was the largest
-// stall and a unit took 9400 cycles).
-template <bool TWO, bool MASKED>
-__device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac, float f_row, int left, float& m, float& l) {
+// chunks are a rolled loop, and there is one copy of it: the hot code of all
+// roles together has to stay within the SM's instruction cache (unrolled,
+// instruction fetch was the largest stall and a unit took 9400 cycles).
+template <bool TWO>
+__device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac, float f_row, float& m, float& l) {
   m = -INFINITY;
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     uint32_t r[32];
     tc_ld32(s_addr + ch * 32, r);
+    const float4 f0 = fac[ch * 2], f1 = fac[ch * 2 + 1];
     tc_wait_ld();
-    if constexpr (MASKED) {
+    float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (ch * 32 + i >= left) r[i] = 0xFF800000u;
+    for (int i = 0; i < 16; i += 4) {
+      a0 = max3(a0, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+      a1 = max3(a1, __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+      b0 = max3(b0, __uint_as_float(r[i + 16]), __uint_as_float(r[i + 17]));
+      b1 = max3(b1, __uint_as_float(r[i + 18]), __uint_as_float(r[i + 19]));
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t* v = r + 16 * h;
-      float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        a = max3(a, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        b = max3(b, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-      }
-      const float4 f = fac[ch * 2 + h];
-      a = fmaxf(a, b);
-      m = fmaxf(m, a == -INFINITY ? a : fmaf(a, f.x * f_row, f.y));
-    }
+    // (a factor of zero would turn -inf into NaN)
+    m = max3(m, fmaf(fmaxf(a0, a1), fmaxf(f0.x * f_row, kLeastFactor), f0.y),
+             fmaf(fmaxf(b0, b1), fmaxf(f1.x * f_row, kLeastFactor), f1.y));
   }
   const float z = m == -INFINITY ? 0.f : kPWeightTop - m;
   l = 0.f;
 #pragma unroll 1
-  for (int ch = 0; ch < 4; ++ch) {
-    uint32_t r[32];
-    tc_ld32(s_addr + ch * 32, r);
+  for (int ch = 0; ch < 8; ++ch) {
+    uint32_t r[16];
+    tc_ld16(s_addr + ch * 16, r);
+    const float4 f = fac[ch];
+    const float k = fmaxf(f.x * f_row, kLeastFactor), c = f.y + z;
+    const uint64_t k2 = pack2(k, k), c2 = pack2(c, c);
+    uint64_t sum = pack2(0.f, 0.f);
+    uint32_t hi16[8], lo16[TWO ? 8 : 1];
     tc_wait_ld();
-    uint32_t hi16[16], lo16[TWO ? 16 : 1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 f = fac[ch * 2 + h];
-      const float k = f.x * f_row, c = f.y + z;
-      const uint64_t k2 = pack2(k, k), c2 = pack2(c, c);
-      uint64_t sum = pack2(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float w0, w1;
-        unpack2(fma2(pack2(__uint_as_float(r[16 * h + i]), __uint_as_float(r[16 * h + i + 1])), k2, c2), w0, w1);
-        w0 = p_ex2(w0), w1 = p_ex2(w1);
-        if constexpr (MASKED) {
-          if (ch * 32 + 16 * h + i >= left) w0 = 0.f;
-          if (ch * 32 + 16 * h + i + 1 >= left) w1 = 0.f;
-        }
-        sum = add2(sum, pack2(w0, w1));
-        const __half2 hh = __floats2half2_rn(w0, w1);
-        hi16[8 * h + i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
-        if constexpr (TWO) {
-          const float2 back = __half22float2(hh);
-          lo16[8 * h + i / 2] = pack_half2(w0 - back.x, w1 - back.y);
-        }
+    for (int i = 0; i < 16; i += 2) {
+      float w0, w1;
+      unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), k2, c2), w0, w1);
+      w0 = p_ex2(w0), w1 = p_ex2(w1);
+      sum = add2(sum, pack2(w0, w1));
+      const __half2 hh = __floats2half2_rn(w0, w1);
+      hi16[i / 2] = *reinterpret_cast<const uint32_t*>(&hh);
+      if constexpr (TWO) {
+        const float2 back = __half22float2(hh);
+        lo16[i / 2] = pack_half2(w0 - back.x, w1 - back.y);
       }
-      float s0, s1;
-      unpack2(sum, s0, s1);
-      l = fmaf(s0 + s1, f.z, l);
     }
-    // P takes the place of the 32 scores it came from: 16 columns of first parts, 16 of second ones
-    tc_st16(s_addr + ch * 32, hi16);
-    if constexpr (TWO) tc_st16(s_addr + ch * 32 + 16, lo16);
+    float s0, s1;
+    unpack2(sum, s0, s1);
+    l = fmaf(s0 + s1, f.z, l);
+    // P takes the place of the 16 scores it came from: 8 columns of first parts, 8 of second ones
+    tc_st8(s_addr + ch * 16, hi16);
+    if constexpr (TWO) tc_st8(s_addr + ch * 16 + 8, lo16);
   }
 }
 
@@ -454,15 +476,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
     attend_prompt_kernel(const __grid_constant__ PromptArgs A, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap) {
   using P = PromptPlan<HD, TWO>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // declared aligned, so that every role's addresses are constants and not registers
+  extern __shared__ __align__(1024) uint8_t smem[];
   float2* stats = reinterpret_cast<float2*>(smem + P::kStats);
   float* rf = reinterpret_cast<float*>(smem + P::kRf);
   float4* factors = reinterpret_cast<float4*>(smem + P::kExp);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t *raw_full = bars, *raw_empty = bars + 3, *k_full = bars + 6, *k_empty = bars + 8, *v_full = bars + 10,
-           *v_empty = bars + 12, *q_full = bars + 14, *q_empty = bars + 15, *s_full = bars + 16, *p_full = bars + 19,
-           *u_full = bars + 22, *u_empty = bars + 23, *last = bars + 24, *seg_full = bars + 32, *seg_empty = bars + 40;
+  uint64_t *k_full = bars + 6, *k_empty = bars + 8, *v_full = bars + 10, *v_empty = bars + 12, *q_full = bars + 14,
+           *q_empty = bars + 15, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
+           *last = bars + 24, *raw_full = bars + 48, *raw_empty = bars + 54, *seg_full = bars + 32, *seg_empty = bars + 40;
   const Seg* segs = reinterpret_cast<const Seg*>(smem + P::kSegOff);
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
@@ -473,8 +495,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned* err = A.C.err;
 
+  if (smem_u32(smem) & 1023) {  // the swizzles count on it
+    if (tid == 0) atomicOr(err, kErrConfig);
+    return;
+  }
   if (tid == 0) {
-    for (int i = 0; i < kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
+    for (int i = 0; i < 2 * kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4), mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (tid == 0) span[0] = total, span[1] = lo, span[2] = hi;  // for the roles that need them, now and then
   }
 
-  if (warp == 16) {  // all of tensor memory: S in three places (128 columns each), U
+  if (warp == kMmaWarp) {  // all of tensor memory: S in three places (128 columns each), U
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_word)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
@@ -570,10 +596,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int left = lim - x * kPUnit;  // positions of the unit that the row sees
         const bool masked = (x + 1) * kPUnit > all;
         float m, l;
-        if (masked)
-          unit_softmax<TWO, true>(lanes + place.st * 128, fac, f_row, left, m, l);
-        else
-          unit_softmax<TWO, false>(lanes + place.st * 128, fac, f_row, left, m, l);
+        if (masked) unit_mask(lanes + place.st * 128, left);
+        unit_softmax<TWO>(lanes + place.st * 128, fac, f_row, m, l);
         stats[(at & 3) * kPRows + row] = make_float2(m, l);
         tc_wait_st();
         tc_fence_before();
@@ -622,7 +646,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tc_ld32(u_addr + ch * 32, r);
           if (grew) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[ch * 32 + i] *= a;
+            for (int i = 0; i < 32; i += 2)
+              unpack2(mul2(pack2(o[ch * 32 + i], o[ch * 32 + i + 1]), pack2(a, a)), o[ch * 32 + i], o[ch * 32 + i + 1]);
           }
           tc_wait_ld();
 #pragma unroll
@@ -685,63 +710,62 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
       seg.step();
     }
-  } else if (warp < 16) {
-    // ---- conversion: q of each item, then K and V of its units, to f16 tiles ----
+  } else if (warp < 20) {
+    // ---- conversion: q of each item and K of its units, or V, to f16 tiles ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegConvert));
-    const int t = tid & 127;
+    const int t = tid & 127, v_side = warp >> 4;  // warps 12..15: K, 16..19: V
+    uint64_t *raw_f = raw_full + v_side * kRawStages, *raw_e = raw_empty + v_side * kRawStages;
     Ring<kRawStages> raw;
     bool ok = true;
-    // one tile of codes to f16, 4 chunks of 16 codes in flight; rows from `valid` on become 0
-    auto tile = [&](uint8_t* dst, int valid) {
-      const uint8_t* src = smem + P::kRawOff + raw.st * P::kRaw;
-      constexpr int kChunks = HD / 16;  // 16-code chunks per row
+    // Half a tile (64 positions) of codes to f16: the chunks of 16 codes of a thread are all read, the codes' place is
+    // given back, then they are converted.  Rows from `valid` on become 0.
+    auto half_tile = [&](uint8_t* dst, int valid) {
+      constexpr int kChunks = HD / 16, kMine = kChunks / 2;  // chunks per row, and of a thread
+      constexpr int kStep = 128 / kChunks;  // rows between a thread's chunks: a multiple of 8, so the swizzles do not change
+      const uint8_t* src = smem + P::kRawOff + (v_side * kRawStages + raw.st) * P::kRaw;
       const int ch = t % kChunks, r0 = t / kChunks;
-      constexpr int kStep = 128 / kChunks;  // rows from one chunk of a thread to the next: a multiple of 8 (16)
-      // so the swizzles do not change
       const int from = HD == 128 ? r0 * 128 + ((ch ^ (r0 & 7)) << 4) : r0 * 64 + ((ch ^ ((r0 >> 1) & 3)) << 4);
+      uint4 cw[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) cw[i] = *reinterpret_cast<const uint4*>(src + from + i * (kStep * HD));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_e[raw.st]);
+      raw.step();
+      if (valid < 64) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (r0 + i * kStep >= valid) cw[i] = make_uint4(0, 0, 0, 0);
+      }
       const int flip = ch >> 2;  // the two halves' stores alternate so that 8 lanes of a row meet 8 different chunks
-      const int to = (ch >> 2) * (kPRows * 128) + r0 * 128;
+      uint8_t* to = dst + (ch >> 2) * (kPRows * 128) + r0 * 128;
       const int c0 = (((ch & 3) * 2 + flip) ^ (r0 & 7)) << 4, c1 = (((ch & 3) * 2 + 1 - flip) ^ (r0 & 7)) << 4;
-#pragma unroll(TWO ? 1 : 2)
-      for (int j = 0; j < kChunks; j += 4) {
-        uint4 cw[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cw[i] = *reinterpret_cast<const uint4*>(src + from + (j + i) * (kStep * HD));
-        }
-        if (valid < kPUnit) {
+      for (int i = 0; i < kMine; ++i) {
+        uint4 h0, h1;
+        if constexpr (FMT == 0) {
+          h0.x = e4m3x2_to_f16x2(cw[i].x & 0xFFFFu), h0.y = e4m3x2_to_f16x2(cw[i].x >> 16);
+          h0.z = e4m3x2_to_f16x2(cw[i].y & 0xFFFFu), h0.w = e4m3x2_to_f16x2(cw[i].y >> 16);
+          h1.x = e4m3x2_to_f16x2(cw[i].z & 0xFFFFu), h1.y = e4m3x2_to_f16x2(cw[i].z >> 16);
+          h1.z = e4m3x2_to_f16x2(cw[i].w & 0xFFFFu), h1.w = e4m3x2_to_f16x2(cw[i].w >> 16);
+        } else {
+          const uint32_t in[4] = {cw[i].x ^ 0x80808080u, cw[i].y ^ 0x80808080u, cw[i].z ^ 0x80808080u, cw[i].w ^ 0x80808080u};
+          uint32_t out[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (r0 + (j + i) * kStep >= valid) cw[i] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 h0, h1;
-          if constexpr (FMT == 0) {
-            h0.x = e4m3x2_to_f16x2(cw[i].x & 0xFFFFu), h0.y = e4m3x2_to_f16x2(cw[i].x >> 16);
-            h0.z = e4m3x2_to_f16x2(cw[i].y & 0xFFFFu), h0.w = e4m3x2_to_f16x2(cw[i].y >> 16);
-            h1.x = e4m3x2_to_f16x2(cw[i].z & 0xFFFFu), h1.y = e4m3x2_to_f16x2(cw[i].z >> 16);
-            h1.z = e4m3x2_to_f16x2(cw[i].w & 0xFFFFu), h1.w = e4m3x2_to_f16x2(cw[i].w >> 16);
-          } else {
-            const uint32_t in[4] = {cw[i].x ^ 0x80808080u, cw[i].y ^ 0x80808080u, cw[i].z ^ 0x80808080u, cw[i].w ^ 0x80808080u};
-            uint32_t out[8];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              out[2 * y] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4140), 0x64806480u);
-              out[2 * y + 1] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4342), 0x64806480u);
-            }
-            h0 = make_uint4(out[0], out[1], out[2], out[3]);
-            h1 = make_uint4(out[4], out[5], out[6], out[7]);
+          for (int y = 0; y < 4; ++y) {
+            out[2 * y] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4140), 0x64806480u);
+            out[2 * y + 1] = hsub2_u32(__byte_perm(in[y], 0x64646464u, 0x4342), 0x64806480u);
           }
-          uint8_t* at = dst + to + (j + i) * (kStep * 128);
-          *reinterpret_cast<uint4*>(at + c0) = flip ? h1 : h0;
-          *reinterpret_cast<uint4*>(at + c1) = flip ? h0 : h1;
+          h0 = make_uint4(out[0], out[1], out[2], out[3]);
+          h1 = make_uint4(out[4], out[5], out[6], out[7]);
         }
+        uint8_t* at = to + i * (kStep * 128);
+        *reinterpret_cast<uint4*>(at + c0) = flip ? h1 : h0;
+        *reinterpret_cast<uint4*>(at + c1) = flip ? h0 : h1;
       }
     };
     // q of a segment: a warp brings in its 32 rows, a row at a time, lane l the dims l E .. l E + E - 1
-    auto load_q = [&](const Seg* it, float* powers) {
-      constexpr int E = HD / 32, kBatch = 8;
+    auto load_q = [&](const Seg* it, float* powers, int items) {
+      constexpr int E = HD / 32, kBatch = TWO ? 4 : 8;
       const int r_first = (warp & 3) * 32;
       int tok = it->tile * A.tokens + r_first / A.group, h = r_first % A.group;
       const int tok_end = min(it->n, (it->tile + 1) * A.tokens);
@@ -756,6 +780,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 ((long long)(it->row0 + tok) * A.q_stride + (long long)(it->head * A.group + h) * HD) * (TWO ? 4 : 2))[lane];
           if (++h == A.group) h = 0, ++tok;
         }
+        // the first rows are on their way while the last product with the old q ends
+        if (r0 == 0 && items > 0 && !(ok = wait_warp(q_empty, (items - 1) & 1, dead, err))) return;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int row = r_first + r0 + b;
@@ -792,72 +818,60 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
-    // jobs K0, K1, K2, V0, K3, V1, ..., V(n-1): the K side runs two units ahead of the V side
-    Ring<kSegs> kseg, vseg;
-    Ring<2> kst;
-    Ring<P::kVStages> vst;
-    int k_at = 0, k_end = 0, k_x = 0, k_len = 0, v_at = 0, v_end = 0, v_x = 0, v_len = 0, items = 0;
-    // factors per 16 positions of the next K unit, fetched one unit ahead by 8 threads
-    int e_next = 0;
-    auto fetch = [&](const Seg* it, int x) {
-      const int p = x * kPUnit + t * 16;
-      if (t < 8 && p < it->length) {
-        const long long at = ((long long)it->slot * A.C.kv_heads + it->head) * A.C.n_blocks + (p >> A.C.block_log2);
-        e_next = A.C.k_exp[at] | A.C.v_exp[at] << 8;
-      }
-    };
-    while (v_at < n_units) {
-      const bool is_k = k_at < n_units && k_at <= v_at + kScores - 1;
-      uint8_t* dst;
-      uint64_t* full;
-      int valid;
-      if (is_k) {
-        if (k_at == k_end) {
-          if (k_at > 0) kseg.step();
-          if (!(ok = wait_warp(&seg_full[kseg.st], kseg.ph, dead, err))) break;
-          const Seg* it = segs + kseg.st;
-          k_end = it->end, k_x = it->u0, k_len = it->length;
-          fetch(it, k_x);
-          // once the last product with the old q is done
-          if (items > 0 && !(ok = wait_warp(q_empty, (items - 1) & 1, dead, err))) break;
-          load_q(it, rf + (items & 3) * kPRows);
-          ++items;
+    Ring<kSegs> seg;
+    int at = 0, items = 0, st = 0;  // st: the tile's place, of 2 (K) or kVStages (V)
+    uint32_t ph = 0;
+    uint64_t *full = v_side ? v_full : k_full, *empty = v_side ? v_empty : k_empty;
+    const int places = v_side ? P::kVStages : 2;
+    uint8_t* tiles = smem + (v_side ? P::kV : P::kK);
+    while (at < n_units) {
+      if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
+      const Seg* it = segs + seg.st;
+      const int end = it->end, length = it->length;
+      int p = it->u0 * kPUnit;
+      // factors per 16 positions, fetched one unit ahead by 8 threads of the K side
+      const long long line = ((long long)it->slot * A.C.kv_heads + it->head) * A.C.n_blocks;
+      int e_next = 0;
+      auto fetch = [&]() {
+        if (!v_side && t < 8 && p + t * 16 < length) {
+          const long long b = line + ((p + t * 16) >> A.C.block_log2);
+          e_next = A.C.k_exp[b] | A.C.v_exp[b] << 8;
         }
-        if (k_at >= 2 && !(ok = wait_warp(&k_empty[kst.st], kst.ph ^ 1, dead, err))) break;
-        if (t < 8)
-          factors[(k_at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(kv8_exp((uint8_t)e_next)), (float)kv8_exp((uint8_t)(e_next >> 8)),
-                                                    pow2i(-kv8_exp((uint8_t)(e_next >> 8))), 0.f);
-        dst = smem + P::kK + kst.st * P::kTile, full = &k_full[kst.st], valid = k_len - k_x * kPUnit;
-        kst.step();
-        ++k_at, ++k_x;
-        if (k_at < k_end) fetch(segs + kseg.st, k_x);
-      } else {
-        if (v_at == v_end) {
-          if (v_at > 0) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[vseg.st]);
-            vseg.step();
-          }
-          v_end = segs[vseg.st].end, v_x = segs[vseg.st].u0, v_len = segs[vseg.st].length;
-        }
-        if (v_at >= P::kVStages && !(ok = wait_warp(&v_empty[vst.st], vst.ph ^ 1, dead, err))) break;
-        dst = smem + P::kV + vst.st * P::kTile, full = &v_full[vst.st], valid = v_len - v_x * kPUnit;
-        vst.step();
-        ++v_at, ++v_x;
+      };
+      fetch();
+      if (!v_side) {
+        load_q(it, rf + (items & 3) * kPRows, items);
+        if (!ok) break;
+        ++items;
       }
-      if (!(ok = wait_warp(&raw_full[raw.st], raw.ph, dead, err))) break;
-      tile(dst, valid);
-      fence_async_shared();
+#pragma unroll 1
+      for (; at < end; ++at) {
+        if (at >= places && !(ok = wait_warp(&empty[st], ph ^ 1, dead, err))) break;
+        if (!v_side && t < 8) {
+          const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
+          factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
+        }
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = wait_warp(&raw_f[raw.st], raw.ph, dead, err))) break;
+          half_tile(tiles + st * P::kTile + half * (64 * 128), length - p);
+          p += 64;
+        }
+        if (!ok) break;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        if (at + 1 < end) fetch();
+        if (++st == places) st = 0, ph ^= 1;
+      }
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(full);
-        mbar_arrive(&raw_empty[raw.st]);
-      }
-      raw.step();
+      if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
+      seg.step();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegIssue));
-    if (warp == 16) {
+    if (warp == kMmaWarp) {
       // ---- MMA: the whole warp keeps step (so that descriptors stay in uniform registers), one lane issues ----
       Ring<kSegs> seg;
       int item = 0, q_end = 0, at_s = 0;
@@ -878,10 +892,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const uint32_t a = tmem + p_at.st * 128, d = tmem + kScores * 128;
           const uint64_t b = v_desc + ((st * P::kTile) >> 4);
           if (elect_one()) {
-#pragma unroll(TWO ? 2 : 8)
+#pragma unroll 2
             for (int y = 0; y < kPUnit / 16; ++y) {
-              tc_mma_ts(d, a + (y >> 1) * 32 + (y & 1) * 8, b + ((y * 16 * 128) >> 4), u_id, y > 0);
-              if constexpr (TWO) tc_mma_ts(d, a + (y >> 1) * 32 + (y & 1) * 8 + 16, b + ((y * 16 * 128) >> 4), u_id, 1);
+              tc_mma_ts(d, a + y * 16, b + ((y * 16 * 128) >> 4), u_id, y > 0);
+              if constexpr (TWO) tc_mma_ts(d, a + y * 16 + 8, b + ((y * 16 * 128) >> 4), u_id, 1);
             }
             tc_commit(u_full);
             tc_commit(&v_empty[st]);
@@ -904,7 +918,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const uint32_t d = tmem + s_at.st * 128;
           const uint64_t b = k_desc + (((at_s & 1) * P::kTile) >> 4);
           if (elect_one()) {
-#pragma unroll(TWO ? 2 : 8)
+#pragma unroll 2
             for (int y = 0; y < HD / 16; ++y) {
               const uint32_t step = ((y >> 2) * (kPRows * 128) + (y & 3) * 32) >> 4;
               tc_mma_ss(d, q_desc + step, b + step, s_id, y > 0);
@@ -923,54 +937,41 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (elect_one()) tc_commit(last);
       __syncwarp();
       mbar_wait(last, 0, err);
-    } else if (warp == 17 && lane == 0) {
-      // ---- TMA: K0, K1, K2, V0, K3, V1, ..., two boxes of 64 positions each ----
-      Ring<kSegs> kseg, vseg;
+    } else if ((warp == kTmaWarp || warp == kTmaWarp + 1) && lane == 0) {
+      // ---- TMA of the codes of K, or of V, 64 positions at a time ----
+      const int v_side = warp - kTmaWarp;
+      const CUtensorMap* map = v_side ? &vmap : &kmap;
+      uint64_t *raw_f = raw_full + v_side * kRawStages, *raw_e = raw_empty + v_side * kRawStages;
+      uint8_t* dst = smem + P::kRawOff + v_side * kRawStages * P::kRaw;
+      Ring<kSegs> seg;
       Ring<kRawStages> raw;
-      int copies = 0, k_at = 0, k_end = 0, k_x = 0, k_y = 0, k_len = 0, v_end = 0, v_x = 0, v_y = 0, v_len = 0;
+      int copies = 0, at = 0;
       bool ok = true;
-      auto copy = [&](const CUtensorMap* map, int y, int left) {
-        if (copies >= kRawStages && !wait_for(&raw_empty[raw.st], raw.ph ^ 1, dead, err)) return false;
-        uint8_t* dst = smem + P::kRawOff + raw.st * P::kRaw;
-        // the second box only where it holds positions of the sequence: rows of the next head or past the end
-        // of the array are not needed (their codes become 0)
-        const bool both = left > 64;
-        mbar_arrive_expect_tx(&raw_full[raw.st], both ? P::kRaw : P::kRaw / 2);
-        p_tma_3d(dst, map, 0, y, A.layer, &raw_full[raw.st]);
-        if (both) p_tma_3d(dst + P::kRaw / 2, map, 0, y + 64, A.layer, &raw_full[raw.st]);
-        raw.step();
-        ++copies;
-        return true;
-      };
-      for (int v_at = 1 - kScores; v_at < n_units && ok; ++v_at) {
-        if (k_at < n_units) {
-          if (k_at == k_end) {
-            if (k_at > 0) kseg.step();
-            if (!(ok = wait_for(&seg_full[kseg.st], kseg.ph, dead, err))) break;
-            const Seg* it = segs + kseg.st;
-            k_end = it->end, k_x = it->u0, k_len = it->length;
-            k_y = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
+      while (at < n_units && ok) {
+        if (!(ok = wait_for(&seg_full[seg.st], seg.ph, dead, err))) break;
+        const Seg* it = segs + seg.st;
+        const int y0 = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
+        const int x1 = 2 * it->u1, length = it->length;
+        for (int x = 2 * it->u0; x < x1 && ok; ++x) {
+          if (copies >= kRawStages && !(ok = wait_for(&raw_e[raw.st], raw.ph ^ 1, dead, err))) break;
+          // a half that holds no position of the sequence is not needed (its codes become 0)
+          if (x * 64 < length) {
+            mbar_arrive_expect_tx(&raw_f[raw.st], P::kRaw);
+            p_tma_3d(dst + raw.st * P::kRaw, map, 0, y0 + x * 64, A.layer, &raw_f[raw.st]);
+          } else {
+            mbar_arrive(&raw_f[raw.st]);
           }
-          if (!(ok = copy(&kmap, k_y + k_x * kPUnit, k_len - k_x * kPUnit))) break;
-          ++k_x, ++k_at;
+          raw.step();
+          ++copies;
         }
-        if (v_at >= 0) {
-          if (v_at == v_end) {
-            if (v_at > 0) {
-              mbar_arrive(&seg_empty[vseg.st]);
-              vseg.step();
-            }
-            const Seg* it = segs + vseg.st;
-            v_end = it->end, v_x = it->u0, v_len = it->length;
-            v_y = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
-          }
-          if (!(ok = copy(&vmap, v_y + v_x * kPUnit, v_len - v_x * kPUnit))) break;
-          ++v_x;
-        }
+        if (!ok) break;
+        at = it->end;
+        mbar_arrive(&seg_empty[seg.st]);
+        seg.step();
       }
       for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
-        mbar_wait(&raw_full[i % kRawStages], (i / kRawStages) & 1, err);
-    } else if (warp == 18 && lane == 0) {
+        mbar_wait(&raw_f[i % kRawStages], (i / kRawStages) & 1, err);
+    } else if (warp == kListWarp && lane == 0) {
       // ---- the CTA's segments ----
       PItem it;
       const long long lo = span[1], hi = span[2];
@@ -996,12 +997,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 template <int HD, int FMT, bool TWO>
 cudaError_t launch(const PromptArgs& A, const Kv8Maps& M, int nsm, cudaStream_t s) {
-  const int smem = 1024 + PromptPlan<HD, TWO>::kPre + 8 * (A.R.n_seq + 1);
+  const int smem = PromptPlan<HD, TWO>::kPre + 8 * (A.R.n_seq + 1);
   attend_prompt_kernel<HD, FMT, TWO><<<nsm, kPThreads, smem, s>>>(A, M.k, M.v);
   return cudaGetLastError();
 }
@@ -1015,7 +1016,7 @@ cudaError_t setup() {
   // the roles' register shares are drawn from what the block is launched with
   if ((a.numRegs + 7) / 8 * 8 < kRegs) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              1024 + PromptPlan<HD, TWO>::kPre + 8 * (kKv8MaxSeq + 1));
+                              PromptPlan<HD, TWO>::kPre + 8 * (kKv8MaxSeq + 1));
 }
 
 }  // namespace
