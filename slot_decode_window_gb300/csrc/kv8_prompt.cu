@@ -720,11 +720,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // Half a tile (64 positions) of codes to f16: the chunks of 16 codes of a thread are all read, the codes' place is
     // given back, then they are converted.  Rows from `valid` on become 0.
     auto half_tile = [&](uint8_t* dst, int valid) {
-      constexpr int kChunks = HD / 16, kMine = kChunks / 2;  // chunks per row, and of a thread
-      constexpr int kStep = 128 / kChunks;  // rows between a thread's chunks: a multiple of 8, so the swizzles do not change
+      // Eight neighbouring lanes take four chunks of row r and four of row r ^ 5 (mod 8): under both swizzles they meet
+      // eight different 16-byte columns, reading the codes and writing either half of the values.  A thread's rows
+      // are 16 (32) apart, so its swizzled columns stay.
+      constexpr int kMine = HD / 32, kStep = HD == 128 ? 16 : 32;
       const uint8_t* src = smem + P::kRawOff + (v_side * kRawStages + raw.st) * P::kRaw;
-      const int ch = t % kChunks, r0 = t / kChunks;
-      const int from = HD == 128 ? r0 * 128 + ((ch ^ (r0 & 7)) << 4) : r0 * 64 + ((ch ^ ((r0 >> 1) & 3)) << 4);
+      const int w = warp & 3, r7 = ((t >> 3) & 3) ^ ((t >> 2) & 1) * 5;
+      const int r0 = (HD == 128 ? w >> 1 : w) * 8 + r7, panel = HD == 128 ? w & 1 : 0;
+      const int from = HD == 128 ? r0 * 128 + (((panel * 4 + (t & 3)) ^ r7) << 4) : r0 * 64 + (((t & 3) ^ (r7 >> 1)) << 4);
       uint4 cw[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) cw[i] = *reinterpret_cast<const uint4*>(src + from + i * (kStep * HD));
@@ -736,9 +739,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int i = 0; i < kMine; ++i)
           if (r0 + i * kStep >= valid) cw[i] = make_uint4(0, 0, 0, 0);
       }
-      const int flip = ch >> 2;  // the two halves' stores alternate so that 8 lanes of a row meet 8 different chunks
-      uint8_t* to = dst + (ch >> 2) * (kPRows * 128) + r0 * 128;
-      const int c0 = (((ch & 3) * 2 + flip) ^ (r0 & 7)) << 4, c1 = (((ch & 3) * 2 + 1 - flip) ^ (r0 & 7)) << 4;
+      uint8_t* to = dst + panel * (kPRows * 128) + r0 * 128;
+      const int c0 = ((t & 3) * 2 ^ r7) << 4;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         uint4 h0, h1;
@@ -759,8 +761,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           h1 = make_uint4(out[4], out[5], out[6], out[7]);
         }
         uint8_t* at = to + i * (kStep * 128);
-        *reinterpret_cast<uint4*>(at + c0) = flip ? h1 : h0;
-        *reinterpret_cast<uint4*>(at + c1) = flip ? h0 : h1;
+        *reinterpret_cast<uint4*>(at + c0) = h0;
+        *reinterpret_cast<uint4*>(at + (c0 ^ 16)) = h1;
       }
     };
     // q of a segment: a warp brings in its 32 rows, a row at a time, lane l the dims l E .. l E + E - 1
