@@ -125,9 +125,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 template <int FMT>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == 0) {
-    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
+    e4m3x4_to_f16x4(w, lo, hi);
   } else {
     const uint32_t u = w ^ 0x80808080u;
     lo = hsub2_u32(prmt(u, 0x64646464u, 0x4140), 0x64806480u);

@@ -20,13 +20,13 @@
 //
 // Roles (24 warps): two warpgroups of softmax (even and odd units, a row a
 // thread), one of correction (a row's output a thread), one of conversion for q
-// and K and one for V, and a warp each for MMA, TMA of K, TMA of V and the list
-// of the CTA's segments.
+// and K and one for V, and a warp each for the products S, the products U, TMA
+// of K (which also makes the list of the CTA's segments) and TMA of V.
 // A role sees what another wrote through the chain of barriers between them;
 // what a reader does not free by a barrier of its own has slots enough that the
-// chain keeps them apart.  S(u) is issued after U(u - 3), so when S(u) can be
-// read the softmax of u - 3 is done, and the correction of u - 4 (U has one
-// place): 4 slots of statistics, written for u and read for u - 4; 4 of the
+// chain keeps them apart.  S(u) is issued once U(u - 3) is done, so when S(u)
+// can be read the softmax of u - 3 is done, and the correction of u - 4 (U has
+// one place): 4 slots of statistics, written for u and read for u - 4; 4 of the
 // rows' powers of two, written for an item once S of the unit before it is
 // done; 8 of the units' factors, written once S(u - 2) is done, that is, after
 // the softmax of u - 5.
@@ -42,7 +42,7 @@ constexpr int kPRows = 128;      // rows per tile
 constexpr int kPThreads = 768;
 constexpr int kRegs = 80;        // registers per thread at launch; the roles' shares below sum to 6 x 80
 constexpr int kSegs = 8;         // slots of the segment list
-constexpr int kMmaWarp = 20, kTmaWarp = 21, kListWarp = 23;  // TMA: 21 for K, 22 for V
+constexpr int kMmaWarp = 20, kTmaWarp = 22;  // products: 20 S, 21 U; TMA: 22 K, 23 V
 constexpr float kPWeightTop = 14.f;
 constexpr float kLeastFactor = 1e-37f;
 constexpr int kRawStages = 3;      // of half a unit's codes, for K and for V
@@ -51,7 +51,7 @@ constexpr int kScores = 3;         // places of S (and then P) in tensor memory
 template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kTile = kPRows * HD * 2;      // a 128-row f16 tile: panels of 64 halves (one swizzle span)
   static constexpr int kRaw = 64 * HD;               // half a unit's codes of K or V
-  static constexpr int kVStages = TWO ? 1 : 2;
+  static constexpr int kVStages = TWO ? 1 : 2;      // tiles; V's ring is of their halves
   static constexpr int kQ = 0;                       // byte offsets from a 1024-byte boundary
   static constexpr int kK = kQ + (TWO ? 2 : 1) * kTile;
   static constexpr int kV = kK + 2 * kTile;
@@ -77,7 +77,7 @@ struct alignas(64) Seg {
   int end;                     // the CTA's units up to this segment's end
   long long first;             // the item's first unit in the whole list
 };
-constexpr int kSegReaders = 8 + 4 + 8 + 1 + 2;  // warps (softmax, correction, conversion, MMA, TMA)
+constexpr int kSegReaders = 8 + 4 + 8 + 1 + 2;  // warps (softmax, correction, conversion, S, TMA)
 
 struct PromptArgs {
   Kv8Dev C;
@@ -238,6 +238,11 @@ template <int E, bool TWO> struct alignas(TWO ? 4 * E : 2 * E) Raw {
     }
   }
 };
+__device__ __forceinline__ uint32_t pack_out(bool bf16, float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  const __half2 y = __floats2half2_rn(a, b);
+  return bf16 ? *reinterpret_cast<const uint32_t*>(&x) : *reinterpret_cast<const uint32_t*>(&y);
+}
 __device__ __forceinline__ void p_store4(void* p, int dtype, long long i, float4 v) {
   if (dtype == 0) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
@@ -482,9 +487,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* rf = reinterpret_cast<float*>(smem + P::kRf);
   float4* factors = reinterpret_cast<float4*>(smem + P::kExp);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t *k_full = bars + 6, *k_empty = bars + 8, *v_full = bars + 10, *v_empty = bars + 12, *q_full = bars + 14,
-           *q_empty = bars + 15, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
-           *last = bars + 24, *raw_full = bars + 48, *raw_empty = bars + 54, *seg_full = bars + 32, *seg_empty = bars + 40;
+  uint64_t *v_full = bars, *v_empty = bars + 4, *k_full = bars + 8, *k_empty = bars + 10, *q_full = bars + 12, *q_empty = bars + 13, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
+           *last = bars + 24, *place_free = bars + 26, *raw_full = bars + 48, *raw_empty = bars + 54, *seg_full = bars + 32, *seg_empty = bars + 40;
   const Seg* segs = reinterpret_cast<const Seg*>(smem + P::kSegOff);
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
@@ -503,11 +507,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int i = 0; i < 2 * kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4), mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < kScores; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < kScores; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&place_free[i], 1);
     mbar_init(u_full, 1), mbar_init(u_empty, 4);
-    mbar_init(q_full, 4), mbar_init(q_empty, 1), mbar_init(last, 1);
+    mbar_init(q_full, 4), mbar_init(q_empty, 1), mbar_init(&last[0], 1), mbar_init(&last[1], 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], kSegReaders);
     *dead = 0;
     fence_mbar_init();
@@ -702,9 +706,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       if (write) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        if constexpr (TWO) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(A.out) + to);
 #pragma unroll
-        for (int i = 0; i < HD; i += 4)
-          p_store4(A.out, A.dtype, to + i, make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
+          for (int i = 0; i < HD; i += 4) dst[i / 4] = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + to);
+          const bool bf = A.dtype == 2;
+#pragma unroll
+          for (int i = 0; i < HD; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = pack_out(bf, o[i + 2 * y] * inv, o[i + 2 * y + 1] * inv);
+            dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
@@ -745,10 +761,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int i = 0; i < kMine; ++i) {
         uint4 h0, h1;
         if constexpr (FMT == 0) {
-          h0.x = e4m3x2_to_f16x2(cw[i].x & 0xFFFFu), h0.y = e4m3x2_to_f16x2(cw[i].x >> 16);
-          h0.z = e4m3x2_to_f16x2(cw[i].y & 0xFFFFu), h0.w = e4m3x2_to_f16x2(cw[i].y >> 16);
-          h1.x = e4m3x2_to_f16x2(cw[i].z & 0xFFFFu), h1.y = e4m3x2_to_f16x2(cw[i].z >> 16);
-          h1.z = e4m3x2_to_f16x2(cw[i].w & 0xFFFFu), h1.w = e4m3x2_to_f16x2(cw[i].w >> 16);
+          e4m3x4_to_f16x4(cw[i].x, h0.x, h0.y), e4m3x4_to_f16x4(cw[i].y, h0.z, h0.w);
+          e4m3x4_to_f16x4(cw[i].z, h1.x, h1.y), e4m3x4_to_f16x4(cw[i].w, h1.z, h1.w);
         } else {
           const uint32_t in[4] = {cw[i].x ^ 0x80808080u, cw[i].y ^ 0x80808080u, cw[i].z ^ 0x80808080u, cw[i].w ^ 0x80808080u};
           uint32_t out[8];
@@ -821,10 +835,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) mbar_arrive(q_full);
     };
     Ring<kSegs> seg;
-    int at = 0, items = 0, st = 0;  // st: the tile's place, of 2 (K) or kVStages (V)
+    int at = 0, items = 0, st = 0;  // st: the half's place in two tiles (K) or kVStages (V)
     uint32_t ph = 0;
-    uint64_t *full = v_side ? v_full : k_full, *empty = v_side ? v_empty : k_empty;
-    const int places = v_side ? P::kVStages : 2;
+    const int places = v_side ? 2 * P::kVStages : 4;
     uint8_t* tiles = smem + (v_side ? P::kV : P::kK);
     while (at < n_units) {
       if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
@@ -848,23 +861,28 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
 #pragma unroll 1
       for (; at < end; ++at) {
-        if (at >= places && !(ok = wait_warp(&empty[st], ph ^ 1, dead, err))) break;
-        if (!v_side && t < 8) {
-          const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
-          factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
+        if (!v_side) {
+          if (at >= 2 && !(ok = wait_warp(&k_empty[st >> 1], ph ^ 1, dead, err))) break;
+          if (t < 8) {
+            const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
+            factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
+          }
         }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
+          if (v_side && at >= P::kVStages && !(ok = wait_warp(&v_empty[st], ph ^ 1, dead, err))) break;
           if (!(ok = wait_warp(&raw_f[raw.st], raw.ph, dead, err))) break;
-          half_tile(tiles + st * P::kTile + half * (64 * 128), length - p);
+          half_tile(tiles + (st >> 1) * P::kTile + half * (64 * 128), length - p);
           p += 64;
+          if (v_side || half) {  // (K's first half: the fence of the second covers it)
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_side ? &v_full[st] : &k_full[st >> 1]);
+          }
+          if (++st == places) st = 0, ph ^= 1;
         }
         if (!ok) break;
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
         if (at + 1 < end) fetch();
-        if (++st == places) st = 0, ph ^= 1;
       }
       if (!ok) break;
       __syncwarp();
@@ -873,72 +891,84 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegIssue));
+    // The products: a warp for S and one for U, each kept in step as a whole (so that descriptors stay in uniform
+    // registers) with one lane issuing; one warp for both was what bound a unit.
     if (warp == kMmaWarp) {
-      // ---- MMA: the whole warp keeps step (so that descriptors stay in uniform registers), one lane issues ----
+      // ---- S = Q K^T, up to three units ahead of U ----
       Ring<kSegs> seg;
-      int item = 0, q_end = 0, at_s = 0;
+      Ring<kScores> place;
+      int item = 0, q_end = 0;
       bool ok = true;
-      const uint64_t q_desc = tc_desc(smem + P::kQ, 1024, 16), k_desc = tc_desc(smem + P::kK, 1024, 16),
-                     v_desc = tc_desc(smem + P::kV, 1024, kPRows * 128);
-      constexpr uint32_t s_id = tc_idesc(kPUnit, false), u_id = tc_idesc(HD, true);
-      // products in the order S0, S1, S2, U0, S3, U1, S4, ...: U(at) frees S's place for S(at + 3), so the softmax
-      // warps always have scores waiting
-      Ring<kScores> p_at, s_at;
-      for (int at = -kScores; at < n_units; ++at) {
-        if (at >= 0) {  // U(at) = P(at) V(at)
-          const int st = P::kVStages == 2 ? at & 1 : 0;
-          if (!(ok = wait_warp(&p_full[p_at.st], p_at.ph, dead, err))) break;
-          if (!(ok = wait_warp(&v_full[st], (P::kVStages == 2 ? at >> 1 : at) & 1, dead, err))) break;
-          if (at >= 1 && !(ok = wait_warp(u_empty, (at - 1) & 1, dead, err))) break;
-          tc_fence_after();
-          const uint32_t a = tmem + p_at.st * 128, d = tmem + kScores * 128;
-          const uint64_t b = v_desc + ((st * P::kTile) >> 4);
-          if (elect_one()) {
-#pragma unroll 2
-            for (int y = 0; y < kPUnit / 16; ++y) {
-              tc_mma_ts(d, a + y * 16, b + ((y * 16 * 128) >> 4), u_id, y > 0);
-              if constexpr (TWO) tc_mma_ts(d, a + y * 16 + 8, b + ((y * 16 * 128) >> 4), u_id, 1);
-            }
-            tc_commit(u_full);
-            tc_commit(&v_empty[st]);
-          }
+      const uint64_t q_desc = tc_desc(smem + P::kQ, 1024, 16), k_desc = tc_desc(smem + P::kK, 1024, 16);
+      constexpr uint32_t s_id = tc_idesc(kPUnit, false);
+      for (int at = 0; at < n_units; ++at) {
+        if (at == q_end) {
+          if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
+          q_end = segs[seg.st].end;
           __syncwarp();
-          p_at.step();
+          if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
+          seg.step();
+          if (!(ok = wait_warp(q_full, item & 1, dead, err))) break;
+          ++item;
         }
-        if (at_s < n_units) {  // S = Q K^T
-          if (at_s == q_end) {
-            if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
-            q_end = segs[seg.st].end;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[seg.st]);
-            seg.step();
-            if (!(ok = wait_warp(q_full, item & 1, dead, err))) break;
-            ++item;
-          }
-          if (!(ok = wait_warp(&k_full[at_s & 1], (at_s >> 1) & 1, dead, err))) break;
-          tc_fence_after();
-          const uint32_t d = tmem + s_at.st * 128;
-          const uint64_t b = k_desc + (((at_s & 1) * P::kTile) >> 4);
-          if (elect_one()) {
+        if (at >= kScores && !(ok = wait_warp(&place_free[place.st], place.ph ^ 1, dead, err))) break;
+        if (!(ok = wait_warp(&k_full[at & 1], (at >> 1) & 1, dead, err))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + place.st * 128;
+        const uint64_t b = k_desc + (((at & 1) * P::kTile) >> 4);
+        if (elect_one()) {
 #pragma unroll 2
-            for (int y = 0; y < HD / 16; ++y) {
-              const uint32_t step = ((y >> 2) * (kPRows * 128) + (y & 3) * 32) >> 4;
-              tc_mma_ss(d, q_desc + step, b + step, s_id, y > 0);
-              if constexpr (TWO) tc_mma_ss(d, q_desc + (P::kTile >> 4) + step, b + step, s_id, 1);
-            }
-            tc_commit(&s_full[s_at.st]);
-            tc_commit(&k_empty[at_s & 1]);
-            if (at_s + 1 == q_end) tc_commit(q_empty);
+          for (int y = 0; y < HD / 16; ++y) {
+            const uint32_t step = ((y >> 2) * (kPRows * 128) + (y & 3) * 32) >> 4;
+            tc_mma_ss(d, q_desc + step, b + step, s_id, y > 0);
+            if constexpr (TWO) tc_mma_ss(d, q_desc + (P::kTile >> 4) + step, b + step, s_id, 1);
           }
-          __syncwarp();
-          s_at.step();
-          ++at_s;
+          tc_commit(&s_full[place.st]);
+          tc_commit(&k_empty[at & 1]);
+          if (at + 1 == q_end) tc_commit(q_empty);
         }
+        __syncwarp();
+        place.step();
       }
       // every product is done before tensor memory is given back
-      if (elect_one()) tc_commit(last);
+      if (elect_one()) tc_commit(&last[0]);
       __syncwarp();
-      mbar_wait(last, 0, err);
+      mbar_wait(&last[0], 0, err);
+    } else if (warp == kMmaWarp + 1) {
+      // ---- U = P V ----
+      Ring<kScores> place;
+      Ring<2 * P::kVStages> vst;
+      bool ok = true;
+      const uint64_t v_desc = tc_desc(smem + P::kV, 1024, kPRows * 128);
+      constexpr uint32_t u_id = tc_idesc(HD, true);
+      const uint32_t d = tmem + kScores * 128;
+      for (int at = 0; at < n_units; ++at) {
+        if (!(ok = wait_warp(&p_full[place.st], place.ph, dead, err))) break;
+        if (at >= 1 && !(ok = wait_warp(u_empty, (at - 1) & 1, dead, err))) break;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = wait_warp(&v_full[vst.st], vst.ph, dead, err))) break;
+          tc_fence_after();
+          const uint32_t a = tmem + place.st * 128 + half * 64;
+          const uint64_t b = v_desc + (((vst.st >> 1) * P::kTile + half * (64 * 128)) >> 4);
+          if (elect_one()) {
+#pragma unroll 2
+            for (int y = 0; y < kPUnit / 32; ++y) {
+              tc_mma_ts(d, a + y * 16, b + ((y * 16 * 128) >> 4), u_id, half > 0 || y > 0);
+              if constexpr (TWO) tc_mma_ts(d, a + y * 16 + 8, b + ((y * 16 * 128) >> 4), u_id, 1);
+            }
+            tc_commit(&v_empty[vst.st]);
+            if (half) tc_commit(u_full), tc_commit(&place_free[place.st]);
+          }
+          __syncwarp();
+          vst.step();
+        }
+        if (!ok) break;
+        place.step();
+      }
+      if (elect_one()) tc_commit(&last[1]);
+      __syncwarp();
+      mbar_wait(&last[1], 0, err);
     } else if ((warp == kTmaWarp || warp == kTmaWarp + 1) && lane == 0) {
       // ---- TMA of the codes of K, or of V, 64 positions at a time ----
       const int v_side = warp - kTmaWarp;
@@ -949,12 +979,32 @@ __global__ void __launch_bounds__(kPThreads, 1)
       Ring<kRawStages> raw;
       int copies = 0, at = 0;
       bool ok = true;
-      while (at < n_units && ok) {
-        if (!(ok = wait_for(&seg_full[seg.st], seg.ph, dead, err))) break;
+      PItem item;
+      if (!v_side) p_begin(item, A, pre, span[1], span[2]);
+      for (int i = 0; at < n_units; ++i) {
+        if (!v_side) {  // the next segment: K's copies are the first to need it
+          if (i > 0) p_next(item, A, pre, span[1] + at, span[2]);
+          if (i >= kSegs && !(ok = wait_for(&seg_empty[seg.st], seg.ph ^ 1, dead, err))) break;
+          Seg* to = const_cast<Seg*>(segs) + seg.st;
+          to->row0 = item.s.row0, to->n = item.s.n, to->length = item.s.length, to->slot = item.s.slot;
+          to->head = item.head, to->tile = item.tile;
+          to->u0 = item.u0, to->u1 = item.u1, to->units = item.units, to->end = at + item.u1 - item.u0;
+          to->first = item.first;
+          mbar_arrive(&seg_full[seg.st]);
+          // its rows of q on their way to L2
+          const int tokens = min(A.tokens, item.s.n - item.tile * A.tokens), size = A.group * HD * (TWO ? 4 : 2);
+          const char* q = static_cast<const char*>(A.q) + ((item.s.row0 + (long long)item.tile * A.tokens) * A.q_stride +
+                                                           (long long)item.head * A.group * HD) * (TWO ? 4 : 2);
+#pragma unroll 1
+          for (int y = 0; y < tokens; ++y, q += A.q_stride * (TWO ? 4 : 2))
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(size) : "memory");
+        } else if (!(ok = wait_for(&seg_full[seg.st], seg.ph, dead, err))) {
+          break;
+        }
         const Seg* it = segs + seg.st;
         const int y0 = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
         const int x1 = 2 * it->u1, length = it->length;
-        for (int x = 2 * it->u0; x < x1 && ok; ++x) {
+        for (int x = 2 * it->u0; x < x1; ++x) {
           if (copies >= kRawStages && !(ok = wait_for(&raw_e[raw.st], raw.ph ^ 1, dead, err))) break;
           // a half that holds no position of the sequence is not needed (its codes become 0)
           if (x * 64 < length) {
@@ -973,26 +1023,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
         mbar_wait(&raw_f[i % kRawStages], (i / kRawStages) & 1, err);
-    } else if (warp == kListWarp && lane == 0) {
-      // ---- the CTA's segments ----
-      PItem it;
-      const long long lo = span[1], hi = span[2];
-      p_begin(it, A, pre, lo, hi);
-      Ring<kSegs> seg;
-      int n = 0;
-      for (int i = 0;; ++i) {
-        if (i >= kSegs && !wait_for(&seg_empty[seg.st], seg.ph ^ 1, dead, err)) break;
-        Seg* to = const_cast<Seg*>(segs) + seg.st;
-        n += it.u1 - it.u0;
-        to->row0 = it.s.row0, to->n = it.s.n, to->length = it.s.length, to->slot = it.s.slot;
-        to->head = it.head, to->tile = it.tile;
-        to->u0 = it.u0, to->u1 = it.u1, to->units = it.units, to->end = n;
-        to->first = it.first;
-        mbar_arrive(&seg_full[seg.st]);
-        seg.step();
-        if (n >= n_units) break;
-        p_next(it, A, pre, lo + n, hi);
-      }
     }
     __syncwarp();
   }
