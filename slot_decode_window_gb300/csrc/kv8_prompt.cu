@@ -46,6 +46,9 @@ constexpr int kMmaWarp = 20, kTmaWarp = 22;  // products: 20 S, 21 U; TMA: 22 K,
 constexpr float kPWeightTop = 14.f;
 constexpr float kLeastFactor = 1e-37f;
 constexpr int kRawStages = 3;      // of half a unit's codes, for K and for V
+// Barriers of a stage for each half, so that a warp, which takes only its half's copies, waits for every phase of the
+// barriers that it reads (one barrier for both would let it take the other half's earlier phase for its own).
+constexpr int kRawBars = 2 * kRawStages;
 constexpr int kScores = 3;         // places of S (and then P) in tensor memory
 
 template <int HD, bool TWO> struct PromptPlan {
@@ -60,7 +63,7 @@ template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kRf = kStats + 4 * kPRows * 8;         // [4][128] the rows' powers of two, by item
   static constexpr int kExp = kRf + 4 * kPRows * 4;           // [8][8] float4: a unit's factors per 16 positions
   static constexpr int kBars = kExp + 8 * 8 * 16;
-  static constexpr int kMisc = kBars + 512;                   // tensor memory address, flags, scan sums
+  static constexpr int kMisc = kBars + 1024;                  // tensor memory address, flags, scan sums
   static constexpr int kSegOff = kMisc + 256;                 // [kSegs] Seg
   static constexpr int kPre = kSegOff + 64 * kSegs;
   // registers per thread by role (softmax keeps the launch's)
@@ -171,8 +174,10 @@ constexpr uint32_t tc_idesc(int n, bool b_mn_major) {
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* dead, unsigned* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
+  while (true) {
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*dead) return false;
     if (clock64() - t0 > (1LL << 31)) {
       *dead = 1;
@@ -180,7 +185,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
       return false;
     }
   }
-  return true;
 }
 
 // The same for a whole warp, with one answer.
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float4* factors = reinterpret_cast<float4*>(smem + P::kExp);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
   uint64_t *v_full = bars, *v_empty = bars + 4, *k_full = bars + 8, *k_empty = bars + 10, *q_full = bars + 12, *q_empty = bars + 13, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
-           *last = bars + 24, *place_free = bars + 26, *raw_full = bars + 48, *raw_empty = bars + 54, *seg_full = bars + 32, *seg_empty = bars + 40;
+           *last = bars + 24, *place_free = bars + 26, *raw_full = bars + 48, *raw_empty = bars + 48 + 2 * kRawBars, *seg_full = bars + 32, *seg_empty = bars + 40;
   const Seg* segs = reinterpret_cast<const Seg*>(smem + P::kSegOff);
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
@@ -504,11 +508,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < 2 * kRawStages; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
+    for (int i = 0; i < 2 * kRawBars; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4), mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&v_full[i], 4), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&v_full[i], 2), mbar_init(&v_empty[i], 1);
     for (int i = 0; i < kScores; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&place_free[i], 1);
     mbar_init(u_full, 1), mbar_init(u_empty, 4);
     mbar_init(q_full, 4), mbar_init(q_empty, 1), mbar_init(&last[0], 1), mbar_init(&last[1], 1);
@@ -729,27 +733,29 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else if (warp < 20) {
     // ---- conversion: q of each item and K of its units, or V, to f16 tiles ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegConvert));
-    const int t = tid & 127, v_side = warp >> 4;  // warps 12..15: K, 16..19: V
-    uint64_t *raw_f = raw_full + v_side * kRawStages, *raw_e = raw_empty + v_side * kRawStages;
-    Ring<kRawStages> raw;
+    // two warps take the first half of every tile (64 positions), two the second
+    const int t = tid & 127, v_side = warp >> 4, half = (warp >> 1) & 1;  // warps 12..15: K, 16..19: V
+    uint64_t *raw_f = raw_full + v_side * kRawBars, *raw_e = raw_empty + v_side * kRawBars;
+    Ring<kRawBars> raw;  // copy h is at barrier h % 6, in stage h % 3; this warp's are those with h % 2 = half
+    if (half) raw.step();
     bool ok = true;
     // Half a tile (64 positions) of codes to f16: the chunks of 16 codes of a thread are all read, the codes' place is
     // given back, then they are converted.  Rows from `valid` on become 0.
     auto half_tile = [&](uint8_t* dst, int valid) {
       // Eight neighbouring lanes take four chunks of row r and four of row r ^ 5 (mod 8): under both swizzles they meet
       // eight different 16-byte columns, reading the codes and writing either half of the values.  A thread's rows
-      // are 16 (32) apart, so its swizzled columns stay.
-      constexpr int kMine = HD / 32, kStep = HD == 128 ? 16 : 32;
-      const uint8_t* src = smem + P::kRawOff + (v_side * kRawStages + raw.st) * P::kRaw;
-      const int w = warp & 3, r7 = ((t >> 3) & 3) ^ ((t >> 2) & 1) * 5;
-      const int r0 = (HD == 128 ? w >> 1 : w) * 8 + r7, panel = HD == 128 ? w & 1 : 0;
+      // are 8 (16) apart, so its swizzled columns stay.
+      constexpr int kMine = HD / 16, kStep = HD == 128 ? 8 : 16;
+      const uint8_t* src = smem + P::kRawOff + (v_side * kRawStages + raw.st % kRawStages) * P::kRaw;
+      const int w = warp & 1, r7 = ((t >> 3) & 3) ^ ((t >> 2) & 1) * 5;
+      const int r0 = (HD == 128 ? 0 : w) * 8 + r7, panel = HD == 128 ? w : 0;
       const int from = HD == 128 ? r0 * 128 + (((panel * 4 + (t & 3)) ^ r7) << 4) : r0 * 64 + (((t & 3) ^ (r7 >> 1)) << 4);
       uint4 cw[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) cw[i] = *reinterpret_cast<const uint4*>(src + from + i * (kStep * HD));
       __syncwarp();
       if (lane == 0) mbar_arrive(&raw_e[raw.st]);
-      raw.step();
+      raw.step(), raw.step();
       if (valid < 64) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
@@ -835,20 +841,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) mbar_arrive(q_full);
     };
     Ring<kSegs> seg;
-    int at = 0, items = 0, st = 0;  // st: the half's place in two tiles (K) or kVStages (V)
+    int at = 0, items = 0, st = 0;  // st: the tile's place, of 2 (K) or kVStages (V)
     uint32_t ph = 0;
-    const int places = v_side ? 2 * P::kVStages : 4;
+    const int places = v_side ? P::kVStages : 2;
     uint8_t* tiles = smem + (v_side ? P::kV : P::kK);
     while (at < n_units) {
       if (!(ok = wait_warp(&seg_full[seg.st], seg.ph, dead, err))) break;
       const Seg* it = segs + seg.st;
       const int end = it->end, length = it->length;
-      int p = it->u0 * kPUnit;
+      int p = it->u0 * kPUnit + half * 64;
       // factors per 16 positions, fetched one unit ahead by 8 threads of the K side
       const long long line = ((long long)it->slot * A.C.kv_heads + it->head) * A.C.n_blocks;
       int e_next = 0;
       auto fetch = [&]() {
-        if (!v_side && t < 8 && p + t * 16 < length) {
+        if (!v_side && t < 8 && p + t * 16 < length) {  // (of the first half's warps)
           const long long b = line + ((p + t * 16) >> A.C.block_log2);
           e_next = A.C.k_exp[b] | A.C.v_exp[b] << 8;
         }
@@ -861,28 +867,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
 #pragma unroll 1
       for (; at < end; ++at) {
-        if (!v_side) {
-          if (at >= 2 && !(ok = wait_warp(&k_empty[st >> 1], ph ^ 1, dead, err))) break;
-          if (t < 8) {
-            const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
-            factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
-          }
+        if (at >= places && !(ok = wait_warp(v_side ? &v_empty[st * 2 + half] : &k_empty[st], ph ^ 1, dead, err))) break;
+        if (!v_side && t < 8) {
+          const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
+          factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
         }
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (v_side && at >= P::kVStages && !(ok = wait_warp(&v_empty[st], ph ^ 1, dead, err))) break;
-          if (!(ok = wait_warp(&raw_f[raw.st], raw.ph, dead, err))) break;
-          half_tile(tiles + (st >> 1) * P::kTile + half * (64 * 128), length - p);
-          p += 64;
-          if (v_side || half) {  // (K's first half: the fence of the second covers it)
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v_side ? &v_full[st] : &k_full[st >> 1]);
-          }
-          if (++st == places) st = 0, ph ^= 1;
-        }
-        if (!ok) break;
+        if (!(ok = wait_warp(&raw_f[raw.st], raw.ph, dead, err))) break;
+        half_tile(tiles + st * P::kTile + half * (64 * 128), length - p);
+        p += kPUnit;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_side ? &v_full[st * 2 + half] : &k_full[st]);
         if (at + 1 < end) fetch();
+        if (++st == places) st = 0, ph ^= 1;
       }
       if (!ok) break;
       __syncwarp();
@@ -973,10 +970,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ---- TMA of the codes of K, or of V, 64 positions at a time ----
       const int v_side = warp - kTmaWarp;
       const CUtensorMap* map = v_side ? &vmap : &kmap;
-      uint64_t *raw_f = raw_full + v_side * kRawStages, *raw_e = raw_empty + v_side * kRawStages;
+      uint64_t *raw_f = raw_full + v_side * kRawBars, *raw_e = raw_empty + v_side * kRawBars;
       uint8_t* dst = smem + P::kRawOff + v_side * kRawStages * P::kRaw;
       Ring<kSegs> seg;
-      Ring<kRawStages> raw;
+      Ring<kRawBars> raw, freed;  // freed: three copies behind, the last user of raw's stage
       int copies = 0, at = 0;
       bool ok = true;
       PItem item;
@@ -1005,11 +1002,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int y0 = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
         const int x1 = 2 * it->u1, length = it->length;
         for (int x = 2 * it->u0; x < x1; ++x) {
-          if (copies >= kRawStages && !(ok = wait_for(&raw_e[raw.st], raw.ph ^ 1, dead, err))) break;
+          if (copies >= kRawStages) {
+            if (!(ok = wait_for(&raw_e[freed.st], freed.ph, dead, err))) break;
+            freed.step();
+          }
           // a half that holds no position of the sequence is not needed (its codes become 0)
           if (x * 64 < length) {
             mbar_arrive_expect_tx(&raw_f[raw.st], P::kRaw);
-            p_tma_3d(dst + raw.st * P::kRaw, map, 0, y0 + x * 64, A.layer, &raw_f[raw.st]);
+            p_tma_3d(dst + raw.st % kRawStages * P::kRaw, map, 0, y0 + x * 64, A.layer, &raw_f[raw.st]);
           } else {
             mbar_arrive(&raw_f[raw.st]);
           }
@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         seg.step();
       }
       for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
-        mbar_wait(&raw_f[i % kRawStages], (i / kRawStages) & 1, err);
+        mbar_wait(&raw_f[i % kRawBars], (i / kRawBars) & 1, err);
     }
     __syncwarp();
   }
