@@ -746,31 +746,52 @@ class Head:
             pass
 
 
-def _values(t, heads: int, head_dim: int, what: str, like=None):
-    """(pointer, row stride in elements, strata_dtype) of a CUDA tensor [T][heads][head_dim] whose rows may be
-    strided; raises for any other layout."""
-    import torch
-    code = {torch.float32: STRATA_F32, torch.float16: STRATA_F16, torch.bfloat16: STRATA_BF16}.get(t.dtype)
+# The calls below are short next to Python's own time, so their checks read each tensor property once.
+_DTYPE = None  # torch dtype -> strata_dtype
+
+
+def _dtypes():
+    global _DTYPE
+    if _DTYPE is None:
+        import torch
+        _DTYPE = {torch.float32: STRATA_F32, torch.float16: STRATA_F16, torch.bfloat16: STRATA_BF16}
+    return _DTYPE
+
+
+def _row_stride(t, shape, what: str) -> int:
+    """The distance between rows, in elements, of a CUDA tensor of this shape [T][heads][head_dim]; raises for any
+    layout whose rows are not contiguous."""
+    T, heads, hd = shape
     st = t.stride()
-    if code is None or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or \
-            st[2] != 1 or (heads > 1 and st[1] != head_dim):
-        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [rows][{heads}][{head_dim}] of float32, float16 "
-                                         "or bfloat16 whose rows are contiguous")
-    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.device != like.device):
-        raise StrataError(STRATA_EINVAL, f"{what}: rows, type or device differ")
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * head_dim), code
+    if not t.is_cuda or tuple(t.shape) != shape or st[2] != 1 or (st[1] != hd and heads != 1) or t.dtype not in _dtypes():
+        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [rows][{heads}][{hd}] of float32, float16 or "
+                                         "bfloat16 whose rows are contiguous")
+    return st[0] if T > 1 else heads * hd
+
+
+def _same(t, like, what: str) -> None:
+    if t.dtype != like.dtype or t.get_device() != like.get_device():
+        raise StrataError(STRATA_EINVAL, f"{what}: type or device differ")
+
+
+def _same_device(t, like, what: str) -> None:
+    if t.get_device() != like.get_device():
+        raise StrataError(STRATA_EINVAL, f"{what}: device differs")
 
 
 def _int32(t, n: int, what: str):
     import torch
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
         raise StrataError(STRATA_EINVAL, f"{what}: want a contiguous CUDA int32 tensor [{n}]")
     return t.data_ptr()
 
 
-def _stream_of(t, stream):
+def _raw_stream(index: int, stream) -> int:
+    """The cudaStream_t of a stream, or of the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    return (stream or torch.cuda.current_stream(t.device)).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -813,23 +834,39 @@ class QkNorm:
                 freqs, s)
         check(st, "strata_qknorm_create")
         self.handle = h
+        self._forward = load().strata_qknorm_forward
 
     def forward(self, q, k, position, q_out=None, k_out=None, stream=None):
         """Enqueue q [T][heads][head_dim] and k [T][kv_heads][head_dim] at position (CUDA int32 [T]); returns
         (q_out, k_out), new tensors unless given (an output may be its own input)."""
-        qp, qs, dt = _values(q, self.heads, self.head_dim, "q")
+        if q.dim() != 3:
+            raise StrataError(STRATA_EINVAL, "q: want [rows][heads][head_dim]")
+        T, kv, hd = q.shape[0], self.kv_heads, self.head_dim
+        shape = (T, self.heads, hd)
+        qs = _row_stride(q, shape, "q")
+        qos = self.heads * hd
         if q_out is None:
-            q_out = _empty(q.shape, q.dtype, q.device, stream)
-        qop, qos, _ = _values(q_out, self.heads, self.head_dim, "q_out", q)
+            q_out = _empty(shape, q.dtype, q.device, stream)
+        else:
+            qos = _row_stride(q_out, shape, "q_out")
+            _same(q_out, q, "q_out")
         kp = ks = kop = kos = 0
-        if self.kv_heads > 0:
-            kp, ks, _ = _values(k, self.kv_heads, self.head_dim, "k", q)
+        if kv > 0:
+            kshape = (T, kv, hd)
+            if k.dim() != 3:
+                raise StrataError(STRATA_EINVAL, "k: want [rows][kv_heads][head_dim]")
+            ks = _row_stride(k, kshape, "k")
+            _same(k, q, "k")
+            kos = kv * hd
             if k_out is None:
-                k_out = _empty(k.shape, k.dtype, k.device, stream)
-            kop, kos, _ = _values(k_out, self.kv_heads, self.head_dim, "k_out", q)
-        T = q.shape[0]
-        st = load().strata_qknorm_forward(self.handle, qp, qs, kp, ks, qop, qos, kop, kos, dt,
-                                          _int32(position, T, "position"), T, _stream_of(q, stream))
+                k_out = _empty(kshape, k.dtype, k.device, stream)
+            else:
+                kos = _row_stride(k_out, kshape, "k_out")
+                _same(k_out, q, "k_out")
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        _same_device(position, q, "position")
+        st = self._forward(self.handle, q.data_ptr(), qs, kp, ks, q_out.data_ptr(), qos, kop, kos, _DTYPE[q.dtype],
+                           _int32(position, T, "position"), T, _raw_stream(q.get_device(), stream))
         if st != STRATA_OK:
             check(st, "strata_qknorm_forward")
         return q_out, k_out
@@ -855,7 +892,9 @@ class KvRows:
     def __init__(self, row_start, slot, length, n_rows: int, max_rows: int):
         n = slot.shape[0]
         self.keep = (row_start, slot, length)
-        self.n_rows, self.device = n_rows, slot.device
+        self.n_rows, self.device = n_rows, slot.get_device()
+        _same_device(row_start, slot, "row_start")
+        _same_device(length, slot, "length")
         self.c = strata_kv8_rows(n, n_rows, max_rows, _int32(row_start, n + 1, "row_start"), _int32(slot, n, "slot"),
                                  _int32(length, n, "length"))
 
@@ -896,18 +935,21 @@ class KvCache8:
             st, h = strata_kv8_create(desc, strata_kv8_cache(*(t.data_ptr() for t in buffers)))
         check(st, "strata_kv8_create")
         self.handle = h
+        self.device = self.k.get_device()
+        lib = load()
+        self._append, self._read, self._attend = lib.strata_kv8_append, lib.strata_kv8_read, lib.strata_kv8_attend
 
-    def _rows(self, rows, t, what):
-        if t.shape[0] != rows.n_rows or t.device != self.k.device or rows.device != t.device:
-            raise StrataError(STRATA_EINVAL, f"{what}: rows or device differ")
-        return rows.c
+    def _stride(self, rows, t, heads: int, what: str) -> int:
+        if t.dim() != 3 or t.get_device() != self.device or rows.device != self.device:
+            raise StrataError(STRATA_EINVAL, f"{what}: want [rows][heads][head_dim] on the cache's device")
+        return _row_stride(t, (rows.n_rows, heads, self.head_dim), what)
 
     def append(self, layer: int, k, v, rows: KvRows, stream=None) -> None:
         """Enqueue the rows' keys and values [n_rows][kv_heads][head_dim] into the layer's caches."""
-        kp, ks, dt = _values(k, self.kv_heads, self.head_dim, "k")
-        vp, vs, _ = _values(v, self.kv_heads, self.head_dim, "v", k)
-        st = load().strata_kv8_append(self.handle, layer, kp, ks, vp, vs, dt, self._rows(rows, k, "append"),
-                                      _stream_of(k, stream))
+        ks, vs = self._stride(rows, k, self.kv_heads, "k"), self._stride(rows, v, self.kv_heads, "v")
+        _same(v, k, "v")
+        st = self._append(self.handle, layer, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPE[k.dtype], rows.c,
+                          _raw_stream(self.device, stream))
         if st != STRATA_OK:
             check(st, "strata_kv8_append")
 
@@ -920,10 +962,10 @@ class KvCache8:
             k = _empty(shape, dtype or torch.float32, self.k.device, stream)
         if v is None:
             v = _empty(shape, k.dtype, self.k.device, stream)
-        kp, ks, dt = _values(k, self.kv_heads, self.head_dim, "k")
-        vp, vs, _ = _values(v, self.kv_heads, self.head_dim, "v", k)
-        st = load().strata_kv8_read(self.handle, layer, kp, ks, vp, vs, dt, self._rows(rows, k, "read"),
-                                    _stream_of(k, stream))
+        ks, vs = self._stride(rows, k, self.kv_heads, "k"), self._stride(rows, v, self.kv_heads, "v")
+        _same(v, k, "v")
+        st = self._read(self.handle, layer, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPE[k.dtype], rows.c,
+                        _raw_stream(self.device, stream))
         if st != STRATA_OK:
             check(st, "strata_kv8_read")
         return k, v
@@ -931,12 +973,15 @@ class KvCache8:
     def attend(self, layer: int, q, rows: KvRows, out=None, scale: Optional[float] = None, stream=None):
         """Enqueue the attention of q [n_rows][heads][head_dim] over the layer's caches; returns out, a new tensor
         unless given; rows of no sequence are not written.  scale: 1 / sqrt(head_dim) unless given."""
-        qp, qs, dt = _values(q, self.heads, self.head_dim, "q")
+        qs = self._stride(rows, q, self.heads, "q")
         if out is None:
-            out = _empty(q.shape, q.dtype, q.device, stream)
-        op, os_, _ = _values(out, self.heads, self.head_dim, "out", q)
-        st = load().strata_kv8_attend(self.handle, layer, qp, qs, op, os_, dt, self.scale if scale is None else scale,
-                                      self._rows(rows, q, "attend"), _stream_of(q, stream))
+            out = _empty((rows.n_rows, self.heads, self.head_dim), q.dtype, q.device, stream)
+            os_ = self.heads * self.head_dim
+        else:
+            os_ = self._stride(rows, out, self.heads, "out")
+            _same(out, q, "out")
+        st = self._attend(self.handle, layer, q.data_ptr(), qs, out.data_ptr(), os_, _DTYPE[q.dtype],
+                          self.scale if scale is None else scale, rows.c, _raw_stream(self.device, stream))
         if st != STRATA_OK:
             check(st, "strata_kv8_attend")
         return out

@@ -20,7 +20,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
                                                           long long v_stride, int nb) {
   constexpr int kPer = Val<T>::kPer;
   __shared__ unsigned red[kThreads / 32];
-  __shared__ int bad;
   int id = blockIdx.x;
   const int b_at = id % nb;
   id /= nb;
@@ -40,17 +39,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
   const int blk = (p0 >> C.block_log2) + b_at;
   const int lo = max(p0, blk << C.block_log2), hi = min(q.length, (blk + 1) << C.block_log2);
   if (lo >= hi) return;
-  // an earlier sequence with rows that names the same slot owns it
-  if (threadIdx.x == 0) bad = 0;
-  __syncthreads();
-  for (int j = threadIdx.x; j < i; j += kThreads)
-    if (R.slot[j] == q.slot && R.row_start[j + 1] > R.row_start[j]) bad = 1;
-  __syncthreads();
-  if (bad) {
-    if (lead) atomicOr(C.err, kErrIndex);
-    return;
-  }
-
+  // the new values, all on their way before anything waits
   const int hd = C.head_dim;
   const int tpt_log2 = (hd == 128 ? 7 : 6) - (kPer == 4 ? 2 : 3);  // threads per token
   const int per_pass = kThreads >> tpt_log2;
@@ -63,8 +52,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int t = t0 + p * per_pass;
-    raw[p] = t < n ? *reinterpret_cast<const uint4*>(base + (long long)t * stride) : make_uint4(0, 0, 0, 0);
+    raw[p] = t < n ? __ldcs(reinterpret_cast<const uint4*>(base + (long long)t * stride)) : make_uint4(0, 0, 0, 0);
   }
+  const long long line = (long long)q.slot * C.kv_heads + head;
+  uint8_t* codes = (is_v ? C.v : C.k) + (line * C.max_ctx + (blk << C.block_log2)) * hd;
+  uint8_t* ep = (is_v ? C.v_exp : C.k_exp) + line * C.n_blocks + blk;
+  const int held = lo - (blk << C.block_log2);
+  const int e_held = held > 0 ? kv8_exp(*ep) : kKv8EMin;
+  // an earlier sequence with rows that names the same slot owns it
+  int taken = 0;
+  for (int j = threadIdx.x; j < i; j += kThreads)
+    if (R.slot[j] == q.slot && R.row_start[j + 1] > R.row_start[j]) taken = 1;
   unsigned a = 0;
   bool odd = false;
 #pragma unroll
@@ -82,18 +80,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
   }
   a = __reduce_max_sync(0xFFFFFFFFu, a);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+  // one barrier: the maxima are there, and every thread has read the held exponent
+  if (__syncthreads_or(taken)) {
+    if (lead) atomicOr(C.err, kErrIndex);
+    return;
+  }
   if (odd) atomicOr(C.err, kErrNonFinite);
-  __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) a = max(a, red[w]);
 
-  const long long line = (long long)q.slot * C.kv_heads + head;
-  uint8_t* codes = (is_v ? C.v : C.k) + (line * C.max_ctx + (blk << C.block_log2)) * hd;
-  uint8_t* ep = (is_v ? C.v_exp : C.k_exp) + line * C.n_blocks + blk;
   int e = kv8_least_exp(__uint_as_float(a), C.format);
-  const int held = lo - (blk << C.block_log2);
   if (held > 0) {
-    const int e_held = kv8_exp(*ep);
     if (e > e_held) {
       const float f = pow2i(e_held - e);
       uint32_t* w = reinterpret_cast<uint32_t*>(codes);
@@ -108,7 +105,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
       e = e_held;
     }
   }
-  __syncthreads();  // every thread has read the held exponent
   if (threadIdx.x == 0) *ep = (uint8_t)(e + kKv8Bias);
   const float f = pow2i(-e);
 #pragma unroll

@@ -33,22 +33,39 @@ struct QkArgs {
 constexpr int kQkThreads = 128;
 constexpr int kQkBatch = 4;  // vectors a warp has in flight
 
-// A warp owns `per_warp` consecutive heads of a row (of q's and then k's):
-// lane l holds the E = head_dim / 32 dims l E .. l E + E - 1 of a head, so a
-// head is one contiguous access, its mean a warp sum, and the E angles that a
-// lane needs are the same for every head and are formed once.  The half-apart
-// partner of a dim is E-aligned in another lane, one shuffle away.
-// The angle in turns is position * turn mod 2^64: the product wraps to the
-// exact fraction, its top 32 bits go to sincospi.
-template <typename T, int E, bool kInter>
+// A warp owns `per_warp` heads of a row (of q's and then k's), kGroup at a time: E neighbouring dims of a head in a
+// lane, 32 / kGroup lanes to a head, 16 bytes a lane wherever the rotation's halves allow it, kQkBatch accesses in
+// flight.  The head's mean is a sum over its lanes; the E angles that a lane needs are the same for every head and are
+// formed once.  The half-apart partner of a dim is in another lane at the same place, one shuffle away (half a
+// rotary_dim is a multiple of E).
+// The angle in turns is position * turn mod 2^64: the product wraps to the exact fraction, its top 32 bits go to
+// sincospi.
+template <typename T, int kHd, int E, bool kInter>
 __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
-  constexpr int kHd = 32 * E;
-  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = kHd / E, kGroup = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes;
   const long long w = (long long)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
   const long long row = w / A.groups;
   if (row >= A.T) return;
   const int h0 = (int)(w % A.groups) * A.per_warp, h1 = min(A.total, h0 + A.per_warp);
-  const int d0 = lane * E, half = A.rotary >> 1;
+  const int d0 = sub * E, half = A.rotary >> 1;
+
+  struct alignas(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Vec { T v[E]; };  // rows are 16-byte aligned
+  Vec x[kQkBatch];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int b = 0; b < kQkBatch; ++b) {
+      const int hh = h + b * kGroup + lane / kLanes;
+      if (hh < h1) {
+        const T* src = hh < A.heads ? static_cast<const T*>(A.q) + row * A.qs + (long long)hh * kHd
+                                    : static_cast<const T*>(A.k) + row * A.ks + (long long)(hh - A.heads) * kHd;
+        x[b] = reinterpret_cast<const Vec*>(src)[sub];
+      } else {
+        x[b] = Vec{};
+      }
+    }
+  };
+  fetch(h0);  // on its way while the angles are formed
 
   float cs[E], sn[E];
   int partner = lane;
@@ -86,22 +103,13 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
     }
   }
 
-  struct alignas(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Vec { T v[E]; };  // rows are 16-byte aligned
-  for (int h = h0; h < h1; h += kQkBatch) {
-    Vec x[kQkBatch];
+  for (int h = h0; h < h1; h += kQkBatch * kGroup) {
+    if (h > h0) fetch(h);
 #pragma unroll
     for (int b = 0; b < kQkBatch; ++b) {
-      const int hh = h + b;
-      if (hh < h1) {
-        const T* src = hh < A.heads ? static_cast<const T*>(A.q) + row * A.qs + (long long)hh * kHd
-                                    : static_cast<const T*>(A.k) + row * A.ks + (long long)(hh - A.heads) * kHd;
-        x[b] = reinterpret_cast<const Vec*>(src)[lane];
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < kQkBatch; ++b) {
-      const int hh = h + b;
-      if (hh >= h1) break;
+      if (h + b * kGroup >= h1) break;
+      const int hh = h + b * kGroup + lane / kLanes;
+      const bool is_q = hh < A.heads;
       float f[E];
 #pragma unroll
       for (int i = 0; i < E; ++i) f[i] = Val<T>::up(x[b].v[i]);
@@ -110,10 +118,10 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
 #pragma unroll
         for (int i = 0; i < E; ++i) s = fmaf(f[i], f[i], s);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         const float r = 1.f / sqrtf(s * (1.f / kHd) + A.eps);
 #pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = f[i] * r * (hh < A.heads ? gq[i] : gk[i]);
+        for (int i = 0; i < E; ++i) f[i] = f[i] * r * (is_q ? gq[i] : gk[i]);
       }
       if (A.rotary > 0) {
         if constexpr (kInter) {
@@ -133,32 +141,44 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
           }
         }
       }
-      Vec y;
+      if (hh < h1) {
+        Vec y;
 #pragma unroll
-      for (int i = 0; i < E; ++i) y.v[i] = Val<T>::down(f[i]);
-      T* dst = hh < A.heads ? static_cast<T*>(A.q_out) + row * A.qos + (long long)hh * kHd
-                            : static_cast<T*>(A.k_out) + row * A.kos + (long long)(hh - A.heads) * kHd;
-      reinterpret_cast<Vec*>(dst)[lane] = y;
+        for (int i = 0; i < E; ++i) y.v[i] = Val<T>::down(f[i]);
+        T* dst = is_q ? static_cast<T*>(A.q_out) + row * A.qos + (long long)hh * kHd
+                      : static_cast<T*>(A.k_out) + row * A.kos + (long long)(hh - A.heads) * kHd;
+        reinterpret_cast<Vec*>(dst)[sub] = y;
+      }
     }
   }
 }
 
-template <typename T, int E>
+template <typename T, int kHd, int E>
 void launch_e(const QkArgs& A, int interleaved, unsigned grid, cudaStream_t s) {
   if (interleaved)
-    qknorm_kernel<T, E, true><<<grid, kQkThreads, 0, s>>>(A);
+    qknorm_kernel<T, kHd, E, true><<<grid, kQkThreads, 0, s>>>(A);
   else
-    qknorm_kernel<T, E, false><<<grid, kQkThreads, 0, s>>>(A);
+    qknorm_kernel<T, kHd, E, false><<<grid, kQkThreads, 0, s>>>(A);
+}
+
+// E: 16 bytes of a lane where the rotation's halves are a multiple of them, else the head over all 32 lanes.
+template <typename T, int kHd>
+void launch_h(const QkArgs& A, int interleaved, unsigned grid, cudaStream_t s) {
+  constexpr int kWide = kHd == 256 ? 8 : 16 / sizeof(T);
+  if (interleaved || A.rotary % (2 * kWide) == 0)
+    launch_e<T, kHd, kWide>(A, interleaved, grid, s);
+  else
+    launch_e<T, kHd, kHd / 32>(A, interleaved, grid, s);
 }
 
 template <typename T>
 void launch_t(const QkArgs& A, int head_dim, int interleaved, unsigned grid, cudaStream_t s) {
   if (head_dim == 64)
-    launch_e<T, 2>(A, interleaved, grid, s);
+    launch_h<T, 64>(A, interleaved, grid, s);
   else if (head_dim == 128)
-    launch_e<T, 4>(A, interleaved, grid, s);
+    launch_h<T, 128>(A, interleaved, grid, s);
   else
-    launch_e<T, 8>(A, interleaved, grid, s);
+    launch_h<T, 256>(A, interleaved, grid, s);
 }
 
 void free_qknorm(strata_qknorm* h) {
@@ -256,11 +276,11 @@ strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_s
   A.gain = h->gain, A.turn = h->turn, A.position = position;
   A.T = T, A.heads = d.heads, A.total = d.heads + d.kv_heads;
   A.rotary = d.rotary_dim, A.norm = d.norm, A.eps = d.eps;
-  // heads per warp: as many as leave every SM 32 warps, so that a long prompt
-  // forms its angles once for several heads and a window spreads over the SMs
+  // heads per warp: as many as leave every SM 48 warps, at most 16, so that a long prompt forms its angles once for
+  // several heads and a window spreads over the SMs
   const long long vectors = (long long)T * A.total;
-  long long per = vectors / (32LL * h->nsm);
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  long long per = vectors / (48LL * h->nsm);
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
   A.per_warp = (int)per;
   A.groups = (A.total + A.per_warp - 1) / A.per_warp;
   const long long warps = (long long)T * A.groups;
