@@ -7,6 +7,28 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Largest magnitudes of 16 bytes of values as they are in memory: for the 16-bit types two at a time (their bits
+// without the sign are ordered as their magnitudes).  bits(): as an f32's.
+template <typename T> struct Abs;
+template <> struct Abs<float> {
+  static __device__ __forceinline__ unsigned most(unsigned a, const uint4& u) {
+    return max(max(max(a, u.x & 0x7FFFFFFFu), u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
+  }
+  static __device__ __forceinline__ unsigned bits(unsigned a) { return a; }
+};
+template <> struct Abs<__nv_bfloat16> {
+  static __device__ __forceinline__ unsigned most(unsigned a, const uint4& u) {
+    return __vmaxu2(__vmaxu2(__vmaxu2(a, u.x & 0x7FFF7FFFu), u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+  }
+  static __device__ __forceinline__ unsigned bits(unsigned a) { return max(a >> 16, a & 0xFFFFu) << 16; }
+};
+template <> struct Abs<__half> {
+  static __device__ __forceinline__ unsigned most(unsigned a, const uint4& u) { return Abs<__nv_bfloat16>::most(a, u); }
+  static __device__ __forceinline__ unsigned bits(unsigned a) {
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)max(a >> 16, a & 0xFFFFu))));
+  }
+};
+
 // --- append -------------------------------------------------------------------
 //
 // One CTA owns one block of one head, of the keys or of the values: it finds
@@ -64,18 +86,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
   for (int j = threadIdx.x; j < i; j += kThreads)
     if (R.slot[j] == q.slot && R.row_start[j + 1] > R.row_start[j]) taken = 1;
   unsigned a = 0;
-  bool odd = false;
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    float f[kPer];
-    Val<T>::unpack(raw[p], f);
+  for (int p = 0; p < NP; ++p) a = Abs<T>::most(a, raw[p]);
+  a = Abs<T>::bits(a);
+  const bool odd = a >= 0x7F800000u;
+  if (odd) {  // something is not finite: the largest of the others
+    a = 0;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const unsigned m = __float_as_uint(f[x]) & 0x7FFFFFFFu;
-      if (m < 0x7F800000u)
-        a = max(a, m);
-      else
-        odd = true;
+    for (int p = 0; p < NP; ++p) {
+      float f[kPer];
+      Val<T>::unpack(raw[p], f);
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        const unsigned m = __float_as_uint(f[x]) & 0x7FFFFFFFu;
+        if (m < 0x7F800000u) a = max(a, m);
+      }
     }
   }
   a = __reduce_max_sync(0xFFFFFFFFu, a);
@@ -114,7 +139,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
     float x[kPer];
     Val<T>::unpack(raw[p], x);
 #pragma unroll
-    for (int y = 0; y < kPer; ++y) x[y] = x[y] == x[y] ? x[y] * f : 0.f;
+    for (int y = 0; y < kPer; ++y) x[y] *= f;
+    if (odd) {
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) x[y] = x[y] == x[y] ? x[y] : 0.f;
+    }
     uint8_t* to = codes + (held + t) * hd + d;
     if constexpr (kPer == 4)
       *reinterpret_cast<uint32_t*>(to) = kv8_encode4(x, C.format);

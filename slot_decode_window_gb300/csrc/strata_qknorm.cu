@@ -26,28 +26,31 @@ struct QkArgs {
   const float* gain;
   const unsigned long long* turn;
   const int* position;
-  int T, heads, total, rotary, norm, per_warp, groups;
+  int T, heads, total, rotary, norm, per_cta, groups;
   float eps;
 };
 
 constexpr int kQkThreads = 128;
-constexpr int kQkBatch = 4;  // vectors a warp has in flight
+constexpr int kQkBatch = 4;  // 16-byte accesses a thread has in flight
 
-// A warp owns `per_warp` heads of a row (of q's and then k's), kGroup at a time: E neighbouring dims of a head in a
-// lane, 32 / kGroup lanes to a head, 16 bytes a lane wherever the rotation's halves allow it, kQkBatch accesses in
-// flight.  The head's mean is a sum over its lanes; the E angles that a lane needs are the same for every head and are
-// formed once.  The half-apart partner of a dim is in another lane at the same place, one shuffle away (half a
-// rotary_dim is a multiple of E).
+// A CTA owns `per_cta` heads of a row (of q's and then k's).  Its threads form the row's angles once, an angle a
+// thread, in shared memory; then a warp takes kGroup heads at a time: E neighbouring dims of a head in a lane,
+// 32 / kGroup lanes to a head, 16 bytes a lane wherever the rotation's halves allow it, kQkBatch accesses in flight.
+// The head's mean is a sum over its lanes; the half-apart partner of a dim is in another lane at the same place, one
+// shuffle away (half a rotary_dim is a multiple of E).
 // The angle in turns is position * turn mod 2^64: the product wraps to the exact fraction, its top 32 bits go to
 // sincospi.
+// HBM bound in a prompt.  With the angles and gains in every warp's registers instead (91 of them, a quarter of the
+// SM's warps, six times the angles) 8191 rows of 32 + 8 bf16 heads took 73.6 us.
 template <typename T, int kHd, int E, bool kInter>
 __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
-  constexpr int kLanes = kHd / E, kGroup = 32 / kLanes;
+  constexpr int kLanes = kHd / E, kGroup = 32 / kLanes, kWarps = kQkThreads / 32;
+  __shared__ float2 turn[kHd / 2];        // cosine and sine of each pair's angle
+  __shared__ alignas(16) float gain[2][kHd];
   const int lane = threadIdx.x & 31, sub = lane % kLanes;
-  const long long w = (long long)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
-  const long long row = w / A.groups;
-  if (row >= A.T) return;
-  const int h0 = (int)(w % A.groups) * A.per_warp, h1 = min(A.total, h0 + A.per_warp);
+  const long long row = blockIdx.x / A.groups;
+  const int h_end = min(A.total, (int)(blockIdx.x % A.groups + 1) * A.per_cta);
+  const int first = (int)(blockIdx.x % A.groups) * A.per_cta + (threadIdx.x >> 5) * kGroup;
   const int d0 = sub * E, half = A.rotary >> 1;
 
   struct alignas(sizeof(T) * E < 16 ? sizeof(T) * E : 16) Vec { T v[E]; };  // rows are 16-byte aligned
@@ -55,8 +58,8 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
   auto fetch = [&](int h) {
 #pragma unroll
     for (int b = 0; b < kQkBatch; ++b) {
-      const int hh = h + b * kGroup + lane / kLanes;
-      if (hh < h1) {
+      const int hh = h + b * kWarps * kGroup + lane / kLanes;
+      if (hh < h_end) {
         const T* src = hh < A.heads ? static_cast<const T*>(A.q) + row * A.qs + (long long)hh * kHd
                                     : static_cast<const T*>(A.k) + row * A.ks + (long long)(hh - A.heads) * kHd;
         x[b] = reinterpret_cast<const Vec*>(src)[sub];
@@ -65,50 +68,44 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
       }
     }
   };
-  fetch(h0);  // on its way while the angles are formed
+  fetch(first);  // on its way while the angles are formed
+  const unsigned long long pos = (unsigned long long)(long long)A.position[row];
+  for (int i = threadIdx.x; i < half; i += kQkThreads) {
+    float2 t;
+    sincospif((float)(int)((pos * A.turn[i]) >> 32) * 0x1p-31f, &t.y, &t.x);
+    turn[i] = t;
+  }
+  if (A.norm)
+    for (int i = threadIdx.x; i < 2 * kHd; i += kQkThreads) (&gain[0][0])[i] = A.gain[i];
+  __syncthreads();
 
   float cs[E], sn[E];
   int partner = lane;
-  if (A.rotary > 0) {
-    const unsigned long long pos = (unsigned long long)(long long)A.position[row];
+#pragma unroll
+  for (int i = 0; i < E; ++i) cs[i] = 1.f, sn[i] = 0.f;
+  if (d0 < A.rotary) {  // (rotary_dim is a multiple of E or of 2)
     if constexpr (kInter) {
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        cs[i] = 1.f, sn[i] = 0.f;
-        if (d0 + i < A.rotary)
-          sincospif((float)(int)((pos * A.turn[(d0 + i) >> 1]) >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-        cs[i + 1] = cs[i], sn[i + 1] = sn[i];
-      }
+      for (int i = 0; i < E; i += 2)
+        if (d0 + i < A.rotary) cs[i] = turn[(d0 + i) >> 1].x, sn[i] = turn[(d0 + i) >> 1].y;
     } else {
       const bool upper = d0 >= half;
-      if (d0 < A.rotary) partner = upper ? lane - half / E : lane + half / E;
+      partner = upper ? lane - half / E : lane + half / E;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        cs[i] = 1.f, sn[i] = 0.f;
-        if (d0 + i < A.rotary) {
-          sincospif((float)(int)((pos * A.turn[d0 + i - (upper ? half : 0)]) >> 32) * 0x1p-31f, &sn[i], &cs[i]);
-          if (!upper) sn[i] = -sn[i];  // first of the pair: a cos - b sin; second: b cos + a sin
-        }
+        const float2 t = turn[d0 + i - (upper ? half : 0)];
+        cs[i] = t.x, sn[i] = upper ? t.y : -t.y;  // first of the pair: a cos - b sin; second: b cos + a sin
       }
-    }
-  }
-  float gq[E], gk[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) gq[i] = gk[i] = 1.f;
-  if (A.norm) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      if (h0 < A.heads) gq[i] = A.gain[d0 + i];
-      if (h1 > A.heads) gk[i] = A.gain[kHd + d0 + i];
     }
   }
 
-  for (int h = h0; h < h1; h += kQkBatch * kGroup) {
-    if (h > h0) fetch(h);
+  constexpr int kStep = kQkBatch * kWarps * kGroup;
+  for (int h = first; h < h_end; h += kStep) {
+    if (h > first) fetch(h);
 #pragma unroll
     for (int b = 0; b < kQkBatch; ++b) {
-      if (h + b * kGroup >= h1) break;
-      const int hh = h + b * kGroup + lane / kLanes;
+      if (h + b * kWarps * kGroup >= h_end) break;
+      const int hh = h + b * kWarps * kGroup + lane / kLanes;
       const bool is_q = hh < A.heads;
       float f[E];
 #pragma unroll
@@ -119,9 +116,10 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
         for (int i = 0; i < E; ++i) s = fmaf(f[i], f[i], s);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        const float r = 1.f / sqrtf(s * (1.f / kHd) + A.eps);
+        const float r = rsqrtf(s * (1.f / kHd) + A.eps);  // (2 ulp)
+        const float* g = gain[is_q ? 0 : 1] + d0;
 #pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = f[i] * r * (is_q ? gq[i] : gk[i]);
+        for (int i = 0; i < E; ++i) f[i] = f[i] * r * g[i];
       }
       if (A.rotary > 0) {
         if constexpr (kInter) {
@@ -141,7 +139,7 @@ __global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
           }
         }
       }
-      if (hh < h1) {
+      if (hh < h_end) {
         Vec y;
 #pragma unroll
         for (int i = 0; i < E; ++i) y.v[i] = Val<T>::down(f[i]);
@@ -276,15 +274,18 @@ strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_s
   A.gain = h->gain, A.turn = h->turn, A.position = position;
   A.T = T, A.heads = d.heads, A.total = d.heads + d.kv_heads;
   A.rotary = d.rotary_dim, A.norm = d.norm, A.eps = d.eps;
-  // heads per warp: as many as leave every SM 48 warps, at most 16, so that a long prompt forms its angles once for
-  // several heads and a window spreads over the SMs
-  const long long vectors = (long long)T * A.total;
-  long long per = vectors / (48LL * h->nsm);
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
-  A.per_warp = (int)per;
-  A.groups = (A.total + A.per_warp - 1) / A.per_warp;
-  const long long warps = (long long)T * A.groups;
-  const unsigned grid = (unsigned)((warps + kQkThreads / 32 - 1) / (kQkThreads / 32));
+  // heads per CTA: a row's, so that its angles are formed once, unless there are too few rows to give every SM 8 CTAs;
+  // then as few as a CTA's warps take at once
+  const long long want = 8LL * h->nsm;
+  long long parts = (want + T - 1) / T;
+  const int least = kQkThreads / 32;
+  const long long most = (A.total + least - 1) / least;
+  if (parts > most) parts = most;
+  A.per_cta = (int)((A.total + parts - 1) / parts);
+  A.groups = (A.total + A.per_cta - 1) / A.per_cta;
+  const long long ctas = (long long)T * A.groups;
+  if (ctas > 0x7FFFFFFFLL) return STRATA_EUNSUPPORTED;
+  const unsigned grid = (unsigned)ctas;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (dtype == STRATA_F32)
     launch_t<float>(A, d.head_dim, d.interleaved, grid, s);
