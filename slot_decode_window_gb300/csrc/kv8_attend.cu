@@ -8,43 +8,48 @@ namespace {
 // Few rows per slot: the cache is read once, at the memory's rate.
 //
 // The rows of a sequence that share a kv head (its rows x group query heads)
-// are the M side of mma.sync tiles; positions are cut into units of 64.  All
-// units of all (sequence, row tile, kv head) items form one list, and each CTA
-// (one per SM) takes an equal contiguous part of it, so that one long
-// conversation and many short ones fill the GPU alike.  A producer thread
-// streams the units' codes by TMA into a ring; each of 8 warps takes 16
-// positions of every second unit and keeps its own softmax state, and the
-// warps join once per item.  An item cut by a CTA border leaves its parts
-// (maximum, sum, unnormalised output) in the workspace; the last CTA to finish
-// joins them in CTA order, so the bits do not depend on timing.
+// are the N side of mma.sync m16n8k16 products whose M side is the cache: S^T =
+// K Q^T (16 positions x rows) and O^T = V^T P^T (16 dims x rows), so that a
+// tile of 8 rows wastes nothing and a lane's accumulators are few.  The weights
+// turn from S^T's layout to P^T's by movmatrix.
+// Positions are cut into units of 64.  All units of all (sequence, row tile, kv
+// head) items form one list, and each CTA (one per SM) takes an equal
+// contiguous part of it, so that one long conversation and many short ones fill
+// the GPU alike.  A producer thread streams the units' codes by TMA into a
+// ring; four warps share a unit (16 positions each), groups of four take units
+// in turn, and every warp keeps its own softmax state; the warps join once per
+// item.  An item cut by a CTA border leaves its parts (maximum, sum,
+// unnormalised output) in the workspace; the last CTA to finish joins them in
+// CTA order, so the bits do not depend on timing.
 //
 // Weights: with scores s_j (base 2) and a block's value exponent ev, the state
 // follows t_j = s_j + ev: w_j = 2^(t_j - max t), O = sum w_j code_j,
 // l = sum w_j 2^-ev, out = O / l.  Whatever the exponents, the largest weight
 // that meets a code is 1 (held times 2^14 so that 16-bit weights keep 38 bits
 // below it), and no block needs its own accumulator.
-// f32 rows: q and the weights enter as two f16 parts (22 bits).  With at most 8
-// rows per tile (kPaired) the parts are rows g and g + 8 of one MMA; above
-// that two MMAs chain into one accumulator (kChained).
+// f32 rows: q and the weights enter as two f16 parts (22 bits) that chain into
+// one accumulator.
 // ---------------------------------------------------------------------------
-enum { kSingle = 0, kPaired = 1, kChained = 2 };
-
 constexpr int kUnit = 64;       // positions per ring stage
-constexpr int kWarps = 8;       // consumer warps
-constexpr int kSplitThreads = (kWarps + 1) * 32;
 constexpr float kWeightTop = 14.f;  // weights are scaled by 2^14
 
-template <int HD> struct SplitPlan {
+// HD: head_dim; NT: tiles of 8 rows (1 or 2); PARTS: f16 parts of q and of the weights (1, or 2 for f32 rows).
+template <int HD, int NT, int PARTS> struct SplitPlan {
+  static constexpr int kRows = 8 * NT;
+  // consumers: as many as their registers allow (with the producer, 13 warps leave 128 a thread, 9 leave 168; 16 + 1
+  // would leave 96)
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kGroups = kWarps / 4;                // units under way at a time
+  static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kTile = kUnit * HD;                  // bytes of one unit's K (or V) codes
-  static constexpr int kStages = HD == 128 ? 8 : 16;        // 128 KB in flight
-  static constexpr int kJoin = kWarps * 16 * (HD + 4) * 4;  // the warps' O (rows padded by 4 floats)
+  static constexpr int kStages = (HD == 128 ? 8 : 16) / kGroups * kGroups + (NT == 1 ? kGroups : 0);  // 128 to 144 KB
+  static constexpr int kJoin = kWarps * kRows * (HD + 4) * 4;  // the warps' O (rows padded by 4 floats)
   static constexpr int kRing = 1024;                        // offsets in dynamic shared memory
   static constexpr int kJoinOff = kRing + kStages * 2 * kTile;
-  static constexpr int kMlOff = kJoinOff + kJoin;           // [kWarps][16][2] maximum, sum
-  static constexpr int kQloOff = kMlOff + kWarps * 16 * 2 * 4;  // low parts of q (kChained): [HD / 16][32] uint4
-  static constexpr int kPreOff = kQloOff + HD / 16 * 32 * 16;
-  static constexpr int kPart = 16 * HD + 32;                // floats of a part in the workspace: O, maxima, sums
+  static constexpr int kMlOff = kJoinOff + kJoin;           // [kWarps][kRows][2] maximum, sum
+  static constexpr int kPreOff = kMlOff + kWarps * kRows * 2 * 4;
 };
+constexpr int split_part(int hd) { return 16 * hd + 32; }  // floats of a part in the workspace: O, maxima, sums
 
 struct AttendArgs {
   Kv8Dev C;
@@ -54,7 +59,7 @@ struct AttendArgs {
   long long q_stride, out_stride;
   float scale2;      // scale * log2(e)
   int dtype, group, layer, tile_rows, grid;
-  float* parts;      // [2 grid][kPart]
+  float* parts;      // [2 grid][split_part]
   unsigned* count;   // [grid] parts done of the item that starts last in a CTA; back to 0 when joined
 };
 
@@ -82,25 +87,6 @@ __device__ __forceinline__ int head_units(const Kv8Seq& s, int group, int tile_r
   int sum = 0;
   for (int mt = 0; mt < row_tiles(s, group, tile_rows); ++mt) sum += tile_units(s, group, tile_rows, mt);
   return sum;
-}
-
-__device__ __forceinline__ float load_value(const void* p, int dtype, long long i) {
-  if (dtype == 0) return static_cast<const float*>(p)[i];
-  if (dtype == 1) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-// Four neighbouring values (the address is a multiple of four values).
-__device__ __forceinline__ float4 load_value4(const void* p, int dtype, long long i) {
-  if (dtype == 0) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  if (dtype == 1) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ void store_value4(void* p, int dtype, long long i, float4 v) {
@@ -146,6 +132,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// An 8 x 8 matrix of 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t turn(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Weight of a part with maximum mw and sum lw under the joint maximum m: 0 for a
 // part that saw nothing (a row of NaN has no maximum but a NaN sum, and stays NaN).
 __device__ __forceinline__ float join_factor(float mw, float lw, float m) {
@@ -183,35 +176,38 @@ __device__ __forceinline__ Item next_item(const AttendArgs& A, const long long* 
   return it;
 }
 
-template <int HD, int FMT, int MODE>
-__global__ void __launch_bounds__(kSplitThreads, 1)
-    attend_split_kernel(AttendArgs A, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using P = SplitPlan<HD>;
-  constexpr int kSteps = HD / 16;   // k-steps of q.K, and half the n-tiles of P.V
-  constexpr int kNt = HD / 8;       // n-tiles of P.V
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+template <int HD, int FMT, int NT, int PARTS>
+__global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
+    attend_split_kernel(const __grid_constant__ AttendArgs A, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  using P = SplitPlan<HD, NT, PARTS>;
+  constexpr int kSteps = HD / 16;   // k-steps of K Q^T, m-tiles of V^T P^T
+  constexpr int kPart = split_part(HD);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + P::kStages;
   int* shared_word = reinterpret_cast<int*>(empty + P::kStages);
   long long* warp_sums = reinterpret_cast<long long*>(smem + 512);
   float* join = reinterpret_cast<float*>(smem + P::kJoinOff);
   float* ml = reinterpret_cast<float*>(smem + P::kMlOff);
-  uint4* qlo = reinterpret_cast<uint4*>(smem + P::kQloOff);
   long long* pre = reinterpret_cast<long long*>(smem + P::kPreOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
+  if (smem_u32(smem) & 1023) {  // the swizzles count on it
+    if (tid == 0) atomicOr(A.C.err, kErrConfig);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < P::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps / 2);
+      mbar_init(&empty[i], 4);
     }
     fence_mbar_init();
   }
   // units before each sequence: a contiguous share per thread, joined by a scan
   const int n_seq = A.R.n_seq;
   {
-    constexpr int kScan = kWarps * 32;
+    constexpr int kScan = 256;
     const int share = (n_seq + kScan - 1) / kScan;
     long long sum = 0;
     if (tid < kScan) {
@@ -229,7 +225,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       const long long t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += t;
     }
-    if (lane == 31 && warp < kWarps) warp_sums[warp] = inc;
+    if (lane == 31 && warp < kScan / 32) warp_sums[warp] = inc;
     __syncthreads();
     if (tid < kScan) {
       long long before = inc - sum;
@@ -245,7 +241,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     if (!s.rows_ok) continue;
     const int blind = s.held_ok ? min(s.n, max(0, s.n - s.length)) : s.n;
     const int w4 = A.C.heads * HD / 4;
-    for (int j = tid; j < blind * w4; j += kSplitThreads)
+    for (int j = tid; j < blind * w4; j += P::kThreads)
       store_value4(A.out, A.dtype, (long long)(s.row0 + j / w4) * A.out_stride + j % w4 * 4, make_float4(0, 0, 0, 0));
   }
 
@@ -266,7 +262,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     seq0 = a;
   }
 
-  if (warp == kWarps) {
+  if (warp == P::kWarps) {
     // ---- producer ----
     if (lane != 0) return;
     int n = 0, seq = seq0;
@@ -294,89 +290,24 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     return;
   }
 
-  // ---- consumers ----
-  const int half = warp >> 2, slab = (warp & 3) * 16;
+  // ---- consumers: warp w takes positions 16 (w mod 4) .. + 15 of units w / 4, w / 4 + kGroups, ... of the CTA's list.
+  // (Stages are a multiple of the groups, so a stage's units are all of one group, which waits for every phase of it.)
+  static_assert(P::kStages % P::kGroups == 0, "a stage belongs to one group of warps");
+  const int mine = warp >> 2, slab = (warp & 3) * 16;
   int n = 0, seq = seq0;
   bool ok = true;
   for (long long u = lo; u < hi;) {
     const Item it = next_item<HD>(A, pre, u, hi, seq);
     seq = it.seq;
     const Kv8Seq& s = it.s;
-    const int rows = min(A.tile_rows, s.n * A.group - it.mt * A.tile_rows);  // of this tile
-    const int p_first = s.length - s.n;                                     // position of the sequence's first row
-
-    // q fragments: lane (g, c) of k-step x holds dims c HD/4 + 4x .. + 3 of rows g and g + 8
-    uint32_t qa[kSteps][4];
-    float rf[2];
-    int lim[2];  // positions that rows g, g + 8 see
-    {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int rr = MODE == kPaired ? g : g + 8 * r;
-        const bool on = rr < rows && !(MODE == kPaired && r);
-        const int m = it.mt * A.tile_rows + rr, tok = m / A.group;
-        lim[r] = rr < rows ? max(0, p_first + tok + 1) : 0;
-        float f[HD / 4];
-#pragma unroll
-        for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
-        if (on) {
-          const long long at =
-              (long long)(s.row0 + tok) * A.q_stride + (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
-#pragma unroll
-          for (int d = 0; d < HD / 4; d += 4) {
-            const float4 v = load_value4(A.q, A.dtype, at + d);
-            f[d] = v.x, f[d + 1] = v.y, f[d + 2] = v.z, f[d + 3] = v.w;
-          }
-        }
-        // a power of two per row brings its largest element to [1, 2)
-        unsigned top = 0;
-#pragma unroll
-        for (int d = 0; d < HD / 4; ++d) top = max(top, __float_as_uint(f[d]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
-        const float down = pow2i(-e);
-        if (!(MODE == kPaired && r)) rf[r] = pow2i(e);
-#pragma unroll
-        for (int x = 0; x < kSteps; ++x) {
-          float h[4], l[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            h[d] = f[4 * x + d] * down;
-            l[d] = h[d] - __half2float(__float2half_rn(h[d]));
-          }
-          if (!(MODE == kPaired && r)) {
-            qa[x][r] = pack_half2(h[0], h[1]);
-            qa[x][2 + r] = pack_half2(h[2], h[3]);
-            if constexpr (MODE == kPaired) {
-              qa[x][1] = pack_half2(l[0], l[1]);
-              qa[x][3] = pack_half2(l[2], l[3]);
-            }
-            if constexpr (MODE == kChained) {  // every warp holds the same low parts: warp 0 keeps them
-              if (warp == 0) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(&qlo[x * 32 + lane]);
-                w[r] = pack_half2(l[0], l[1]);
-                w[2 + r] = pack_half2(l[2], l[3]);
-              }
-            }
-          }
-        }
-      }
-      if constexpr (MODE == kPaired) rf[1] = rf[0];
-      if constexpr (MODE == kChained) asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-    }
-    const int min_pos = p_first + it.mt * A.tile_rows / A.group;  // position of the tile's first row
-
-    float o[kNt][4];
-#pragma unroll
-    for (int i = 0; i < kNt; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int rows = min(P::kRows, s.n * A.group - it.mt * P::kRows);  // of this tile
+    const int p_first = s.length - s.n;                               // position of the sequence's first row
 
     const long long line = (long long)s.slot * A.C.kv_heads + it.head;
     const uint8_t* keb = A.C.k_exp + line * A.C.n_blocks;
     const uint8_t* veb = A.C.v_exp + line * A.C.n_blocks;
-    // this warp's units of the part: every second one of the CTA's list
-    int x = it.u0 + ((n ^ half) & 1);
+    // this warp's units of the part
+    int x = it.u0 + (mine + P::kGroups - n % P::kGroups) % P::kGroups;
     auto exps = [&](int unit, int& ek, int& ev) {
       const int p = unit * kUnit + slab;
       ek = ev = 0;
@@ -387,119 +318,169 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     };
     int ek_next, ev_next;
     exps(x, ek_next, ev_next);
-    for (; x < it.u1; x += 2) {
+
+    // q as the B operand: lane (g, c) of k-step y holds dims c HD/4 + 4y .. + 3 of row 8 nt + g
+    uint32_t qb[PARTS][NT][kSteps][2];
+    float rf[NT][2];   // powers of two of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
+    int lim[NT][2];    // positions that they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int rr = 8 * nt + g, m = it.mt * P::kRows + rr;
+      float f[HD / 4];
+#pragma unroll
+      for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
+      if (rr < rows) {
+        const long long at = (long long)(s.row0 + m / A.group) * A.q_stride +
+                             (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
+        if constexpr (PARTS == 2) {
+#pragma unroll
+          for (int d = 0; d < HD / 4; d += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at + d);
+            f[d] = v.x, f[d + 1] = v.y, f[d + 2] = v.z, f[d + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < HD / 4; d += 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at + d);
+            if (A.dtype == 1)
+              Val<__half>::unpack(v, f + d);
+            else
+              Val<__nv_bfloat16>::unpack(v, f + d);
+          }
+        }
+      }
+      // a power of two per row brings its largest element to [1, 2)
+      unsigned top = 0;
+#pragma unroll
+      for (int d = 0; d < HD / 4; ++d) top = max(top, __float_as_uint(f[d]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
+      const float down = pow2i(-e);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = 8 * nt + 2 * c + y;
+        rf[nt][y] = pow2i(__shfl_sync(0xFFFFFFFFu, e, (2 * c + y) * 4));
+        lim[nt][y] = r < rows ? max(0, p_first + (it.mt * P::kRows + r) / A.group + 1) : 0;
+      }
+#pragma unroll
+      for (int y = 0; y < kSteps; ++y) {
+        float h[4], l[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          h[d] = f[4 * y + d] * down;
+          l[d] = h[d] - __half2float(__float2half_rn(h[d]));
+        }
+        qb[0][nt][y][0] = pack_half2(h[0], h[1]), qb[0][nt][y][1] = pack_half2(h[2], h[3]);
+        if constexpr (PARTS == 2) qb[1][nt][y][0] = pack_half2(l[0], l[1]), qb[1][nt][y][1] = pack_half2(l[2], l[3]);
+      }
+    }
+    const int min_pos = p_first + it.mt * P::kRows / A.group;  // position of the tile's first row
+
+    // O^T: lane (g, c) of m-tile i holds dims g HD/8 + 2i and + 1 of rows 8 nt + 2c and + 1
+    float o[kSteps][NT][4];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+
+#pragma unroll 1
+    for (; x < it.u1; x += P::kGroups) {
       const int at = n + x - it.u0, st = at % P::kStages;
       const int ek = kv8_exp((uint8_t)ek_next), ev = kv8_exp((uint8_t)ev_next);
-      exps(x + 2, ek_next, ev_next);
-      if (ok) ok = mbar_wait(&full[st], (at / P::kStages) & 1, A.C.err);
+      exps(x + P::kGroups, ek_next, ev_next);
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (at / P::kStages) & 1, A.C.err));
       const int p0 = x * kUnit + slab;
       if (ok && p0 < s.length) {
         const uint8_t* kt = smem + P::kRing + st * 2 * P::kTile;
         const uint8_t* vt = kt + P::kTile;
-        // scores of 16 positions: n-tile j, column g is position p0 + 8j + g
-        float sc[2][4];
+        // S^T: positions p0 + g and + 8 (h), rows 2c, 2c + 1
+        float sc[NT][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t kw[kSteps];
-          const int row = slab + 8 * j + g;
-          if constexpr (HD == 128) {
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        {
+          uint32_t kw[2][kSteps];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 w = *reinterpret_cast<const uint4*>(kt + row * 128 + (((2 * c + h) ^ (row & 7)) << 4));
-              kw[4 * h] = w.x, kw[4 * h + 1] = w.y, kw[4 * h + 2] = w.z, kw[4 * h + 3] = w.w;
+          for (int h = 0; h < 2; ++h) {
+            const int row = slab + 8 * h + g;
+            if constexpr (HD == 128) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint4 w = *reinterpret_cast<const uint4*>(kt + row * 128 + (((2 * c + y) ^ (row & 7)) << 4));
+                kw[h][4 * y] = w.x, kw[h][4 * y + 1] = w.y, kw[h][4 * y + 2] = w.z, kw[h][4 * y + 3] = w.w;
+              }
+            } else {
+              const uint4 w = *reinterpret_cast<const uint4*>(kt + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+              kw[h][0] = w.x, kw[h][1] = w.y, kw[h][2] = w.z, kw[h][3] = w.w;
             }
-          } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(kt + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
-            kw[0] = w.x, kw[1] = w.y, kw[2] = w.z, kw[3] = w.w;
           }
-          sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
 #pragma unroll
           for (int y = 0; y < kSteps; ++y) {
-            uint32_t b0, b1;
-            codes_to_f16<FMT>(kw[y], b0, b1);
-            mma_acc(sc[j], qa[y], b0, b1);
-            if constexpr (MODE == kChained) {
-              const uint4 w = qlo[y * 32 + lane];
-              const uint32_t ql[4] = {w.x, w.y, w.z, w.w};
-              mma_acc(sc[j], ql, b0, b1);
-            }
+            uint32_t a[4];
+            codes_to_f16<FMT>(kw[0][y], a[0], a[2]);
+            codes_to_f16<FMT>(kw[1][y], a[1], a[3]);
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_acc(sc[nt], a, qb[part][nt][y][0], qb[part][nt][y][1]);
           }
         }
         // t = score * log2(e) + ev, masked where a row does not see the position
         const float kf = A.scale2 * pow2i(ek), evf = (float)ev;
-        float t[2][4];
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+        float mx[NT][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (MODE == kPaired) {
-            t[j][0] = fmaf(sc[j][0] + sc[j][2], kf * rf[0], evf);
-            t[j][1] = fmaf(sc[j][1] + sc[j][3], kf * rf[0], evf);
-          } else {
-            t[j][0] = fmaf(sc[j][0], kf * rf[0], evf);
-            t[j][1] = fmaf(sc[j][1], kf * rf[0], evf);
-            t[j][2] = fmaf(sc[j][2], kf * rf[1], evf);
-            t[j][3] = fmaf(sc[j][3], kf * rf[1], evf);
-          }
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sc[nt][y] = fmaf(sc[nt][y], kf * rf[nt][y & 1], evf);
         if (p0 + 15 > min_pos) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (p0 + g + 8 * (y >> 1) >= lim[nt][y & 1]) sc[nt][y] = -INFINITY;
+        }
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float v = fmaxf(sc[nt][y], sc[nt][y + 2]);
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            mx[nt][y] = v;
+            grew |= v > m[nt][y];
+          }
+        if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int p = p0 + 8 * j + 2 * c + y;
-              if (p >= lim[0]) t[j][y] = -INFINITY;
-              if (MODE != kPaired && p >= lim[1]) t[j][2 + y] = -INFINITY;
+              const float to = fmaxf(m[nt][y], mx[nt][y]), a = to == -INFINITY ? 1.f : ex2(m[nt][y] - to);
+              m[nt][y] = to, l[nt][y] *= a;
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) o[i][nt][y] *= a, o[i][nt][y + 2] *= a;
             }
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mx0 = fmaxf(mx0, fmaxf(t[j][0], t[j][1]));
-          if constexpr (MODE != kPaired) mx1 = fmaxf(mx1, fmaxf(t[j][2], t[j][3]));
-        }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, 2));
-        if constexpr (MODE != kPaired) {
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, 1));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, 2));
-        }
-        if (__any_sync(0xFFFFFFFFu, mx0 > m0 || mx1 > m1)) {
-          const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-          const float a0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), a1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-          m0 = n0, m1 = n1, l0 *= a0, l1 *= a1;
-#pragma unroll
-          for (int i = 0; i < kNt; ++i) {
-            o[i][0] *= a0, o[i][1] *= a0;
-            o[i][2] *= MODE == kPaired ? a0 : a1, o[i][3] *= MODE == kPaired ? a0 : a1;
-          }
-        }
-        const float z0 = m0 == -INFINITY ? 0.f : kWeightTop - m0, z1 = m1 == -INFINITY ? 0.f : kWeightTop - m1;
         const float back = pow2i(-ev);
-        uint32_t pa[4], pl[4];
-        {
-          float w[2][4];
+        uint32_t pb[PARTS][NT][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            w[j][0] = ex2(t[j][0] + z0), w[j][1] = ex2(t[j][1] + z0);
-            if constexpr (MODE != kPaired) w[j][2] = ex2(t[j][2] + z1), w[j][3] = ex2(t[j][3] + z1);
-          }
-          l0 = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), back, l0);
-          if constexpr (MODE != kPaired) l1 = fmaf((w[0][2] + w[0][3]) + (w[1][2] + w[1][3]), back, l1);
-          auto rest = [](float v) { return v - __half2float(__float2half_rn(v)); };
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            pa[2 * j] = pack_half2(w[j][0], w[j][1]);
-            if constexpr (MODE == kPaired) {
-              pa[2 * j + 1] = pack_half2(rest(w[j][0]), rest(w[j][1]));
-            } else {
-              pa[2 * j + 1] = pack_half2(w[j][2], w[j][3]);
-            }
-            if constexpr (MODE == kChained) {
-              pl[2 * j] = pack_half2(rest(w[j][0]), rest(w[j][1]));
-              pl[2 * j + 1] = pack_half2(rest(w[j][2]), rest(w[j][3]));
-            }
+          for (int y = 0; y < 4; ++y) w[y] = ex2(sc[nt][y] + (m[nt][y & 1] == -INFINITY ? 0.f : kWeightTop - m[nt][y & 1]));
+          l[nt][0] = fmaf(w[0] + w[2], back, l[nt][0]), l[nt][1] = fmaf(w[1] + w[3], back, l[nt][1]);
+          pb[0][nt][0] = turn(pack_half2(w[0], w[1])), pb[0][nt][1] = turn(pack_half2(w[2], w[3]));
+          if constexpr (PARTS == 2) {
+            auto rest = [](float v) { return v - __half2float(__float2half_rn(v)); };
+            pb[1][nt][0] = turn(pack_half2(rest(w[0]), rest(w[1])));
+            pb[1][nt][1] = turn(pack_half2(rest(w[2]), rest(w[3])));
           }
         }
-        // O += P V: lane (g, c) reads HD/8 dims from dim g HD/8 of positions 2c, 2c+1, 2c+8, 2c+9
+        // O^T += V^T P^T: lane (g, c) reads HD/8 dims from dim g HD/8 of positions 2c, 2c+1, 2c+8, 2c+9
         constexpr int kWords = HD / 32;
         uint32_t vw[4][kWords];
 #pragma unroll
@@ -523,17 +504,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // bytes 2h, 2h + 1 of the word: n-tiles 4i + 2h, 4i + 2h + 1
+          for (int h = 0; h < 2; ++h) {  // bytes 2h, 2h + 1 of the word: dims g and g + 8 of m-tile 2i + h
             const uint32_t sel = h ? 0x7362 : 0x5140;
-            uint32_t b0a, b0b, b1a, b1b;
-            codes_to_f16<FMT>(prmt(vw[0][i], vw[1][i], sel), b0a, b0b);
-            codes_to_f16<FMT>(prmt(vw[2][i], vw[3][i], sel), b1a, b1b);
-            mma_acc(o[4 * i + 2 * h], pa, b0a, b1a);
-            mma_acc(o[4 * i + 2 * h + 1], pa, b0b, b1b);
-            if constexpr (MODE == kChained) {
-              mma_acc(o[4 * i + 2 * h], pl, b0a, b1a);
-              mma_acc(o[4 * i + 2 * h + 1], pl, b0b, b1b);
-            }
+            uint32_t a[4];
+            codes_to_f16<FMT>(prmt(vw[0][i], vw[1][i], sel), a[0], a[1]);
+            codes_to_f16<FMT>(prmt(vw[2][i], vw[3][i], sel), a[2], a[3]);
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_acc(o[2 * i + h][nt], a, pb[part][nt][0], pb[part][nt][1]);
           }
         }
       }
@@ -543,134 +522,125 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     n += it.u1 - it.u0;
 
     // ---- join the warps ----
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
     constexpr int kRowF = HD + 4;
-    float* mine = join + warp * 16 * kRowF;
-    if (c == 0) {
-      ml[(warp * 16 + g) * 2] = m0, ml[(warp * 16 + g) * 2 + 1] = l0;
-      ml[(warp * 16 + g + 8) * 2] = MODE == kPaired ? -INFINITY : m1, ml[(warp * 16 + g + 8) * 2 + 1] = MODE == kPaired ? 0.f : l1;
-    }
-    // o[i][0], o[i][1] are dims 2c kNt + i and (2c + 1) kNt + i
+    float* own = join + warp * P::kRows * kRowF;
 #pragma unroll
-    for (int i = 0; i < kNt; i += 4) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4 a = make_float4(o[i][h], o[i + 1][h], o[i + 2][h], o[i + 3][h]);
-        const float4 b = make_float4(o[i][2 + h], o[i + 1][2 + h], o[i + 2][2 + h], o[i + 3][2 + h]);
-        const int d = (2 * c + h) * kNt + i;
-        if constexpr (MODE == kPaired) {
-          a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-        } else {
-          *reinterpret_cast<float4*>(mine + (g + 8) * kRowF + d) = b;
-        }
-        *reinterpret_cast<float4*>(mine + g * kRowF + d) = a;
+      for (int y = 0; y < 2; ++y) {
+        float v = l[nt][y];
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        const int r = 8 * nt + 2 * c + y;
+        if (g == 0) ml[(warp * P::kRows + r) * 2] = m[nt][y], ml[(warp * P::kRows + r) * 2 + 1] = v;
+#pragma unroll
+        for (int i = 0; i < kSteps; i += 2)
+          *reinterpret_cast<float4*>(own + r * kRowF + g * (HD / 8) + 2 * i) =
+              make_float4(o[i][nt][y], o[i][nt][y + 2], o[i + 1][nt][y], o[i + 1][nt][y + 2]);
       }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
     const bool whole = it.u0 == 0 && it.u1 == it.units;
     const int c0 = (int)(((it.first + 1) * G - 1) / total);
-    float* part = A.parts + (long long)(2 * blockIdx.x + (u == lo ? 0 : 1)) * P::kPart;
+    float* part = A.parts + (long long)(2 * blockIdx.x + (u == lo ? 0 : 1)) * kPart;
     constexpr int kQ = HD / 4;  // float4s of a row
-    for (int j = tid; j < rows * kQ; j += kWarps * 32) {
+    for (int j = tid; j < rows * kQ; j += P::kWarps * 32) {
       const int r = j / kQ, d = j % kQ * 4;
-      float m = -INFINITY;
+      float mj = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * 16 + r) * 2]);
+      for (int w = 0; w < P::kWarps; ++w) mj = fmaxf(mj, ml[(w * P::kRows + r) * 2]);
       float4 acc = make_float4(0, 0, 0, 0);
-      float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = ml[(w * 16 + r) * 2], lw = ml[(w * 16 + r) * 2 + 1];
-        const float f = join_factor(mw, lw, m);
-        const float4 v = *reinterpret_cast<const float4*>(join + (w * 16 + r) * kRowF + d);
-        l = fmaf(f, lw, l);
+      float lj = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < P::kWarps; ++w) {
+        const float mw = ml[(w * P::kRows + r) * 2], lw = ml[(w * P::kRows + r) * 2 + 1];
+        const float f = join_factor(mw, lw, mj);
+        const float4 v = *reinterpret_cast<const float4*>(join + (w * P::kRows + r) * kRowF + d);
+        lj = fmaf(f, lw, lj);
         acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
       }
       if (whole) {
-        const int mm = it.mt * A.tile_rows + r;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int mm = it.mt * P::kRows + r;
+        const float inv = lj == 0.f ? 0.f : 1.f / lj;
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
         store_value4(A.out, A.dtype,
                      (long long)(s.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
       } else {
         *reinterpret_cast<float4*>(part + r * HD + d) = acc;
-        if (d == 0) part[16 * HD + r] = m, part[16 * HD + 16 + r] = l;
+        if (d == 0) part[16 * HD + r] = mj, part[16 * HD + 16 + r] = lj;
       }
     }
     if (!whole) {
       // the last CTA to finish its part joins them, in CTA order
       __threadfence();
-      asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
       const int c1 = (int)(((it.first + it.units) * G - 1) / total);
       if (tid == 0) {
         __threadfence();
         *shared_word = atomicInc(&A.count[c0], (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
         __threadfence();
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
       if (*shared_word) {
         const int s0 = 2 * c0 + (total * c0 / G == it.first ? 0 : 1);
-        for (int j = tid; j < rows * kQ; j += kWarps * 32) {
+        for (int j = tid; j < rows * kQ; j += P::kWarps * 32) {
           const int r = j / kQ, d = j % kQ * 4;
-          float m = -INFINITY;
+          float mj = -INFINITY;
+#pragma unroll 4
           for (int y = c0; y <= c1; ++y)
-            m = fmaxf(m, __ldcg(A.parts + (long long)(y == c0 ? s0 : 2 * y) * P::kPart + 16 * HD + r));
+            mj = fmaxf(mj, __ldcg(A.parts + (long long)(y == c0 ? s0 : 2 * y) * kPart + 16 * HD + r));
           float4 acc = make_float4(0, 0, 0, 0);
-          float l = 0.f;
+          float lj = 0.f;
 #pragma unroll 4
           for (int y = c0; y <= c1; ++y) {
-            const float* from = A.parts + (long long)(y == c0 ? s0 : 2 * y) * P::kPart;
+            const float* from = A.parts + (long long)(y == c0 ? s0 : 2 * y) * kPart;
             const float mw = __ldcg(from + 16 * HD + r), lw = __ldcg(from + 16 * HD + 16 + r);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(from + r * HD + d));
-            const float f = join_factor(mw, lw, m);
-            l = fmaf(f, lw, l);
+            const float f = join_factor(mw, lw, mj);
+            lj = fmaf(f, lw, lj);
             acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
           }
-          const int mm = it.mt * A.tile_rows + r;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int mm = it.mt * P::kRows + r;
+          const float inv = lj == 0.f ? 0.f : 1.f / lj;
           acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
           store_value4(A.out, A.dtype,
                        (long long)(s.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
         }
       }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // join, ml and qlo may be written again
+    asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");  // join and ml may be written again
     u += it.u1 - it.u0;
   }
 }
 
-template <int HD>
-int split_smem(int n_seq) {
-  return 1024 + SplitPlan<HD>::kPreOff + 8 * (n_seq + 1);
-}
-
-template <int HD, int FMT, int MODE>
-cudaError_t launch_split(const AttendArgs& A, const Kv8Maps& M, cudaStream_t s) {
-  attend_split_kernel<HD, FMT, MODE><<<A.grid, kSplitThreads, split_smem<HD>(A.R.n_seq), s>>>(A, M.k, M.v);
-  return cudaGetLastError();
-}
+template <int HD, int FMT, int NT, int PARTS>
+struct Split {
+  using P = SplitPlan<HD, NT, PARTS>;
+  static int smem(int n_seq) { return P::kPreOff + 8 * (n_seq + 1); }
+  static cudaError_t setup() {
+    return cudaFuncSetAttribute(attend_split_kernel<HD, FMT, NT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem(kKv8MaxSeq));
+  }
+  static cudaError_t launch(const AttendArgs& A, const Kv8Maps& M, cudaStream_t s) {
+    attend_split_kernel<HD, FMT, NT, PARTS><<<A.grid, P::kThreads, smem(A.R.n_seq), s>>>(A, M.k, M.v);
+    return cudaGetLastError();
+  }
+};
 
 template <int HD, int FMT>
 cudaError_t setup_split() {
-  const int smem = split_smem<HD>(kKv8MaxSeq);
-  cudaError_t e = cudaSuccess;
-  auto set = [&](auto* fn) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  };
-  set(attend_split_kernel<HD, FMT, kSingle>);
-  set(attend_split_kernel<HD, FMT, kPaired>);
-  set(attend_split_kernel<HD, FMT, kChained>);
+  cudaError_t e = Split<HD, FMT, 1, 1>::setup();
+  if (e == cudaSuccess) e = Split<HD, FMT, 1, 2>::setup();
+  if (e == cudaSuccess) e = Split<HD, FMT, 2, 1>::setup();
+  if (e == cudaSuccess) e = Split<HD, FMT, 2, 2>::setup();
   return e;
 }
 
 template <int HD, int FMT>
-cudaError_t launch_split_mode(const AttendArgs& A, const Kv8Maps& M, int mode, cudaStream_t s) {
-  if (mode == kSingle) return launch_split<HD, FMT, kSingle>(A, M, s);
-  if (mode == kPaired) return launch_split<HD, FMT, kPaired>(A, M, s);
-  return launch_split<HD, FMT, kChained>(A, M, s);
+cudaError_t launch_split(const AttendArgs& A, const Kv8Maps& M, cudaStream_t s) {
+  const bool two = A.dtype == 0;
+  if (A.tile_rows == 8) return two ? Split<HD, FMT, 1, 2>::launch(A, M, s) : Split<HD, FMT, 1, 1>::launch(A, M, s);
+  return two ? Split<HD, FMT, 2, 2>::launch(A, M, s) : Split<HD, FMT, 2, 1>::launch(A, M, s);
 }
 
 }  // namespace
@@ -686,8 +656,7 @@ cudaError_t setup_kv8_attend(int head_dim, int format) {
 
 // After the error word's 256 bytes: a counter per CTA, then two parts per CTA.
 long long kv8_attend_workspace(int nsm, int head_dim) {
-  const int split = head_dim == 128 ? SplitPlan<128>::kPart : SplitPlan<64>::kPart;
-  const int part = max(split, kv8_prompt_part_floats(head_dim));
+  const int part = max(split_part(head_dim), kv8_prompt_part_floats(head_dim));
   return 256 + ((long long)nsm * 4 + 255) / 256 * 256 + 2LL * nsm * part * 4;
 }
 
@@ -704,12 +673,10 @@ cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& 
   A.C = C, A.R = R, A.q = q, A.out = out, A.q_stride = q_stride, A.out_stride = out_stride;
   A.scale2 = scale * 1.4426950408889634f;
   A.dtype = dtype, A.group = group, A.layer = layer, A.grid = nsm;
-  const int mode = dtype != 0 ? kSingle : R.max_rows * group <= 8 ? kPaired : kChained;
-  A.tile_rows = mode == kPaired ? 8 : 16;
+  A.tile_rows = R.max_rows * group <= 8 ? 8 : 16;
   A.count = count, A.parts = parts;
-  if (C.head_dim == 128)
-    return C.format == 0 ? launch_split_mode<128, 0>(A, M, mode, s) : launch_split_mode<128, 1>(A, M, mode, s);
-  return C.format == 0 ? launch_split_mode<64, 0>(A, M, mode, s) : launch_split_mode<64, 1>(A, M, mode, s);
+  if (C.head_dim == 128) return C.format == 0 ? launch_split<128, 0>(A, M, s) : launch_split<128, 1>(A, M, s);
+  return C.format == 0 ? launch_split<64, 0>(A, M, s) : launch_split<64, 1>(A, M, s);
 }
 
 }  // namespace strata
