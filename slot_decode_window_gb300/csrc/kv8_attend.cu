@@ -12,11 +12,12 @@ namespace {
 // K Q^T (16 positions x rows) and O^T = V^T P^T (16 dims x rows), so that a
 // tile of 8 rows wastes nothing and a lane's accumulators are few.  The weights
 // turn from S^T's layout to P^T's by movmatrix.
-// Positions are cut into units of 64.  All units of all (sequence, row tile, kv
+// Positions are cut into units of 64 (128 for
+// heads of 64, so that a copy and a step of a warp stay as long).  All units of all (sequence, row tile, kv
 // head) items form one list, and each CTA (one per SM) takes an equal
 // contiguous part of it, so that one long conversation and many short ones fill
 // the GPU alike.  A producer thread streams the units' codes by TMA into a
-// ring; four warps share a unit (16 positions each), groups of four take units
+// ring; four warps share a unit, groups of four take units
 // in turn, and every warp keeps its own softmax state; the warps join once per
 // item.  An item cut by a CTA border leaves its parts (maximum, sum,
 // unnormalised output) in the workspace; the last CTA to finish joins them in
@@ -30,7 +31,6 @@ namespace {
 // f32 rows: q and the weights enter as two f16 parts (22 bits) that chain into
 // one accumulator.
 // ---------------------------------------------------------------------------
-constexpr int kUnit = 64;       // positions per ring stage
 constexpr float kWeightTop = 14.f;  // weights are scaled by 2^14
 
 // HD: head_dim; NT: tiles of 8 rows (1 or 2); PARTS: f16 parts of q and of the weights (1, or 2 for f32 rows).
@@ -41,13 +41,15 @@ template <int HD, int NT, int PARTS> struct SplitPlan {
   static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kGroups = kWarps / 4;                // units under way at a time
   static constexpr int kThreads = (kWarps + 1) * 32;
-  static constexpr int kTile = kUnit * HD;                  // bytes of one unit's K (or V) codes
-  static constexpr int kStages = (HD == 128 ? 8 : 16) / kGroups * kGroups + (NT == 1 ? kGroups : 0);  // 128 to 144 KB
+  static constexpr int kSlabs = 128 / HD;                   // of 16 positions: a warp's part of a unit
+  static constexpr int kUnit = 64 * kSlabs;                 // positions of a ring stage
+  static constexpr int kTile = kUnit * HD;                  // bytes of one unit's K (or V) codes: 8 KB
+  static constexpr int kStages = NT == 1 ? 9 : 8;           // 144 or 128 KB in flight; a multiple of kGroups
   static constexpr int kJoin = kWarps * kRows * (HD + 4) * 4;  // the warps' O (rows padded by 4 floats)
   static constexpr int kRing = 1024;                        // offsets in dynamic shared memory
   static constexpr int kJoinOff = kRing + kStages * 2 * kTile;
   static constexpr int kMlOff = kJoinOff + kJoin;           // [kWarps][kRows][2] maximum, sum
-  static constexpr int kPreOff = kMlOff + kWarps * kRows * 2 * 4;
+  static constexpr int kSeqOff = kMlOff + kWarps * kRows * 2 * 4;  // [n_seq] first row, rows, slot, length
 };
 constexpr int split_part(int hd) { return 16 * hd + 32; }  // floats of a part in the workspace: O, maxima, sums
 
@@ -58,7 +60,7 @@ struct AttendArgs {
   void* out;
   long long q_stride, out_stride;
   float scale2;      // scale * log2(e)
-  int dtype, group, layer, tile_rows, grid;
+  int dtype, group, layer, tile_rows, unit, grid;
   float* parts;      // [2 grid][split_part]
   unsigned* count;   // [grid] parts done of the item that starts last in a CTA; back to 0 when joined
 };
@@ -71,21 +73,17 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
 }
 
 // Units of row tile mt: positions that its last row sees.
-__device__ __forceinline__ int tile_units(const Kv8Seq& s, int group, int tile_rows, int mt) {
-  const int last = min(s.n, (tile_rows * (mt + 1) - 1) / group + 1);
-  const int seen = s.length - s.n + last;
-  return seen <= 0 ? 0 : (seen + kUnit - 1) / kUnit;
-}
-
-__device__ __forceinline__ int row_tiles(const Kv8Seq& s, int group, int tile_rows) {
-  return (s.n * group + tile_rows - 1) / tile_rows;
+__device__ __forceinline__ int tile_units(int n, int length, const AttendArgs& A, int mt) {
+  const int last = min(n, (A.tile_rows * (mt + 1) - 1) / A.group + 1);
+  const int seen = length - n + last;
+  return seen <= 0 ? 0 : (seen + A.unit - 1) / A.unit;
 }
 
 // Units of all row tiles of one kv head.
-__device__ __forceinline__ int head_units(const Kv8Seq& s, int group, int tile_rows) {
-  if (!s.held_ok) return 0;
+__device__ __forceinline__ int head_units(int n, int length, const AttendArgs& A) {
+  const int tiles = (n * A.group + A.tile_rows - 1) / A.tile_rows;
   int sum = 0;
-  for (int mt = 0; mt < row_tiles(s, group, tile_rows); ++mt) sum += tile_units(s, group, tile_rows, mt);
+  for (int mt = 0; mt < tiles; ++mt) sum += tile_units(n, length, A, mt);
   return sum;
 }
 
@@ -147,28 +145,28 @@ __device__ __forceinline__ float join_factor(float mw, float lw, float m) {
 
 // A CTA's next item: the part [u0, u1) of its units, positions counted from the item's first unit.
 struct Item {
-  Kv8Seq s;
+  int row0, n, slot, length;  // the sequence
   int seq, head, mt;
-  int u0, u1, units;     // within the item
-  long long first;       // the item's first unit in the whole list
+  int u0, u1, units;          // within the item
+  long long first;            // the item's first unit in the whole list
 };
 
-template <int HD>
-__device__ __forceinline__ Item next_item(const AttendArgs& A, const long long* pre, long long u, long long end,
-                                          int seq) {
+__device__ __forceinline__ Item next_item(const AttendArgs& A, const long long* pre, const int4* seqs, long long u,
+                                          long long end, int seq) {
   Item it;
   while (pre[seq + 1] <= u) ++seq;
   it.seq = seq;
-  it.s = kv8_seq(A.R, A.C, seq);
+  const int4 s = seqs[seq];
+  it.row0 = s.x, it.n = s.y, it.slot = s.z, it.length = s.w;
   long long r = u - pre[seq];
-  const int per_head = head_units(it.s, A.group, A.tile_rows);
+  const int per_head = head_units(it.n, it.length, A);
   it.head = (int)(r / per_head);
   r -= (long long)it.head * per_head;
   it.mt = 0;
-  it.units = tile_units(it.s, A.group, A.tile_rows, 0);
+  it.units = tile_units(it.n, it.length, A, 0);
   while (r >= it.units) {
     r -= it.units;
-    it.units = tile_units(it.s, A.group, A.tile_rows, ++it.mt);
+    it.units = tile_units(it.n, it.length, A, ++it.mt);
   }
   it.u0 = (int)r;
   it.u1 = (int)min((long long)it.units, r + (end - u));
@@ -190,7 +188,9 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
   long long* warp_sums = reinterpret_cast<long long*>(smem + 512);
   float* join = reinterpret_cast<float*>(smem + P::kJoinOff);
   float* ml = reinterpret_cast<float*>(smem + P::kMlOff);
-  long long* pre = reinterpret_cast<long long*>(smem + P::kPreOff);
+  Item* cur = reinterpret_cast<Item*>(smem + 640);  // the consumers' item, for the join: not held in registers meanwhile
+  int4* seqs = reinterpret_cast<int4*>(smem + P::kSeqOff);
+  long long* pre = reinterpret_cast<long long*>(seqs + A.R.n_seq);  // units before each sequence
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
   if (smem_u32(smem) & 1023) {  // the swizzles count on it
@@ -210,12 +210,14 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     constexpr int kScan = 256;
     const int share = (n_seq + kScan - 1) / kScan;
     long long sum = 0;
+    int blind = 0;  // whether some rows see nothing
     if (tid < kScan) {
       for (int i = tid * share; i < min(n_seq, (tid + 1) * share); ++i) {
         const Kv8Seq s = kv8_seq(A.R, A.C, i);
-        const int u = head_units(s, A.group, A.tile_rows);
-        sum += (long long)u * A.C.kv_heads;
+        seqs[i] = make_int4(s.row0, s.n, s.slot, s.length);
+        if (s.held_ok) sum += (long long)head_units(s.n, s.length, A) * A.C.kv_heads;
         pre[i + 1] = sum;
+        blind |= s.rows_ok && (!s.held_ok || s.length < s.n);
         if (!s.held_ok && blockIdx.x == 0) atomicOr(A.C.err, kErrIndex);
       }
     }
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       if (lane >= o) inc += t;
     }
     if (lane == 31 && warp < kScan / 32) warp_sums[warp] = inc;
-    __syncthreads();
+    blind = __syncthreads_or(blind);
     if (tid < kScan) {
       long long before = inc - sum;
       for (int w = 0; w < warp; ++w) before += warp_sums[w];
@@ -234,15 +236,15 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
-  }
-  // rows that see nothing (or whose slot or length is out of range) are zero
-  for (int i = blockIdx.x; i < n_seq; i += gridDim.x) {
-    const Kv8Seq s = kv8_seq(A.R, A.C, i);
-    if (!s.rows_ok) continue;
-    const int blind = s.held_ok ? min(s.n, max(0, s.n - s.length)) : s.n;
-    const int w4 = A.C.heads * HD / 4;
-    for (int j = tid; j < blind * w4; j += P::kThreads)
-      store_value4(A.out, A.dtype, (long long)(s.row0 + j / w4) * A.out_stride + j % w4 * 4, make_float4(0, 0, 0, 0));
+    // rows that see nothing (or whose slot or length is out of range) are zero
+    for (int i = blockIdx.x; blind && i < n_seq; i += gridDim.x) {
+      const Kv8Seq s = kv8_seq(A.R, A.C, i);
+      if (!s.rows_ok) continue;
+      const int rows = s.held_ok ? min(s.n, max(0, s.n - s.length)) : s.n;
+      const int w4 = A.C.heads * HD / 4;
+      for (int j = tid; j < rows * w4; j += P::kThreads)
+        store_value4(A.out, A.dtype, (long long)(s.row0 + j / w4) * A.out_stride + j % w4 * 4, make_float4(0, 0, 0, 0));
+    }
   }
 
   const long long total = pre[n_seq];
@@ -268,9 +270,21 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     int n = 0, seq = seq0;
     bool ok = true;
     for (long long u = lo; u < hi && ok;) {
-      const Item it = next_item<HD>(A, pre, u, hi, seq);
+      const Item it = next_item(A, pre, seqs, u, hi, seq);
       seq = it.seq;
-      const long long row = ((long long)it.s.slot * A.C.kv_heads + it.head) * A.C.max_ctx;
+      const long long line = (long long)it.slot * A.C.kv_heads + it.head, row = line * A.C.max_ctx;
+      {  // what the consumers will load when they come to the item, on its way to L2: q's rows, the first exponents
+        const int size = PARTS == 2 ? 4 : 2, t0 = it.mt * P::kRows / A.group;
+        const int t1 = min(it.n, (it.mt * P::kRows + P::kRows - 1) / A.group + 1);
+        const char* q = static_cast<const char*>(A.q) +
+                        ((it.row0 + t0) * A.q_stride + (long long)it.head * A.group * HD) * size;
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t, q += A.q_stride * size)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(A.group * HD * size) : "memory");
+        const long long e = line * A.C.n_blocks + ((it.u0 * P::kUnit) >> A.C.block_log2);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(A.C.k_exp + e));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(A.C.v_exp + e));
+      }
       for (int x = it.u0; x < it.u1; ++x, ++n) {
         const int st = n % P::kStages;
         if (n >= P::kStages && !mbar_wait(&empty[st], (n / P::kStages - 1) & 1, A.C.err)) {
@@ -278,9 +292,16 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
           break;
         }
         uint8_t* dst = smem + P::kRing + st * 2 * P::kTile;
-        mbar_arrive_expect_tx(&full[st], 2 * P::kTile);
-        tma_3d(dst, &kmap, 0, (int)(row + (long long)x * kUnit), A.layer, &full[st]);
-        tma_3d(dst + P::kTile, &vmap, 0, (int)(row + (long long)x * kUnit), A.layer, &full[st]);
+        // boxes of 64 positions; one that holds none of the sequence's is left out (its place is not read)
+        const int boxes = P::kSlabs == 1 || x * P::kUnit + 64 < it.length ? P::kSlabs : 1;
+        mbar_arrive_expect_tx(&full[st], 2 * boxes * 64 * HD);
+#pragma unroll
+        for (int b = 0; b < P::kSlabs; ++b) {
+          if (b >= boxes) break;
+          const int y = (int)(row + (long long)x * P::kUnit + 64 * b);
+          tma_3d(dst + b * 64 * HD, &kmap, 0, y, A.layer, &full[st]);
+          tma_3d(dst + P::kTile + b * 64 * HD, &vmap, 0, y, A.layer, &full[st]);
+        }
       }
       u += it.u1 - it.u0;
     }
@@ -290,92 +311,96 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     return;
   }
 
-  // ---- consumers: warp w takes positions 16 (w mod 4) .. + 15 of units w / 4, w / 4 + kGroups, ... of the CTA's list.
+  // ---- consumers: warp w takes quarter w mod 4 of the positions of units w / 4, w / 4 + kGroups, ... of the CTA's list.
   // (Stages are a multiple of the groups, so a stage's units are all of one group, which waits for every phase of it.)
   static_assert(P::kStages % P::kGroups == 0, "a stage belongs to one group of warps");
-  const int mine = warp >> 2, slab = (warp & 3) * 16;
+  const int mine = warp >> 2, slab0 = (warp & 3) * 16 * P::kSlabs;
   int n = 0, seq = seq0;
   bool ok = true;
   for (long long u = lo; u < hi;) {
-    const Item it = next_item<HD>(A, pre, u, hi, seq);
-    seq = it.seq;
-    const Kv8Seq& s = it.s;
-    const int rows = min(P::kRows, s.n * A.group - it.mt * P::kRows);  // of this tile
-    const int p_first = s.length - s.n;                               // position of the sequence's first row
-
-    const long long line = (long long)s.slot * A.C.kv_heads + it.head;
-    const uint8_t* keb = A.C.k_exp + line * A.C.n_blocks;
-    const uint8_t* veb = A.C.v_exp + line * A.C.n_blocks;
-    // this warp's units of the part
-    int x = it.u0 + (mine + P::kGroups - n % P::kGroups) % P::kGroups;
-    auto exps = [&](int unit, int& ek, int& ev) {
-      const int p = unit * kUnit + slab;
-      ek = ev = 0;
-      if (unit < it.u1 && p < s.length) {
-        ek = keb[p >> A.C.block_log2];
-        ev = veb[p >> A.C.block_log2];
-      }
-    };
-    int ek_next, ev_next;
-    exps(x, ek_next, ev_next);
-
-    // q as the B operand: lane (g, c) of k-step y holds dims c HD/4 + 4y .. + 3 of row 8 nt + g
-    uint32_t qb[PARTS][NT][kSteps][2];
-    float rf[NT][2];   // powers of two of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
-    int lim[NT][2];    // positions that they see
+    int u0, u1, length, min_pos;
+    long long line;
+    uint32_t qb[PARTS][NT][kSteps][2];  // q as the B operand
+    float rf[NT][2];                    // powers of two of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
+    int lim[NT][2];                     // positions that they see
+    {
+      const Item it = next_item(A, pre, seqs, u, hi, seq);
+      if (tid == 0) *cur = it;
+      seq = it.seq;
+      u0 = it.u0, u1 = it.u1, length = it.length;
+      line = ((long long)it.slot * A.C.kv_heads + it.head) * A.C.n_blocks;
+      const int rows = min(P::kRows, it.n * A.group - it.mt * P::kRows);  // of this tile
+      const int p_first = length - it.n;                                 // position of the sequence's first row
+      min_pos = p_first + it.mt * P::kRows / A.group;                    // position of the tile's first row
+      // lane (g, c) of k-step y holds dims c HD/4 + 4y .. + 3 of row 8 nt + g
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int rr = 8 * nt + g, m = it.mt * P::kRows + rr;
-      float f[HD / 4];
+      for (int nt = 0; nt < NT; ++nt) {
+        const int rr = 8 * nt + g, m = it.mt * P::kRows + rr;
+        float f[HD / 4];
 #pragma unroll
-      for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
-      if (rr < rows) {
-        const long long at = (long long)(s.row0 + m / A.group) * A.q_stride +
-                             (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
-        if constexpr (PARTS == 2) {
+        for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
+        if (rr < rows) {
+          const long long at = (long long)(it.row0 + m / A.group) * A.q_stride +
+                               (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
+          if constexpr (PARTS == 2) {
 #pragma unroll
-          for (int d = 0; d < HD / 4; d += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at + d);
-            f[d] = v.x, f[d + 1] = v.y, f[d + 2] = v.z, f[d + 3] = v.w;
-          }
-        } else {
+            for (int d = 0; d < HD / 4; d += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at + d);
+              f[d] = v.x, f[d + 1] = v.y, f[d + 2] = v.z, f[d + 3] = v.w;
+            }
+          } else {
 #pragma unroll
-          for (int d = 0; d < HD / 4; d += 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at + d);
-            if (A.dtype == 1)
-              Val<__half>::unpack(v, f + d);
-            else
-              Val<__nv_bfloat16>::unpack(v, f + d);
+            for (int d = 0; d < HD / 4; d += 8) {
+              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at + d);
+              if (A.dtype == 1)
+                Val<__half>::unpack(v, f + d);
+              else
+                Val<__nv_bfloat16>::unpack(v, f + d);
+            }
           }
         }
-      }
-      // a power of two per row brings its largest element to [1, 2)
-      unsigned top = 0;
+        // a power of two per row brings its largest element to [1, 2)
+        unsigned top = 0;
 #pragma unroll
-      for (int d = 0; d < HD / 4; ++d) top = max(top, __float_as_uint(f[d]) & 0x7FFFFFFFu);
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
-      const float down = pow2i(-e);
+        for (int d = 0; d < HD / 4; ++d) top = max(top, __float_as_uint(f[d]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int e = top == 0 ? 0 : min(max((int)(top >> 23) - 127, -120), 120);
+        const float down = pow2i(-e);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = 8 * nt + 2 * c + y;
-        rf[nt][y] = pow2i(__shfl_sync(0xFFFFFFFFu, e, (2 * c + y) * 4));
-        lim[nt][y] = r < rows ? max(0, p_first + (it.mt * P::kRows + r) / A.group + 1) : 0;
-      }
-#pragma unroll
-      for (int y = 0; y < kSteps; ++y) {
-        float h[4], l[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          h[d] = f[4 * y + d] * down;
-          l[d] = h[d] - __half2float(__float2half_rn(h[d]));
+        for (int y = 0; y < 2; ++y) {
+          const int r = 8 * nt + 2 * c + y;
+          rf[nt][y] = pow2i(__shfl_sync(0xFFFFFFFFu, e, (2 * c + y) * 4));
+          lim[nt][y] = r < rows ? max(0, p_first + (it.mt * P::kRows + r) / A.group + 1) : 0;
         }
-        qb[0][nt][y][0] = pack_half2(h[0], h[1]), qb[0][nt][y][1] = pack_half2(h[2], h[3]);
-        if constexpr (PARTS == 2) qb[1][nt][y][0] = pack_half2(l[0], l[1]), qb[1][nt][y][1] = pack_half2(l[2], l[3]);
+#pragma unroll
+        for (int y = 0; y < kSteps; ++y) {
+          float h[4], l[4];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            h[d] = f[4 * y + d] * down;
+            l[d] = h[d] - __half2float(__float2half_rn(h[d]));
+          }
+          qb[0][nt][y][0] = pack_half2(h[0], h[1]), qb[0][nt][y][1] = pack_half2(h[2], h[3]);
+          if constexpr (PARTS == 2) qb[1][nt][y][0] = pack_half2(l[0], l[1]), qb[1][nt][y][1] = pack_half2(l[2], l[3]);
+        }
       }
     }
-    const int min_pos = p_first + it.mt * P::kRows / A.group;  // position of the tile's first row
+    // this warp's units of the part, and the exponent bytes of its slabs, fetched a step ahead
+    int x = u0 + (mine + P::kGroups - n % P::kGroups) % P::kGroups;
+    int ek_next[P::kSlabs], ev_next[P::kSlabs];
+    auto fetch = [&](int unit) {
+#pragma unroll
+      for (int b = 0; b < P::kSlabs; ++b) {
+        const int p = unit * P::kUnit + slab0 + 16 * b;
+        ek_next[b] = ev_next[b] = kKv8Bias;
+        if (p < length) {
+          ek_next[b] = A.C.k_exp[line + (p >> A.C.block_log2)];
+          ev_next[b] = A.C.v_exp[line + (p >> A.C.block_log2)];
+        }
+      }
+    };
+    fetch(x);
 
     // O^T: lane (g, c) of m-tile i holds dims g HD/8 + 2i and + 1 of rows 8 nt + 2c and + 1
     float o[kSteps][NT][4];
@@ -388,24 +413,27 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
 #pragma unroll 1
-    for (; x < it.u1; x += P::kGroups) {
-      const int at = n + x - it.u0, st = at % P::kStages;
-      const int ek = kv8_exp((uint8_t)ek_next), ev = kv8_exp((uint8_t)ev_next);
-      exps(x + P::kGroups, ek_next, ev_next);
+    for (; x < u1; x += P::kGroups) {
+      const int at = n + x - u0, st = at % P::kStages;
+      int ek[P::kSlabs], ev[P::kSlabs];
+#pragma unroll
+      for (int b = 0; b < P::kSlabs; ++b) ek[b] = kv8_exp((uint8_t)ek_next[b]), ev[b] = kv8_exp((uint8_t)ev_next[b]);
+      fetch(x + P::kGroups);
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (at / P::kStages) & 1, A.C.err));
-      const int p0 = x * kUnit + slab;
-      if (ok && p0 < s.length) {
+      const int p0 = x * P::kUnit + slab0;
+      if (ok && p0 < length) {
         const uint8_t* kt = smem + P::kRing + st * 2 * P::kTile;
         const uint8_t* vt = kt + P::kTile;
-        // S^T: positions p0 + g and + 8 (h), rows 2c, 2c + 1
-        float sc[NT][4];
+        // S^T: positions p0 + 16 b + g and + 8 (y / 2), rows 2c, 2c + 1 (y mod 2)
+        float sc[P::kSlabs][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-        {
+        for (int b = 0; b < P::kSlabs; ++b) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) sc[b][nt][0] = sc[b][nt][1] = sc[b][nt][2] = sc[b][nt][3] = 0.f;
           uint32_t kw[2][kSteps];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int row = slab + 8 * h + g;
+            const int row = slab0 + 16 * b + 8 * h + g;
             if constexpr (HD == 128) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
@@ -425,29 +453,31 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_acc(sc[nt], a, qb[part][nt][y][0], qb[part][nt][y][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_acc(sc[b][nt], a, qb[part][nt][y][0], qb[part][nt][y][1]);
           }
-        }
-        // t = score * log2(e) + ev, masked where a row does not see the position
-        const float kf = A.scale2 * pow2i(ek), evf = (float)ev;
-        float mx[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) sc[nt][y] = fmaf(sc[nt][y], kf * rf[nt][y & 1], evf);
-        if (p0 + 15 > min_pos) {
+          // t = score * log2(e) + ev, masked where a row does not see the position
+          const float kf = A.scale2 * pow2i(ek[b]), evf = (float)ev[b];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (p0 + g + 8 * (y >> 1) >= lim[nt][y & 1]) sc[nt][y] = -INFINITY;
+            for (int y = 0; y < 4; ++y) sc[b][nt][y] = fmaf(sc[b][nt][y], kf * rf[nt][y & 1], evf);
+          if (p0 + 16 * b + 15 > min_pos) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                if (p0 + 16 * b + g + 8 * (y >> 1) >= lim[nt][y & 1]) sc[b][nt][y] = -INFINITY;
+          }
         }
+        float mx[NT][2];
         bool grew = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float v = fmaxf(sc[nt][y], sc[nt][y + 2]);
+            float v = fmaxf(sc[0][nt][y], sc[0][nt][y + 2]);
+#pragma unroll
+            for (int b = 1; b < P::kSlabs; ++b) v = fmaxf(v, fmaxf(sc[b][nt][y], sc[b][nt][y + 2]));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
@@ -465,61 +495,65 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
               for (int i = 0; i < kSteps; ++i) o[i][nt][y] *= a, o[i][nt][y + 2] *= a;
             }
         }
-        const float back = pow2i(-ev);
-        uint32_t pb[PARTS][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int b = 0; b < P::kSlabs; ++b) {
+          const float back = pow2i(-ev[b]);
+          uint32_t pb[PARTS][NT][2];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) w[y] = ex2(sc[nt][y] + (m[nt][y & 1] == -INFINITY ? 0.f : kWeightTop - m[nt][y & 1]));
-          l[nt][0] = fmaf(w[0] + w[2], back, l[nt][0]), l[nt][1] = fmaf(w[1] + w[3], back, l[nt][1]);
-          pb[0][nt][0] = turn(pack_half2(w[0], w[1])), pb[0][nt][1] = turn(pack_half2(w[2], w[3]));
-          if constexpr (PARTS == 2) {
-            auto rest = [](float v) { return v - __half2float(__float2half_rn(v)); };
-            pb[1][nt][0] = turn(pack_half2(rest(w[0]), rest(w[1])));
-            pb[1][nt][1] = turn(pack_half2(rest(w[2]), rest(w[3])));
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = ex2(sc[b][nt][y] + (m[nt][y & 1] == -INFINITY ? 0.f : kWeightTop - m[nt][y & 1]));
+            l[nt][0] = fmaf(w[0] + w[2], back, l[nt][0]), l[nt][1] = fmaf(w[1] + w[3], back, l[nt][1]);
+            pb[0][nt][0] = turn(pack_half2(w[0], w[1])), pb[0][nt][1] = turn(pack_half2(w[2], w[3]));
+            if constexpr (PARTS == 2) {
+              auto rest = [](float v) { return v - __half2float(__float2half_rn(v)); };
+              pb[1][nt][0] = turn(pack_half2(rest(w[0]), rest(w[1])));
+              pb[1][nt][1] = turn(pack_half2(rest(w[2]), rest(w[3])));
+            }
           }
-        }
-        // O^T += V^T P^T: lane (g, c) reads HD/8 dims from dim g HD/8 of positions 2c, 2c+1, 2c+8, 2c+9
-        constexpr int kWords = HD / 32;
-        uint32_t vw[4][kWords];
+          // O^T += V^T P^T: lane (g, c) reads HD/8 dims from dim g HD/8 of positions 2c, 2c+1, 2c+8, 2c+9
+          constexpr int kWords = HD / 32;
+          uint32_t vw[4][kWords];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int row = slab + 2 * c + (y & 1) + 8 * (y >> 1);
-          if constexpr (HD == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vt + row * 128 + ((g ^ (row & 7)) << 4));
-            vw[y][0] = w.x, vw[y][1] = w.y, vw[y][2] = w.z, vw[y][3] = w.w;
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(vt + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-            vw[y][0] = w.x, vw[y][1] = w.y;
+          for (int y = 0; y < 4; ++y) {
+            const int row = slab0 + 16 * b + 2 * c + (y & 1) + 8 * (y >> 1);
+            if constexpr (HD == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vt + row * 128 + ((g ^ (row & 7)) << 4));
+              vw[y][0] = w.x, vw[y][1] = w.y, vw[y][2] = w.z, vw[y][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(vt + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+              vw[y][0] = w.x, vw[y][1] = w.y;
+            }
           }
-        }
-        if (p0 + 16 > s.length) {  // positions that nothing has been written to: any bits, NaN among them
+          if (p0 + 16 * b + 16 > length) {  // positions that nothing has been written to: any bits, NaN among them
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (p0 + 2 * c + (y & 1) + 8 * (y >> 1) >= s.length)
+            for (int y = 0; y < 4; ++y)
+              if (p0 + 16 * b + 2 * c + (y & 1) + 8 * (y >> 1) >= length)
 #pragma unroll
-              for (int i = 0; i < kWords; ++i) vw[y][i] = 0;
-        }
+                for (int i = 0; i < kWords; ++i) vw[y][i] = 0;
+          }
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
+          for (int i = 0; i < kWords; ++i) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // bytes 2h, 2h + 1 of the word: dims g and g + 8 of m-tile 2i + h
-            const uint32_t sel = h ? 0x7362 : 0x5140;
-            uint32_t a[4];
-            codes_to_f16<FMT>(prmt(vw[0][i], vw[1][i], sel), a[0], a[1]);
-            codes_to_f16<FMT>(prmt(vw[2][i], vw[3][i], sel), a[2], a[3]);
+            for (int h = 0; h < 2; ++h) {  // bytes 2h, 2h + 1 of the word: dims g and g + 8 of m-tile 2i + h
+              const uint32_t sel = h ? 0x7362 : 0x5140;
+              uint32_t a[4];
+              codes_to_f16<FMT>(prmt(vw[0][i], vw[1][i], sel), a[0], a[1]);
+              codes_to_f16<FMT>(prmt(vw[2][i], vw[3][i], sel), a[2], a[3]);
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+              for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_acc(o[2 * i + h][nt], a, pb[part][nt][0], pb[part][nt][1]);
+                for (int nt = 0; nt < NT; ++nt) mma_acc(o[2 * i + h][nt], a, pb[part][nt][0], pb[part][nt][1]);
+            }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
-    n += it.u1 - it.u0;
+    n += u1 - u0;
 
     // ---- join the warps ----
     constexpr int kRowF = HD + 4;
@@ -540,6 +574,8 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
               make_float4(o[i][nt][y], o[i][nt][y + 2], o[i + 1][nt][y], o[i + 1][nt][y + 2]);
       }
     asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
+    const Item it = *cur;
+    const int rows = min(P::kRows, it.n * A.group - it.mt * P::kRows);
     const bool whole = it.u0 == 0 && it.u1 == it.units;
     const int c0 = (int)(((it.first + 1) * G - 1) / total);
     float* part = A.parts + (long long)(2 * blockIdx.x + (u == lo ? 0 : 1)) * kPart;
@@ -564,7 +600,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
         const float inv = lj == 0.f ? 0.f : 1.f / lj;
         acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
         store_value4(A.out, A.dtype,
-                     (long long)(s.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
+                     (long long)(it.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
       } else {
         *reinterpret_cast<float4*>(part + r * HD + d) = acc;
         if (d == 0) part[16 * HD + r] = mj, part[16 * HD + 16 + r] = lj;
@@ -582,41 +618,53 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       }
       asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
       if (*shared_word) {
-        const int s0 = 2 * c0 + (total * c0 / G == it.first ? 0 : 1);
+        const int s0 = 2 * c0 + (total * c0 / G == it.first ? 0 : 1), np = c1 - c0 + 1;
+        auto part_of = [&](int y) { return A.parts + (long long)(y == 0 ? s0 : 2 * (c0 + y)) * kPart; };
+        // all parts' statistics at once, then each part's weight for each row
+        float* stat = join;  // [np][rows][2]
+        for (int j = tid; j < np * rows; j += P::kWarps * 32) {
+          const float* from = part_of(j / rows) + 16 * HD + j % rows;
+          stat[2 * j] = __ldcg(from), stat[2 * j + 1] = __ldcg(from + 16);
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
         for (int j = tid; j < rows * kQ; j += P::kWarps * 32) {
           const int r = j / kQ, d = j % kQ * 4;
           float mj = -INFINITY;
-#pragma unroll 4
-          for (int y = c0; y <= c1; ++y)
-            mj = fmaxf(mj, __ldcg(A.parts + (long long)(y == c0 ? s0 : 2 * y) * kPart + 16 * HD + r));
+          for (int y = 0; y < np; ++y) mj = fmaxf(mj, stat[2 * (y * rows + r)]);
           float4 acc = make_float4(0, 0, 0, 0);
           float lj = 0.f;
-#pragma unroll 4
-          for (int y = c0; y <= c1; ++y) {
-            const float* from = A.parts + (long long)(y == c0 ? s0 : 2 * y) * kPart;
-            const float mw = __ldcg(from + 16 * HD + r), lw = __ldcg(from + 16 * HD + 16 + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + r * HD + d));
-            const float f = join_factor(mw, lw, mj);
-            lj = fmaf(f, lw, lj);
-            acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+          for (int y0 = 0; y0 < np; y0 += 4) {
+            float4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (y0 + y < np) v[y] = __ldcg(reinterpret_cast<const float4*>(part_of(y0 + y) + r * HD + d));
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if (y0 + y >= np) break;
+              const float mw = stat[2 * ((y0 + y) * rows + r)], lw = stat[2 * ((y0 + y) * rows + r) + 1];
+              const float f = join_factor(mw, lw, mj);
+              lj = fmaf(f, lw, lj);
+              acc.x = fmaf(f, v[y].x, acc.x), acc.y = fmaf(f, v[y].y, acc.y);
+              acc.z = fmaf(f, v[y].z, acc.z), acc.w = fmaf(f, v[y].w, acc.w);
+            }
           }
           const int mm = it.mt * P::kRows + r;
           const float inv = lj == 0.f ? 0.f : 1.f / lj;
           acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
           store_value4(A.out, A.dtype,
-                       (long long)(s.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
+                       (long long)(it.row0 + mm / A.group) * A.out_stride + (long long)(it.head * A.group + mm % A.group) * HD + d, acc);
         }
       }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");  // join and ml may be written again
-    u += it.u1 - it.u0;
+    u += u1 - u0;
   }
 }
 
 template <int HD, int FMT, int NT, int PARTS>
 struct Split {
   using P = SplitPlan<HD, NT, PARTS>;
-  static int smem(int n_seq) { return P::kPreOff + 8 * (n_seq + 1); }
+  static int smem(int n_seq) { return P::kSeqOff + 16 * n_seq + 8 * (n_seq + 1); }
   static cudaError_t setup() {
     return cudaFuncSetAttribute(attend_split_kernel<HD, FMT, NT, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem(kKv8MaxSeq));
@@ -674,6 +722,7 @@ cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& 
   A.scale2 = scale * 1.4426950408889634f;
   A.dtype = dtype, A.group = group, A.layer = layer, A.grid = nsm;
   A.tile_rows = R.max_rows * group <= 8 ? 8 : 16;
+  A.unit = 64 * (128 / C.head_dim);
   A.count = count, A.parts = parts;
   if (C.head_dim == 128) return C.format == 0 ? launch_split<128, 0>(A, M, s) : launch_split<128, 1>(A, M, s);
   return C.format == 0 ? launch_split<64, 0>(A, M, s) : launch_split<64, 1>(A, M, s);
