@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
   }
 
   const long long total = pre[n_seq];
-  const int G = (int)min((long long)gridDim.x, total);
+  // as many CTAs as give each group of warps a unit: more would only make more parts to join
+  const int G = (int)min((long long)gridDim.x, (total + P::kGroups - 1) / P::kGroups);
   if ((int)blockIdx.x >= G) return;
   const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
   int seq0 = 0;
@@ -332,32 +333,34 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       const int rows = min(P::kRows, it.n * A.group - it.mt * P::kRows);  // of this tile
       const int p_first = length - it.n;                                 // position of the sequence's first row
       min_pos = p_first + it.mt * P::kRows / A.group;                    // position of the tile's first row
-      // lane (g, c) of k-step y holds dims c HD/4 + 4y .. + 3 of row 8 nt + g
+      // lane (g, c) of k-step y holds dims c HD/4 + 4y .. + 3 of row 8 nt + g; all loads are on their way at once
+      // (rows past the tile's load its last one, and become 0)
+      constexpr int kVec = HD / 4 * (PARTS == 2 ? 4 : 2) / 16;
+      uint4 raw[NT][kVec];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int rr = 8 * nt + g, m = it.mt * P::kRows + rr;
+        const int m = it.mt * P::kRows + min(8 * nt + g, rows - 1);
+        const long long at = (long long)(it.row0 + m / A.group) * A.q_stride +
+                             (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
+        const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(A.q) + at * (PARTS == 2 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) raw[nt][i] = from[i];
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
         float f[HD / 4];
 #pragma unroll
-        for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
-        if (rr < rows) {
-          const long long at = (long long)(it.row0 + m / A.group) * A.q_stride +
-                               (long long)(it.head * A.group + m % A.group) * HD + c * (HD / 4);
-          if constexpr (PARTS == 2) {
+        for (int i = 0; i < kVec; ++i) {
+          if constexpr (PARTS == 2)
+            Val<float>::unpack(raw[nt][i], f + 4 * i);
+          else if (A.dtype == 1)
+            Val<__half>::unpack(raw[nt][i], f + 8 * i);
+          else
+            Val<__nv_bfloat16>::unpack(raw[nt][i], f + 8 * i);
+        }
+        if (8 * nt + g >= rows) {
 #pragma unroll
-            for (int d = 0; d < HD / 4; d += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at + d);
-              f[d] = v.x, f[d + 1] = v.y, f[d + 2] = v.z, f[d + 3] = v.w;
-            }
-          } else {
-#pragma unroll
-            for (int d = 0; d < HD / 4; d += 8) {
-              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at + d);
-              if (A.dtype == 1)
-                Val<__half>::unpack(v, f + d);
-              else
-                Val<__nv_bfloat16>::unpack(v, f + d);
-            }
-          }
+          for (int d = 0; d < HD / 4; ++d) f[d] = 0.f;
         }
         // a power of two per row brings its largest element to [1, 2)
         unsigned top = 0;
