@@ -192,7 +192,8 @@ def test_attend_never_sees_past_a_row(B, fmt, dtype, rows_):
             assert (one[0].float() - outs[0][r].float()).abs().max() <= tol * scale
 
 
-def test_attend_blocks_of_far_apart_exponents(B):
+@pytest.mark.parametrize("n", [2, 40])
+def test_attend_blocks_of_far_apart_exponents(B, n):
     """Exponents from one end of the range to the other in one row: weights and values span 2^90."""
     for fmt in ("e4m3", "int8"):
         for dtype in ("f32", "bf16"):
@@ -201,20 +202,21 @@ def test_attend_blocks_of_far_apart_exponents(B):
             cache.v_exp[0, 0, 0] = torch.tensor([79, 120, 174, 100, 127, 90, 140, 80], dtype=torch.uint8)
             cache.k_exp[0, 0, 0] = torch.tensor([118, 122, 79, 121, 117, 120, 119, 120], dtype=torch.uint8)
             state = held(cache, 0, fmt)
-            rows, seqs = rows_of(B, [(2, 0, 128)])
-            q = _values(8, (2, 2, 64), dtype, spread=0.0)
+            rows, seqs = rows_of(B, [(n, 0, 128)])
+            q = _values(8, (n, 2, 64), dtype, spread=0.0)
             out = cache.attend(0, q, rows)
             cache.sync()
             check_attend(out, q, state, seqs, 16, 0.125)
 
 
-def test_attend_large_and_small_queries_and_scales(B):
+@pytest.mark.parametrize("n", [3, 40])
+def test_attend_large_and_small_queries_and_scales(B, n):
     cache = B.KvCache8(1, 1, 4, 2, 128, 300, block=32)
     fill(cache, "e4m3", 9)
     state = held(cache, 0, "e4m3")
-    rows, seqs = rows_of(B, [(3, 0, 300)])
+    rows, seqs = rows_of(B, [(n, 0, 300)])
     for mul, scale in ((2.0 ** 20, 2.0 ** -24), (2.0 ** -30, 2.0 ** 26), (1.0, 0.0), (1.0, -0.1)):
-        q = _values(9, (3, 4, 128), "f32", spread=0.5) * mul
+        q = _values(9, (n, 4, 128), "f32", spread=0.5) * mul
         out = cache.attend(0, q, rows, scale=scale)
         cache.sync()
         want = ok.attend(q.double().cpu().numpy(), *state, seqs, 32, scale)
@@ -261,7 +263,6 @@ def test_offsets_past_32_bits(B):
     assert cache.k.numel() > 1 << 32
     rows, seqs = rows_of(B, [(100, slots - 1, ctx)])
     k, v, q = (_values(i, (100, kvh, hd), "bf16", spread=0.5) for i in (1, 2, 3))
-    short = B.KvCache8(1, 1, kvh, kvh, hd, 100, block=64)
     # the same rows at the same places within their blocks: positions ctx - 100 on, and 28 on of a small cache
     small = B.KvCache8(1, 1, kvh, kvh, hd, 128, block=64)
     cache.k[0, slots - 1, :, :ctx - 100] = 0
@@ -287,7 +288,9 @@ def test_offsets_past_32_bits(B):
             err = (out[r, h].double().cpu() - want).abs().max()
             assert err <= 2.0 ** -8 * want.abs().max() + 2.0 ** -9 * (p.abs() @ vv[:r + 1, h].abs()).max() / (
                 p.sum() + (ctx - 100) * np.exp(-m))
-    del short
+    one = cache.attend(0, q[99:], rows_of(B, [(1, slots - 1, ctx)])[0], scale=0.5)  # the few-row path's offsets
+    cache.sync()
+    assert (one[0].float() - out[99].float()).abs().max() <= 2.0 ** -7 * out[99].float().abs().max()
 
 
 def test_captured_calls_follow_their_buffers(B):
@@ -443,3 +446,123 @@ def test_steps_of_a_conversation_together(B):
         if step in (1, 3):
             lengths[step // 2] -= 1  # the last proposal was rejected
     qk.close(), cache.close()
+
+
+@pytest.mark.parametrize("n", [1, 3, 50])
+def test_attend_at_the_most_sequences_and_padded_rows(B, n):
+    """1024 sequences in one call (one more is refused), some without rows or positions; rows behind the last one stay
+    as they were; on another stream than the tensors'."""
+    heads, kvh, hd = 4, 1, 64
+    cache = B.KvCache8(1, 64, heads, kvh, hd, 150, block=16, format="int8")
+    fill(cache, "int8", 18)
+    state = held(cache, 0, "int8")
+    some = [(i * 7) % (n + 1) if i % 5 else n for i in range(1024)]
+    seqs = [(r, i % 64, max(r, (i * 13) % 150)) for i, r in enumerate(some)]
+    T = sum(some)
+    rows, os_ = rows_of(B, seqs, n_rows=T + 9)
+    q = _values(3, (T + 9, heads, hd), "bf16", spread=0.5)
+    out = torch.full_like(q, 3.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    cache.attend(0, q, rows, out=out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    cache.sync()
+    assert (out[T:] == 3).all()
+    # the oracle on a few of them
+    pick = [0, 5, 512, 1019, 1020, 1023]
+    part = [(s[0], s[1], s[2], s[3]) for s in (os_[i] for i in pick) if s[1] > 0]
+    assert part
+    check_attend(out, q, state, part, 16, 0.125)
+    with pytest.raises(B.StrataError):
+        cache.attend(0, q, rows_of(B, seqs + [(0, 0, 0)], n_rows=T + 9)[0], out=out)
+
+
+def test_two_captured_graphs_of_one_handle_in_turn(B):
+    """Two graphs share the handle's workspace; replayed one after the other, with split rows in both, each gives what
+    the call gives by itself."""
+    cache = B.KvCache8(1, 2, 8, 2, 128, 3000, block=64)
+    fill(cache, "e4m3", 19)
+    calls = []
+    for n, seqs in ((1, [(1, 0, 2900), (1, 1, 700)]), (60, [(60, 1, 2999), (2, 0, 70)])):
+        rows, _ = rows_of(B, seqs)
+        q = _values(n, (rows.n_rows, 8, 128), "bf16", spread=0.5)
+        want = cache.attend(0, q, rows)
+        cache.sync()
+        out = torch.zeros_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cache.attend(0, q, rows, out=out)
+        calls.append((g, want, out, q, rows))
+    for i in (0, 1, 1, 0, 0, 1):
+        g, want, out = calls[i][:3]
+        out.zero_()
+        g.replay()
+        cache.sync()
+        assert torch.equal(out, want)
+
+
+def test_appends_on_two_streams_to_different_slots(B):
+    """append uses no workspace: two at once on one handle, each to its own slots."""
+    cache = B.KvCache8(1, 2, 2, 2, 128, 4000, block=32)
+    fill(cache, "e4m3", 20)
+    state = held(cache, 0, "e4m3")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = []
+    for i in range(2):
+        rows, os_ = rows_of(B, [(3000, i, 3500)])
+        k, v = _values(30 + i, (3000, 2, 128), "f16"), _values(40 + i, (3000, 2, 128), "f16")
+        calls.append((rows, os_, k, v))
+    torch.cuda.synchronize()
+    for st, (rows, _, k, v) in zip(streams, calls):
+        cache.append(0, k, v, rows, stream=st)
+    cache.sync()
+    for _, os_, k, v in calls:
+        ok.append(state[0], state[1], k.float().cpu().numpy(), os_, 32, "e4m3")
+        ok.append(state[2], state[3], v.float().cpu().numpy(), os_, 32, "e4m3")
+    _same(cache, state, "e4m3")
+
+
+def test_a_layer_by_its_parts(B):
+    """The attention half as calls beside the MoE window: a decode step's hidden rows through q, k, v products, norms
+    and rotation, append, attention, the o product and strata_moe_window_forward, against the fp64 oracle."""
+    import oracle
+    from slot_decode_window_gb300 import workloads as wlm
+    from tests.helpers import margin_accept, omoe
+    d, heads, kvh, hd = 256, 4, 2, 64
+    wl = wlm.WORKLOADS["tiny"]
+    layer = wlm.make_moe_layer(wl.moe, seed=0, cfg_id=wl.cfg_id, device="cuda")
+    assert wl.moe.hidden == d
+    g = torch.Generator(device="cuda").manual_seed(4)
+    wqkv = torch.randn((heads + 2 * kvh) * hd, d, generator=g, device="cuda") / d ** 0.5
+    wo = torch.randn(d, heads * hd, generator=g, device="cuda") / (heads * hd) ** 0.5
+    cache = B.KvCache8(1, 3, heads, kvh, hd, 40, block=16)
+    fill(cache, "e4m3", 21)
+    state = held(cache, 0, "e4m3")
+    qk, win = B.QkNorm(heads, kvh, hd, theta=1e4), B.Window(layer, max_rows=8)
+    freqs = [1e4 ** (-2.0 * i / hd) for i in range(hd // 2)]
+    rows, seqs = rows_of(B, [(2, 2, 21), (1, 0, 9), (2, 1, 40)])
+    position = np.array([19, 20, 8, 38, 39])
+    x = torch.randn(5, d, generator=g, device="cuda")
+    fused = (x.double() @ wqkv.double().T).float().view(5, heads + 2 * kvh, hd)
+    q, k, v = fused[:, :heads], fused[:, heads:heads + kvh], fused[:, heads + kvh:]
+    qr, kr = qk.forward(q, k, i32(list(position)))
+    cache.append(0, kr, v, rows)
+    att = cache.attend(0, qr, rows)
+    x1 = (x.double() + att.view(5, -1).double() @ wo.double().T).float()
+    y, rt = win.forward(x1, routing=True)
+    win.sync(), cache.sync()
+    # the same in 64 bits, from the same fused rows
+    qn, kn = ok.qknorm(q.cpu().numpy(), position, freqs), ok.qknorm(k.cpu().numpy(), position, freqs)
+    assert np.abs(qr.double().cpu().numpy() - qn).max() <= 2.0 ** -19 * np.abs(qn).max()
+    assert np.abs(kr.double().cpu().numpy() - kn).max() <= 2.0 ** -19 * np.abs(kn).max()
+    ok.append(state[0], state[1], kr.cpu().numpy(), seqs, 16, "e4m3")
+    ok.append(state[2], state[3], v.cpu().numpy(), seqs, 16, "e4m3")
+    _same(cache, state, "e4m3")
+    check_attend(att, qr, state, seqs, 16, hd ** -0.5)
+    ref = oracle.moe_window(x1.cpu().numpy(), omoe(layer))
+    keep = np.array([margin_accept(omoe(layer))(r) for r in x1.cpu().numpy()])
+    assert keep.any()
+    assert np.array_equal(rt["topk_idx"].cpu().numpy()[keep], ref["topk_idx"][keep])
+    rms = np.sqrt(np.mean(ref["y"] ** 2))
+    assert np.abs(y.double().cpu().numpy() - ref["y"])[keep].max() <= 2e-3 * rms
+    win.close(), qk.close(), cache.close()
