@@ -79,11 +79,14 @@ __device__ __forceinline__ int tile_units(int n, int length, const AttendArgs& A
   return seen <= 0 ? 0 : (seen + A.unit - 1) / A.unit;
 }
 
-// Units of all row tiles of one kv head.
-__device__ __forceinline__ int head_units(int n, int length, const AttendArgs& A) {
+// Cost of all row tiles of one kv head: their units, and `start` more for each tile that has any.
+__device__ __forceinline__ int head_cost(int n, int length, const AttendArgs& A, int start) {
   const int tiles = (n * A.group + A.tile_rows - 1) / A.tile_rows;
   int sum = 0;
-  for (int mt = 0; mt < tiles; ++mt) sum += tile_units(n, length, A, mt);
+  for (int mt = 0; mt < tiles; ++mt) {
+    const int u = tile_units(n, length, A, mt);
+    sum += u > 0 ? u + start : 0;
+  }
   return sum;
 }
 
@@ -143,36 +146,45 @@ __device__ __forceinline__ float join_factor(float mw, float lw, float m) {
   return mw == -INFINITY && lw == 0.f ? 0.f : ex2(mw - m);
 }
 
-// A CTA's next item: the part [u0, u1) of its units, positions counted from the item's first unit.
+// A CTA's next item.  The list that the CTAs share is one of costs: an item's is `start` (what beginning an item costs a
+// CTA, in units) and then its units.  A CTA whose share ends within the start does nothing of the item (u0 = u1 = 0).
 struct Item {
   int row0, n, slot, length;  // the sequence
   int seq, head, mt;
-  int u0, u1, units;          // within the item
-  long long first;            // the item's first unit in the whole list
+  int u0, u1, units;          // the CTA's part, of the item's units
+  int cost;                   // what the part takes up of the list
+  long long first;            // the place of the item's first unit in the list
 };
 
 __device__ __forceinline__ Item next_item(const AttendArgs& A, const long long* pre, const int4* seqs, long long u,
-                                          long long end, int seq) {
+                                          long long end, int seq, int start) {
   Item it;
   while (pre[seq + 1] <= u) ++seq;
   it.seq = seq;
   const int4 s = seqs[seq];
   it.row0 = s.x, it.n = s.y, it.slot = s.z, it.length = s.w;
   long long r = u - pre[seq];
-  const int per_head = head_units(it.n, it.length, A);
+  const int per_head = head_cost(it.n, it.length, A, start);
   it.head = (int)(r / per_head);
   r -= (long long)it.head * per_head;
   it.mt = 0;
   it.units = tile_units(it.n, it.length, A, 0);
-  while (r >= it.units) {
-    r -= it.units;
+  while (it.units == 0 || r >= it.units + start) {
+    if (it.units > 0) r -= it.units + start;
     it.units = tile_units(it.n, it.length, A, ++it.mt);
   }
-  it.u0 = (int)r;
-  it.u1 = (int)min((long long)it.units, r + (end - u));
-  it.first = u - r;
+  it.first = u - r + start;
+  it.u0 = (int)max(0ll, r - start);
+  it.u1 = (int)min((long long)it.units, max(0ll, end - it.first));
+  it.cost = (int)(min(end, it.first + it.units) - u);
   return it;
 }
+
+// Units that beginning an item is worth (its q, its join), where every CTA has at least kStartFrom units to do.  With 64
+// conversations of other lengths, 3.4 items a CTA, equal units alone left the slowest CTA at 114 us and the median at 93;
+// a start of 0, 2, 4, 8 units: 132.9, 130.1, 124.5, 122.0 us for the call.  Short lists keep equal units: there a start
+// would leave CTAs without any.
+constexpr int kStart = 8, kStartFrom = 24;
 
 template <int HD, int FMT, int NT, int PARTS>
 __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
   float* ml = reinterpret_cast<float*>(smem + P::kMlOff);
   Item* cur = reinterpret_cast<Item*>(smem + 640);  // the consumers' item, for the join: not held in registers meanwhile
   int4* seqs = reinterpret_cast<int4*>(smem + P::kSeqOff);
-  long long* pre = reinterpret_cast<long long*>(seqs + A.R.n_seq);  // units before each sequence
+  long long* pre = reinterpret_cast<long long*>(seqs + A.R.n_seq);  // costs before each sequence
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
   if (smem_u32(smem) & 1023) {  // the swizzles count on it
@@ -204,21 +216,36 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     }
     fence_mbar_init();
   }
-  // units before each sequence: a contiguous share per thread, joined by a scan
+  // the cost of all before each sequence: a contiguous share per thread, joined by a scan
   const int n_seq = A.R.n_seq;
+  int start;  // what an item's start counts for
   {
     constexpr int kScan = 256;
     const int share = (n_seq + kScan - 1) / kScan;
-    long long sum = 0;
     int blind = 0;  // whether some rows see nothing
+    long long units = 0;
     if (tid < kScan) {
       for (int i = tid * share; i < min(n_seq, (tid + 1) * share); ++i) {
         const Kv8Seq s = kv8_seq(A.R, A.C, i);
-        seqs[i] = make_int4(s.row0, s.n, s.slot, s.length);
-        if (s.held_ok) sum += (long long)head_units(s.n, s.length, A) * A.C.kv_heads;
-        pre[i + 1] = sum;
+        seqs[i] = make_int4(s.row0, s.held_ok ? s.n : 0, s.slot, s.length);
+        if (s.held_ok) units += head_cost(s.n, s.length, A, 0);
         blind |= s.rows_ok && (!s.held_ok || s.length < s.n);
         if (!s.held_ok && blockIdx.x == 0) atomicOr(A.C.err, kErrIndex);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
+    if (lane == 0 && warp < kScan / 32) warp_sums[kScan / 32 + warp] = units;
+    blind = __syncthreads_or(blind);
+    units = 0;
+    for (int w = 0; w < kScan / 32; ++w) units += warp_sums[kScan / 32 + w];
+    start = units * A.C.kv_heads >= (long long)kStartFrom * gridDim.x ? kStart : 0;
+    long long sum = 0;
+    if (tid < kScan) {
+      for (int i = tid * share; i < min(n_seq, (tid + 1) * share); ++i) {
+        const int4 s = seqs[i];
+        sum += (long long)head_cost(s.y, s.w, A, start) * A.C.kv_heads;
+        pre[i + 1] = sum;
       }
     }
     long long inc = sum;
@@ -228,7 +255,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       if (lane >= o) inc += t;
     }
     if (lane == 31 && warp < kScan / 32) warp_sums[warp] = inc;
-    blind = __syncthreads_or(blind);
+    __syncthreads();
     if (tid < kScan) {
       long long before = inc - sum;
       for (int w = 0; w < warp; ++w) before += warp_sums[w];
@@ -254,7 +281,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
   const long long lo = total * blockIdx.x / G, hi = total * (blockIdx.x + 1) / G;
   int seq0 = 0;
   {
-    int a = 0, b = n_seq;  // the sequence that holds unit lo: pre[seq0] <= lo < pre[seq0 + 1]
+    int a = 0, b = n_seq;  // the sequence that holds place lo: pre[seq0] <= lo < pre[seq0 + 1]
     while (b - a > 1) {
       const int m = (a + b) >> 1;
       if (pre[m] <= lo)
@@ -271,10 +298,10 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     int n = 0, seq = seq0;
     bool ok = true;
     for (long long u = lo; u < hi && ok;) {
-      const Item it = next_item(A, pre, seqs, u, hi, seq);
+      const Item it = next_item(A, pre, seqs, u, hi, seq, start);
       seq = it.seq;
       const long long line = (long long)it.slot * A.C.kv_heads + it.head, row = line * A.C.max_ctx;
-      {  // what the consumers will load when they come to the item, on its way to L2: q's rows, the first exponents
+      if (it.u0 < it.u1) {  // what the consumers will load when they come to the item, on its way to L2: q's rows, the first exponents
         const int size = PARTS == 2 ? 4 : 2, t0 = it.mt * P::kRows / A.group;
         const int t1 = min(it.n, (it.mt * P::kRows + P::kRows - 1) / A.group + 1);
         const char* q = static_cast<const char*>(A.q) +
@@ -304,7 +331,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
           tma_3d(dst + P::kTile + b * 64 * HD, &vmap, 0, y, A.layer, &full[st]);
         }
       }
-      u += it.u1 - it.u0;
+      u += it.cost;
     }
     if (!ok)  // the copies in flight land before this thread leaves
       for (int i = max(0, n - P::kStages); i < n; ++i)
@@ -319,15 +346,19 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
   int n = 0, seq = seq0;
   bool ok = true;
   for (long long u = lo; u < hi;) {
-    int u0, u1, length, min_pos;
+    int u0, u1, length, min_pos, cost;
     long long line;
     uint32_t qb[PARTS][NT][kSteps][2];  // q as the B operand
     float rf[NT][2];                    // powers of two of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
     int lim[NT][2];                     // positions that they see
     {
-      const Item it = next_item(A, pre, seqs, u, hi, seq);
+      const Item it = next_item(A, pre, seqs, u, hi, seq, start);
+      seq = it.seq, cost = it.cost;
+      if (it.u0 >= it.u1) {
+        u += cost;
+        continue;
+      }
       if (tid == 0) *cur = it;
-      seq = it.seq;
       u0 = it.u0, u1 = it.u1, length = it.length;
       line = ((long long)it.slot * A.C.kv_heads + it.head) * A.C.n_blocks;
       const int rows = min(P::kRows, it.n * A.group - it.mt * P::kRows);  // of this tile
@@ -621,7 +652,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       }
       asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");
       if (*shared_word) {
-        const int s0 = 2 * c0 + (total * c0 / G == it.first ? 0 : 1), np = c1 - c0 + 1;
+        const int s0 = 2 * c0 + (total * c0 / G >= it.first - start ? 0 : 1), np = c1 - c0 + 1;
         auto part_of = [&](int y) { return A.parts + (long long)(y == 0 ? s0 : 2 * (c0 + y)) * kPart; };
         // all parts' statistics at once, then each part's weight for each row
         float* stat = join;  // [np][rows][2]
@@ -660,7 +691,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(P::kWarps * 32) : "memory");  // join and ml may be written again
-    u += u1 - u0;
+    u += cost;
   }
 }
 
