@@ -31,7 +31,7 @@ struct QkArgs {
 };
 
 constexpr int kQkThreads = 128;
-constexpr int kQkBatch = 4;  // 16-byte accesses a thread has in flight
+constexpr int kQkBatch = 1;  // 16-byte accesses a thread has in flight
 
 // A CTA owns `per_cta` heads of a row (of q's and then k's).  Its threads form the row's angles once, an angle a
 // thread, in shared memory; then a warp takes kGroup heads at a time: E neighbouring dims of a head in a lane,
@@ -40,10 +40,11 @@ constexpr int kQkBatch = 4;  // 16-byte accesses a thread has in flight
 // shuffle away (half a rotary_dim is a multiple of E).
 // The angle in turns is position * turn mod 2^64: the product wraps to the exact fraction, its top 32 bits go to
 // sincospi.
-// HBM bound in a prompt.  With the angles and gains in every warp's registers instead (91 of them, a quarter of the
-// SM's warps, six times the angles) 8191 rows of 32 + 8 bf16 heads took 73.6 us.
+// HBM bound in a prompt.  8191 rows of 32 + 8 bf16 heads: with the angles and gains in every warp's registers (91 of
+// them, six times the angles) 74 us; in shared memory 64 us with four accesses a thread in flight (79 registers), 45 us
+// with one and twelve CTAs an SM (40 registers), which is what is here.
 template <typename T, int kHd, int E, bool kInter>
-__global__ void __launch_bounds__(kQkThreads) qknorm_kernel(QkArgs A) {
+__global__ void __launch_bounds__(kQkThreads, 12) qknorm_kernel(QkArgs A) {
   constexpr int kLanes = kHd / E, kGroup = 32 / kLanes, kWarps = kQkThreads / 32;
   __shared__ float2 turn[kHd / 2];        // cosine and sine of each pair's angle
   __shared__ alignas(16) float gain[2][kHd];
