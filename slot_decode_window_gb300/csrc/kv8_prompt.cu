@@ -54,7 +54,8 @@ constexpr int kScores = 3;         // places of S (and then P) in tensor memory
 template <int HD, bool TWO> struct PromptPlan {
   static constexpr int kTile = kPRows * HD * 2;      // a 128-row f16 tile: panels of 64 halves (one swizzle span)
   static constexpr int kRaw = 64 * HD;               // half a unit's codes of K or V
-  static constexpr int kVStages = TWO ? 1 : 2;      // tiles; V's ring is of their halves
+  static constexpr int kVStages = TWO ? 1 : 2;      // tiles of V: of the one, each half is converted while the other is in use
+  static constexpr int kVParts = TWO ? 2 : 1;       // what V's barriers cover: halves, or whole tiles
   static constexpr int kQ = 0;                       // byte offsets from a 1024-byte boundary
   static constexpr int kK = kQ + (TWO ? 2 : 1) * kTile;
   static constexpr int kV = kK + 2 * kTile;
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 4), mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&v_full[i], 2), mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&v_full[i], TWO ? 2 : 4), mbar_init(&v_empty[i], 1);
     for (int i = 0; i < kScores; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4), mbar_init(&place_free[i], 1);
     mbar_init(u_full, 1), mbar_init(u_empty, 4);
     mbar_init(q_full, 4), mbar_init(q_empty, 1), mbar_init(&last[0], 1), mbar_init(&last[1], 1);
@@ -658,15 +659,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
               unpack2(mul2(pack2(o[ch * 32 + i], o[ch * 32 + i + 1]), pack2(a, a)), o[ch * 32 + i], o[ch * 32 + i + 1]);
           }
           tc_wait_ld();
+          if (ch == HD / 32 - 1) {  // the last of U is in registers: its place is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_empty);
+          }
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             unpack2(fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pack2(b, b),
                          pack2(o[ch * 32 + i], o[ch * 32 + i + 1])),
                     o[ch * 32 + i], o[ch * 32 + i + 1]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_empty);
       }
       n += it->u1 - it->u0;
       const int tok = it->tile * A.tokens + row_tok;
@@ -867,7 +870,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
 #pragma unroll 1
       for (; at < end; ++at) {
-        if (at >= places && !(ok = wait_warp(v_side ? &v_empty[st * 2 + half] : &k_empty[st], ph ^ 1, dead, err))) break;
+        if (at >= places && !(ok = wait_warp(v_side ? &v_empty[TWO ? half : st] : &k_empty[st], ph ^ 1, dead, err))) break;
         if (!v_side && t < 8) {
           const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
           factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
@@ -877,7 +880,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         p += kPUnit;
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_side ? &v_full[st * 2 + half] : &k_full[st]);
+        if (lane == 0) mbar_arrive(v_side ? &v_full[TWO ? half : st] : &k_full[st]);
         if (at + 1 < end) fetch();
         if (++st == places) st = 0, ph ^= 1;
       }
@@ -934,7 +937,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     } else if (warp == kMmaWarp + 1) {
       // ---- U = P V ----
       Ring<kScores> place;
-      Ring<2 * P::kVStages> vst;
+      Ring<P::kVStages * P::kVParts> vst;
       bool ok = true;
       const uint64_t v_desc = tc_desc(smem + P::kV, 1024, kPRows * 128);
       constexpr uint32_t u_id = tc_idesc(HD, true);
@@ -943,19 +946,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (!(ok = wait_warp(&p_full[place.st], place.ph, dead, err))) break;
         if (at >= 1 && !(ok = wait_warp(u_empty, (at - 1) & 1, dead, err))) break;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int part = 0; part < P::kVParts; ++part) {
           if (!(ok = wait_warp(&v_full[vst.st], vst.ph, dead, err))) break;
           tc_fence_after();
-          const uint32_t a = tmem + place.st * 128 + half * 64;
-          const uint64_t b = v_desc + (((vst.st >> 1) * P::kTile + half * (64 * 128)) >> 4);
+          const uint32_t a = tmem + place.st * 128 + part * 64;
+          const uint64_t b = v_desc + ((TWO ? part * (64 * 128) : vst.st * P::kTile) >> 4);
           if (elect_one()) {
 #pragma unroll 2
-            for (int y = 0; y < kPUnit / 32; ++y) {
-              tc_mma_ts(d, a + y * 16, b + ((y * 16 * 128) >> 4), u_id, half > 0 || y > 0);
+            for (int y = 0; y < kPUnit / 16 / P::kVParts; ++y) {
+              tc_mma_ts(d, a + y * 16, b + ((y * 16 * 128) >> 4), u_id, part > 0 || y > 0);
               if constexpr (TWO) tc_mma_ts(d, a + y * 16 + 8, b + ((y * 16 * 128) >> 4), u_id, 1);
             }
+            if (part == P::kVParts - 1) tc_commit(u_full), tc_commit(&place_free[place.st]);
             tc_commit(&v_empty[vst.st]);
-            if (half) tc_commit(u_full), tc_commit(&place_free[place.st]);
           }
           __syncwarp();
           vst.step();
