@@ -157,7 +157,24 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this thread's tensor memory loads.  The registers they fill are operands, so that no use of them can be
+// moved in front of it.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor: 128-byte swizzle, 8-row groups `sbo` bytes
@@ -412,7 +429,7 @@ __device__ __forceinline__ void unit_mask(uint32_t s_addr, int left) {
   for (int ch = 0; ch < 8; ++ch) {
     uint32_t r[16];
     tc_ld16(s_addr + ch * 16, r);
-    tc_wait_ld();
+    tc_wait_ld(r);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (ch * 16 + i >= left) r[i] = 0xFF800000u;
@@ -434,7 +451,7 @@ __device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac,
     uint32_t r[32];
     tc_ld32(s_addr + ch * 32, r);
     const float4 f0 = fac[ch * 2], f1 = fac[ch * 2 + 1];
-    tc_wait_ld();
+    tc_wait_ld(r);
     float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -458,7 +475,7 @@ __device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac,
     const uint64_t k2 = pack2(k, k), c2 = pack2(c, c);
     uint64_t sum = pack2(0.f, 0.f);
     uint32_t hi16[8], lo16[TWO ? 8 : 1];
-    tc_wait_ld();
+    tc_wait_ld(r);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       float w0, w1;
@@ -658,7 +675,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int i = 0; i < 32; i += 2)
               unpack2(mul2(pack2(o[ch * 32 + i], o[ch * 32 + i + 1]), pack2(a, a)), o[ch * 32 + i], o[ch * 32 + i + 1]);
           }
-          tc_wait_ld();
+          tc_wait_ld(r);
           if (ch == HD / 32 - 1) {  // the last of U is in registers: its place is free
             tc_fence_before();
             __syncwarp();
