@@ -195,7 +195,8 @@ struct Kv8Maps {
 };
 // Shared-memory limits of the attention kernels for a shape, on the current device (once per handle).
 cudaError_t setup_kv8_attend(int head_dim, int format);
-// Workspace: 256 bytes that begin with the error word, then the attention's.
+// Workspace: 256 bytes that begin with the error word, a counter per SM (both start at zero), then the joins' parts.
+long long kv8_attend_zeroed(int nsm);
 long long kv8_attend_workspace(int nsm, int head_dim);
 cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& M, int layer, void* workspace, int nsm,
                               const void* q, long long q_stride, void* out, long long out_stride, int dtype,

@@ -736,10 +736,10 @@ cudaError_t setup_kv8_attend(int head_dim, int format) {
   return e != cudaSuccess ? e : setup_kv8_prompt(head_dim, format);
 }
 
-// After the error word's 256 bytes: a counter per CTA, then two parts per CTA.
-long long kv8_attend_workspace(int nsm, int head_dim) {
-  const int part = max(split_part(head_dim), kv8_prompt_part_floats(head_dim));
-  return 256 + ((long long)nsm * 4 + 255) / 256 * 256 + 2LL * nsm * part * 4;
+long long kv8_attend_zeroed(int nsm) { return 256 + ((long long)nsm * 4 + 255) / 256 * 256; }
+
+long long kv8_attend_workspace(int nsm, int head_dim) {  // two parts per CTA
+  return kv8_attend_zeroed(nsm) + 2LL * nsm * max(split_part(head_dim), kv8_prompt_part_floats(head_dim)) * 4;
 }
 
 cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& M, int layer, void* workspace, int nsm,
@@ -748,7 +748,7 @@ cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& 
   const int group = C.heads / C.kv_heads;
   uint8_t* w = static_cast<uint8_t*>(workspace) + 256;
   unsigned* count = reinterpret_cast<unsigned*>(w);
-  float* parts = reinterpret_cast<float*>(w + ((size_t)nsm * 4 + 255) / 256 * 256);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv8_attend_zeroed(nsm));
   if ((long long)R.max_rows * group > 32)
     return launch_kv8_prompt(C, R, M, layer, count, parts, nsm, q, q_stride, out, out_stride, dtype, scale, s);
   AttendArgs A;

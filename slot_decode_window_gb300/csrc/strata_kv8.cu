@@ -103,6 +103,11 @@ Kv8Rows rows_dev(const strata_kv8_rows* r) {
   return {r->n_seq, r->n_rows, r->max_rows < r->n_rows ? r->max_rows : r->n_rows, r->row_start, r->slot, r->length};
 }
 
+// The part of the workspace that starts at zero: the error word and the joins' counters.
+bool clear(const strata_kv8* h) {
+  return cudaMemset(h->ws, 0, (size_t)kv8_attend_zeroed(h->nsm)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+}
+
 strata_status launched(cudaError_t e) {
   if (e == cudaSuccess) return STRATA_OK;
   cudaGetLastError();
@@ -144,7 +149,7 @@ strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_ca
     free_kv8(h);
     return STRATA_ENOMEM;
   }
-  if (cudaMemset(h->ws, 0, (size_t)h->ws_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (!clear(h)) {
     cudaGetLastError();
     free_kv8(h);
     return STRATA_ECUDA;
@@ -217,7 +222,7 @@ strata_status strata_kv8_sync(strata_kv8* h) {
     return STRATA_ECUDA;
   }
   if (err == 0) return STRATA_OK;
-  if (cudaMemset(h->ws, 0, (size_t)h->ws_bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (!clear(h)) {
     cudaGetLastError();
     return STRATA_ECUDA;
   }
