@@ -330,7 +330,8 @@ __device__ inline long long p_ordered_before(const Kv8Seq& s, int tokens, int k)
          p_units_before(s, tokens, tiles - (k >> 1));
 }
 
-// The items of a CTA's part of the list in turn; begin() finds the first, next() steps.
+// The items of a CTA's part of the list in turn; begin() finds the first (a whole warp does, 32 places tried at a time:
+// one thread by halves took some 16 us), next() steps.
 struct PItem {
   Kv8Seq s;
   int seq, head, i, tile, units;  // i: the tile's place in the order
@@ -355,11 +356,10 @@ __device__ inline void p_begin(PItem& it, const PromptArgs& A, const long long* 
   r -= it.head * per;
   int t0 = 0, t1 = p_tiles(it.s, A.tokens);  // before(t0) <= r < before(t1)
   while (t1 - t0 > 1) {
-    const int m = (t0 + t1) >> 1;
-    if (p_ordered_before(it.s, A.tokens, m) <= r)
-      t0 = m;
-    else
-      t1 = m;
+    const int step = (t1 - t0 + 31) / 32, at = t0 + ((int)(threadIdx.x & 31) + 1) * step;
+    const bool below = at < t1 && p_ordered_before(it.s, A.tokens, at) <= r;
+    t0 += __popc(__ballot_sync(0xFFFFFFFFu, below)) * step;
+    t1 = min(t1, t0 + step);
   }
   it.i = t0;
   it.tile = p_tile_at(it.s, A.tokens, t0);
@@ -986,9 +986,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (elect_one()) tc_commit(&last[1]);
       __syncwarp();
       mbar_wait(&last[1], 0, err);
-    } else if ((warp == kTmaWarp || warp == kTmaWarp + 1) && lane == 0) {
+    } else {
       // ---- TMA of the codes of K, or of V, 64 positions at a time ----
       const int v_side = warp - kTmaWarp;
+      PItem item;
+      if (!v_side) p_begin(item, A, pre, span[1], span[2]);
+      if (lane == 0) {
       const CUtensorMap* map = v_side ? &vmap : &kmap;
       uint64_t *raw_f = raw_full + v_side * kRawBars, *raw_e = raw_empty + v_side * kRawBars;
       uint8_t* dst = smem + P::kRawOff + v_side * kRawStages * P::kRaw;
@@ -996,8 +999,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       Ring<kRawBars> raw, freed;  // freed: three copies behind, the last user of raw's stage
       int copies = 0, at = 0;
       bool ok = true;
-      PItem item;
-      if (!v_side) p_begin(item, A, pre, span[1], span[2]);
       for (int i = 0; at < n_units; ++i) {
         if (!v_side) {  // the next segment: K's copies are the first to need it
           if (i > 0) p_next(item, A, pre, span[1] + at, span[2]);
@@ -1043,6 +1044,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
         mbar_wait(&raw_f[i % kRawBars], (i / kRawBars) & 1, err);
+      }
     }
     __syncwarp();
   }
