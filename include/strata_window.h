@@ -599,7 +599,9 @@ typedef struct {
 typedef struct {
   int32_t n_seq;             /* 0..1024 (0: nothing is done) */
   int32_t n_rows;            /* rows of the value arrays (0: nothing is done) */
-  int32_t max_rows;          /* no sequence has more rows than this */
+  int32_t max_rows;          /* no sequence has more rows than this.  It bounds the launch, and with the query heads per
+                                kv head it picks the attention's kernel for the whole call (few rows: up to 32 of
+                                rows x heads; a batch of single rows and one prompt is faster as two calls) */
   const int32_t* row_start;  /* device [n_seq + 1] */
   const int32_t* slot;       /* device [n_seq] */
   const int32_t* length;     /* device [n_seq] */

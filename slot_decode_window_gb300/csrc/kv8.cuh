@@ -56,13 +56,7 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Rows& R, const Kv8Dev& C, int
 __device__ __forceinline__ int kv8_exp(uint8_t byte) { return min(max((int)byte - kKv8Bias, kKv8EMin), kKv8EMax); }
 
 // 2^e for e in [-126, 127].
-__host__ __device__ __forceinline__ float pow2i(int e) {
-#ifdef __CUDA_ARCH__
-  return __int_as_float((e + 127) << 23);
-#else
-  return e >= 0 ? (float)(1ull << (e < 63 ? e : 63)) : 1.f / (float)(1ull << (-e < 63 ? -e : 63));
-#endif
-}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // The least e with a <= qmax 2^e, clamped.  448 = 1.75 * 2^8, 127 = 1.984375 * 2^6.
 __device__ __forceinline__ int kv8_least_exp(float a, int format) {

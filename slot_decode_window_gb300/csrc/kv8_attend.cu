@@ -30,6 +30,10 @@ namespace {
 // below it), and no block needs its own accumulator.
 // f32 rows: q and the weights enter as two f16 parts (22 bits) that chain into
 // one accumulator.
+// Measured (32 / 8 heads of 128, bf16): 64 rows over 1.6 k to 8.2 k positions
+// 111.6 us (85% of the measured HBM rate), one over 131071 52.9 us (75%; the
+// start and the join of 19 parts are the rest).  With the rows on the M side
+// and 8 warps of 168 registers these took 164 and 62 us.
 // ---------------------------------------------------------------------------
 constexpr float kWeightTop = 14.f;  // weights are scaled by 2^14
 

