@@ -746,61 +746,55 @@ class Head:
             pass
 
 
-# The calls below are short next to Python's own time, so their checks read each tensor property once.
+# The calls below are short next to Python's own time (a window's take 2 to 16 us on the GPU), so their checks read each
+# tensor property once and what they need of torch is looked up once, by the first handle.
+_torch = None
 _DTYPE = None  # torch dtype -> strata_dtype
 
 
-def _dtypes():
-    global _DTYPE
-    if _DTYPE is None:
+def _with_torch():
+    global _torch, _DTYPE
+    if _torch is None:
         import torch
         _DTYPE = {torch.float32: STRATA_F32, torch.float16: STRATA_F16, torch.bfloat16: STRATA_BF16}
-    return _DTYPE
+        _torch = torch
+    return _torch
 
 
 def _row_stride(t, shape, what: str) -> int:
     """The distance between rows, in elements, of a CUDA tensor of this shape [T][heads][head_dim]; raises for any
     layout whose rows are not contiguous."""
-    T, heads, hd = shape
     st = t.stride()
-    if not t.is_cuda or tuple(t.shape) != shape or st[2] != 1 or (st[1] != hd and heads != 1) or t.dtype not in _dtypes():
-        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [rows][{heads}][{hd}] of float32, float16 or "
-                                         "bfloat16 whose rows are contiguous")
-    return st[0] if T > 1 else heads * hd
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] != 1) or not t.is_cuda or \
+            t.dtype not in _DTYPE:
+        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [{shape[0]}][{shape[1]}][{shape[2]}] of float32, "
+                                         "float16 or bfloat16 whose rows are contiguous")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _same(t, like, what: str) -> None:
-    if t.dtype != like.dtype or t.get_device() != like.get_device():
+    if t.dtype is not like.dtype or t.get_device() != like.get_device():
         raise StrataError(STRATA_EINVAL, f"{what}: type or device differ")
 
 
-def _same_device(t, like, what: str) -> None:
-    if t.get_device() != like.get_device():
-        raise StrataError(STRATA_EINVAL, f"{what}: device differs")
-
-
-def _int32(t, n: int, what: str):
-    import torch
-    if not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
-        raise StrataError(STRATA_EINVAL, f"{what}: want a contiguous CUDA int32 tensor [{n}]")
+def _int32(t, n: int, device: int, what: str):
+    """The pointer of a contiguous CUDA int32 tensor [n] of the device."""
+    if t.dtype is not _torch.int32 or t.shape != (n,) or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        raise StrataError(STRATA_EINVAL, f"{what}: want a contiguous CUDA int32 tensor [{n}] on the call's device")
     return t.data_ptr()
 
 
 def _raw_stream(index: int, stream) -> int:
     """The cudaStream_t of a stream, or of the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if stream is not None else _torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
     """A new tensor of the stream that the call runs on."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 class QkNorm:
@@ -813,7 +807,7 @@ class QkNorm:
     def __init__(self, heads: int, kv_heads: int, head_dim: int, rotary_dim: Optional[int] = None, freqs=None,
                  theta: float = 10000.0, interleaved: bool = False, norm: bool = True, eps: float = 1e-6,
                  q_gain=None, k_gain=None, device=None, stream=None):
-        import torch
+        torch = _with_torch()
         rd = head_dim if rotary_dim is None else rotary_dim
         if freqs is None:
             freqs = [theta ** (-2.0 * i / rd) for i in range(rd // 2)] if rd > 0 else []
@@ -839,9 +833,7 @@ class QkNorm:
     def forward(self, q, k, position, q_out=None, k_out=None, stream=None):
         """Enqueue q [T][heads][head_dim] and k [T][kv_heads][head_dim] at position (CUDA int32 [T]); returns
         (q_out, k_out), new tensors unless given (an output may be its own input)."""
-        if q.dim() != 3:
-            raise StrataError(STRATA_EINVAL, "q: want [rows][heads][head_dim]")
-        T, kv, hd = q.shape[0], self.kv_heads, self.head_dim
+        T, kv, hd = q.shape[0] if q.dim() == 3 else -1, self.kv_heads, self.head_dim
         shape = (T, self.heads, hd)
         qs = _row_stride(q, shape, "q")
         qos = self.heads * hd
@@ -852,21 +844,19 @@ class QkNorm:
             _same(q_out, q, "q_out")
         kp = ks = kop = kos = 0
         if kv > 0:
-            kshape = (T, kv, hd)
-            if k.dim() != 3:
-                raise StrataError(STRATA_EINVAL, "k: want [rows][kv_heads][head_dim]")
-            ks = _row_stride(k, kshape, "k")
+            shape = (T, kv, hd)
+            ks = _row_stride(k, shape, "k")
             _same(k, q, "k")
             kos = kv * hd
             if k_out is None:
-                k_out = _empty(kshape, k.dtype, k.device, stream)
+                k_out = _empty(shape, k.dtype, k.device, stream)
             else:
-                kos = _row_stride(k_out, kshape, "k_out")
+                kos = _row_stride(k_out, shape, "k_out")
                 _same(k_out, q, "k_out")
             kp, kop = k.data_ptr(), k_out.data_ptr()
-        _same_device(position, q, "position")
+        device = q.get_device()
         st = self._forward(self.handle, q.data_ptr(), qs, kp, ks, q_out.data_ptr(), qos, kop, kos, _DTYPE[q.dtype],
-                           _int32(position, T, "position"), T, _raw_stream(q.get_device(), stream))
+                           _int32(position, T, device, "position"), T, _raw_stream(device, stream))
         if st != STRATA_OK:
             check(st, "strata_qknorm_forward")
         return q_out, k_out
@@ -890,13 +880,12 @@ class KvRows:
     sequence are left as they were), max_rows the most rows of one sequence."""
 
     def __init__(self, row_start, slot, length, n_rows: int, max_rows: int):
-        n = slot.shape[0]
+        _with_torch()
+        n, device = slot.shape[0], slot.get_device()
         self.keep = (row_start, slot, length)
-        self.n_rows, self.device = n_rows, slot.get_device()
-        _same_device(row_start, slot, "row_start")
-        _same_device(length, slot, "length")
-        self.c = strata_kv8_rows(n, n_rows, max_rows, _int32(row_start, n + 1, "row_start"), _int32(slot, n, "slot"),
-                                 _int32(length, n, "length"))
+        self.n_rows, self.device = n_rows, device
+        self.c = strata_kv8_rows(n, n_rows, max_rows, _int32(row_start, n + 1, device, "row_start"),
+                                 _int32(slot, n, device, "slot"), _int32(length, n, device, "length"))
 
 
 class KvCache8:
@@ -909,7 +898,7 @@ class KvCache8:
 
     def __init__(self, n_layers: int, n_slots: int, heads: int, kv_heads: int, head_dim: int, max_ctx: int,
                  block: int = 64, format: str = "e4m3", buffers=None, device=None):
-        import torch
+        torch = _with_torch()
         fmt = {"e4m3": STRATA_KV8_E4M3, "int8": STRATA_KV8_INT8}.get(format)
         if fmt is None:
             raise StrataError(STRATA_EINVAL, "KvCache8: format is e4m3 or int8")
@@ -956,14 +945,19 @@ class KvCache8:
     def read(self, layer: int, rows: KvRows, dtype=None, k=None, v=None, stream=None):
         """Enqueue the rows' positions as values; returns (k, v), [n_rows][kv_heads][head_dim] of dtype (float32),
         new tensors unless given; rows of no sequence are not written."""
-        import torch
         shape = (rows.n_rows, self.kv_heads, self.head_dim)
+        ks = vs = self.kv_heads * self.head_dim
         if k is None:
-            k = _empty(shape, dtype or torch.float32, self.k.device, stream)
+            k = _empty(shape, dtype or (v.dtype if v is not None else _torch.float32), self.k.device, stream)
+            if k.dtype not in _DTYPE or rows.device != self.device:
+                raise StrataError(STRATA_EINVAL, "read: want float32, float16 or bfloat16 and rows on the cache's device")
+        else:
+            ks = self._stride(rows, k, self.kv_heads, "k")
         if v is None:
             v = _empty(shape, k.dtype, self.k.device, stream)
-        ks, vs = self._stride(rows, k, self.kv_heads, "k"), self._stride(rows, v, self.kv_heads, "v")
-        _same(v, k, "v")
+        else:
+            vs = self._stride(rows, v, self.kv_heads, "v")
+            _same(v, k, "v")
         st = self._read(self.handle, layer, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPE[k.dtype], rows.c,
                         _raw_stream(self.device, stream))
         if st != STRATA_OK:

@@ -407,6 +407,10 @@ def test_refusals(B):
             cache.attend(0, bad, rows)
     with pytest.raises(B.StrataError):
         cache.append(0, q[:, :2], q[:, :2].half(), rows)
+    for kw in (dict(dtype=torch.float64), dict(k=q[:, :2].double()), dict(k=q[:, :2], v=q[:, :2].half()),
+               dict(v=q[:, :3]), dict(k=q[:1, :2])):
+        with pytest.raises(B.StrataError):
+            cache.read(0, rows, **kw)
     with pytest.raises(B.StrataError):
         B.KvRows(torch.zeros(3, dtype=torch.int64, device="cuda"), i32([0, 1]), i32([1, 1]), 2, 1)
     with pytest.raises(B.StrataError):
