@@ -547,7 +547,7 @@ strata_status strata_qknorm_create(const strata_qknorm_desc* desc, const float* 
 /* T rows: q [T][heads][head_dim] to q_out, k [T][kv_heads][head_dim] to k_out
  * (k and k_out may be NULL when kv_heads is 0).  position: device int32 [T],
  * any value.  An output may be its own input (same pointer and stride); any
- * other overlap is not allowed.  T = 0 does nothing.  A row's bits do not
+ * other overlap is not allowed (EINVAL where it starts at the same address).  T = 0 does nothing.  A row's bits do not
  * depend on the other rows.  Returns EINVAL, ECUDA.  One handle may run on
  * several streams at once. */
 strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -633,7 +633,8 @@ strata_status strata_kv8_append(strata_kv8* h, int32_t layer, const void* k, int
 
 /* Read the rows' positions back: code * 2^e, rounded once to dtype (exact in
  * f32; f16 overflows to infinity as any rounding to it).  A sequence with
- * length[i] below its rows is left out. */
+ * length[i] below its rows is left out.  k and v must not overlap (EINVAL at
+ * the same address). */
 strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_stride, void* v, int64_t v_stride,
                               int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream);
 
@@ -647,7 +648,7 @@ strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_s
  * contents at positions from length[i] on never reach an output, whatever
  * their bits; below it codes are numbers (append writes no other).  Sequences
  * may share a slot.  q and out are [n_rows][heads][head_dim] of the same dtype
- * and must not overlap.  scale is finite.
+ * and must not overlap (EINVAL at the same address).  scale is finite.
  * The rows written by an earlier strata_kv8_append on the same stream are
  * seen.  The handle's workspace joins the parts of long rows, so calls of
  * strata_kv8_attend on one handle, replays of captured ones among them, must

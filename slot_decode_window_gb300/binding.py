@@ -822,6 +822,7 @@ class QkNorm:
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         with torch.cuda.device(device):
             s = (stream or torch.cuda.current_stream()).cuda_stream
+            self.device = torch.cuda.current_device()
             st, h = strata_qknorm_create(
                 strata_qknorm_desc(heads, kv_heads, head_dim, rd, int(interleaved), int(norm), eps),
                 q_gain.data_ptr() if q_gain is not None else None, k_gain.data_ptr() if k_gain is not None else None,
@@ -844,6 +845,8 @@ class QkNorm:
             _same(q_out, q, "q_out")
         kp = ks = kop = kos = 0
         if kv > 0:
+            if k is None:
+                raise StrataError(STRATA_EINVAL, "k: wanted by kv_heads > 0")
             shape = (T, kv, hd)
             ks = _row_stride(k, shape, "k")
             _same(k, q, "k")
@@ -855,6 +858,8 @@ class QkNorm:
                 _same(k_out, q, "k_out")
             kp, kop = k.data_ptr(), k_out.data_ptr()
         device = q.get_device()
+        if device != self.device:
+            raise StrataError(STRATA_EINVAL, "q: want a tensor on the handle's device")
         st = self._forward(self.handle, q.data_ptr(), qs, kp, ks, q_out.data_ptr(), qos, kop, kos, _DTYPE[q.dtype],
                            _int32(position, T, device, "position"), T, _raw_stream(device, stream))
         if st != STRATA_OK:

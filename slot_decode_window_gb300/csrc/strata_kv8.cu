@@ -186,6 +186,7 @@ strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_s
   const int width = h->desc.kv_heads * h->desc.head_dim;
   if ((st = check_values(k, k_stride, width, dtype)) != STRATA_OK) return st;
   if ((st = check_values(v, v_stride, width, dtype)) != STRATA_OK) return st;
+  if (k == v) return STRATA_EINVAL;
   if (fault_is("launch")) return STRATA_ECUDA;
   DeviceScope on(h->device);
   if (!on.ok) return launched(cudaErrorInvalidDevice);
@@ -202,7 +203,7 @@ strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int
   const int width = h->desc.heads * h->desc.head_dim;
   if ((st = check_values(q, q_stride, width, dtype)) != STRATA_OK) return st;
   if ((st = check_values(out, out_stride, width, dtype)) != STRATA_OK) return st;
-  if (!std::isfinite(scale)) return STRATA_EINVAL;
+  if (q == out || !std::isfinite(scale)) return STRATA_EINVAL;
   if (fault_is("launch")) return STRATA_ECUDA;
   DeviceScope on(h->device);
   if (!on.ok) return launched(cudaErrorInvalidDevice);

@@ -264,6 +264,10 @@ strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_s
   const int size = dtype == STRATA_F32 ? 4 : 2, qw = d.heads * d.head_dim, kw = d.kv_heads * d.head_dim;
   if (!rows_ok(q, q_stride, qw, size) || !rows_ok(q_out, q_out_stride, qw, size) || !position) return STRATA_EINVAL;
   if (kw > 0 && (!rows_ok(k, k_stride, kw, size) || !rows_ok(k_out, k_out_stride, kw, size))) return STRATA_EINVAL;
+  // an output over its own input row for row, or elsewhere
+  if (T > 1 && q == q_out && q_stride != q_out_stride) return STRATA_EINVAL;
+  if (kw > 0 && (q_out == k_out || q_out == k || k_out == q)) return STRATA_EINVAL;
+  if (kw > 0 && T > 1 && k == k_out && k_stride != k_out_stride) return STRATA_EINVAL;
   if (fault_is("launch")) return STRATA_ECUDA;
   DeviceScope on(h->device);
   if (!on.ok) {

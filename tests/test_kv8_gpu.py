@@ -1,6 +1,10 @@
 """The 8-bit KV caches on the GPU against the fp64 oracle: writing (codes and
 exponents bit for bit), reading back (bit for bit), attention (within the bound
 derived in tests/kv8_helpers.py), refusals, and a run of the calls together."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -570,3 +574,54 @@ def test_a_layer_by_its_parts(B):
     rms = np.sqrt(np.mean(ref["y"] ** 2))
     assert np.abs(y.double().cpu().numpy() - ref["y"])[keep].max() <= 2e-3 * rms
     win.close(), qk.close(), cache.close()
+
+
+def test_refuses_outputs_over_inputs(B):
+    cache = B.KvCache8(1, 1, 2, 2, 64, 40, block=16)
+    fill(cache, "e4m3", 3)
+    rows, _ = rows_of(B, [(2, 0, 6)])
+    q = torch.ones(2, 2, 64, device="cuda")
+    with pytest.raises(B.StrataError):
+        cache.attend(0, q, rows, out=q)
+    with pytest.raises(B.StrataError):
+        cache.read(0, rows, k=q, v=q)
+    cache.sync()
+    assert (q == 1).all()
+
+
+FIRST = """
+import torch
+from slot_decode_window_gb300 import binding as B
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+torch.manual_seed(5)
+caches = [B.KvCache8(1, 1, 8, 2, 64, 200, block=16) for _ in range(2)]
+qk = B.QkNorm(8, 2, 64)
+q, k, v = (torch.randn(40, h, 64, device="cuda") for h in (8, 2, 2))
+pos = torch.arange(40, dtype=torch.int32, device="cuda")
+calls = [(B.KvRows(i32([0, 40]), i32([0]), i32([40]), 40, 40), slice(0, 40)),
+         (B.KvRows(i32([0, 1]), i32([0]), i32([41]), 1, 1), slice(0, 1))]
+def run(cache):
+    out = []
+    qq, kk = qk.forward(q, k, pos)
+    for rows, part in calls:  # the kernels for many rows and for few
+        cache.append(0, kk[part], v[part], rows)
+        out += [cache.attend(0, qq[part], rows), *cache.read(0, rows)]
+    return out
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run(caches[0])
+g.replay()
+want = run(caches[1])
+for c in caches:
+    c.sync()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0].abs().max() > 0
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured(B):
+    """No call has run before the capture: nothing that a launch needs is made by an earlier one."""
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stderr[-2000:]

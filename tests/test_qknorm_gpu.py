@@ -130,3 +130,30 @@ def test_refusals(B):
     assert B.strata_qknorm_forward(qk.handle, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) == B.STRATA_OK  # no rows
     empty = qk.forward(q[:0], k[:0], pos[:0])
     assert empty[0].shape == (0, 2, 64)
+
+
+def test_refuses_overlaps_and_other_devices(B):
+    qk = B.QkNorm(2, 2, 64)
+    wide = torch.zeros(3, 4, 64, device="cuda")
+    q, k, pos = torch.ones(3, 2, 64, device="cuda"), torch.ones(3, 2, 64, device="cuda"), i32([0, 1, 2])
+    for kw in (dict(q_out=k), dict(k_out=q), dict(q_out=wide[:, :2], k_out=wide[:, :2])):
+        with pytest.raises(B.StrataError):
+            qk.forward(q, k, pos, **kw)
+    flat = torch.ones(3 * 256, device="cuda")
+    tight, spread = flat[:384].view(3, 2, 64), flat.view(3, 4, 64)[:, :2]  # one start, two strides
+    for a, b in ((tight, spread), (spread, tight)):
+        with pytest.raises(B.StrataError):
+            qk.forward(a, k, pos, q_out=b)
+        with pytest.raises(B.StrataError):
+            qk.forward(q, a, pos, k_out=b)
+    with pytest.raises(B.StrataError):
+        qk.forward(q, None, pos)
+    torch.cuda.synchronize()
+    assert (q == 1).all() and (k == 1).all() and (flat == 1).all() and (wide == 0).all()
+    one = qk.forward(tight[:1], k[:1], pos[:1], q_out=spread[:1])[0]  # one row has no stride
+    both = qk.forward(q, k, pos, q_out=wide[:, :2], k_out=wide[:, 2:])  # halves of one buffer do not overlap
+    want = qk.forward(q, k, pos)
+    assert torch.equal(one, want[0][:1]) and all(torch.equal(a, b) for a, b in zip(both, want))
+    qk.device += 1  # a handle of another device
+    with pytest.raises(B.StrataError):
+        qk.forward(q, k, pos)
