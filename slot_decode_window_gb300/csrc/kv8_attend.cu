@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       const Item it = next_item(A, pre, seqs, u, hi, seq, start);
       seq = it.seq;
       const long long line = (long long)it.slot * A.C.kv_heads + it.head, row = line * A.C.max_ctx;
-      if (it.u0 < it.u1) {  // what the consumers will load when they come to the item, on its way to L2: q's rows, the first exponents
+      // what the consumers will load when they come to the item, on its way to L2: q's rows, the first exponents
+      if (it.u0 < it.u1) {
         const int size = PARTS == 2 ? 4 : 2, t0 = it.mt * P::kRows / A.group;
         const int t1 = min(it.n, (it.mt * P::kRows + P::kRows - 1) / A.group + 1);
         const char* q = static_cast<const char*>(A.q) +

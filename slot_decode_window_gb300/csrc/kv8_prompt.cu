@@ -514,8 +514,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   float* rf = reinterpret_cast<float*>(smem + P::kRf);
   float4* factors = reinterpret_cast<float4*>(smem + P::kExp);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t *v_full = bars, *v_empty = bars + 4, *k_full = bars + 8, *k_empty = bars + 10, *q_full = bars + 12, *q_empty = bars + 13, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
-           *last = bars + 24, *place_free = bars + 26, *raw_full = bars + 48, *raw_empty = bars + 48 + 2 * kRawBars, *seg_full = bars + 32, *seg_empty = bars + 40;
+  uint64_t *v_full = bars, *v_empty = bars + 4, *k_full = bars + 8, *k_empty = bars + 10, *q_full = bars + 12,
+           *q_empty = bars + 13, *s_full = bars + 16, *p_full = bars + 19, *u_full = bars + 22, *u_empty = bars + 23,
+           *last = bars + 24, *place_free = bars + 26, *seg_full = bars + 32, *seg_empty = bars + 40,
+           *raw_full = bars + 48, *raw_empty = bars + 48 + 2 * kRawBars;
   const Seg* segs = reinterpret_cast<const Seg*>(smem + P::kSegOff);
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
@@ -997,58 +999,58 @@ __global__ void __launch_bounds__(kPThreads, 1)
       PItem item;
       if (!v_side) p_begin(item, A, pre, span[1], span[2]);
       if (lane == 0) {
-      const CUtensorMap* map = v_side ? &vmap : &kmap;
-      uint64_t *raw_f = raw_full + v_side * kRawBars, *raw_e = raw_empty + v_side * kRawBars;
-      uint8_t* dst = smem + P::kRawOff + v_side * kRawStages * P::kRaw;
-      Ring<kSegs> seg;
-      Ring<kRawBars> raw, freed;  // freed: three copies behind, the last user of raw's stage
-      int copies = 0, at = 0;
-      bool ok = true;
-      for (int i = 0; at < n_units; ++i) {
-        if (!v_side) {  // the next segment: K's copies are the first to need it
-          if (i > 0) p_next(item, A, pre, span[1] + at, span[2]);
-          if (i >= kSegs && !(ok = wait_for(&seg_empty[seg.st], seg.ph ^ 1, dead, err))) break;
-          Seg* to = const_cast<Seg*>(segs) + seg.st;
-          to->row0 = item.s.row0, to->n = item.s.n, to->length = item.s.length, to->slot = item.s.slot;
-          to->head = item.head, to->tile = item.tile;
-          to->u0 = item.u0, to->u1 = item.u1, to->units = item.units, to->end = at + item.u1 - item.u0;
-          to->first = item.first;
-          mbar_arrive(&seg_full[seg.st]);
-          // its rows of q on their way to L2
-          const int tokens = min(A.tokens, item.s.n - item.tile * A.tokens), size = A.group * HD * (TWO ? 4 : 2);
-          const char* q = static_cast<const char*>(A.q) + ((item.s.row0 + (long long)item.tile * A.tokens) * A.q_stride +
-                                                           (long long)item.head * A.group * HD) * (TWO ? 4 : 2);
+        const CUtensorMap* map = v_side ? &vmap : &kmap;
+        uint64_t *raw_f = raw_full + v_side * kRawBars, *raw_e = raw_empty + v_side * kRawBars;
+        uint8_t* dst = smem + P::kRawOff + v_side * kRawStages * P::kRaw;
+        Ring<kSegs> seg;
+        Ring<kRawBars> raw, freed;  // freed: three copies behind, the last user of raw's stage
+        int copies = 0, at = 0;
+        bool ok = true;
+        for (int i = 0; at < n_units; ++i) {
+          if (!v_side) {  // the next segment: K's copies are the first to need it
+            if (i > 0) p_next(item, A, pre, span[1] + at, span[2]);
+            if (i >= kSegs && !(ok = wait_for(&seg_empty[seg.st], seg.ph ^ 1, dead, err))) break;
+            Seg* to = const_cast<Seg*>(segs) + seg.st;
+            to->row0 = item.s.row0, to->n = item.s.n, to->length = item.s.length, to->slot = item.s.slot;
+            to->head = item.head, to->tile = item.tile;
+            to->u0 = item.u0, to->u1 = item.u1, to->units = item.units, to->end = at + item.u1 - item.u0;
+            to->first = item.first;
+            mbar_arrive(&seg_full[seg.st]);
+            // its rows of q on their way to L2
+            const int tokens = min(A.tokens, item.s.n - item.tile * A.tokens), size = A.group * HD * (TWO ? 4 : 2);
+            const char* q = static_cast<const char*>(A.q) + ((item.s.row0 + (long long)item.tile * A.tokens) * A.q_stride +
+                                                             (long long)item.head * A.group * HD) * (TWO ? 4 : 2);
 #pragma unroll 1
-          for (int y = 0; y < tokens; ++y, q += A.q_stride * (TWO ? 4 : 2))
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(size) : "memory");
-        } else if (!(ok = wait_for(&seg_full[seg.st], seg.ph, dead, err))) {
-          break;
-        }
-        const Seg* it = segs + seg.st;
-        const int y0 = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
-        const int x1 = 2 * it->u1, length = it->length;
-        for (int x = 2 * it->u0; x < x1; ++x) {
-          if (copies >= kRawStages) {
-            if (!(ok = wait_for(&raw_e[freed.st], freed.ph, dead, err))) break;
-            freed.step();
+            for (int y = 0; y < tokens; ++y, q += A.q_stride * (TWO ? 4 : 2))
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(size) : "memory");
+          } else if (!(ok = wait_for(&seg_full[seg.st], seg.ph, dead, err))) {
+            break;
           }
-          // a half that holds no position of the sequence is not needed (its codes become 0)
-          if (x * 64 < length) {
-            mbar_arrive_expect_tx(&raw_f[raw.st], P::kRaw);
-            p_tma_3d(dst + raw.st % kRawStages * P::kRaw, map, 0, y0 + x * 64, A.layer, &raw_f[raw.st]);
-          } else {
-            mbar_arrive(&raw_f[raw.st]);
+          const Seg* it = segs + seg.st;
+          const int y0 = (int)(((long long)it->slot * A.C.kv_heads + it->head) * A.C.max_ctx);
+          const int x1 = 2 * it->u1, length = it->length;
+          for (int x = 2 * it->u0; x < x1; ++x) {
+            if (copies >= kRawStages) {
+              if (!(ok = wait_for(&raw_e[freed.st], freed.ph, dead, err))) break;
+              freed.step();
+            }
+            // a half that holds no position of the sequence is not needed (its codes become 0)
+            if (x * 64 < length) {
+              mbar_arrive_expect_tx(&raw_f[raw.st], P::kRaw);
+              p_tma_3d(dst + raw.st % kRawStages * P::kRaw, map, 0, y0 + x * 64, A.layer, &raw_f[raw.st]);
+            } else {
+              mbar_arrive(&raw_f[raw.st]);
+            }
+            raw.step();
+            ++copies;
           }
-          raw.step();
-          ++copies;
+          if (!ok) break;
+          at = it->end;
+          mbar_arrive(&seg_empty[seg.st]);
+          seg.step();
         }
-        if (!ok) break;
-        at = it->end;
-        mbar_arrive(&seg_empty[seg.st]);
-        seg.step();
-      }
-      for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
-        mbar_wait(&raw_f[i % kRawBars], (i / kRawBars) & 1, err);
+        for (int i = max(0, copies - kRawStages); i < copies; ++i)  // the copies have landed before the CTA ends
+          mbar_wait(&raw_f[i % kRawBars], (i / kRawBars) & 1, err);
       }
     }
     __syncwarp();
