@@ -68,6 +68,14 @@ __device__ __forceinline__ int kv8_least_exp(float a, int format) {
   return min(max(e, kKv8EMin), kKv8EMax);
 }
 
+// What the products of a row of q (brought to [1, 2) by 1 / power) with a block's codes are multiplied by, besides the
+// block's 2^ek, to be scores in base 2.  Products are below 2^17 and 2^ek at most 2^47, so with a factor of at most 2^63
+// every score of a row without infinities or NaN is finite, and so is zero times the factors.  Rows beyond it (scale |q|
+// of some 1e18 and more) keep the order of their scores and differences that are far larger than the softmax tells apart.
+__device__ __forceinline__ float kv8_row_factor(float scale2, float power) {
+  return fminf(fmaxf(scale2 * power, -0x1p63f), 0x1p63f);
+}
+
 // Two e4m3 codes to f16x2 and back (round to nearest even, saturating).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;

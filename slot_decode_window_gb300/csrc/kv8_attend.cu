@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     int u0, u1, length, min_pos, cost;
     long long line;
     uint32_t qb[PARTS][NT][kSteps][2];  // q as the B operand
-    float rf[NT][2];                    // powers of two of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
+    float rf[NT][2];                    // score factors of rows 8 nt + 2c and + 1 (the columns of S^T that this lane holds)
     int lim[NT][2];                     // positions that they see
     {
       const Item it = next_item(A, pre, seqs, u, hi, seq, start);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int r = 8 * nt + 2 * c + y;
-          rf[nt][y] = pow2i(__shfl_sync(0xFFFFFFFFu, e, (2 * c + y) * 4));
+          rf[nt][y] = kv8_row_factor(A.scale2, pow2i(__shfl_sync(0xFFFFFFFFu, e, (2 * c + y) * 4)));
           lim[nt][y] = r < rows ? max(0, p_first + (it.mt * P::kRows + r) / A.group + 1) : 0;
         }
 #pragma unroll
@@ -447,6 +447,8 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     for (int i = 0; i < kSteps; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    // m: what the weights are relative to, kWeightTop below the maximum of t.  Rounded up, so that no weight exceeds
+    // 2^kWeightTop where a step of m is larger than that (from m = 2^25 on; f16 holds 2^kWeightTop but not four times it).
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
               for (int nt = 0; nt < NT; ++nt) mma_acc(sc[b][nt], a, qb[part][nt][y][0], qb[part][nt][y][1]);
           }
           // t = score * log2(e) + ev, masked where a row does not see the position
-          const float kf = A.scale2 * pow2i(ek[b]), evf = (float)ev[b];
+          const float kf = pow2i(ek[b]), evf = (float)ev[b];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-            mx[nt][y] = v;
+            mx[nt][y] = v = __fsub_ru(v, kWeightTop);
             grew |= v > m[nt][y];
           }
         if (__any_sync(0xFFFFFFFFu, grew)) {
@@ -542,8 +544,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
           for (int nt = 0; nt < NT; ++nt) {
             float w[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = ex2(sc[b][nt][y] + (m[nt][y & 1] == -INFINITY ? 0.f : kWeightTop - m[nt][y & 1]));
+            for (int y = 0; y < 4; ++y) w[y] = ex2(sc[b][nt][y] - (m[nt][y & 1] == -INFINITY ? 0.f : m[nt][y & 1]));
             l[nt][0] = fmaf(w[0] + w[2], back, l[nt][0]), l[nt][1] = fmaf(w[1] + w[3], back, l[nt][1]);
             pb[0][nt][0] = turn(pack_half2(w[0], w[1])), pb[0][nt][1] = turn(pack_half2(w[2], w[3]));
             if constexpr (PARTS == 2) {

@@ -49,7 +49,8 @@ constexpr int kRegs = 80;        // registers per thread at launch; the roles' s
 constexpr int kSegs = 8;         // slots of the segment list
 constexpr int kMmaWarp = 20, kTmaWarp = 22;  // products: 20 S, 21 U; TMA: 22 K, 23 V
 constexpr float kPWeightTop = 14.f;
-constexpr float kLeastFactor = 1e-37f;
+constexpr float kLeastFactor = 0x1p-100f;
+constexpr float kFar = 4096.f;   // rows whose weights need a larger constant than this take unit_shift
 constexpr int kRawStages = 3;      // of half a unit's codes, for K and for V
 // Barriers of a stage for each half, so that a warp, which takes only its half's copies, waits for every phase of the
 // barriers that it reads (one barrier for both would let it take the other half's earlier phase for its own).
@@ -443,6 +444,27 @@ __device__ __forceinline__ void unit_mask(uint32_t s_addr, int left) {
   tc_wait_st();
 }
 
+// The scores of a row whose maximum is far from zero become (t - m - ev) / kLeastFactor, which unit_softmax turns into
+// t - m when it goes on with a factor and a maximum of zero.  For the other rows it adds ev, kPWeightTop and -m in one
+// rounded constant, whose half step grows with m: from m = 2^25 on it would lift a weight past f16's range, and units
+// would disagree on what their weights are relative to.  Not inlined: no trained model's scores come here, and in the
+// hot code it cost 2 % of a prompt (as it is: 634 us against 626 for 8191 rows).
+__device__ __noinline__ void unit_shift(uint32_t s_addr, const float4* fac, float f_row, bool far, float m) {
+#pragma unroll 1
+  for (int ch = 0; ch < 8; ++ch) {
+    uint32_t r[16];
+    tc_ld16(s_addr + ch * 16, r);
+    const float4 f = fac[ch];
+    const float k = fmaxf(f.x * f_row, kLeastFactor);
+    tc_wait_ld(r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (far) r[i] = __float_as_uint((fmaf(__uint_as_float(r[i]), k, f.y) - m - f.y) * (1.f / kLeastFactor));
+    tc_st16(s_addr + ch * 16, r);
+  }
+  tc_wait_st();
+}
+
 // A row's softmax over one unit: the 128 scores at s_addr become weights (16-bit
 // parts) relative to the unit's maximum m; l is their sum over 2^ev.  The
 // chunks are a rolled loop, and there is one copy of it: the hot code of all
@@ -469,7 +491,12 @@ __device__ __forceinline__ void unit_softmax(uint32_t s_addr, const float4* fac,
     m = max3(m, fmaf(fmaxf(a0, a1), fmaxf(f0.x * f_row, kLeastFactor), f0.y),
              fmaf(fmaxf(b0, b1), fmaxf(f1.x * f_row, kLeastFactor), f1.y));
   }
-  const float z = m == -INFINITY ? 0.f : kPWeightTop - m;
+  float z = m == -INFINITY ? 0.f : kPWeightTop - m;
+  const bool far = fabsf(z) >= kFar;
+  if (__builtin_expect(__any_sync(0xFFFFFFFFu, far), 0)) {
+    unit_shift(s_addr, fac, f_row, far, m);
+    if (far) f_row = 0.f, z = kPWeightTop;
+  }
   l = 0.f;
 #pragma unroll 1
   for (int ch = 0; ch < 8; ++ch) {
@@ -624,8 +651,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int at = n + x - u0;
         if (!(ok = wait_warp(&s_full[place.st], place.ph, dead, err))) break;
         tc_fence_after();
-        if (!have) f_row = rf[(item & 3) * kPRows + row], have = true;
-        const float4* fac = factors + (at & 7) * 8;  // per 16 positions: scale 2^ek, ev, 2^-ev
+        if (!have) f_row = kv8_row_factor(A.scale2, rf[(item & 3) * kPRows + row]), have = true;
+        const float4* fac = factors + (at & 7) * 8;  // per 16 positions: 2^ek, ev, 2^-ev
         const int left = lim - x * kPUnit;  // positions of the unit that the row sees
         const bool masked = (x + 1) * kPUnit > all;
         float m, l;
@@ -897,7 +924,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (at >= places && !(ok = wait_warp(v_side ? &v_empty[TWO ? half : st] : &k_empty[st], ph ^ 1, dead, err))) break;
         if (!v_side && t < 8) {
           const int ek = kv8_exp((uint8_t)e_next), ev = kv8_exp((uint8_t)(e_next >> 8));
-          factors[(at & 7) * 8 + t] = make_float4(A.scale2 * pow2i(ek), (float)ev, pow2i(-ev), 0.f);
+          factors[(at & 7) * 8 + t] = make_float4(pow2i(ek), (float)ev, pow2i(-ev), 0.f);
         }
         if (!(ok = wait_warp(&raw_f[raw.st], raw.ph, dead, err))) break;
         half_tile(tiles + st * P::kTile + half * (64 * 128), length - p);

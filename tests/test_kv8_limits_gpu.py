@@ -1,0 +1,86 @@
+"""The 8-bit caches' calls at the ends of what their documentation allows: scores of any size, sums over long caches,
+batches of very unlike sequences, sequences that are left out, and a workspace that a forbidden overlap disturbed."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv8 as ok
+from tests.kv8_helpers import DTYPES, check_attend, fill, half_step, held, i32, rows_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from slot_decode_window_gb300 import binding, build
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    binding.load()
+    return binding
+
+
+def _randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+@pytest.mark.parametrize("n", [2, 3, 40])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("way", [1, -1])
+@pytest.mark.parametrize("power", [14, 20, 24, 25, 26, 27, 28, 30, 60, 90])
+def test_attend_scores_of_any_size(B, n, dtype, way, power):
+    """Three equal keys, in units of their own, score 2^power times what keys do otherwise and far above the rest (way
+    = -1: all scores are negative, theirs least so): a row is the mean of their values.
+
+    Bound: equal scores give equal weights, whatever they are, and every other weight is below 2^-60 of them, so what
+    is left are f32 roundings (the sums, the joins, exp2 and the quotient: under 16 of 2^-24 relative to the values'
+    mean magnitude) and the result's own."""
+    heads, kvh, hd, block, length = 4, 2, 128, 32, 300
+    cache = B.KvCache8(1, 1, heads, kvh, hd, length, block=block)
+    fill(cache, "e4m3", 1)
+    u = _randn(1, kvh, hd)
+    k, v = 0.1 * _randn(2, length, kvh, hd), _randn(3, length, kvh, hd).clamp(-3.9, 3.9)
+    k += 0 if way > 0 else -3 * u
+    same = [5, 130, 250]
+    k[same] = way * u  # (way = -1: -u scores above -3 u)
+    k.clamp_(-15.5, 15.5)
+    k[..., 0] = 16.0  # every block has the same exponent
+    v[..., 0] = 4.0
+    cache.append(0, k, v, rows_of(B, [(length, 0, length)])[0])
+    state = held(cache, 0, "e4m3")
+    q = u.repeat_interleave(heads // kvh, 0) + 0.02 * _randn(4, n, heads, hd)
+    q[..., 0] = 0
+    q = q.to(DTYPES[dtype])
+    scale = 2.0 ** power
+    rows, _ = rows_of(B, [(n, 0, length)])
+    out = cache.attend(0, q, rows, scale=scale)
+    again = cache.attend(0, -q, rows, scale=-scale)
+    cache.sync()
+    assert torch.equal(out, again)
+    kk, vv = ok.held_values(state[0], state[1], 0, 0, length, block), ok.held_values(state[2], state[3], 0, 0, length, block)
+    got, qq = out.double().cpu().numpy(), q.double().cpu().numpy()
+    for r in range(n):
+        for h in range(heads):
+            s = scale * np.log2(np.e) * (kk[h // 2, :length - n + r + 1] @ qq[r, h])
+            rest = np.delete(s, same)
+            assert (s[same] == s[5]).all() and s[5] - rest.max() > 60 and (way > 0 or s.max() < 0)
+            want, size = vv[h // 2, same].mean(0), np.abs(vv[h // 2, same]).mean(0)
+            off = 16 * 2.0 ** -24 * size
+            bound = off + half_step(q.dtype) * (np.abs(want) + off)
+            assert (np.abs(got[r, h] - want) <= bound).all(), (r, h, np.abs(got[r, h] - want).max())
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_attend_zero_keys_under_the_largest_factors(B, n):
+    """Keys of zero in blocks of the largest exponent, queries near the end of f32's range: every score is 0, and the
+    product of the powers of two that it is multiplied with does not fit f32."""
+    cache = B.KvCache8(1, 1, 4, 2, 128, 200, block=16)
+    fill(cache, "e4m3", 2)
+    cache.k.zero_()
+    cache.k_exp.fill_(ok.E_MAX + ok.BIAS)
+    state = held(cache, 0, "e4m3")
+    rows, seqs = rows_of(B, [(n, 0, 200)])
+    for scale in (1.0, -3.0):
+        q = _randn(5, n, 4, 128) * 2.0 ** 110
+        out = cache.attend(0, q, rows, scale=scale)
+        cache.sync()
+        check_attend(out, q, state, seqs, 16, abs(scale))
