@@ -47,6 +47,7 @@ template <int HD, int NT, int PARTS> struct SplitPlan {
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kSlabs = 128 / HD;                   // of 16 positions: a warp's part of a unit
   static constexpr int kUnit = 64 * kSlabs;                 // positions of a ring stage
+  static constexpr int kFold = 16 / kSlabs;                 // units of a warp between folds of O (f32 rows)
   static constexpr int kTile = kUnit * HD;                  // bytes of one unit's K (or V) codes: 8 KB
   static constexpr int kStages = NT == 1 ? 9 : 8;           // 144 or 128 KB in flight; a multiple of kGroups
   static constexpr int kJoin = kWarps * kRows * (HD + 4) * 4;  // the warps' O (rows padded by 4 floats)
@@ -452,6 +453,39 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    constexpr int kRowF = HD + 4;
+    float* own = join + warp * P::kRows * kRowF;
+    // f32 rows: every kFold units O goes to the warp's place of the join, relative to the m that stands behind each row
+    // there, and starts anew.  The tensor core's adds cut off: a sum left in one accumulator is up to 7e-8 short for each
+    // of them, without end (a CTA's 131071 positions came out 1e-4 short, folded 2e-7 at any length).  64 f32 rows over
+    // 4 k to 8.2 k positions: 173.6 us, 164.4 without; folded every 8 units 176.1, every 4 181.3, each unit's sum added by
+    // itself 195.1.  16-bit rows, with half the adds, stay as they are: their sums are 5e-5 short after 131071 positions
+    // in one CTA and half a step of f16 short after 1.3 million, and even folds 256 units apart cost 64 bf16 rows 4 %.
+    int held = 0;  // units that this warp has seen of the item
+    auto fold = [&](bool first) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float* row = own + (8 * nt + 2 * c + y) * kRowF;
+          const float then = first ? -INFINITY : row[HD], a = then == m[nt][y] ? 1.f : ex2(then - m[nt][y]);
+#pragma unroll
+          for (int i = 0; i < kSteps; i += 2) {
+            float4* to = reinterpret_cast<float4*>(row + g * (HD / 8) + 2 * i);
+            const float4 v = first ? make_float4(0, 0, 0, 0) : *to;
+            *to = make_float4(fmaf(v.x, a, o[i][nt][y]), fmaf(v.y, a, o[i][nt][y + 2]), fmaf(v.z, a, o[i + 1][nt][y]),
+                              fmaf(v.w, a, o[i + 1][nt][y + 2]));
+            o[i][nt][y] = o[i][nt][y + 2] = o[i + 1][nt][y] = o[i + 1][nt][y + 2] = 0.f;
+          }
+        }
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (g == 0) own[(8 * nt + 2 * c + y) * kRowF + HD] = m[nt][y];
+      __syncwarp();
+    };
 
 #pragma unroll 1
     for (; x < u1; x += P::kGroups) {
@@ -592,12 +626,13 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
+      if constexpr (PARTS == 2)
+        if (++held % P::kFold == 0) fold(held == P::kFold);
     }
     n += u1 - u0;
 
     // ---- join the warps ----
-    constexpr int kRowF = HD + 4;
-    float* own = join + warp * P::kRows * kRowF;
+    if constexpr (PARTS == 2) fold(held < P::kFold);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -609,7 +644,7 @@ __global__ void __launch_bounds__(SplitPlan<HD, NT, PARTS>::kThreads, 1)
         const int r = 8 * nt + 2 * c + y;
         if (g == 0) ml[(warp * P::kRows + r) * 2] = m[nt][y], ml[(warp * P::kRows + r) * 2 + 1] = v;
 #pragma unroll
-        for (int i = 0; i < kSteps; i += 2)
+        for (int i = 0; PARTS == 1 && i < kSteps; i += 2)
           *reinterpret_cast<float4*>(own + r * kRowF + g * (HD / 8) + 2 * i) =
               make_float4(o[i][nt][y], o[i][nt][y + 2], o[i + 1][nt][y], o[i + 1][nt][y + 2]);
       }

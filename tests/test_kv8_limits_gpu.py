@@ -84,3 +84,40 @@ def test_attend_zero_keys_under_the_largest_factors(B, n):
         out = cache.attend(0, q, rows, scale=scale)
         cache.sync()
         check_attend(out, q, state, seqs, 16, abs(scale))
+
+
+@pytest.mark.parametrize("fmt,kvh,group,n,hd", [("e4m3", 8, 1, 1, 128), ("int8", 4, 8, 2, 128), ("int8", 8, 1, 1, 64),
+                                                ("e4m3", 4, 8, 2, 64)])
+def test_attend_long_sums_of_f32_rows_do_not_drift(B, fmt, kvh, group, n, hd):
+    """More items than CTAs, each of 131071 positions, so that whole items are summed by one CTA: positive values under
+    nearly equal weights, whose mean error over rows and dims shows what sums lose on one side.
+
+    Bound: products that cut off lose under 2^-23 of a sum at each of the 32 adds (16 times 16 positions, two parts)
+    that it stays in one accumulator, half of that for a sum that grows evenly: 16 * 2^-23.  What rounds errs to
+    both sides: the denominator's adds (one a unit of 64 positions and warp, at most 12 warps a CTA in groups of 4) by
+    less than 2^-24 of the sum each, independently for each of the rows looked at; six standard deviations of their mean."""
+    length, n_seq, heads = 131071, 152, kvh * group
+    cache = B.KvCache8(1, 2, heads, kvh, hd, length, block=64, format=fmt)
+    fill(cache, fmt, 3, spread=0.0)
+    cache.v &= 0x7F
+    q = 0.02 * _randn(6, n_seq * n, heads, hd)
+    rows, _ = rows_of(B, [(n, i % 2, length) for i in range(n_seq)])
+    out = cache.attend(0, q, rows)
+    cache.sync()
+    off, seqs = [], (0, 51, 76, 151)
+    for h in range(kvh):
+        for slot in range(2):
+            k, v = (torch.from_numpy(ok.held_values(ok.code_values(c[0, :, h:h + 1].cpu().numpy(), fmt),
+                                                    e[0, :, h:h + 1].cpu().numpy().astype(int) - ok.BIAS, slot, 0, length, 64)[0]).cuda()
+                    for c, e in ((cache.k, cache.k_exp), (cache.v, cache.v_exp)))
+            for i in seqs:
+                if i % 2 != slot:
+                    continue
+                for r in range(n):
+                    at, seen = i * n + r, length - n + r + 1
+                    p = torch.softmax(q[at, h * group:(h + 1) * group].double() @ k[:seen].T * hd ** -0.5, -1)
+                    want = p @ v[:seen]
+                    off.append(((out[at, h * group:(h + 1) * group].double() - want) / want).mean(-1))
+    off = torch.cat(off)
+    units = length / 64 / (3 if n * group <= 8 else 2)
+    assert abs(off.mean().item()) <= 16 * 2.0 ** -23 + 6 * 2.0 ** -24 * (units / len(off)) ** 0.5, off.mean().item()
