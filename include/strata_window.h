@@ -626,8 +626,9 @@ strata_status strata_kv8_create(const strata_kv8_desc* desc, const strata_kv8_ca
  * (rejected proposals written over) keeps the block's exponent.
  * A NaN is held as 0 and an infinity as the largest code; either makes the
  * next sync report EDEVICE.  Sequences of one call name different slots: of
- * sequences with rows that name the same slot the first is written, the others
- * are left out (EDEVICE); so is a sequence with length[i] below its rows. */
+ * sequences with rows that name the same slot the first that is not left out
+ * for another reason is written, the others are left out (EDEVICE).  A sequence
+ * with length[i] below its rows is left out too. */
 strata_status strata_kv8_append(strata_kv8* h, int32_t layer, const void* k, int64_t k_stride, const void* v,
                                 int64_t v_stride, int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream);
 

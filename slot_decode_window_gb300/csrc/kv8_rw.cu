@@ -83,10 +83,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
   uint8_t* ep = (is_v ? C.v_exp : C.k_exp) + line * C.n_blocks + blk;
   const int held = lo - (blk << C.block_log2);
   const int e_held = held > 0 ? kv8_exp(*ep) : kKv8EMin;
-  // an earlier sequence with rows that names the same slot owns it
+  // an earlier sequence with rows that names the same slot owns it, unless it is itself left out
   int taken = 0;
   for (int j = threadIdx.x; j < i; j += kThreads)
-    if (R.slot[j] == q.slot && R.row_start[j + 1] > R.row_start[j]) taken = 1;
+    if (R.slot[j] == q.slot) {
+      const Kv8Seq other = kv8_seq(R, C, j);
+      if (other.held_ok && other.n > 0 && other.length >= other.n) taken = 1;
+    }
   unsigned a = 0;
 #pragma unroll
   for (int p = 0; p < NP; ++p) a = Abs<T>::most(a, raw[p]);

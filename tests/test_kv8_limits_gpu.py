@@ -121,3 +121,27 @@ def test_attend_long_sums_of_f32_rows_do_not_drift(B, fmt, kvh, group, n, hd):
     off = torch.cat(off)
     units = length / 64 / (3 if n * group <= 8 else 2)
     assert abs(off.mean().item()) <= 16 * 2.0 ** -23 + 6 * 2.0 ** -24 * (units / len(off)) ** 0.5, off.mean().item()
+
+
+def _reported(B, cache):
+    with pytest.raises(B.StrataError) as e:
+        cache.sync()
+    assert e.value.status == B.STRATA_EDEVICE
+    cache.sync()  # reported once
+
+
+@pytest.mark.parametrize("start,length", [([0, 2, 4], [41, 9]), ([0, 2, 4], [-1, 9]), ([0, 2, 4], [1, 9]),
+                                          ([0, 3, 5], [9, 9]), ([4, 2, 4], [9, 9])])
+def test_append_a_sequence_that_is_left_out_takes_no_slot(B, start, length):
+    """The first of two sequences of one slot has a length out of range or below its rows, too many rows, or rows out of
+    order: the second is written."""
+    cache = B.KvCache8(1, 2, 4, 2, 64, 40, block=16)
+    fill(cache, "e4m3", 22)
+    state = held(cache, 0, "e4m3")
+    k, v = _randn(7, 6, 2, 64), _randn(8, 6, 2, 64)
+    cache.append(0, k, v, B.KvRows(i32(start), i32([1, 1]), i32(length), n_rows=6, max_rows=2))
+    _reported(B, cache)
+    for c, e, x in ((state[0], state[1], k), (state[2], state[3], v)):
+        ok.append(c, e, x.cpu().numpy(), [(start[1], start[2] - start[1], 1, length[1])], 16, "e4m3")
+    for got, want in zip(held(cache, 0, "e4m3"), state):
+        np.testing.assert_array_equal(got, want)
