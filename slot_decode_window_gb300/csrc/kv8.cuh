@@ -53,6 +53,53 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Rows& R, const Kv8Dev& C, int
   return s;
 }
 
+// Work that is cut into pieces of a sequence: pieces(n) of n rows, at least one (so that some CTA looks at every
+// sequence).  A launch either has as many places for each sequence as the longest may need, or one list of all
+// sequences' pieces.  kv8_find, for a whole block of kThreads: the sequence and the piece at place u of the list (seq < 0
+// past its end), and the list's length.
+struct Kv8Piece { int seq, at; long long all; };
+template <int kThreads, class Pieces>
+__device__ __forceinline__ Kv8Piece kv8_find(const Kv8Rows& R, long long u, Pieces pieces) {
+  static_assert(4 * kThreads >= kKv8MaxSeq, "sequences per thread");
+  __shared__ long long warp_sums[kThreads / 32];
+  __shared__ Kv8Piece found;
+  const int share = (R.n_seq + kThreads - 1) / kThreads, first = threadIdx.x * share, lane = threadIdx.x & 31;
+  long long count[4], sum = 0;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const int i = first + y;
+    count[y] = 0;
+    if (y < share && i < R.n_seq) {
+      const int a = R.row_start[i], b = R.row_start[i + 1];
+      count[y] = a >= 0 && a <= b && b <= R.n_rows && b - a <= R.max_rows ? max(1LL, pieces(b - a)) : 1;
+    }
+    sum += count[y];
+  }
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += t;
+  }
+  if (threadIdx.x == kThreads - 1) found.seq = -1;
+  if (lane == 31) warp_sums[threadIdx.x >> 5] = upto;
+  __syncthreads();
+  long long before = upto - sum;
+  for (int w = 0; w < (int)threadIdx.x >> 5; ++w) before += warp_sums[w];
+  if (threadIdx.x == kThreads - 1) found.all = before + sum;
+  if (u >= before && u < before + sum) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if (u >= before && u < before + count[y]) found.seq = first + y, found.at = (int)(u - before);
+      before += count[y];
+    }
+  }
+  __syncthreads();
+  const Kv8Piece p = found;
+  __syncthreads();  // the next call writes again
+  return p;
+}
+
 __device__ __forceinline__ int kv8_exp(uint8_t byte) { return min(max((int)byte - kKv8Bias, kKv8EMin), kKv8EMax); }
 
 // 2^e for e in [-126, 127].

@@ -39,18 +39,11 @@ template <> struct Abs<__half> {
 // issue bound (68% of the slots), so magnitudes are taken two at a time and what is not finite has a path of its own
 // (43.1 us before both).  A window's rows: 2.2 us.
 template <typename T, int NP>
-__global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, const T* __restrict__ kin,
-                                                          long long k_stride, const T* __restrict__ vin,
-                                                          long long v_stride, int nb) {
+__device__ __forceinline__ void append_block(const Kv8Dev& C, const Kv8Rows& R, const T* __restrict__ kin,
+                                             long long k_stride, const T* __restrict__ vin, long long v_stride, int i,
+                                             int b_at, int head, bool is_v) {
   constexpr int kPer = Val<T>::kPer;
   __shared__ unsigned red[kThreads / 32];
-  int id = blockIdx.x;
-  const int b_at = id % nb;
-  id /= nb;
-  const int head = id % C.kv_heads;
-  id /= C.kv_heads;
-  const bool is_v = id & 1;
-  const int i = id >> 1;
   const Kv8Seq q = kv8_seq(R, C, i);
   const bool lead = threadIdx.x == 0 && b_at == 0 && head == 0 && !is_v;
   if (!q.held_ok || q.length < q.n) {
@@ -157,21 +150,66 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, c
   }
 }
 
+// Blocks that n consecutive positions can touch.
+__host__ __device__ constexpr long long append_pieces(int n, int B) { return n > 0 ? (n + (long long)B - 2) / B + 1 : 0; }
+
+// kList: the CTAs share the list of all sequences' blocks; else each sequence has nb places.
+template <typename T, int NP, bool kList>
+__global__ void __launch_bounds__(kThreads) append_kernel(Kv8Dev C, Kv8Rows R, const T* __restrict__ kin,
+                                                          long long k_stride, const T* __restrict__ vin,
+                                                          long long v_stride, int nb) {
+  const int lines = 2 * C.kv_heads;  // keys and values of each head
+  if constexpr (kList) {
+    for (long long id = blockIdx.x;; id += gridDim.x) {
+      const Kv8Piece p = kv8_find<kThreads>(R, id / lines, [&](int n) { return append_pieces(n, 1 << C.block_log2); });
+      if (p.seq < 0) return;
+      const int line = (int)(id % lines);
+      append_block<T, NP>(C, R, kin, k_stride, vin, v_stride, p.seq, p.at, line >> 1, line & 1);
+      if (id + gridDim.x >= p.all * lines) return;
+    }
+  } else {
+    int id = blockIdx.x;
+    const int b_at = id % nb;
+    id /= nb;
+    const int head = id % C.kv_heads;
+    id /= C.kv_heads;
+    append_block<T, NP>(C, R, kin, k_stride, vin, v_stride, id >> 1, b_at, head, id & 1);
+  }
+}
+
+// CTAs of a launch over pieces of sequences: `each` places for every sequence, or a list of `most` pieces (which the
+// rows cannot need more of unless sequences lie over one another; the CTAs go on until the list's end).  A sequence's
+// place is found without a search, so short and even batches take the first; the second once the first would start
+// more than twice the CTAs.  8 heads of 128, bf16, blocks of 16, places / list in us: 64 sequences of 256 rows, append 46 /
+// 73 and read 17.5 / 23.5; 63 of 256 and one of 512, 60 / 74 and 21 / 24; one of 1024 (2.9 and 3.9 times the CTAs), 88 /
+// 77 and 30 / 25.5; 63 single rows and one prompt of 8129, 437 / 42 and 138 / 17; 1023 and one of 100000, read 25 ms /
+// 205 us.
+constexpr long long kMaxGrid = 0x7FFFFFFF;
+struct PieceGrid { bool list; unsigned grid; };
+PieceGrid piece_grid(const Kv8Dev& C, const Kv8Rows& R, long long each, long long most) {
+  const long long lines = 2LL * C.kv_heads;
+  const bool list = R.n_seq * each > 2 * most || lines * R.n_seq * each > kMaxGrid;
+  return {list, (unsigned)min(lines * (list ? most : R.n_seq * each), kMaxGrid)};
+}
+
 template <typename T>
 cudaError_t append_typed(const Kv8Dev& C, const Kv8Rows& R, const void* k, long long k_stride, const void* v,
                          long long v_stride, cudaStream_t s) {
-  // blocks that max_rows consecutive positions can touch
   const int B = 1 << C.block_log2;
-  const int nb = (min(R.max_rows, C.max_ctx) + B - 2) / B + 1;
-  const long long grid = 2LL * R.n_seq * C.kv_heads * nb;
-  if (grid > 0x7FFFFFFFLL) return cudaErrorNotSupported;
+  const int nb = (int)append_pieces(min(R.max_rows, C.max_ctx), B);
+  const PieceGrid g = piece_grid(C, R, nb, R.n_rows / B + 2LL * R.n_seq);
   const T *kk = static_cast<const T*>(k), *vv = static_cast<const T*>(v);
   // passes of the CTA over the tokens that a block can gain in this call
   const int most = min(B, R.max_rows);
   const int per_pass = kThreads * Val<T>::kPer / C.head_dim;
   const int np = (most + per_pass - 1) / per_pass;
-#define STRATA_APPEND(NP) \
-  append_kernel<T, NP><<<(unsigned)grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nb)
+#define STRATA_APPEND(NP)                                                                              \
+  do {                                                                                                 \
+    if (g.list)                                                                                        \
+      append_kernel<T, NP, true><<<g.grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nb);    \
+    else                                                                                               \
+      append_kernel<T, NP, false><<<g.grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nb);   \
+  } while (0)
   if (np <= 1)
     STRATA_APPEND(1);
   else if (np <= 2)
@@ -195,16 +233,10 @@ cudaError_t append_typed(const Kv8Dev& C, const Kv8Rows& R, const void* k, long 
 constexpr int kReadPasses = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) read_kernel(Kv8Dev C, Kv8Rows R, T* __restrict__ kout, long long k_stride,
-                                                        T* __restrict__ vout, long long v_stride, int nchunk) {
+__device__ __forceinline__ void read_chunk(const Kv8Dev& C, const Kv8Rows& R, T* __restrict__ kout, long long k_stride,
+                                           T* __restrict__ vout, long long v_stride, int i, int chunk, int head,
+                                           bool is_v) {
   constexpr int kPer = Val<T>::kPer;
-  int id = blockIdx.x;
-  const int chunk = id % nchunk;
-  id /= nchunk;
-  const int head = id % C.kv_heads;
-  id /= C.kv_heads;
-  const bool is_v = id & 1;
-  const int i = id >> 1;
   const Kv8Seq q = kv8_seq(R, C, i);
   const bool ok = q.held_ok && q.length >= q.n;
   if (!ok && threadIdx.x == 0 && chunk == 0 && head == 0 && !is_v) atomicOr(C.err, kErrIndex);
@@ -254,15 +286,41 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Kv8Dev C, Kv8Rows R, T* 
   }
 }
 
+// kList: as append_kernel's.
+template <typename T, bool kList>
+__global__ void __launch_bounds__(kThreads) read_kernel(Kv8Dev C, Kv8Rows R, T* __restrict__ kout, long long k_stride,
+                                                        T* __restrict__ vout, long long v_stride, int nchunk) {
+  const int lines = 2 * C.kv_heads;
+  if constexpr (kList) {
+    const int per_cta = kThreads * Val<T>::kPer / C.head_dim * kReadPasses;
+    for (long long id = blockIdx.x;; id += gridDim.x) {
+      const Kv8Piece p = kv8_find<kThreads>(R, id / lines, [&](int n) { return (n + (long long)per_cta - 1) / per_cta; });
+      if (p.seq < 0) return;
+      const int line = (int)(id % lines);
+      read_chunk<T>(C, R, kout, k_stride, vout, v_stride, p.seq, p.at, line >> 1, line & 1);
+      if (id + gridDim.x >= p.all * lines) return;
+    }
+  } else {
+    int id = blockIdx.x;
+    const int chunk = id % nchunk;
+    id /= nchunk;
+    const int head = id % C.kv_heads;
+    id /= C.kv_heads;
+    read_chunk<T>(C, R, kout, k_stride, vout, v_stride, id >> 1, chunk, head, id & 1);
+  }
+}
+
 template <typename T>
 cudaError_t read_typed(const Kv8Dev& C, const Kv8Rows& R, void* k, long long k_stride, void* v, long long v_stride,
                        cudaStream_t s) {
   const int per_cta = kThreads * Val<T>::kPer / C.head_dim * kReadPasses;
   const int nchunk = (R.max_rows + per_cta - 1) / per_cta;
-  const long long grid = 2LL * R.n_seq * C.kv_heads * nchunk;
-  if (grid > 0x7FFFFFFFLL) return cudaErrorNotSupported;
-  read_kernel<T><<<(unsigned)grid, kThreads, 0, s>>>(C, R, static_cast<T*>(k), k_stride, static_cast<T*>(v), v_stride,
-                                                     nchunk);
+  const PieceGrid g = piece_grid(C, R, nchunk, R.n_rows / per_cta + (long long)R.n_seq);
+  T *kk = static_cast<T*>(k), *vv = static_cast<T*>(v);
+  if (g.list)
+    read_kernel<T, true><<<g.grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nchunk);
+  else
+    read_kernel<T, false><<<g.grid, kThreads, 0, s>>>(C, R, kk, k_stride, vv, v_stride, nchunk);
   return cudaGetLastError();
 }
 

@@ -105,10 +105,10 @@ def test_attend_long_sums_of_f32_rows_do_not_drift(B, fmt, kvh, group, n, hd):
     out = cache.attend(0, q, rows)
     cache.sync()
     off, seqs = [], (0, 51, 76, 151)
+    table = torch.from_numpy(ok.code_values(np.arange(256), fmt)).cuda()
     for h in range(kvh):
         for slot in range(2):
-            k, v = (torch.from_numpy(ok.held_values(ok.code_values(c[0, :, h:h + 1].cpu().numpy(), fmt),
-                                                    e[0, :, h:h + 1].cpu().numpy().astype(int) - ok.BIAS, slot, 0, length, 64)[0]).cuda()
+            k, v = (table[c[0, slot, h].int()] * torch.exp2(e[0, slot, h].double() - ok.BIAS).repeat_interleave(64)[:length, None]
                     for c, e in ((cache.k, cache.k_exp), (cache.v, cache.v_exp)))
             for i in seqs:
                 if i % 2 != slot:
@@ -145,3 +145,86 @@ def test_append_a_sequence_that_is_left_out_takes_no_slot(B, start, length):
         ok.append(c, e, x.cpu().numpy(), [(start[1], start[2] - start[1], 1, length[1])], 16, "e4m3")
     for got, want in zip(held(cache, 0, "e4m3"), state):
         np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("fmt,dtype,hd,kvh,block", [("e4m3", "f32", 128, 2, 16), ("int8", "bf16", 64, 3, 32),
+                                                    ("e4m3", "f16", 128, 1, 128), ("int8", "f32", 64, 1, 64)])
+@pytest.mark.parametrize("n_seq", [9, 70, 300])
+def test_append_and_read_of_very_unlike_sequences(B, fmt, dtype, hd, kvh, block, n_seq):
+    """Single rows, sequences without rows, a prompt and some that are left out in one call, where the places of the
+    longest sequence for each would be many times the rows: codes, exponents and values bit for bit, and what is left
+    out is not touched."""
+    big, ctx = 601, 700
+    cache = B.KvCache8(1, n_seq, kvh, kvh, hd, ctx, block=block, format=fmt)
+    fill(cache, fmt, n_seq)
+    state = held(cache, 0, fmt)
+    rng = np.random.default_rng(n_seq)
+    n = rng.choice([0, 1, 1, 1, 2, 20], n_seq)
+    at = n_seq // 2
+    n[at], n[0] = big, 1
+    start = np.concatenate([[0], np.cumsum(n)])
+    length = np.minimum(ctx, n + rng.integers(0, 70, n_seq))
+    slot = rng.permutation(n_seq)
+    rows = int(start[-1])
+    bad = [i for i in (1, n_seq - 2) if i != at]  # a length out of range; a slot out of range
+    length[1], slot[n_seq - 2] = ctx + 1, -1
+    r = B.KvRows(i32(start), i32(slot), i32(length), n_rows=rows + 5, max_rows=big)
+    k, v = (_randn(s, rows + 5, kvh, hd).to(DTYPES[dtype]) for s in (9, 10))
+    cache.append(0, k, v, r)
+    _reported(B, cache)
+    good = [(int(start[i]), int(n[i]), int(slot[i]), int(length[i])) for i in range(n_seq) if i not in bad]
+    for c, e, x in ((state[0], state[1], k), (state[2], state[3], v)):
+        ok.append(c, e, x.float().cpu().numpy(), good, block, fmt)
+    for got, want in zip(held(cache, 0, fmt), state):
+        np.testing.assert_array_equal(got, want)
+    ko, vo = (torch.full_like(k, 7.0) for _ in range(2))
+    cache.read(0, r, k=ko, v=vo)
+    _reported(B, cache)
+    for got, c, e in ((ko, state[0], state[1]), (vo, state[2], state[3])):
+        want = torch.full(got.shape, 7.0)
+        for i in bad:
+            want[start[i]:start[i + 1]] = 0
+        for row0, m, s, end in good:
+            x = ok.held_values(c, e, s, end - m, end, block).transpose(1, 0, 2)
+            want[row0:row0 + m] = torch.from_numpy(np.ascontiguousarray(x)).float()
+        assert torch.equal(got.cpu(), want.to(got.dtype))
+
+
+def test_append_and_read_of_sequences_over_one_another(B):
+    """row_start that goes back: every other sequence is out of order, those between share their rows, so the pieces are
+    more than the rows could need."""
+    cache = B.KvCache8(1, 40, 2, 2, 64, 200, block=16)
+    fill(cache, "e4m3", 23)
+    state = held(cache, 0, "e4m3")
+    start = [0, 120] * 30 + [0]
+    slot = [i // 2 for i in range(60)]
+    length = [150] * 60
+    k, v = _randn(11, 130, 2, 64), _randn(12, 130, 2, 64)
+    r = B.KvRows(i32(start), i32(slot), i32(length), n_rows=130, max_rows=125)
+    cache.append(0, k, v, r)
+    _reported(B, cache)
+    for c, e, x in ((state[0], state[1], k), (state[2], state[3], v)):
+        ok.append(c, e, x.cpu().numpy(), [(0, 120, i, 150) for i in range(30)], 16, "e4m3")
+    for got, want in zip(held(cache, 0, "e4m3"), state):
+        np.testing.assert_array_equal(got, want)
+    ko, vo = (torch.full_like(k, 7.0) for _ in range(2))
+    cache.read(0, B.KvRows(i32(start), i32([3] * 60), i32(length), n_rows=130, max_rows=125), k=ko, v=vo)
+    _reported(B, cache)
+    for got, c, e in ((ko, state[0], state[1]), (vo, state[2], state[3])):
+        want = ok.held_values(c, e, 3, 30, 150, 16).transpose(1, 0, 2)
+        assert np.array_equal(got[:120].cpu().numpy(), want.astype(np.float32)) and (got[120:] == 7).all()
+
+
+def test_append_of_the_most_sequences_beside_one_long_prompt(B):
+    """1024 sequences of which one has 2^18 + 3 rows, 64 kv heads and blocks of 16: the same bits as that one alone."""
+    n, kvh, hd = (1 << 18) + 3, 64, 64
+    x = _randn(13, n, 1, hd).bfloat16() * torch.exp2(torch.arange(kvh, device="cuda") % 7 - 3.0)[:, None].bfloat16()
+    cache = [B.KvCache8(1, 1, kvh, kvh, hd, n, block=16) for _ in range(2)]
+    for c, seqs in zip(cache, ([(0, 0, 0)] * 500 + [(n, 0, n)] + [(0, 0, 0)] * 523, [(n, 0, n)])):
+        for t in (c.k, c.v, c.k_exp, c.v_exp):
+            t.zero_()
+        c.append(0, x, x, rows_of(B, seqs)[0])
+        c.sync()
+    assert torch.equal(cache[0].k, cache[1].k) and torch.equal(cache[0].k_exp, cache[1].k_exp)
+    assert torch.equal(cache[0].v, cache[1].v) and torch.equal(cache[0].v_exp, cache[1].v_exp)
+    assert cache[0].k.any() and torch.equal(cache[0].k, cache[0].v)
