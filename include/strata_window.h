@@ -656,14 +656,18 @@ strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_s
  * The rows written by an earlier strata_kv8_append on the same stream are
  * seen.  The handle's workspace joins the parts of long rows, so calls of
  * strata_kv8_attend on one handle, replays of captured ones among them, must
- * not overlap on the GPU (append and read use none).  The same call gives the
+ * not overlap on the GPU (append and read use none): their results, and those
+ * of later calls, are undefined until strata_kv8_sync has reported what the
+ * overlap left in the workspace, if anything, and cleared it.  The same call gives the
  * same bits; a row's bits may depend on the other sequences' lengths. */
 strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int64_t q_stride, void* out,
                                 int64_t out_stride, int32_t dtype, float scale, const strata_kv8_rows* rows,
                                 void* cuda_stream);
 
-/* Wait for the handle's device; report (and clear) any error the GPU recorded:
- * EDEVICE in that case.  Not during a capture. */
+/* Wait for the handle's device; report (and clear) any error the GPU recorded
+ * and joins of strata_kv8_attend that were left unfinished (calls that
+ * overlapped): EDEVICE in that case.  Not during a capture, nor while another
+ * thread makes calls on the handle.  Returns EDEVICE, ENOMEM (host), ECUDA. */
 strata_status strata_kv8_sync(strata_kv8* h);
 
 /* Cache bytes of the desc (codes and exponents of all layers) and the

@@ -899,6 +899,10 @@ class KvCache8:
     The codes (k, v: uint8 [n_layers][n_slots][kv_heads][max_ctx][head_dim]) and exponent bytes (k_exp, v_exp:
     uint8 [...][ceil(max_ctx / block)]) are torch tensors, made here or given as ``buffers`` (contiguous, of these
     sizes).  format: "e4m3" or "int8".  Calls are asynchronous; sync() raises what the GPU recorded.
+
+    attend() uses the handle's workspace: its calls on one KvCache8, whatever the layer, and replays of captured ones must
+    not run at the same time.  On one stream they do not; across streams, order them with events.  (append() and read()
+    need no such order.)  What an overlap may leave behind spoils later calls until sync() has raised it.
     """
 
     def __init__(self, n_layers: int, n_slots: int, heads: int, kv_heads: int, head_dim: int, max_ctx: int,
@@ -971,7 +975,8 @@ class KvCache8:
 
     def attend(self, layer: int, q, rows: KvRows, out=None, scale: Optional[float] = None, stream=None):
         """Enqueue the attention of q [n_rows][heads][head_dim] over the layer's caches; returns out, a new tensor
-        unless given; rows of no sequence are not written.  scale: 1 / sqrt(head_dim) unless given."""
+        unless given; rows of no sequence are not written.  scale: 1 / sqrt(head_dim) unless given.  Must not run at
+        the same time as another attend() of this cache (see KvCache8)."""
         qs = self._stride(rows, q, self.heads, "q")
         if out is None:
             out = _empty((rows.n_rows, self.heads, self.head_dim), q.dtype, q.device, stream)

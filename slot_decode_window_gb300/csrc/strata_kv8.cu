@@ -1,6 +1,7 @@
 // C ABI of the slots' 8-bit KV caches: argument checks, the handle's error word
 // and the launches of kv8_rw.cu and kv8_attend.cu.
 #include <cmath>
+#include <memory>
 #include <new>
 
 #include "handle.h"
@@ -207,19 +208,29 @@ strata_status strata_kv8_attend(strata_kv8* h, int32_t layer, const void* q, int
   if (fault_is("launch")) return STRATA_ECUDA;
   DeviceScope on(h->device);
   if (!on.ok) return launched(cudaErrorInvalidDevice);
-  return launched(launch_kv8_attend(layer_dev(h, layer), rows_dev(rows), h->maps, layer, h->ws, h->nsm, q, q_stride,
-                                    out, out_stride, dtype, scale, static_cast<cudaStream_t>(cuda_stream)));
+  st = launched(launch_kv8_attend(layer_dev(h, layer), rows_dev(rows), h->maps, layer, h->ws, h->nsm, q, q_stride, out,
+                                  out_stride, dtype, scale, static_cast<cudaStream_t>(cuda_stream)));
+  if (st == STRATA_OK && fault_is("overlap"))  // what two calls at once may leave: joins that are not through
+    st = launched(cudaMemsetAsync(static_cast<char*>(h->ws) + 256, 1, (size_t)h->nsm * 4,
+                                  static_cast<cudaStream_t>(cuda_stream)));
+  return st;
 }
 
 strata_status strata_kv8_sync(strata_kv8* h) {
   if (!h) return STRATA_EINVAL;
   DeviceScope on(h->device);
-  unsigned err = 0;
+  // The error word and the joins' counters.  On an idle device every counter is back at zero; one that is not (calls
+  // that overlapped, a wait that gave up) would spoil the joins of every later call.
+  const size_t bytes = (size_t)kv8_attend_zeroed(h->nsm);
+  const std::unique_ptr<unsigned[]> state(new (std::nothrow) unsigned[bytes / 4]);
+  if (!state) return STRATA_ENOMEM;
   if (!on.ok || cudaDeviceSynchronize() != cudaSuccess ||
-      cudaMemcpy(&err, h->C.err, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess) {
+      cudaMemcpy(state.get(), h->ws, bytes, cudaMemcpyDeviceToHost) != cudaSuccess) {
     cudaGetLastError();
     return STRATA_ECUDA;
   }
+  unsigned err = 0;
+  for (size_t i = 0; i < bytes / 4; ++i) err |= state[i];
   if (err == 0) return STRATA_OK;
   if (!clear(h)) {
     cudaGetLastError();

@@ -228,3 +228,24 @@ def test_append_of_the_most_sequences_beside_one_long_prompt(B):
     assert torch.equal(cache[0].k, cache[1].k) and torch.equal(cache[0].k_exp, cache[1].k_exp)
     assert torch.equal(cache[0].v, cache[1].v) and torch.equal(cache[0].v_exp, cache[1].v_exp)
     assert cache[0].k.any() and torch.equal(cache[0].k, cache[0].v)
+
+
+def test_sync_reports_and_clears_joins_that_were_left_unfinished(B, monkeypatch):
+    """Counters of the joins that are not back at zero, as an overlap of two attends may leave them (put there by the
+    host): the next sync reports them and the call after it is right again."""
+    cache = B.KvCache8(1, 1, 8, 2, 128, 6000, block=64)
+    fill(cache, "e4m3", 24)
+    state = held(cache, 0, "e4m3")
+    for n in (1, 60):
+        rows, seqs = rows_of(B, [(n, 0, 6000)])
+        q = _randn(14, n, 8, 128)
+        want = cache.attend(0, q, rows)
+        cache.sync()
+        check_attend(want, q, state, seqs, 64, 128 ** -0.5)
+        monkeypatch.setenv("STRATA_FAULT", "overlap")
+        cache.attend(0, q, rows)
+        monkeypatch.delenv("STRATA_FAULT")
+        _reported(B, cache)
+        again = cache.attend(0, q, rows)
+        cache.sync()
+        assert torch.equal(again, want)
