@@ -818,11 +818,14 @@ class QkNorm:
                 if not g.is_cuda or g.dtype != torch.float32 or tuple(g.shape) != (head_dim,) or \
                         not g.is_contiguous():
                     raise StrataError(STRATA_EINVAL, "QkNorm: a gain is a contiguous CUDA float32 [head_dim]")
-                device = device or g.device
+                if device is None:
+                    device = g.device
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         with torch.cuda.device(device):
             s = (stream or torch.cuda.current_stream()).cuda_stream
             self.device = torch.cuda.current_device()
+            if any(g is not None and g.get_device() != self.device for g in (q_gain, k_gain)):
+                raise StrataError(STRATA_EINVAL, "QkNorm: want the gains on the handle's device")
             st, h = strata_qknorm_create(
                 strata_qknorm_desc(heads, kv_heads, head_dim, rd, int(interleaved), int(norm), eps),
                 q_gain.data_ptr() if q_gain is not None else None, k_gain.data_ptr() if k_gain is not None else None,
@@ -917,7 +920,7 @@ class KvCache8:
         shape = (n_layers, n_slots, kv_heads, max_ctx, head_dim)
         eshape = shape[:3] + ((max_ctx + block - 1) // block,)
         if buffers is None:
-            buffers = tuple(torch.empty(x, dtype=torch.uint8, device=device or "cuda")
+            buffers = tuple(torch.empty(x, dtype=torch.uint8, device="cuda" if device is None else device)
                             for x in (shape, shape, eshape, eshape))
         for t, x in zip(buffers, (shape, shape, eshape, eshape)):
             n = 1
