@@ -437,9 +437,9 @@ def strata_stack_forward_kv(handle, x_ptr: int, T: int, y_ptr: int, slot_ptr: in
 
 
 def strata_qknorm_create(desc: strata_qknorm_desc, q_gain_ptr=None, k_gain_ptr=None, freqs=None, stream: int = 0):
-    """freqs: a sequence of rotary_dim/2 radians per position.  Returns (status, handle or None)."""
+    """freqs: rotary_dim/2 radians per position, a sequence, an array or a tensor.  Returns (status, handle or None)."""
     h = ctypes.c_void_p()
-    arr = (ctypes.c_double * len(freqs))(*[float(f) for f in freqs]) if freqs else None
+    arr = (ctypes.c_double * len(freqs))(*[float(f) for f in freqs]) if freqs is not None and len(freqs) > 0 else None
     st = load().strata_qknorm_create(ctypes.byref(desc), q_gain_ptr, k_gain_ptr, arr, stream, ctypes.byref(h))
     return st, (h.value if st == STRATA_OK else None)
 
@@ -801,7 +801,8 @@ class QkNorm:
     """Norms of the query and key heads with the rotation by position.
 
     q_gain, k_gain: CUDA float32 [head_dim] or None (unit gain).  freqs:
-    rotary_dim/2 radians per position; None forms theta ** (-2 i / rotary_dim).
+    rotary_dim/2 radians per position (a sequence, an array or a tensor); None
+    forms theta ** (-2 i / rotary_dim).
     """
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, rotary_dim: Optional[int] = None, freqs=None,

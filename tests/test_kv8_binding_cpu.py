@@ -2,7 +2,9 @@
 it asks of it."""
 import types
 
+import numpy as np
 import pytest
+import torch
 
 from slot_decode_window_gb300 import binding as B
 from slot_decode_window_gb300 import build as BLD
@@ -86,3 +88,12 @@ def test_norms_refuse_gains_of_another_device(torch_, device, q, k):
     with pytest.raises(B.StrataError) as e:
         B.QkNorm(2, 1, 64, device=device, q_gain=gains[0], k_gain=gains[1])
     assert e.value.status == B.STRATA_EINVAL and not torch_.created_on
+
+
+@pytest.mark.parametrize("form", [list, tuple, np.array, torch.tensor])
+@pytest.mark.parametrize("n", [0, 4])
+def test_frequencies_come_as_any_sequence(form, n):
+    """Lists, arrays and tensors reach the library alike: infinite ones are found there, and none where some are due."""
+    BLD.build()
+    d = B.strata_qknorm_desc(2, 1, 64, 8, 0, 1, 1e-6)
+    assert B.strata_qknorm_create(d, None, None, form([float("inf")] * n)) == (B.STRATA_EINVAL, None)
