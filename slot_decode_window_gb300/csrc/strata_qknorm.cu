@@ -289,9 +289,7 @@ strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_s
   if (parts > most) parts = most;
   A.per_cta = (int)((A.total + parts - 1) / parts);
   A.groups = (A.total + A.per_cta - 1) / A.per_cta;
-  const long long ctas = (long long)T * A.groups;
-  if (ctas > 0x7FFFFFFFLL) return STRATA_EUNSUPPORTED;
-  const unsigned grid = (unsigned)ctas;
+  const unsigned grid = (unsigned)T * A.groups;  // T, or fewer than `want` + T where T is below it
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (dtype == STRATA_F32)
     launch_t<float>(A, d.head_dim, d.interleaved, grid, s);
