@@ -593,7 +593,8 @@ typedef struct {
  * length[i] - (row_start[i+1] - r).  Rows from row_start[n_seq] on belong to
  * no sequence (a padded batch): outputs there are left as they were.
  * A sequence with row_start out of order or outside 0..n_rows, or with more
- * than max_rows rows, is skipped; one with a slot or length out of range is
+ * than max_rows rows, is skipped (rows that two others then both name have no
+ * defined output); one with a slot or length out of range is
  * left out (nothing is written to the caches; zeros are written to its rows of
  * an output).  Both make the next strata_kv8_sync report EDEVICE. */
 typedef struct {

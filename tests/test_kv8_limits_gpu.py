@@ -249,3 +249,71 @@ def test_sync_reports_and_clears_joins_that_were_left_unfinished(B, monkeypatch)
         again = cache.attend(0, q, rows)
         cache.sync()
         assert torch.equal(again, want)
+
+
+def _valid(start, slot, length, n_rows, max_rows, n_slots, ctx):
+    """(sequences whose rows may be touched, those of them that are not left out), as the header has it."""
+    rows = [(a, b - a, s, n) for a, b, s, n in zip(start, start[1:], slot, length)
+            if 0 <= a <= b <= n_rows and b - a <= max_rows]
+    return rows, [q for q in rows if 0 <= q[2] < n_slots and 0 <= q[3] <= ctx]
+
+
+@pytest.mark.parametrize("by", [1, 20])  # few rows, many rows
+@pytest.mark.parametrize("start,slot,length,most", [
+    ([0, -1, 2], [1, 0], [5, 6], 2), ([4, 2, 4], [1, 0], [5, 6], 2), ([0, 7, 7], [1, 0], [5, 6], 8),
+    ([0, 3, 4], [1, 0], [5, 6], 2), ([0, 2, 1, 3], [1, 0, 2], [5, 6, 7], 2),
+    ([0, 2, 4], [3, 0], [5, 6], 2), ([0, 2, 4], [-1, 0], [5, 6], 2), ([0, 2, 4], [1, 0], [50, 6], 2),
+    ([0, 2, 4], [1, 0], [-1, 6], 2), ([0, 2, 4], [1, 0], [6, 50], 2)])
+def test_what_is_skipped_or_left_out_is_not_touched(B, start, slot, length, most, by):
+    """Every row and code against the header's rules: rows of a skipped sequence stay, rows of one that is left out become
+    zero, and neither changes the caches.  Rows that two sequences name (row_start goes back) have no defined output."""
+    start, length, most, n_rows, ctx = [a * by for a in start], [n * by for n in length], most * by, 6 * by, 40 * by
+    cache = B.KvCache8(1, 3, 4, 2, 64, ctx, block=16)
+    fill(cache, "e4m3", 25)
+    state = held(cache, 0, "e4m3")
+    q, k, v = _randn(15, n_rows, 4, 64), _randn(16, n_rows, 2, 64), _randn(17, n_rows, 2, 64)
+    r = B.KvRows(i32(start), i32(slot), i32(length), n_rows=n_rows, max_rows=most)
+    rows, good = _valid(start, slot, length, n_rows, most, 3, ctx)
+    out = torch.full_like(q, 3.0)
+    cache.attend(0, q, r, out=out)
+    _reported(B, cache)
+    ko, vo = torch.full_like(k, 3.0), torch.full_like(v, 3.0)
+    cache.read(0, r, k=ko, v=vo)
+    _reported(B, cache)
+    mine, owners = np.full(n_rows, -1), np.zeros(n_rows, int)
+    for i, x in enumerate(rows):
+        mine[x[0]:x[0] + x[1]] = i if x in good else -2
+        owners[x[0]:x[0] + x[1]] += 1
+    assert (out[mine == -1] == 3).all() and (ko[mine == -1] == 3).all() and (vo[mine == -1] == 3).all()
+    assert (out[mine == -2] == 0).all() and (ko[mine == -2] == 0).all() and (vo[mine == -2] == 0).all()
+    for row0, n, s, end in good:
+        one = owners[row0:row0 + n] == 1
+        for got, c, e in ((ko, state[0], state[1]), (vo, state[2], state[3])):
+            want = ok.held_values(c, e, s, end - n, end, 16).transpose(1, 0, 2).astype(np.float32)
+            assert np.array_equal(got[row0:row0 + n].cpu().numpy()[one], want[one])
+        for j in np.flatnonzero(one):  # as a sequence of this row alone, at the position that it has
+            check_attend(out[row0 + j:row0 + j + 1], q[row0 + j:row0 + j + 1], state, [(0, 1, s, end - n + j + 1)], 16, 0.125)
+    cache.append(0, k, v, r)
+    _reported(B, cache)
+    for c, e, x in ((state[0], state[1], k), (state[2], state[3], v)):
+        ok.append(c, e, x.cpu().numpy(), good, 16, "e4m3")
+    for got, want in zip(held(cache, 0, "e4m3"), state):
+        np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("heads,kvh", [(8, 2), (3, 3), (16, 1)])
+@pytest.mark.parametrize("seqs", [[(400, 0, 37)], [(400, 0, 37), (70, 1, 300)], [(70, 1, 300), (400, 0, 37), (1, 2, 0)],
+                                  [(400, 0, 0), (129, 2, 128)], [(400, 0, 400), (300, 1, 1), (300, 2, 129)]])
+def test_attend_whole_tiles_of_rows_that_see_nothing(B, heads, kvh, seqs):
+    """Lengths so far below the rows that row tiles at a sequence's start have nothing to do."""
+    for dtype in ("f32", "bf16"):
+        cache = B.KvCache8(1, 3, heads, kvh, 64, 400, block=32, format="int8")
+        fill(cache, "int8", 26)
+        state = held(cache, 0, "int8")
+        rows, os_ = rows_of(B, seqs, n_rows=sum(s[0] for s in seqs) + 3)
+        q = _randn(18, rows.n_rows, heads, 64).to(DTYPES[dtype])
+        out = torch.full_like(q, 3.0)
+        cache.attend(0, q, rows, out=out)
+        cache.sync()
+        assert (out[-3:] == 3).all()
+        check_attend(out, q, state, os_, 32, 0.125)
