@@ -502,9 +502,10 @@ strata_status strata_tier_destroy(strata_tier* tier);
  *
  * The stack above fuses a layer's attention over fp16 caches into its one
  * launch for windows of at most 8 rows.  These calls serve the same slots with
- * half the cache bytes, for windows and for prompts, and beside
- * strata_moe_window_forward they are the other half of a layer that a caller
- * runs by its parts.  The Strata pages describe no counterpart.
+ * half the cache bytes, for windows and for prompts.  Beside
+ * strata_moe_window_forward they are the other half of a window's layer that a
+ * caller runs by its parts, with the q, k, v and o products its own.  The
+ * Strata pages describe no counterpart.
  *
  * All of them are asynchronous on cuda_stream, allocate nothing, copy nothing
  * to the host and may be captured into a CUDA graph; the device arrays that
@@ -547,9 +548,9 @@ strata_status strata_qknorm_create(const strata_qknorm_desc* desc, const float* 
 /* T rows: q [T][heads][head_dim] to q_out, k [T][kv_heads][head_dim] to k_out
  * (k and k_out may be NULL when kv_heads is 0).  position: device int32 [T],
  * any value.  An output may be its own input (same pointer and stride); any
- * other overlap is not allowed (EINVAL where it starts at the same address).  T = 0 does nothing.  A row's bits do not
- * depend on the other rows.  Returns EINVAL, ECUDA.  One handle may run on
- * several streams at once. */
+ * other overlap is not allowed (EINVAL where it starts at the same address).
+ * T = 0 does nothing.  A row's bits do not depend on the other rows.  Returns
+ * EINVAL, ECUDA.  One handle may run on several streams at once. */
 strata_status strata_qknorm_forward(strata_qknorm* h, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                     void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, int32_t dtype,
                                     const int32_t* position, int32_t T, void* cuda_stream);
@@ -635,8 +636,8 @@ strata_status strata_kv8_append(strata_kv8* h, int32_t layer, const void* k, int
 
 /* Read the rows' positions back: code * 2^e, rounded once to dtype (exact in
  * f32; f16 overflows to infinity as any rounding to it).  A sequence with
- * length[i] below its rows is left out.  k and v must not overlap (EINVAL at
- * the same address). */
+ * length[i] below its rows is left out as one with a length out of range is:
+ * zeros, EDEVICE.  k and v must not overlap (EINVAL at the same address). */
 strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_stride, void* v, int64_t v_stride,
                               int32_t dtype, const strata_kv8_rows* rows, void* cuda_stream);
 

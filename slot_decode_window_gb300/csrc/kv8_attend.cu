@@ -28,12 +28,22 @@ namespace {
 // l = sum w_j 2^-ev, out = O / l.  Whatever the exponents, the largest weight
 // that meets a code is 1 (held times 2^14 so that 16-bit weights keep 38 bits
 // below it), and no block needs its own accumulator.
-// f32 rows: q and the weights enter as two f16 parts (22 bits) that chain into
-// one accumulator.
+// What is rounded to 16 bits, for the matrix unit's sake: codes are exact in
+// f16.  16-bit rows: q after a power of two per row (bf16 elements below 2^-17
+// of the row's largest lose bits, a 2^-25 of it at most) and the weights (11
+// bits, on their way into O only: a relative 2^-11 at most, to both sides, that
+// averages out over positions; l sums them in f32), against the 8 or 11 bits
+// that the result is rounded to.  f32 rows: both as two f16 parts (22 bits) that
+// chain into one accumulator: 1.6e-7 off at 512 positions, fp32 products 1.1e-7.
+// Scores, statistics and sums are f32; t_j is one f32 sum, so weights resolve
+// 2^-24 of the largest |t_j|.
 // Measured (32 / 8 heads of 128, bf16): 64 rows over 1.6 k to 8.2 k positions
-// 111.6 us (85% of the measured HBM rate), one over 131071 52.9 us (75%; the
+// 112.5 us (84% of the measured HBM rate), one over 131071 52.8 us (75%; the
 // start and the join of 19 parts are the rest).  With the rows on the M side
 // and 8 warps of 168 registers these took 164 and 62 us.
+// Registers: heads of 128 spill at the limits below (bytes stored, one tile of
+// rows / two: 24 to 28 / 152 for 16-bit rows, 152 to 160 / 320 for f32 rows);
+// heads of 64 none for 16-bit rows, up to 24 for f32 rows.
 // ---------------------------------------------------------------------------
 constexpr float kWeightTop = 14.f;  // weights are scaled by 2^14
 
@@ -186,9 +196,11 @@ __device__ __forceinline__ Item next_item(const AttendArgs& A, const long long* 
 }
 
 // Units that beginning an item is worth (its q, its join), where every CTA has at least kStartFrom units to do.  With 64
-// conversations of other lengths, 3.4 items a CTA, equal units alone left the slowest CTA at 114 us and the median at 93;
-// a start of 0, 2, 4, 8 units: 132.9, 130.1, 124.5, 122.0 us for the call.  Short lists keep equal units: there a start
-// would leave CTAs without any.
+// conversations of other lengths, 3.4 items a CTA, equal units alone left the slowest CTA 20 us behind the median.  A
+// start of 0, 4, 8, 12, 16 units: 124.4, 116.3, 112.6, 108.0, 108.0 us there, and 37.4, 35.3, 33.3, 34.8, 33.8 us with 24
+// slots x 2 rows of 16 heads of 64; the same from 8 to 96 conversations (12 up to 4 % below 8, 0 up to 10 % above).  Short
+// lists keep equal units: there a start would leave CTAs without any (from 12, 24, 48 units: 111.6, 112.6, 112.1 and
+// 33.8, 33.3, 37.4 us).
 constexpr int kStart = 8, kStartFrom = 24;
 
 template <int HD, int FMT, int NT, int PARTS>
@@ -790,6 +802,13 @@ cudaError_t launch_kv8_attend(const Kv8Dev& C, const Kv8Rows& R, const Kv8Maps& 
   uint8_t* w = static_cast<uint8_t*>(workspace) + 256;
   unsigned* count = reinterpret_cast<unsigned*>(w);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv8_attend_zeroed(nsm));
+  // Few rows or many: the rows that the host knows, max_rows x group.  Measured few / many in us, 32 / 4 heads of 128, for
+  // 16, 24, 32, 40, 48, 64, 128 of them.  4 sequences of 1002 positions: bf16 23/31, 23/31, 24/31, 25/31, 27/31, 26/31,
+  // 33/33, f32 29/32, 29/33, 31/33, 33/33, 33/33, 36/33, 44/35.  Of 16000: bf16 34/62, 41/63, 41/64, 54/64, 54/64, 65/63,
+  // 103/64, f32 50/68, 64/70, 64/70, 87/70, 87/70, 109/72, 178/72.  24 of 8000, where every SM has enough to read: bf16
+  // 58/76, 92/76, 93/77, 131/76, 132/76, 169/77, 281/78, f32 92/93, 157/93, 159/95, 227/94, 229/95, 298/95, 504/97.  So
+  // long lists cross at 16, where a second row tile reads the caches again, and short ones at 40 to 128; the lengths that
+  // would tell them apart are on the device, and 32 lies between.
   if ((long long)R.max_rows * group > 32)
     return launch_kv8_prompt(C, R, M, layer, count, parts, nsm, q, q_stride, out, out_stride, dtype, scale, s);
   AttendArgs A;

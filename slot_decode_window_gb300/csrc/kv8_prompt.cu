@@ -18,10 +18,15 @@
 // and no accumulator lives longer than one unit: the tensor core's truncating
 // adds do not pile up over a long cache.
 //
-// Measured (32 / 8 heads of 128): 8191 bf16 rows from the first token 627 us
-// (877 TFLOP/s, 46% of the measured cuBLAS rate); 1531 + 1152 f32 rows at 9001
-// and 6776 positions 496 us (two products for each: 68% of that rate).  Bound by
-// the roles' per-unit work and hand-overs, not by the tensor cores (27% active).
+// q and the weights are rounded to f16 parts as in kv8_attend.cu; f32 rows end
+// 8e-7 from 64 bits (rms, prompts and chunks), products in fp32 1.5e-6.
+//
+// Measured (32 / 8 heads of 128): 8191 bf16 rows from the first token 635 us
+// (866 TFLOP/s, 45% of the measured cuBLAS rate); 1531 + 1152 f32 rows at 9001
+// and 6776 positions 493 us (two products for each: 69% of that rate).  Bound by
+// the roles' per-unit work and hand-overs, not by the tensor cores (27% active
+// at 4095 rows).
+// Every variant spills at the launch's 80 registers (148 to 232 bytes stored).
 //
 // Roles (24 warps): two warpgroups of softmax (even and odd units, a row a
 // thread), one of correction (a row's output a thread), one of conversion for q

@@ -42,8 +42,8 @@ constexpr int kQkBatch = 1;  // 16-byte accesses a thread has in flight
 // sincospi.
 // HBM bound in a prompt.  8191 rows of 32 + 8 bf16 heads: with the angles and gains in every warp's registers (91 of
 // them, six times the angles) 74 us; in shared memory 64 us with four accesses a thread in flight (79 registers), 45 us
-// with one and twelve CTAs an SM (40 registers), which is what is here (39.4 us called in turn, 63% of the measured HBM
-// rate).
+// with one and twelve CTAs an SM (40 registers, of which half-apart pairs spill 4 to 28 bytes in seven variants), which is
+// what is here (39.4 us called in turn, 63% of the measured HBM rate).
 template <typename T, int kHd, int E, bool kInter>
 __global__ void __launch_bounds__(kQkThreads, 12) qknorm_kernel(QkArgs A) {
   constexpr int kLanes = kHd / E, kGroup = 32 / kLanes, kWarps = kQkThreads / 32;

@@ -190,29 +190,30 @@ def test_append_and_read_of_very_unlike_sequences(B, fmt, dtype, hd, kvh, block,
         assert torch.equal(got.cpu(), want.to(got.dtype))
 
 
-def test_append_and_read_of_sequences_over_one_another(B):
+@pytest.mark.parametrize("n", [120, 600])
+def test_append_and_read_of_sequences_over_one_another(B, n):
     """row_start that goes back: every other sequence is out of order, those between share their rows, so the pieces are
     more than the rows could need."""
-    cache = B.KvCache8(1, 40, 2, 2, 64, 200, block=16)
+    cache = B.KvCache8(1, 40, 2, 2, 64, n + 80, block=16)
     fill(cache, "e4m3", 23)
     state = held(cache, 0, "e4m3")
-    start = [0, 120] * 30 + [0]
+    start = [0, n] * 30 + [0]
     slot = [i // 2 for i in range(60)]
-    length = [150] * 60
-    k, v = _randn(11, 130, 2, 64), _randn(12, 130, 2, 64)
-    r = B.KvRows(i32(start), i32(slot), i32(length), n_rows=130, max_rows=125)
+    length = [n + 30] * 60
+    k, v = _randn(11, n + 10, 2, 64), _randn(12, n + 10, 2, 64)
+    r = B.KvRows(i32(start), i32(slot), i32(length), n_rows=n + 10, max_rows=n + 5)
     cache.append(0, k, v, r)
     _reported(B, cache)
     for c, e, x in ((state[0], state[1], k), (state[2], state[3], v)):
-        ok.append(c, e, x.cpu().numpy(), [(0, 120, i, 150) for i in range(30)], 16, "e4m3")
+        ok.append(c, e, x.cpu().numpy(), [(0, n, i, n + 30) for i in range(30)], 16, "e4m3")
     for got, want in zip(held(cache, 0, "e4m3"), state):
         np.testing.assert_array_equal(got, want)
     ko, vo = (torch.full_like(k, 7.0) for _ in range(2))
-    cache.read(0, B.KvRows(i32(start), i32([3] * 60), i32(length), n_rows=130, max_rows=125), k=ko, v=vo)
+    cache.read(0, B.KvRows(i32(start), i32([3] * 60), i32(length), n_rows=n + 10, max_rows=n + 5), k=ko, v=vo)
     _reported(B, cache)
     for got, c, e in ((ko, state[0], state[1]), (vo, state[2], state[3])):
-        want = ok.held_values(c, e, 3, 30, 150, 16).transpose(1, 0, 2)
-        assert np.array_equal(got[:120].cpu().numpy(), want.astype(np.float32)) and (got[120:] == 7).all()
+        want = ok.held_values(c, e, 3, 30, n + 30, 16).transpose(1, 0, 2)
+        assert np.array_equal(got[:n].cpu().numpy(), want.astype(np.float32)) and (got[n:] == 7).all()
 
 
 def test_append_of_the_most_sequences_beside_one_long_prompt(B):
