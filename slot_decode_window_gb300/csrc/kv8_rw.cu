@@ -35,7 +35,7 @@ template <> struct Abs<__half> {
 // the largest new magnitude, fixes the exponent, requantises what the block
 // holds if the exponent grew, and writes the new codes.  Its new values stay in
 // registers between the two passes (NP 16-byte loads a thread, all in flight),
-// so they are read once.  24 k bf16 rows of 8 heads of 128 (150 MB in and out): 34.8 us, 63% of the measured HBM rate;
+// so they are read once.  24 k bf16 rows of 8 heads of 128 (150 MB in and out): 34.2 us, 64% of the measured HBM rate;
 // issue bound (68% of the slots), so magnitudes are taken two at a time and what is not finite has a path of its own
 // (43.1 us before both).  A window's rows: 2.2 us.
 template <typename T, int NP>

@@ -318,3 +318,72 @@ def test_attend_whole_tiles_of_rows_that_see_nothing(B, heads, kvh, seqs):
         cache.sync()
         assert (out[-3:] == 3).all()
         check_attend(out, q, state, os_, 32, 0.125)
+
+
+@pytest.mark.parametrize("n", [1, 6, 12, 70])  # one row tile of 8, of 16, two of 16, the many-row kernel
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt,heads,kvh,hd", [("int8", 4, 2, 128), ("int8", 4, 2, 64), ("e4m3", 4, 2, 64), ("e4m3", 6, 2, 128)])
+@pytest.mark.parametrize("length", [300, 2300])  # in one part, and in parts that are joined
+def test_attend_large_scores_in_every_variant(B, n, dtype, fmt, heads, kvh, hd, length):
+    """As test_attend_scores_of_any_size, at 2^26 and with the equal keys far apart: a row is the mean of their values, under
+    the bound derived there."""
+    block, scale, group = 32, 2.0 ** 26, heads // kvh
+    cache = B.KvCache8(1, 1, heads, kvh, hd, length, block=block, format=fmt)
+    fill(cache, fmt, 1)
+    u = _randn(1, kvh, hd).sign()
+    k, v = 0.1 * _randn(2, length, kvh, hd), _randn(3, length, kvh, hd).clamp(-3.9, 3.9)
+    same = [5, 130, length - 80]
+    k[same] = u
+    k[..., 0] = 16.0
+    v[..., 0] = 4.0
+    cache.append(0, k, v, rows_of(B, [(length, 0, length)])[0])
+    kc, ke, vc, ve = held(cache, 0, fmt)
+    q = u.repeat_interleave(group, 0) + 0.02 * _randn(4, n, heads, hd)
+    q[..., 0] = 0
+    q = q.to(DTYPES[dtype])
+    out = cache.attend(0, q, rows_of(B, [(n, 0, length)])[0], scale=scale)
+    cache.sync()
+    kk, vv = ok.held_values(kc, ke, 0, 0, length, block), ok.held_values(vc, ve, 0, 0, length, block)
+    got, qq = out.double().cpu().numpy(), q.double().cpu().numpy()
+    for r in range(n):
+        for h in range(heads):
+            s = scale * np.log2(np.e) * (kk[h // group, :length - n + r + 1] @ qq[r, h])
+            assert (s[same] == s[5]).all() and s[5] - np.delete(s, same).max() > 60
+            want, size = vv[h // group, same].mean(0), np.abs(vv[h // group, same]).mean(0)
+            off = 16 * 2.0 ** -24 * size
+            assert (np.abs(got[r, h] - want) <= off + half_step(q.dtype) * (np.abs(want) + off)).all(), (r, h)
+
+
+def test_captured_append_and_read_of_unlike_sequences_follow_their_buffers(B):
+    """The list of pieces is made on the device: captured once, replayed as other sequences take the rows."""
+    n_seq, n_rows, most = 60, 700, 640
+    one, two = (B.KvCache8(1, n_seq, 2, 2, 64, 700, block=16, format="int8") for _ in range(2))
+    for c in (one, two):
+        fill(c, "int8", 27)
+    start, slot, length = i32([0] * (n_seq + 1)), i32(range(n_seq)), i32([0] * n_seq)
+    rows = B.KvRows(start, slot, length, n_rows=n_rows, max_rows=most)
+    k, v = _randn(19, n_rows, 2, 64), _randn(20, n_rows, 2, 64)
+    out, want = ([torch.empty_like(k), torch.empty_like(k)] for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one.append(0, k, v, rows)
+        one.read(0, rows, k=out[0], v=out[1])
+    for big in (0, 59, 31):
+        n = [1 if i % 3 else 0 for i in range(n_seq)]
+        n[big] = most
+        start.copy_(i32([0] + list(np.cumsum(n))))
+        length.copy_(i32([x + (7 * i + big) % 50 for i, x in enumerate(n)]))
+        k.normal_(), v.normal_()
+        for t in out + want:
+            t.fill_(5.0)
+        graph.replay()
+        for i in range(n_seq):  # one sequence at a time
+            if n[i]:
+                a = int(start[i])
+                alone, _ = rows_of(B, [(n[i], i, int(length[i]))])
+                two.append(0, k[a:a + n[i]], v[a:a + n[i]], alone)
+                two.read(0, alone, k=want[0][a:a + n[i]], v=want[1][a:a + n[i]])
+        one.sync(), two.sync()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        for a, b in ((one.k, two.k), (one.v, two.v), (one.k_exp, two.k_exp), (one.v_exp, two.v_exp)):
+            assert torch.equal(a, b)
