@@ -648,9 +648,9 @@ strata_status strata_kv8_read(strata_kv8* h, int32_t layer, void* k, int64_t k_s
  * (length below the rows) attends to nothing: zeros.  Sums and softmax
  * statistics are fp32; products take 16-bit parts of q and of the softmax
  * weights, one for f16 and bf16 rows and two (22 bits) for f32 rows.  Scores
- * are f32 and may be of any size that the softmax's differences survive: a
- * finite row of q gives a finite result (beyond scale * max|q| of some 1e18 its
- * scores keep their order only).  Cache
+ * are f32 and may be of any size: a finite row of q gives a finite result,
+ * but for an f16's overflow (beyond scale * max|q| of some 1e18 its scores
+ * keep their order only).  Cache
  * contents at positions from length[i] on never reach an output, whatever
  * their bits; below it codes are numbers (append writes no other).  Sequences
  * may share a slot.  q and out are [n_rows][heads][head_dim] of the same dtype
