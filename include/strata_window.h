@@ -679,6 +679,187 @@ strata_status strata_kv8_query(const strata_kv8* h, int64_t* cache_bytes, int64_
 /* Free the handle (the caches are the caller's).  NULL is accepted. */
 strata_status strata_kv8_destroy(strata_kv8* h);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a layer as calls, for windows and for prompts: the products with
+ * its block-quantized matrices, its tokens sorted by expert and back, and the
+ * norms around a block with the gate and the residual.
+ *
+ * With strata_qknorm_* and strata_kv8_* a caller runs a layer of any number of
+ * rows by its parts: norm, q/k/v product, head norms, caches and attention, o
+ * product, residual and norm, router, rows sorted by expert, the experts'
+ * products, and back.  strata_moe_window_forward and strata_stack_forward fuse
+ * the same for windows of at most 8 rows.  The Strata pages describe no
+ * counterpart.
+ *
+ * As the calls above: asynchronous on cuda_stream, no allocation and no copy to
+ * the host, may be captured into a CUDA graph, the handle's device is made
+ * current for the call; value types are strata_dtype, value pointers 16-byte
+ * aligned, *_stride the distance between rows in elements, a multiple of 16
+ * bytes (EINVAL otherwise).  Offsets are 64-bit throughout.
+ * ------------------------------------------------------------------------- */
+
+/* Products with 4-bit matrices: y = W x for each row, W the block format above
+ * (bits 4, block 32: weight = scale * q + min), one matrix or a stack of n whose
+ * rows are sorted by matrix.  With a second stack (`up`) of the same shape
+ * y = silu(W x) * (U x), silu(z) = z / (1 + e^-z). */
+typedef struct strata_linear strata_linear;
+
+typedef struct {
+  int32_t n;         /* matrices: 1..1024 */
+  int32_t in;        /* columns: a multiple of 64, at most 65536 */
+  int32_t out;       /* rows: a multiple of 16, at most 2^22 */
+  int32_t bits;      /* 4 */
+  int32_t block;     /* 32 */
+  int32_t max_rows;  /* most rows of a call: 1..2^20 */
+} strata_linear_desc;
+
+/* Create on the current device.  weight, up: device matrices [n][out][in] (up
+ * may be NULL), copied on cuda_stream into the handle's own layout (create
+ * waits; the caller may free them then).  The handle keeps a workspace for the
+ * rows of a call: 4 bytes per element of max_rows rows (none for n = 1 and
+ * max_rows <= 8).  Returns EINVAL, EUNSUPPORTED, ENOMEM, ECUDA. */
+strata_status strata_linear_create(const strata_linear_desc* desc, const strata_qmat* weight, const strata_qmat* up,
+                                   void* cuda_stream, strata_linear** out);
+
+/* T rows: x [T][in] to y [T][out], both dtype; they must not overlap (EINVAL at
+ * the same address).  offsets: device int32 [n + 1], matrix i takes the rows
+ * offsets[i] to offsets[i + 1] - 1 (strata_sort_plan's); NULL for n = 1: all
+ * rows.  Rows of no matrix are left as they were.  A matrix whose range is out
+ * of order or outside 0..T is left out, and the next strata_linear_sync reports
+ * EDEVICE.  T = 0 does nothing.
+ * Sums are f32.  Up to 8 rows of n = 1 (offsets NULL) are one launch on the exact weights
+ * and the exact f16, bf16 or (24 bits) f32 rows, and a row's bits do not depend
+ * on the others.  More take 16-bit parts: f16 and bf16 rows exactly, with
+ * weights rounded to f16; f32 rows and their weights in two parts (22 bits).
+ * Rows are scaled by a power of two of their own, so values of any size keep
+ * this.  A row with infinities or NaN gives numbers of no meaning in that row
+ * only.  Calls of more rows use the workspace: on one handle they, and replays of
+ * captured ones, must not overlap on the GPU.  The same call gives the same
+ * bits.  Returns EINVAL (T above max_rows among it), ECUDA. */
+strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_stride, void* y, int64_t y_stride,
+                                    int32_t dtype, int32_t T, const int32_t* offsets, void* cuda_stream);
+
+/* Wait for the handle's device; report (and clear) any error the GPU recorded:
+ * EDEVICE in that case.  Not during a capture. */
+strata_status strata_linear_sync(strata_linear* h);
+
+/* Bytes of the handle's matrices and of its workspace; either may be NULL. */
+strata_status strata_linear_query(const strata_linear* h, int64_t* weight_bytes, int64_t* workspace_bytes);
+
+/* Free it (its launches must have finished).  NULL is accepted. */
+strata_status strata_linear_destroy(strata_linear* h);
+
+/* Tokens sorted by expert and back.  An entry t * k + j is the j-th expert of
+ * row t, as in strata_routing_out; an entry whose expert is outside 0..E-1 (-1:
+ * a padded row, a masked expert) is no expert's. */
+typedef struct strata_sort strata_sort;
+
+typedef struct {
+  int32_t n_experts;    /* E: 1..1024 */
+  int32_t top_k;        /* k: 1..min(E, 16) */
+  int32_t renorm_topk;  /* of route: 0: softmax over all E; 1: renormalised over the k */
+} strata_sort_desc;
+
+/* Device arrays of a plan, the caller's; counts may be NULL. */
+typedef struct {
+  int32_t* counts;   /* [E] entries per expert */
+  int32_t* offsets;  /* [E + 1] exclusive prefix sum of counts */
+  int32_t* entries;  /* [T*k] entries by expert (ascending), ascending within an expert; -1 behind the last expert's */
+  int32_t* place;    /* [T*k] where each entry is in entries; -1 for no expert's */
+} strata_sort_order;
+
+strata_status strata_sort_create(const strata_sort_desc* desc, strata_sort** out);
+
+/* The router's choice: logits device fp32 [T][E] (rows `stride` elements apart,
+ * 4-byte aligned), bias fp32 [E] added first, or NULL.  topk_idx, topk_w [T][k]:
+ * the k experts of largest logit, descending, equal ones by the lower index,
+ * and their softmax weights (fp32).  A logit of -inf or NaN is never chosen:
+ * where fewer than k are left, -1 and weight 0.  (+inf: as the largest finite
+ * number.) */
+strata_status strata_sort_route(strata_sort* h, const float* logits, int64_t stride, const float* bias, int32_t T,
+                                int32_t* topk_idx, float* topk_w, void* cuda_stream);
+
+/* The order of T*k entries (at most 2^28): topk_idx device int32 [T][k]. */
+strata_status strata_sort_plan(strata_sort* h, const int32_t* topk_idx, int32_t T, const strata_sort_order* order,
+                               void* cuda_stream);
+
+/* Rows in the experts' order: xs[place[t*k + j]] = x[t], each `width` elements
+ * (a multiple of 16 bytes).  xs has T*k rows; those behind the last expert's
+ * are left as they were.  x and xs must not overlap (EINVAL at the same
+ * address).  A place outside 0..T*k-1 is passed over, here and below. */
+strata_status strata_sort_gather(strata_sort* h, const int32_t* place, const void* x, int64_t x_stride, void* xs,
+                                 int64_t xs_stride, int32_t dtype, int32_t T, int32_t width, void* cuda_stream);
+
+/* And back: y[t] = base[t] + sum_j w[t][j] z[place[t*k + j]] over its entries
+ * that are an expert's, j ascending, in f32.  w: device fp32 [T][k], or NULL
+ * for ones (this is the gradient of strata_sort_gather, with dxs as z); base
+ * [T][width] of the same dtype, or NULL; y may be base (same pointer and
+ * stride), no other overlap (EINVAL at the same address). */
+strata_status strata_sort_combine(strata_sort* h, const int32_t* place, const void* z, int64_t z_stride, const float* w,
+                                  const void* base, int64_t base_stride, void* y, int64_t y_stride, int32_t dtype,
+                                  int32_t T, int32_t width, void* cuda_stream);
+
+/* Its gradient: dz[place[t*k + j]] = w[t][j] dy[t] and dw[t][j] = <dy[t],
+ * z[place[t*k + j]]> (f32 sums; 0 for an entry that is no expert's); rows of dz
+ * behind the last expert's are left as they were, base's gradient is dy.  w
+ * NULL: ones.  dz may be z (same pointer and stride); dz or dw may be NULL (z
+ * too when dw is). */
+strata_status strata_sort_combine_backward(strata_sort* h, const int32_t* place, const void* dy, int64_t dy_stride,
+                                           const void* z, int64_t z_stride, const float* w, void* dz, int64_t dz_stride,
+                                           float* dw, int32_t dtype, int32_t T, int32_t width, void* cuda_stream);
+
+/* Free it (its launches must have finished).  NULL is accepted. */
+strata_status strata_sort_destroy(strata_sort* h);
+
+/* Norms after and before a block, with the gate and the residual between:
+ *   u = y / sqrt(mean(y^2) + eps) * after_gain         (after = 1; else u = y)
+ *   g = the gate, or 1 / (1 + e^-gate) (sigmoid = 1)    (gate = NONE: 1)
+ *   h = residual_scale * x + block_scale * g * u
+ *   n = h / sqrt(mean(h^2) + eps) * before_gain         (before = 1)
+ * x is the residual stream, y the block's output, h the new stream and n the
+ * next block's input, from the unrounded h.  fp32 arithmetic. */
+typedef struct strata_blocknorm strata_blocknorm;
+
+typedef enum {
+  STRATA_GATE_NONE = 0,
+  STRATA_GATE_CHANNEL = 1,  /* fp32 [hidden], the handle's */
+  STRATA_GATE_ROW = 2,      /* fp32 [T] of a call */
+  STRATA_GATE_ELEMENT = 3   /* [T][hidden] of a call, its dtype */
+} strata_gate;
+
+typedef struct {
+  int32_t hidden;          /* a multiple of 8, at most 16384 */
+  int32_t after, before;   /* 0 or 1 */
+  int32_t gate;            /* strata_gate */
+  int32_t sigmoid;         /* 0 or 1 */
+  float eps;               /* >= 0, finite */
+  float residual_scale, block_scale;  /* finite */
+} strata_blocknorm_desc;
+
+/* Create on the current device.  after_gain, before_gain, channel_gate: device
+ * fp32 [hidden] (copied on cuda_stream; create waits), NULL for ones;
+ * channel_gate is wanted by STRATA_GATE_CHANNEL.  Returns EINVAL, EUNSUPPORTED,
+ * ENOMEM, ECUDA. */
+strata_status strata_blocknorm_create(const strata_blocknorm_desc* desc, const float* after_gain,
+                                      const float* before_gain, const float* channel_gate, void* cuda_stream,
+                                      strata_blocknorm** out);
+
+/* T rows of x, y, h_out and n_out, [T][hidden] each.  y may be NULL where there
+ * is no after norm and no gate (h = residual_scale * x: the norm before a first
+ * block); h_out may be NULL with before = 1 (the stream is not kept); n_out is
+ * NULL with before = 0.  gate: fp32 [T] (STRATA_GATE_ROW, 4-byte aligned) or
+ * [T][hidden] (STRATA_GATE_ELEMENT, gate_stride), else NULL.  An output may be x
+ * or y (same pointer and stride); any other overlap is not allowed (EINVAL at the
+ * same address).  T = 0 does nothing.  A row's bits do not depend on the other
+ * rows.  One handle may run on several streams at once. */
+strata_status strata_blocknorm_forward(strata_blocknorm* h, const void* x, int64_t x_stride, const void* y,
+                                       int64_t y_stride, const void* gate, int64_t gate_stride, void* h_out,
+                                       int64_t h_stride, void* n_out, int64_t n_stride, int32_t dtype, int32_t T,
+                                       void* cuda_stream);
+
+/* Free it (its launches must have finished).  NULL is accepted. */
+strata_status strata_blocknorm_destroy(strata_blocknorm* h);
+
 /* Free the handle and everything it owns.  NULL is accepted (returns OK). */
 strata_status strata_window_destroy(strata_window* h);
 

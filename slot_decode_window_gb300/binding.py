@@ -29,9 +29,14 @@ EXPORTED = ("strata_window_create", "strata_moe_window_forward", "strata_window_
             "strata_head_query", "strata_head_set_profiling", "strata_head_timings", "strata_head_destroy",
             "strata_window_slots", "strata_stack_set_kv", "strata_stack_forward_kv", "strata_qknorm_create",
             "strata_qknorm_forward", "strata_qknorm_destroy", "strata_kv8_create", "strata_kv8_append",
-            "strata_kv8_read", "strata_kv8_attend", "strata_kv8_sync", "strata_kv8_query", "strata_kv8_destroy")
+            "strata_kv8_read", "strata_kv8_attend", "strata_kv8_sync", "strata_kv8_query", "strata_kv8_destroy",
+            "strata_linear_create", "strata_linear_forward", "strata_linear_sync", "strata_linear_query",
+            "strata_linear_destroy", "strata_sort_create", "strata_sort_route", "strata_sort_plan",
+            "strata_sort_gather", "strata_sort_combine", "strata_sort_combine_backward", "strata_sort_destroy",
+            "strata_blocknorm_create", "strata_blocknorm_forward", "strata_blocknorm_destroy")
 STRATA_F32, STRATA_F16, STRATA_BF16 = range(3)
 STRATA_KV8_E4M3, STRATA_KV8_INT8 = range(2)
+STRATA_GATE_NONE, STRATA_GATE_CHANNEL, STRATA_GATE_ROW, STRATA_GATE_ELEMENT = range(4)
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -129,6 +134,23 @@ class strata_kv8_cache(ctypes.Structure):
 class strata_kv8_rows(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_seq", "n_rows", "max_rows")] + \
         [(n, ctypes.c_void_p) for n in ("row_start", "slot", "length")]
+
+
+class strata_linear_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "in", "out", "bits", "block", "max_rows")]
+
+
+class strata_sort_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_experts", "top_k", "renorm_topk")]
+
+
+class strata_sort_order(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("counts", "offsets", "entries", "place")]
+
+
+class strata_blocknorm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "after", "before", "gate", "sigmoid")] + \
+        [(n, ctypes.c_float) for n in ("eps", "residual_scale", "block_scale")]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -237,6 +259,25 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.strata_kv8_query.restype = ctypes.c_int
     lib.strata_kv8_destroy.argtypes = [vp]
     lib.strata_kv8_destroy.restype = ctypes.c_int
+    lib.strata_linear_create.argtypes = [P(strata_linear_desc), P(strata_qmat), P(strata_qmat), vp, P(vp)]
+    lib.strata_linear_forward.argtypes = [vp, vp, i64, vp, i64, i32, i32, vp, vp]
+    lib.strata_linear_sync.argtypes = [vp]
+    lib.strata_linear_query.argtypes = [vp, P(i64), P(i64)]
+    lib.strata_linear_destroy.argtypes = [vp]
+    lib.strata_sort_create.argtypes = [P(strata_sort_desc), P(vp)]
+    lib.strata_sort_route.argtypes = [vp, vp, i64, vp, i32, vp, vp, vp]
+    lib.strata_sort_plan.argtypes = [vp, vp, i32, P(strata_sort_order), vp]
+    lib.strata_sort_gather.argtypes = [vp, vp, vp, i64, vp, i64, i32, i32, i32, vp]
+    lib.strata_sort_combine.argtypes = [vp, vp, vp, i64, vp, vp, i64, vp, i64, i32, i32, i32, vp]
+    lib.strata_sort_combine_backward.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, i32, i32, i32, vp]
+    lib.strata_sort_destroy.argtypes = [vp]
+    lib.strata_blocknorm_create.argtypes = [P(strata_blocknorm_desc), vp, vp, vp, vp, P(vp)]
+    lib.strata_blocknorm_forward.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp]
+    lib.strata_blocknorm_destroy.argtypes = [vp]
+    for name in ("linear_create", "linear_forward", "linear_sync", "linear_query", "linear_destroy", "sort_create",
+                 "sort_route", "sort_plan", "sort_gather", "sort_combine", "sort_combine_backward", "sort_destroy",
+                 "blocknorm_create", "blocknorm_forward", "blocknorm_destroy"):
+        getattr(lib, "strata_" + name).restype = ctypes.c_int
     lib.strata_status_str.argtypes = [ctypes.c_int]
     lib.strata_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -489,6 +530,87 @@ def strata_kv8_query(handle):
 
 def strata_kv8_destroy(handle) -> int:
     return load().strata_kv8_destroy(handle)
+
+
+def strata_linear_create(desc: strata_linear_desc, weight: strata_qmat, up: Optional[strata_qmat] = None, stream: int = 0):
+    """Returns (status, handle or None)."""
+    h = ctypes.c_void_p()
+    st = load().strata_linear_create(desc, weight, up, stream, ctypes.byref(h))
+    return st, (h.value if st == STRATA_OK else None)
+
+
+def strata_linear_forward(handle, x_ptr, x_stride: int, y_ptr, y_stride: int, dtype: int, T: int, offsets_ptr=None,
+                          stream: int = 0) -> int:
+    return load().strata_linear_forward(handle, x_ptr, x_stride, y_ptr, y_stride, dtype, T, offsets_ptr, stream)
+
+
+def strata_linear_sync(handle) -> int:
+    return load().strata_linear_sync(handle)
+
+
+def strata_linear_query(handle):
+    """Returns (status, weight_bytes, workspace_bytes)."""
+    a, b = ctypes.c_int64(), ctypes.c_int64()
+    st = load().strata_linear_query(handle, ctypes.byref(a), ctypes.byref(b))
+    return st, a.value, b.value
+
+
+def strata_linear_destroy(handle) -> int:
+    return load().strata_linear_destroy(handle)
+
+
+def strata_sort_create(desc: strata_sort_desc):
+    """Returns (status, handle or None)."""
+    h = ctypes.c_void_p()
+    st = load().strata_sort_create(desc, ctypes.byref(h))
+    return st, (h.value if st == STRATA_OK else None)
+
+
+def strata_sort_route(handle, logits_ptr, stride: int, bias_ptr, T: int, idx_ptr, w_ptr, stream: int = 0) -> int:
+    return load().strata_sort_route(handle, logits_ptr, stride, bias_ptr, T, idx_ptr, w_ptr, stream)
+
+
+def strata_sort_plan(handle, idx_ptr, T: int, order: strata_sort_order, stream: int = 0) -> int:
+    return load().strata_sort_plan(handle, idx_ptr, T, order, stream)
+
+
+def strata_sort_gather(handle, place_ptr, x_ptr, x_stride: int, xs_ptr, xs_stride: int, dtype: int, T: int, width: int,
+                       stream: int = 0) -> int:
+    return load().strata_sort_gather(handle, place_ptr, x_ptr, x_stride, xs_ptr, xs_stride, dtype, T, width, stream)
+
+
+def strata_sort_combine(handle, place_ptr, z_ptr, z_stride: int, w_ptr, base_ptr, base_stride: int, y_ptr, y_stride: int,
+                        dtype: int, T: int, width: int, stream: int = 0) -> int:
+    return load().strata_sort_combine(handle, place_ptr, z_ptr, z_stride, w_ptr, base_ptr, base_stride, y_ptr, y_stride,
+                                      dtype, T, width, stream)
+
+
+def strata_sort_combine_backward(handle, place_ptr, dy_ptr, dy_stride: int, z_ptr, z_stride: int, w_ptr, dz_ptr,
+                                 dz_stride: int, dw_ptr, dtype: int, T: int, width: int, stream: int = 0) -> int:
+    return load().strata_sort_combine_backward(handle, place_ptr, dy_ptr, dy_stride, z_ptr, z_stride, w_ptr, dz_ptr,
+                                               dz_stride, dw_ptr, dtype, T, width, stream)
+
+
+def strata_sort_destroy(handle) -> int:
+    return load().strata_sort_destroy(handle)
+
+
+def strata_blocknorm_create(desc: strata_blocknorm_desc, after_ptr=None, before_ptr=None, channel_ptr=None,
+                            stream: int = 0):
+    """Returns (status, handle or None)."""
+    h = ctypes.c_void_p()
+    st = load().strata_blocknorm_create(desc, after_ptr, before_ptr, channel_ptr, stream, ctypes.byref(h))
+    return st, (h.value if st == STRATA_OK else None)
+
+
+def strata_blocknorm_forward(handle, x_ptr, x_stride: int, y_ptr, y_stride: int, gate_ptr, gate_stride: int, h_ptr,
+                             h_stride: int, n_ptr, n_stride: int, dtype: int, T: int, stream: int = 0) -> int:
+    return load().strata_blocknorm_forward(handle, x_ptr, x_stride, y_ptr, y_stride, gate_ptr, gate_stride, h_ptr,
+                                           h_stride, n_ptr, n_stride, dtype, T, stream)
+
+
+def strata_blocknorm_destroy(handle) -> int:
+    return load().strata_blocknorm_destroy(handle)
 
 
 def check(status: int, what: str) -> None:
@@ -1005,6 +1127,318 @@ class KvCache8:
     def close(self) -> None:
         if getattr(self, "handle", None):
             strata_kv8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _rows(t, shape, what: str) -> int:
+    """The distance between rows, in elements, of a CUDA tensor [T][width] whose rows are contiguous."""
+    st = t.stride()
+    if t.shape != shape or (st[1] != 1 and shape[1] > 1) or not t.is_cuda or t.dtype not in _DTYPE:
+        raise StrataError(STRATA_EINVAL, f"{what}: want a CUDA tensor [{shape[0]}][{shape[1]}] of float32, float16 or "
+                                         "bfloat16 whose rows are contiguous")
+    return st[0] if shape[0] > 1 else shape[1]
+
+
+def _on(t, device: int, what: str) -> None:
+    if t.get_device() != device:
+        raise StrataError(STRATA_EINVAL, f"{what}: want a tensor on the handle's device")
+
+
+def _words(t, shape, dtype, device: int, what: str):
+    """The pointer of a contiguous CUDA tensor of this shape and 4-byte type on the device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise StrataError(STRATA_EINVAL, f"{what}: want a contiguous {dtype} tensor {list(shape)} on the handle's device")
+    return t.data_ptr()
+
+
+class Linear:
+    """Products with a stack of 4-bit matrices (block format: codes uint8 [n][rows][cols / 2], scale and min 16-bit
+    [n][rows][cols / 32], on one CUDA device), as ``workloads.QMat``; with ``up`` (the same shape) silu(W x) * (U x).
+    The handle keeps its own copy.  max_rows: most rows of a call.
+
+    Calls of more than 8 rows, or with offsets, use the handle's workspace: they, and replays of captured ones, must not
+    run at the same time.  On one stream they do not; across streams, order them with events.
+    """
+
+    def __init__(self, weight, up=None, max_rows: int = 8, stream=None):
+        torch = _with_torch()
+        n, rows, cols = weight.codes.shape[0], weight.rows, weight.cols
+        device = weight.codes.get_device()
+        for q in (weight, up):
+            if q is None:
+                continue
+            if (q.rows, q.cols, q.bits, q.block) != (rows, cols, weight.bits, weight.block) or q.bits < 1 or q.block < 1:
+                raise StrataError(STRATA_EINVAL, "Linear: up has weight's shape and format")
+            for t, size, width in ((q.codes, 1, cols * q.bits // 8), (q.scale, 2, cols // q.block),
+                                   (q.min, 2, cols // q.block)):
+                if not t.is_cuda or t.element_size() != size or t.shape != (n, rows, width) or not t.is_contiguous() or \
+                        t.get_device() != device:
+                    raise StrataError(STRATA_EINVAL, "Linear: want contiguous CUDA codes [n][rows][cols*bits/8] and 16-bit "
+                                                     "scale, min [n][rows][cols/block] on one device")
+        self.n, self.rows, self.cols, self.max_rows, self.device = n, rows, cols, max_rows, device
+        with torch.cuda.device(device):
+            s = (stream or torch.cuda.current_stream()).cuda_stream
+            st, h = strata_linear_create(strata_linear_desc(n, cols, rows, weight.bits, weight.block, max_rows),
+                                         _qmat(weight), _qmat(up) if up is not None else None, s)
+        check(st, "strata_linear_create")
+        self.handle = h
+        self._forward = load().strata_linear_forward
+
+    def forward(self, x, y=None, offsets=None, stream=None):
+        """Enqueue x [T][cols]; returns y [T][rows] of the same type, a new tensor unless given.  offsets (CUDA int32
+        [n + 1], wanted where n > 1): matrix i takes rows offsets[i] to offsets[i + 1] - 1; rows of no matrix are not
+        written."""
+        T = x.shape[0] if x.dim() == 2 else -1
+        xs = _rows(x, (T, self.cols), "x")
+        _on(x, self.device, "x")
+        ys = self.rows
+        if y is None:
+            y = _empty((T, self.rows), x.dtype, x.device, stream)
+        else:
+            ys = _rows(y, (T, self.rows), "y")
+            _same(y, x, "y")
+        op = _int32(offsets, self.n + 1, self.device, "offsets") if offsets is not None else None
+        st = self._forward(self.handle, x.data_ptr(), xs, y.data_ptr(), ys, _DTYPE[x.dtype], T, op,
+                           _raw_stream(self.device, stream))
+        if st != STRATA_OK:
+            check(st, "strata_linear_forward")
+        return y
+
+    def sync(self) -> None:
+        check(strata_linear_sync(self.handle), "strata_linear_sync")
+
+    def bytes(self):
+        """(bytes of the matrices, bytes of the workspace)."""
+        st, a, b = strata_linear_query(self.handle)
+        check(st, "strata_linear_query")
+        return a, b
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            strata_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SortPlan:
+    """The order of T*k entries: counts [E], offsets [E + 1], entries [T*k] by expert, place [T*k] of each entry (-1: no
+    expert's), CUDA int32 tensors."""
+
+    def __init__(self, counts, offsets, entries, place, T: int):
+        self.counts, self.offsets, self.entries, self.place, self.T = counts, offsets, entries, place, T
+
+
+class ExpertSort:
+    """Tokens sorted by expert and back: the router's choice, the order of the entries, the rows in it, and the experts'
+    results weighted back, with the gradient.  An entry t * k + j is row t's j-th expert."""
+
+    def __init__(self, n_experts: int, top_k: int, renorm: bool = False, device=None):
+        torch = _with_torch()
+        with torch.cuda.device(device):
+            self.device = torch.cuda.current_device()
+            st, h = strata_sort_create(strata_sort_desc(n_experts, top_k, int(renorm)))
+        check(st, "strata_sort_create")
+        self.n_experts, self.top_k, self.handle = n_experts, top_k, h
+        lib = load()
+        self._route, self._plan, self._gather = lib.strata_sort_route, lib.strata_sort_plan, lib.strata_sort_gather
+        self._combine, self._backward = lib.strata_sort_combine, lib.strata_sort_combine_backward
+
+    def route(self, logits, bias=None, stream=None):
+        """Enqueue the choice from logits float32 [T][E] (rows contiguous) with bias [E] or None; returns (topk_idx
+        int32, topk_w float32) [T][k].  -inf and NaN are never chosen (-1, weight 0)."""
+        E, k, dev = self.n_experts, self.top_k, self.device
+        T = logits.shape[0] if logits.dim() == 2 else -1
+        if logits.dtype is not _torch.float32:
+            raise StrataError(STRATA_EINVAL, "logits: want float32")
+        stride = _rows(logits, (T, E), "logits")
+        _on(logits, dev, "logits")
+        idx = _empty((T, k), _torch.int32, logits.device, stream)
+        w = _empty((T, k), _torch.float32, logits.device, stream)
+        st = self._route(self.handle, logits.data_ptr(), stride,
+                         _words(bias, (E,), _torch.float32, dev, "bias") if bias is not None else None, T, idx.data_ptr(),
+                         w.data_ptr(), _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_sort_route")
+        return idx, w
+
+    def plan(self, topk_idx, stream=None) -> SortPlan:
+        """Enqueue the order of topk_idx int32 [T][k]; entries outside 0..E-1 are no expert's."""
+        E, k, dev = self.n_experts, self.top_k, self.device
+        T = topk_idx.shape[0]
+        p = _words(topk_idx, (T, k), _torch.int32, dev, "topk_idx")
+        n = T * k
+        mem = _empty((2 * E + 1 + 2 * n,), _torch.int32, topk_idx.device, stream)
+        counts, offsets, entries, place = mem[:E], mem[E:2 * E + 1], mem[2 * E + 1:2 * E + 1 + n], mem[2 * E + 1 + n:]
+        at = mem.data_ptr()
+        st = self._plan(self.handle, p, T, strata_sort_order(at, at + 4 * E, at + 4 * (2 * E + 1), at + 4 * (2 * E + 1 + n)),
+                        _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_sort_plan")
+        return SortPlan(counts, offsets, entries, place, T)
+
+    def _weights(self, w, T: int):
+        return _words(w, (T, self.top_k), _torch.float32, self.device, "w") if w is not None else None
+
+    def gather(self, plan: SortPlan, x, out=None, stream=None):
+        """Enqueue the rows of x [T][width] in the experts' order; returns [T*k][width], a new tensor unless given; rows
+        behind the last expert's are not written.  Its gradient: combine(plan, dxs)."""
+        T, dev, width = plan.T, self.device, x.shape[-1]
+        xs = _rows(x, (T, width), "x")
+        _on(x, dev, "x")
+        os_ = width
+        if out is None:
+            out = _empty((T * self.top_k, width), x.dtype, x.device, stream)
+        else:
+            os_ = _rows(out, (T * self.top_k, width), "out")
+            _same(out, x, "out")
+        st = self._gather(self.handle, plan.place.data_ptr(), x.data_ptr(), xs, out.data_ptr(), os_, _DTYPE[x.dtype], T,
+                          width, _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_sort_gather")
+        return out
+
+    def combine(self, plan: SortPlan, z, w=None, base=None, out=None, stream=None):
+        """Enqueue base[t] + sum_j w[t][j] z[place] (w float32 [T][k], None: ones; base [T][width] or None); returns
+        [T][width], a new tensor unless given (it may be base)."""
+        T, dev, width = plan.T, self.device, z.shape[-1]
+        zs = _rows(z, (T * self.top_k, width), "z")
+        _on(z, dev, "z")
+        bs = os_ = width
+        if base is not None:
+            bs = _rows(base, (T, width), "base")
+            _same(base, z, "base")
+        if out is None:
+            out = _empty((T, width), z.dtype, z.device, stream)
+        else:
+            os_ = _rows(out, (T, width), "out")
+            _same(out, z, "out")
+        st = self._combine(self.handle, plan.place.data_ptr(), z.data_ptr(), zs, self._weights(w, T),
+                           base.data_ptr() if base is not None else None, bs, out.data_ptr(), os_, _DTYPE[z.dtype], T,
+                           width, _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_sort_combine")
+        return out
+
+    def combine_backward(self, plan: SortPlan, dy, z, w=None, dz=None, stream=None):
+        """Enqueue combine's gradient for dy [T][width]: (dz [T*k][width], a new tensor unless given (it may be z), dw
+        float32 [T][k]); rows of dz behind the last expert's are not written."""
+        T, dev, width = plan.T, self.device, z.shape[-1]
+        zs = _rows(z, (T * self.top_k, width), "z")
+        ds = _rows(dy, (T, width), "dy")
+        _on(z, dev, "z")
+        _same(dy, z, "dy")
+        os_ = width
+        if dz is None:
+            dz = _empty((T * self.top_k, width), z.dtype, z.device, stream)
+        else:
+            os_ = _rows(dz, (T * self.top_k, width), "dz")
+            _same(dz, z, "dz")
+        dw = _empty((T, self.top_k), _torch.float32, z.device, stream)
+        st = self._backward(self.handle, plan.place.data_ptr(), dy.data_ptr(), ds, z.data_ptr(), zs, self._weights(w, T),
+                            dz.data_ptr(), os_, dw.data_ptr(), _DTYPE[z.dtype], T, width, _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_sort_combine_backward")
+        return dz, dw
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            strata_sort_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class BlockNorm:
+    """Norms after and before a block with the gate and the residual:
+    h = residual_scale * x + block_scale * gate * norm(y) * after, and norm(h) * before.
+
+    after, before: the gains, CUDA float32 [hidden], or True for ones, or None for no norm.  gate: "none", "channel"
+    (channel_gate: CUDA float32 [hidden]), "row" or "element" (given to forward).  sigmoid: the gate is taken through it.
+    """
+
+    def __init__(self, hidden: int, after=None, before=None, gate: str = "none", channel_gate=None, sigmoid: bool = False,
+                 eps: float = 1e-6, residual_scale: float = 1.0, block_scale: float = 1.0, device=None, stream=None):
+        torch = _with_torch()
+        kind = {"none": STRATA_GATE_NONE, "channel": STRATA_GATE_CHANNEL, "row": STRATA_GATE_ROW,
+                "element": STRATA_GATE_ELEMENT}.get(gate)
+        if kind is None or (channel_gate is not None) != (kind == STRATA_GATE_CHANNEL):
+            raise StrataError(STRATA_EINVAL, "BlockNorm: gate is none, channel (with channel_gate), row or element")
+        given = [g for g in (after, before, channel_gate) if g is not None and g is not True]
+        for g in given:
+            if not g.is_cuda or g.dtype != torch.float32 or tuple(g.shape) != (hidden,) or not g.is_contiguous():
+                raise StrataError(STRATA_EINVAL, "BlockNorm: a gain or gate is a contiguous CUDA float32 [hidden]")
+            if device is None:
+                device = g.device
+        self.hidden, self.gate, self.before = hidden, kind, before is not None
+        with torch.cuda.device(device):
+            s = (stream or torch.cuda.current_stream()).cuda_stream
+            self.device = torch.cuda.current_device()
+            if any(g.get_device() != self.device for g in given):
+                raise StrataError(STRATA_EINVAL, "BlockNorm: want gains and gate on the handle's device")
+            ptr = [g.data_ptr() if g is not None and g is not True else None for g in (after, before, channel_gate)]
+            st, h = strata_blocknorm_create(
+                strata_blocknorm_desc(hidden, int(after is not None), int(self.before), kind, int(sigmoid), eps,
+                                      residual_scale, block_scale), *ptr, s)
+        check(st, "strata_blocknorm_create")
+        self.handle = h
+        self._forward = load().strata_blocknorm_forward
+
+    def forward(self, x, y=None, gate=None, h_out=None, n_out=None, keep: bool = True, stream=None):
+        """Enqueue x and y [T][hidden] (y None where there is no after norm and no gate), gate float32 [T] ("row") or
+        [T][hidden] of x's type ("element"); returns (h, n), new tensors unless given (each may be x or y).  keep False:
+        h is not written (None); n is None without a before norm."""
+        T, d, dev = x.shape[0] if x.dim() == 2 else -1, self.hidden, self.device
+        shape = (T, d)
+        xs = _rows(x, shape, "x")
+        _on(x, dev, "x")
+        ys = gs = hs = ns = d
+        gp = None
+        if y is not None:
+            ys = _rows(y, shape, "y")
+            _same(y, x, "y")
+        if gate is not None:
+            if self.gate == STRATA_GATE_ROW:
+                gp = _words(gate, (T,), _torch.float32, dev, "gate")
+            else:
+                gs = _rows(gate, shape, "gate")
+                _same(gate, x, "gate")
+                gp = gate.data_ptr()
+        if h_out is not None:
+            hs = _rows(h_out, shape, "h_out")
+            _same(h_out, x, "h_out")
+        elif keep:
+            h_out = _empty(shape, x.dtype, x.device, stream)
+        if n_out is not None:
+            ns = _rows(n_out, shape, "n_out")
+            _same(n_out, x, "n_out")
+        elif self.before:
+            n_out = _empty(shape, x.dtype, x.device, stream)
+        st = self._forward(self.handle, x.data_ptr(), xs, y.data_ptr() if y is not None else None, ys, gp, gs,
+                           h_out.data_ptr() if h_out is not None else None, hs,
+                           n_out.data_ptr() if n_out is not None else None, ns, _DTYPE[x.dtype], T,
+                           _raw_stream(dev, stream))
+        if st != STRATA_OK:
+            check(st, "strata_blocknorm_forward")
+        return h_out, n_out
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            strata_blocknorm_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -1,0 +1,56 @@
+// The products' matrices in the handle's own layout, and the launches of their
+// kernels (linear_pack.cu, linear_few.cu, linear_many.cu).
+//
+// A matrix [out][in] is out/16 tiles of in/64 steps.  A step (640 bytes, 0.625 a
+// weight as in the block format) is 512 bytes of codes and 8 records:
+//   codes: lane (g = lane/4, c = lane%4) has 16 bytes, a word for row g and one
+//     for row g + 8 of the step's first block of 32 columns, then the same of its
+//     second; a word holds columns 8c..8c+7 of the block, column 8c+2i in bits
+//     4i..4i+3 and column 8c+2i+1 in bits 16+4i..16+4i+3
+//   record g (16 bytes, f16): scales of row g (first block, second), of row
+//     g + 8, then the mins in the same order
+// Scales and mins carry a power of two of their row, which brings its largest
+// weight to [64, 128); the row's results are multiplied by its inverse, `undo`.
+// (A block whose scale is below 2^-20 of the row's largest weight loses low bits
+// of it: at most 2^-29 of that weight.)
+#pragma once
+#include "kv8.cuh"
+
+namespace strata {
+
+constexpr int kLinStep = 64, kLinStepBytes = 640, kLinTile = 16;
+constexpr int kLinFewRows = 8;
+constexpr int kF32 = 0, kF16 = 1, kBF16 = 2;  // strata_dtype
+
+struct LinMat {
+  const uint8_t* packed;  // [n][out/16][in/64][640]
+  const float* undo;      // [n][out]
+};
+
+struct LinArgs {
+  LinMat w[2];        // the stack, and the one behind the gate (glu)
+  int n, in, out, glu;
+  const void* x;
+  void* y;
+  long long xs, ys;
+  int dtype, T;
+  const int* offsets;  // [n + 1], or null (n = 1)
+  unsigned* err;
+};
+
+// The rows of matrix i: begin, end.  A range that is out of order or outside 0..T is empty and noted.
+__device__ __forceinline__ bool lin_rows(const LinArgs& A, int i, int& begin, int& end) {
+  begin = 0, end = A.T;
+  if (!A.offsets) return true;
+  begin = A.offsets[i], end = A.offsets[i + 1];
+  if (begin >= 0 && begin <= end && end <= A.T) return true;
+  end = begin = 0;
+  return false;
+}
+
+long long linear_packed_bytes(int n, int in, int out);
+cudaError_t launch_linear_pack(const void* codes, const uint16_t* scale, const uint16_t* mn, int n, int in, int out,
+                               uint8_t* packed, float* undo, cudaStream_t s);
+cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s);
+
+}  // namespace strata
