@@ -15,6 +15,7 @@ struct strata_linear {
   uint8_t* mem = nullptr;  // error word, then the matrices and their rows' powers of two
   unsigned* err = nullptr;
   LinMat w[2] = {};
+  void* ws = nullptr;
   long long weight_bytes = 0, ws_bytes = 0;
 };
 
@@ -25,6 +26,7 @@ void free_linear(strata_linear* h) {
   if (h->mem) {
     DeviceScope on(h->device);
     cudaFree(h->mem);
+    cudaFree(h->ws);
   }
   delete h;
 }
@@ -79,6 +81,19 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
     return STRATA_ENOMEM;
   }
   h->err = reinterpret_cast<unsigned*>(h->mem);
+  if (desc->n > 1 || desc->max_rows > kLinFewRows) {
+    h->ws_bytes = linear_many_workspace(desc->in, desc->max_rows);
+    if (cudaMalloc(&h->ws, (size_t)h->ws_bytes) != cudaSuccess) {
+      cudaGetLastError();
+      free_linear(h);
+      return STRATA_ENOMEM;
+    }
+    if (setup_linear_many() != cudaSuccess) {
+      cudaGetLastError();
+      free_linear(h);
+      return STRATA_ECUDA;
+    }
+  }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaMemsetAsync(h->mem, 0, 256, s);
   for (int m = 0; m < h->mats && e == cudaSuccess; ++m) {
@@ -116,7 +131,9 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
   A.w[0] = h->w[0], A.w[1] = h->w[1];
   A.n = d.n, A.in = d.in, A.out = d.out, A.glu = h->mats == 2;
   A.x = x, A.y = y, A.xs = x_stride, A.ys = y_stride, A.dtype = dtype, A.T = T, A.offsets = offsets, A.err = h->err;
-  if (launch_linear_few(A, h->nsm, static_cast<cudaStream_t>(cuda_stream)) != cudaSuccess) {
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool few = d.n == 1 && T <= kLinFewRows;
+  if ((few ? launch_linear_few(A, h->nsm, s) : launch_linear_many(A, h->ws, d.max_rows, h->nsm, s)) != cudaSuccess) {
     cudaGetLastError();
     return STRATA_ECUDA;
   }
