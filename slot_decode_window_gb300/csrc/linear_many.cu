@@ -8,56 +8,79 @@
 // linear_rows_kernel fills.  Weight rows on the M side leave the rows of x free
 // to be few: an expert with 20 rows costs 32 columns, not 128.
 //
-// f16 and bf16 rows: one product, W rounded to f16.  f32 rows: x and W in two
-// f16 parts each (22 bits), hi hi + hi lo + lo hi; the accumulators' adds
-// truncate, so after every 512 columns they are added to f32 registers, with
-// two sets of accumulators in turn.
+// bf16 rows: one product, W rounded to f16 (2^-11 of a weight against the 2^-8 of
+// the results' own rounding).  f16 and f32 rows: exact weights,
+//   W x = s (q - 8) x + (8 s + m) sum x   over a block of 32 columns:
+// s (q - 8) has 15 bits, two f16 parts (hi and what is left, both exact); after
+// every 8 steps comes a step whose "weights" are m and 8 s of its 16 blocks and
+// whose "x" are their sums, in two f16 parts.  f16 rows: hi x + lo x.  f32 rows: x
+// in two f16 parts (22 bits), lo hi + hi lo + hi hi; the accumulators' adds
+// truncate, so every two steps they are added to f32 registers, with two sets of
+// accumulators in turn.
 //
-// Roles (18 warps): 8 of conversion (each its quarter of the lanes of one half,
-// its codes through a ring of its own with cp.async), 8 of results (each a
-// quarter of the lanes and half of the rows of x), one of copies of x, one that
-// issues the products.  CTAs (one per SM) take the tiles of all matrices in
-// turn, weight rows fastest, so that concurrent CTAs share rows of x in L2.
+// Roles (28 warps): 16 of conversion (16 weight rows each, a quarter of the lanes
+// of tensor memory to every four of them, codes through a ring of its own), 8 of
+// results (each a quarter of the lanes and half of the rows of x), one of copies
+// of x, one for each half that issues its products (one warp for both spent more
+// time between a step's products and the next one's than the tensor cores have
+// work queued); one warp fills the warpgroup.  CTAs (one
+// per SM) take the tiles of all matrices in turn, weight rows fastest, so that
+// concurrent CTAs share rows of x in L2.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 
 namespace strata {
 namespace {
 
-constexpr int kManyThreads = 18 * 32, kLoadWarp = 16, kMmaWarp = 17;
-constexpr int kFifo = 8;                      // steps of codes a conversion warp has under way
-constexpr int kFifoStep = 2 * kLinStepBytes;  // its two tiles' step
-constexpr int kChunk = 8;                     // steps between sums of f32 rows
+constexpr int kConvert = 16, kResults = 8;    // warps
+constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1;
+constexpr int kManyThreads = (kConvert + kResults + 4) * 32;
+// Registers a thread: at launch, and by role; the roles' shares are drawn from the launch's.
+constexpr int kRegs = 72, kRegConvert = 56, kRegResults = 120, kRegIssue = 40;
+static_assert(kConvert * kRegConvert + kResults * kRegResults + 4 * kRegIssue <= (kConvert + kResults + 4) * kRegs, "register split");
+constexpr int kSlots = 4, kSlotSteps = 2;     // ring of codes of a conversion warp
+constexpr int kSlot = kSlotSteps * kLinStepBytes;
+constexpr int kChunk = 2;                     // steps between sums of f32 rows
+constexpr int kGroup = 8;                     // steps to a step of their blocks' sums
 constexpr int kMaxMats = 1024;
 
-template <bool TWO> struct ManyPlan {
-  static constexpr int kParts = TWO ? 2 : 1;
-  static constexpr int kCols = TWO ? 64 : 192;   // most rows of x in a tile
-  static constexpr int kSets = TWO ? 2 : 1;      // of accumulators
+template <int DT> struct ManyPlan {
+  static constexpr bool kSums = DT != kBF16;     // exact weights
+  static constexpr int kXParts = DT == kF32 ? 2 : 1, kWParts = kSums ? 2 : 1;
+  static constexpr int kCols = DT == kF32 ? 64 : DT == kF16 ? 128 : 192;  // most rows of x in a tile
+  static constexpr int kSets = DT == kF32 ? 2 : 1;  // of accumulators
   static constexpr int kA = 2 * kSets * kCols;   // first column of the weights in tensor memory
-  static constexpr int kStages = TWO ? 7 : 5;    // of x
+  static constexpr int kStages = DT == kBF16 ? 5 : 7;  // of x
   static constexpr int kPart = kCols * 128;      // bytes of a part of a stage of x
-  static constexpr int kStage = kPart * kParts;
+  static constexpr int kStage = kPart * kXParts;
   static constexpr int kFifoOff = kStages * kStage;
-  static constexpr int kBars = kFifoOff + 8 * kFifo * kFifoStep;
-  static constexpr int kMisc = kBars + 256;
+  static constexpr int kBars = kFifoOff + kConvert * kSlots * kSlot;
+  static constexpr int kMisc = kBars + 1024;
   static constexpr int kPre = kMisc + 64;        // [n + 1] tiles before each matrix
-  static_assert(kA + 4 * 32 * kParts <= 512, "tensor memory");
+  static_assert(kA + 4 * 32 * kWParts <= 512, "tensor memory");
   static_assert(kPre + (kMaxMats + 1) * 4 <= 232448, "shared memory");
 };
 
+__host__ __device__ inline int sum_steps(int nks) { return (nks + kGroup - 1) / kGroup; }
+// Whether a step of sums follows step ks.
+__device__ __forceinline__ bool sums_follow(int ks, int nks) { return ks % kGroup == kGroup - 1 || ks == nks - 1; }
+
 struct ManyArgs {
   LinArgs L;
-  const uint8_t* xt;     // [parts][in / 64][pad][128 bytes], swizzled
+  const uint8_t* xt;     // [parts][in / 64][pad][128 bytes], swizzled, then [groups][pad][128 bytes] of sums (f16, f32)
   const float* undo_x;   // [pad]
   long long pad;         // rows of the workspace
 };
+
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // --- rows of x into the workspace --------------------------------------------------
 
 // A warp takes a row: its largest magnitude, then the values times a power of two that brings it to [2^14, 2^15), as f16
 // (f32: two of them).  A lane writes 16 bytes: pairs j of the four groups of eight columns of a block, the order in which
-// the conversion warps' stores put the codes; the 16-byte pieces of a row's 128 are swizzled by the row.
+// the conversion warps' stores put the codes; the 16-byte pieces of a row's 128 are swizzled by the row.  The blocks' sums
+// go to steps of their own, in the order of `convert_sums`; blocks past the last are zeros.
 template <int DT>
 __global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long long xs, int T, int in, uint8_t* xt, long long pad,
                                                           float* undo) {
@@ -89,36 +112,54 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long lo
   const float mul = pow2i(up);
   if (lane == 0) undo[row] = pow2i(-up);
   const long long part = (long long)(in / 64) * pad * 128;
-  for (int i = lane; i < in / 8; i += 32) {
+  uint8_t* sums = xt + part * ManyPlan<DT>::kXParts;
+  const int pieces = in / 8, all = ManyPlan<DT>::kSums ? sum_steps(in / 64) * kGroup * 8 : pieces;
+  for (int i = lane; i < all; i += 32) {  // (`all` is a multiple of 8: the four lanes of a block stay together)
     const int first = (i >> 2) * 32 + (i & 3) * 2, ks = i >> 3, at = (i & 7) ^ (row & 7);
-    uint32_t hi[4], lo[4];
+    const unsigned quad = 0xFu << (lane & 28);
+    float sum = 0.f;
+    if (i < pieces) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float a, b;
-      if constexpr (DT == kF32) {
-        const float2 t = *reinterpret_cast<const float2*>(src + (first + 8 * c) * 4);
-        a = t.x, b = t.y;
-      } else {
-        const uint32_t t = *reinterpret_cast<const uint32_t*>(src + (first + 8 * c) * 2);
-        if constexpr (DT == kF16) {
-          const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&t));
-          a = h.x, b = h.y;
+      for (int c = 0; c < 4; ++c) {
+        float a, b;
+        if constexpr (DT == kF32) {
+          const float2 t = *reinterpret_cast<const float2*>(src + (first + 8 * c) * 4);
+          a = t.x, b = t.y;
         } else {
-          a = __uint_as_float(t << 16), b = __uint_as_float(t & 0xFFFF0000u);
+          const uint32_t t = *reinterpret_cast<const uint32_t*>(src + (first + 8 * c) * 2);
+          if constexpr (DT == kF16) {
+            const float2 h = __half22float2(as_half2(t));
+            a = h.x, b = h.y;
+          } else {
+            a = __uint_as_float(t << 16), b = __uint_as_float(t & 0xFFFF0000u);
+          }
+        }
+        a *= mul, b *= mul;
+        sum += a + b;
+        const __half2 h = __floats2half2_rn(a, b);
+        hi[c] = as_u32(h);
+        if constexpr (DT == kF32) {
+          const float2 back = __half22float2(h);
+          lo[c] = pack_half2(a - back.x, b - back.y);
         }
       }
-      a *= mul, b *= mul;
-      const __half2 h = __floats2half2_rn(a, b);
-      hi[c] = *reinterpret_cast<const uint32_t*>(&h);
-      if constexpr (DT == kF32) {
-        const float2 back = __half22float2(h);
-        lo[c] = pack_half2(a - back.x, b - back.y);
-      }
+      uint4* dst = reinterpret_cast<uint4*>(xt + ((long long)ks * pad + row) * 128 + at * 16);
+      *dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (DT == kF32)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(xt + ((long long)ks * pad + row) * 128 + at * 16);
-    *dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (DT == kF32)
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (ManyPlan<DT>::kSums) {
+      // the block's sum / 32 (at most 2^15) in two parts, to the columns of its min (lane 0 of the four) and its 8 s (lane 1)
+      sum += __shfl_xor_sync(quad, sum, 1);
+      sum += __shfl_xor_sync(quad, sum, 2);
+      sum *= 0x1p-5f;
+      const int kind = i & 3, blk = (i >> 2) & 1, step = ks % kGroup, piece = (step >> 2) * 4 + blk * 2 + kind;
+      const __half h = __float2half_rn(sum);
+      if (kind < 2)
+        *reinterpret_cast<uint32_t*>(sums + ((long long)(ks / kGroup) * pad + row) * 128 + (piece ^ (row & 7)) * 16 + (step & 3) * 4) =
+            pack_half2(__half2float(h), sum - __half2float(h));
+    }
   }
 }
 
@@ -170,8 +211,25 @@ __device__ __forceinline__ void tc_st_16x128_x8(uint32_t addr, const uint32_t (&
       : "memory");
 }
 
-__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ void tc_st_16x128_x4(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Products and commits of the lane whose `lead` is not 0, without a branch.
+__device__ __forceinline__ void tc_mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
+}
 
 // A step of a tile, row g and row g + 8 of this lane, into the registers of a 16x128b store: the word's pair i goes to
 // column 4 i + c of its block's 16, register 2 i (row g) or 2 i + 1 (row g + 8).  A masked code is the subnormal q 2^-24
@@ -194,42 +252,58 @@ __device__ __forceinline__ void convert(const uint4& code, const uint4& rec, uin
   }
 }
 
-// The same in two parts: (16 + q) s + (m - 16 s) in f32, its f16 and what is left.
-__device__ __forceinline__ void convert_two(const uint4& code, const uint4& rec, uint32_t (&hi)[16], uint32_t (&lo)[16]) {
-  const uint32_t words[4] = {code.x, code.y, code.z, code.w};
-  const uint32_t sr[2] = {rec.x, rec.y}, mr[2] = {rec.z, rec.w};
+// s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the product's
+// f16 leaves at most 5 bits.
+__device__ __forceinline__ void convert_two(const uint4& code, const uint4& rec, int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f);
 #pragma unroll
-  for (int wi = 0; wi < 4; ++wi) {
-    const int row = wi & 1, blk = wi >> 1;
-    const float2 sp = __half22float2(as_half2(sr[row])), mp = __half22float2(as_half2(mr[row]));
-    const float s = blk ? sp.y : sp.x, m = fmaf(-16.f, s, blk ? mp.y : mp.x);
-    const uint32_t w = words[wi];
+  for (int row = 0; row < 2; ++row) {
+    const uint32_t word = blk ? row ? code.w : code.z : row ? code.y : code.x;
+    const __half2 s = as_half2(row ? rec.y : rec.x), sv = blk ? __high2half2(s) : __low2half2(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t a = w << (19 - 4 * i), b = i == 0 ? w << 3 : w >> (4 * i - 3);
-      const float v0 = fmaf(__uint_as_float((a & 0x00780000u) | 0x41800000u), s, m);
-      const float v1 = fmaf(__uint_as_float((b & 0x00780000u) | 0x41800000u), s, m);
-      const __half2 h = __floats2half2_rn(v0, v1);
-      const float2 back = __half22float2(h);
-      hi[blk * 8 + 2 * i + row] = as_u32(h);
-      lo[blk * 8 + 2 * i + row] = pack_half2(v0 - back.x, v1 - back.y);
+      const uint32_t w = i < 2 ? word : word >> 8;
+      const __half2 q = i & 1 ? __hadd2(as_half2((w & 0x00F000F0u) | 0x54005400u), high)
+                              : __hadd2(as_half2((w & 0x000F000Fu) | 0x64006400u), low);
+      const __half2 h = __hmul2(q, sv);
+      hi[2 * i + row] = as_u32(h);
+      lo[2 * i + row] = as_u32(__hfma2(q, sv, __hneg2(h)));
+    }
+  }
+}
+
+// The weights of a step of sums from the records of steps c and 4 + c of the group: the min (times 32) in column 4 i + c for
+// even i, 8 s (times 32) for odd i, i = 4 (step / 4) + 2 block + kind; a column's two f16 meet the sum's two parts.
+__device__ __forceinline__ void convert_sums(const uint4 (&rec)[2], uint32_t (&r)[16]) {
+  const __half2 k32 = __float2half2_rn(32.f), k256 = __float2half2_rn(256.f);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const __half2 s[2] = {__hmul2(as_half2(rec[p].x), k256), __hmul2(as_half2(rec[p].y), k256)};
+    const __half2 m[2] = {__hmul2(as_half2(rec[p].z), k32), __hmul2(as_half2(rec[p].w), k32)};
+#pragma unroll
+    for (int row = 0; row < 2; ++row) {
+      r[p * 8 + 0 + row] = as_u32(__low2half2(m[row]));
+      r[p * 8 + 2 + row] = as_u32(__low2half2(s[row]));
+      r[p * 8 + 4 + row] = as_u32(__high2half2(m[row]));
+      r[p * 8 + 6 + row] = as_u32(__high2half2(s[row]));
     }
   }
 }
 
 // --- results ------------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t pack16(int dtype, float a, float b) {
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (DT == kF16) return pack_half2(a, b);
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-  const __half2 y = __floats2half2_rn(a, b);
-  return dtype == kBF16 ? *reinterpret_cast<const uint32_t*>(&x) : as_u32(y);
+  return *reinterpret_cast<const uint32_t*>(&x);
 }
 
 // A lane's 16 results of one weight row f for rows r0.. of x.  16-bit types: neighbouring lanes trade, so that each
 // stores two weight rows of one row of x.
-template <bool TWO>
+template <int DT>
 __device__ __forceinline__ void store16(const LinArgs& L, const float (&v)[16], int r0, int begin, int end, int f, int lane) {
-  if constexpr (TWO) {
+  if constexpr (DT == kF32) {
     float* y = static_cast<float*>(L.y) + f;
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -241,24 +315,32 @@ __device__ __forceinline__ void store16(const LinArgs& L, const float (&v)[16], 
     for (int j = 0; j < 16; j += 2) {
       const float give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
       const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-      const uint32_t two = odd ? pack16(L.dtype, got, keep) : pack16(L.dtype, keep, got);
+      const uint32_t two = odd ? pack16<DT>(got, keep) : pack16<DT>(keep, got);
       const int r = r0 + j + odd;
       if (r >= begin && r < end && f < L.out) *reinterpret_cast<uint32_t*>(y + (long long)r * L.ys) = two;
     }
   }
 }
 
+__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(p) + i);
+    v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+  }
+}
+
 // --- the kernel ---------------------------------------------------------------------
 
-template <bool TWO, bool GLU>
+template <int DT, bool GLU>
 __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __grid_constant__ ManyArgs A) {
-  using P = ManyPlan<TWO>;
+  using P = ManyPlan<DT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const LinArgs& L = A.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
   uint64_t *x_full = bars, *x_empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 18, *d_full = bars + 20,
-           *d_empty = bars + 22, *last = bars + 24;
+           *d_empty = bars + 22, *last = bars + 24, *code_full = bars + 32;  // [kConvert][kSlots]
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
   int* pre = reinterpret_cast<int*>(smem + P::kPre);
@@ -270,10 +352,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   const int nks = L.in / kLinStep, w_tiles = L.out / kLinTile;
   const int m_tiles = (L.out + (GLU ? 127 : 255)) / (GLU ? 128 : 256);
   if (tid == 0) {
-    for (int i = 0; i < P::kStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], 8), mbar_init(&a_empty[i], 1);
-    for (int i = 0; i < P::kSets; ++i) mbar_init(&d_full[i], 1), mbar_init(&d_empty[i], 8);
-    mbar_init(last, 1);
+    for (int i = 0; i < P::kStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 2);
+    for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], kConvert), mbar_init(&a_empty[i], 2);
+    for (int i = 0; i < P::kSets; ++i) mbar_init(&d_full[i], 2), mbar_init(&d_empty[i], kResults);
+    for (int i = 0; i < kConvert * kSlots; ++i) mbar_init(&code_full[i], 1);
+    mbar_init(last, 2);
     *dead = 0;
     fence_mbar_init();
   }
@@ -302,93 +385,113 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_word;
+  const uint32_t tmem = *tmem_word;  // (0: all of tensor memory is this CTA's, which the products' addresses count on)
   const int total = pre[L.n];
 
-  if (warp < 8) {
-    // ---- conversion: codes of two tiles of 16 weight rows, a step at a time ----
-    const int quarter = warp & 3, half = warp >> 2;
-    uint8_t* fifo = smem + P::kFifoOff + warp * (kFifo * kFifoStep);
-    const uint32_t lanes = tmem + ((uint32_t)quarter << 21) + P::kA + half * 32 * P::kParts;
-    // what is fetched next: a step of an item's two tiles
-    int f_item = blockIdx.x, f_ks = 0, f_slot = 0;
-    const uint8_t *src0 = nullptr, *src1 = nullptr;
-    auto find = [&]() {
-      src0 = src1 = nullptr;
-      if (f_item >= total) return;
-      const Tile t = tile_at<P::kCols>(L, pre, m_tiles, f_item);
-      const LinMat& w = L.w[GLU ? half : 0];
-      const int wt = (GLU ? t.mt * 8 : t.mt * 16 + half * 8) + quarter * 2;
-      const uint8_t* base = w.packed + ((long long)t.mat * w_tiles + wt) * nks * kLinStepBytes;
-      if (wt < w_tiles) src0 = base;
-      if (wt + 1 < w_tiles) src1 = base + (long long)nks * kLinStepBytes;
-    };
+  if (warp < kConvert) {
+    // ---- conversion: the codes of 16 weight rows of a half, a step at a time ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConvert));
+    const int quarter = warp & 3, half = (warp >> 2) & 1, upper = warp >> 3;
+    uint8_t* ring = smem + P::kFifoOff + warp * (kSlots * kSlot);
+    uint64_t* full = code_full + warp * kSlots;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32 + upper * 16) << 16) + P::kA + half * 32 * P::kWParts;
+    const int wt0 = half * (GLU ? 0 : 8) + quarter * 2 + upper;
+    // what is copied next: steps of an item's tile (a tile past the last one is not copied; its lanes' results are not used)
+    int f_item = blockIdx.x, f_left = 0, f_slot = 0, copies = 0;
+    const uint8_t* src = nullptr;
     auto fetch = [&]() {
-      uint8_t* slot = fifo + f_slot * kFifoStep;
-      if (src0) {
-        cp_async16(slot + lane * 16, src0 + lane * 16);
-        if (lane < 8) cp_async16(slot + 512 + lane * 16, src0 + 512 + lane * 16);
-        src0 += kLinStepBytes;
+      while (f_left == 0) {
+        if (f_item >= total) return;
+        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, f_item);
+        const int wt = t.mt * (GLU ? 8 : 16) + wt0;
+        src = L.w[GLU ? half : 0].packed + ((long long)t.mat * w_tiles + wt) * nks * kLinStepBytes;
+        f_item += gridDim.x;
+        if (wt < w_tiles) f_left = nks;
       }
-      if (src1) {
-        cp_async16(slot + kLinStepBytes + lane * 16, src1 + lane * 16);
-        if (lane < 8) cp_async16(slot + kLinStepBytes + 512 + lane * 16, src1 + 512 + lane * 16);
-        src1 += kLinStepBytes;
+      const int steps = min(f_left, kSlotSteps);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[f_slot], steps * kLinStepBytes);
+        bulk_g2s(ring + f_slot * kSlot, src, steps * kLinStepBytes, &full[f_slot]);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (++f_slot == kFifo) f_slot = 0;
-      if (f_item < total && ++f_ks == nks) {
-        f_ks = 0, f_item += gridDim.x;
-        find();
-      }
+      src += kSlot, f_left -= steps, ++copies;
+      if (++f_slot == kSlots) f_slot = 0;
     };
-    find();
-    for (int i = 0; i < kFifo - 1; ++i) fetch();
-    int at = 0, slot_at = 0;
+#pragma unroll 1
+    for (int i = 0; i < kSlots; ++i) fetch();
+    int slot = 0, st = 0;
+    uint32_t slot_ph = 0, a_ph = 1;  // (a fresh barrier passes a wait for the phase before its first)
     bool ok = true;
+    uint4 kept[2] = {};  // the records of steps c and 4 + c of a group
     for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
       const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-      const int wt = (GLU ? t.mt * 8 : t.mt * 16 + half * 8) + quarter * 2;
-      for (int ks = 0; ks < nks; ++ks, ++at) {
-        __syncwarp();  // the slot of the step before has been read
-        fetch();
-        asm volatile("cp.async.wait_group %0;" ::"n"(kFifo - 1) : "memory");
-        __syncwarp();
-        const uint8_t* slot = fifo + slot_at * kFifoStep;
-        if (++slot_at == kFifo) slot_at = 0;
-        const int st = at & 1;
-        const uint32_t to = lanes + st * 64 * P::kParts;
-        bool waited = false;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (wt + h >= w_tiles) break;  // its lanes' results are not used
-          const uint4 code = *reinterpret_cast<const uint4*>(slot + h * kLinStepBytes + lane * 16);
-          const uint4 rec = *reinterpret_cast<const uint4*>(slot + h * kLinStepBytes + 512 + (lane >> 2) * 16);
-          uint32_t r[16], r_lo[TWO ? 16 : 1];
-          if constexpr (TWO)
-            convert_two(code, rec, r, r_lo);
-          else
-            convert(code, rec, r);
-          if (!waited) {
-            waited = true;
-            if (at >= 2 && !(ok = wait_warp(&a_empty[st], ((at >> 1) - 1) & 1, dead, err))) break;
-            tc_fence_after();
+      const bool live = t.mt * (GLU ? 8 : 16) + wt0 < w_tiles;
+#pragma unroll 1
+      for (int ks = 0; ks < nks; ++ks) {
+        const int in_slot = ks % kSlotSteps;
+        if (live && in_slot == 0 && !(ok = wait_warp(&full[slot], slot_ph, dead, err))) break;
+        uint32_t to = lanes + st * 64 * P::kWParts;
+        const uint8_t* step = ring + slot * kSlot + in_slot * kLinStepBytes;
+        const uint4 code = *reinterpret_cast<const uint4*>(step + lane * 16);
+        const uint4 rec = *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16);
+        if constexpr (!P::kSums) {
+          uint32_t r[16];
+          convert(code, rec, r);
+          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+          tc_fence_after();
+          if (live) tc_st_16x128_x8(to, r);
+        } else {
+          uint32_t hi[8], lo[8];
+          convert_two(code, rec, 0, hi, lo);
+          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+          tc_fence_after();
+          if (live) {
+            tc_st_16x128_x4(to, hi);
+            tc_st_16x128_x4(to + 32, lo);
+            convert_two(code, rec, 1, hi, lo);
+            tc_st_16x128_x4(to + 16, hi);
+            tc_st_16x128_x4(to + 48, lo);
           }
-          tc_st_16x128_x8(to + ((uint32_t)(16 * h) << 16), r);
-          if constexpr (TWO) tc_st_16x128_x8(to + 32 + ((uint32_t)(16 * h) << 16), r_lo);
+          if ((ks & 3) == (lane & 3)) {
+            if (ks & 4)
+              kept[1] = rec;
+            else
+              kept[0] = rec;
+          }
         }
-        if (!ok) break;
-        if (!waited && at >= 2 && !(ok = wait_warp(&a_empty[st], ((at >> 1) - 1) & 1, dead, err))) break;
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&a_full[st]);
+        if (st) a_ph ^= 1;
+        st ^= 1;
+        if (live && (in_slot == kSlotSteps - 1 || ks == nks - 1)) {  // the slot has been read
+          if (++slot == kSlots) slot = 0, slot_ph ^= 1;
+          fetch();
+        }
+        if constexpr (P::kSums) {
+          if (!sums_follow(ks, nks)) continue;
+          to = lanes + st * 64 * P::kWParts;
+          uint32_t r[16];
+          convert_sums(kept, r);
+          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+          tc_fence_after();
+          if (live) tc_st_16x128_x8(to, r);
+          kept[0] = kept[1] = make_uint4(0, 0, 0, 0);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a_full[st]);
+          if (st) a_ph ^= 1;
+          st ^= 1;
+        }
       }
     }
-    cp_async_wait_all();
-  } else if (warp < 16) {
+    for (int i = max(0, copies - kSlots); i < copies; ++i)  // the copies have landed before the CTA ends
+      mbar_wait(&full[i % kSlots], (i / kSlots) & 1, err);
+  } else if (warp < kConvert + kResults) {
     // ---- results: 32 weight rows of each half, half of the tile's rows of x ----
-    const int quarter = warp & 3, side = (warp - 8) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegResults));
+    const int quarter = warp & 3, side = (warp - kConvert) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     int chunk = 0;
     bool ok = true;
@@ -403,11 +506,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         const int f = GLU ? f0 : f0 + h * 128;
         undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) : 0.f;
       }
-      if constexpr (!TWO) {
+      if constexpr (DT != kF32) {
         if (!(ok = wait_warp(&d_full[0], chunk & 1, dead, err))) break;
         tc_fence_after();
         for (int c = 0; c < mine; c += 16) {
-          const float ux = __ldg(A.undo_x + r0 + c + (lane & 15));
+          float ux[16];
+          load16(A.undo_x + r0 + c, ux);
           float v[2][16];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -416,13 +520,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             tc_ld16(lanes + h * P::kCols + side * mine + c, r);
             tc_wait_ld(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[h][j] = __uint_as_float(r[j]) * undo[h] * __shfl_sync(0xFFFFFFFFu, ux, j);
-            if constexpr (!GLU) store16<TWO>(L, v[h], r0 + c, t.begin, t.end, f0 + h * 128, lane);
+            for (int j = 0; j < 16; ++j) v[h][j] = __uint_as_float(r[j]) * undo[h] * ux[j];
+            if constexpr (!GLU) store16<DT>(L, v[h], r0 + c, t.begin, t.end, f0 + h * 128, lane);
           }
           if constexpr (GLU) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[0][j] = silu_f32(v[0][j]) * v[1][j];
-            store16<TWO>(L, v[0], r0 + c, t.begin, t.end, f0, lane);
+            store16<DT>(L, v[0], r0 + c, t.begin, t.end, f0, lane);
           }
         }
         tc_fence_before();
@@ -460,89 +564,104 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (c * 16 >= mine) break;
-          const float ux = __ldg(A.undo_x + r0 + c * 16 + (lane & 15));
+          float ux[16];
+          load16(A.undo_x + r0 + c * 16, ux);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[h][c][j] *= undo[h] * __shfl_sync(0xFFFFFFFFu, ux, j);
+            for (int j = 0; j < 16; ++j) acc[h][c][j] *= undo[h] * ux[j];
           if constexpr (GLU) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[0][c][j] = silu_f32(acc[0][c][j]) * acc[1][c][j];
           }
 #pragma unroll
           for (int h = 0; h < (GLU ? 1 : 2); ++h)
-            if (h < halves) store16<TWO>(L, acc[h][c], r0 + c * 16, t.begin, t.end, f0 + h * 128, lane);
+            if (h < halves) store16<DT>(L, acc[h][c], r0 + c * 16, t.begin, t.end, f0 + h * 128, lane);
         }
       }
     }
-  } else if (warp == kLoadWarp) {
-    // ---- copies of x ----
-    if (lane == 0) {
-      int copies = 0;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegIssue));
+    if (warp == kLoadWarp && lane == 0) {
+      // ---- copies of x ----
+      int copies = 0, st = 0;
+      uint32_t ph = 1;
       bool ok = true;
       for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
         const uint32_t bytes = (uint32_t)t.cols * 128;
-        for (int ks = 0; ks < nks; ++ks, ++copies) {
-          const int st = copies % P::kStages, round = copies / P::kStages;
-          if (round > 0 && !(ok = wait_for(&x_empty[st], (round - 1) & 1, dead, err))) break;
-          mbar_arrive_expect_tx(&x_full[st], bytes * P::kParts);
-#pragma unroll
-          for (int p = 0; p < P::kParts; ++p)
-            bulk_g2s(smem + st * P::kStage + p * P::kPart, A.xt + (((long long)p * nks + ks) * A.pad + t.row0) * 128, bytes,
-                     &x_full[st]);
+#pragma unroll 1
+        for (int ks = 0, sums = 0; ks < nks; ++copies) {
+          if (!(ok = wait_for(&x_empty[st], ph, dead, err))) break;
+          const int parts = sums ? 1 : P::kXParts;
+          mbar_arrive_expect_tx(&x_full[st], bytes * parts);
+          for (int p = 0; p < parts; ++p)
+            bulk_g2s(smem + st * P::kStage + p * P::kPart,
+                     A.xt + ((sums ? (long long)P::kXParts * nks + ks / kGroup : (long long)p * nks + ks) * A.pad + t.row0) * 128,
+                     bytes, &x_full[st]);
+          if (++st == P::kStages) st = 0, ph ^= 1;
+          if (P::kSums && !sums && sums_follow(ks, nks))
+            sums = 1;
+          else
+            sums = 0, ++ks;
         }
       }
       for (int i = max(0, copies - P::kStages); i < copies; ++i)  // the copies have landed before the CTA ends
         mbar_wait(&x_full[i % P::kStages], (i / P::kStages) & 1, err);
-    }
-    __syncwarp();
-  } else {
-    // ---- products ----
-    int at = 0, chunk = 0;
-    bool ok = true;
-    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-      const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-      const int halves = GLU || t.mt * 256 + 128 < L.out ? 2 : 1;
-      const uint32_t id = 1u << 4 | (uint32_t)(t.cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // f16, f32, M = 128
-      int set = 0;
-      for (int ks = 0; ks < nks; ++ks, ++at) {
-        const bool first = TWO ? ks % kChunk == 0 : ks == 0;
-        if (first) {
-          set = chunk % P::kSets;
-          const int round = chunk / P::kSets;
-          if (round > 0 && !(ok = wait_warp(&d_empty[set], (round - 1) & 1, dead, err))) break;
-          ++chunk;
-        }
-        const int st = at & 1, xst = at % P::kStages;
-        if (!(ok = wait_warp(&x_full[xst], (at / P::kStages) & 1, dead, err))) break;
-        if (!(ok = wait_warp(&a_full[st], (at >> 1) & 1, dead, err))) break;
-        tc_fence_after();
-        if (elect_one()) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ---- products: the warp stays together, so that addresses and descriptors are formed in uniform registers, and one
+      // lane's predicate is on the instructions ----
+      const uint32_t lead = elect_one();
+      const int half = warp - kMmaWarp;
+      int st = 0, xst = 0, set = 0;
+      uint32_t a_ph = 0, x_ph = 0, d_ph = 1;
+      bool ok = true;
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
+        const int halves = GLU || t.mt * 256 + 128 < L.out ? 2 : 1;
+        const uint32_t id = 1u << 4 | (uint32_t)(t.cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // f16, f32, M = 128
+#pragma unroll 1
+        for (int ks = 0, sums = 0; ks < nks;) {
+          const bool first = !sums && (DT == kF32 ? ks % kChunk == 0 : ks == 0);
+          if (first && !(ok = wait_warp(&d_empty[set], d_ph, dead, err))) break;
+          if (!(ok = wait_warp(&x_full[xst], x_ph, dead, err))) break;
+          if (!(ok = wait_warp(&a_full[st], a_ph, dead, err))) break;
+          tc_fence_after();
+          const bool follow = P::kSums && !sums && sums_follow(ks, nks);
           const uint64_t b = tc_desc(smem + xst * P::kStage, 1024, 0);
-          const uint64_t b_lo = tc_desc(smem + xst * P::kStage + (P::kParts - 1) * P::kPart, 1024, 0);
-          for (int h = 0; h < halves; ++h) {
-            const uint32_t d = tmem + (set * 2 + h) * P::kCols;
-            const uint32_t a = tmem + P::kA + (st * 2 + h) * 32 * P::kParts;
+          const uint32_t d = (set * 2 + half) * P::kCols, a = P::kA + (st * 2 + half) * 32 * P::kWParts;
+          if (half < halves) {
+            // the small parts first: an add truncates by the accumulator's size
+            if (P::kSums && !sums) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              tc_mma_ts(d, a + y * 8, b + y * 2, id, !first || y > 0);
-              if constexpr (TWO) {
-                tc_mma_ts(d, a + y * 8, b_lo + y * 2, id, 1);
-                tc_mma_ts(d, a + 32 + y * 8, b + y * 2, id, 1);
+              for (int y = 0; y < 4; ++y) {
+                tc_mma_ts_if(lead, d, a + 32 + y * 8, b + y * 2, id, !first || y > 0);
+                if constexpr (P::kXParts == 2) tc_mma_ts_if(lead, d, a + y * 8, b + (P::kPart >> 4) + y * 2, id, 1);
               }
             }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, P::kSums || !first || y > 0);
           }
-          tc_commit(&a_empty[st]);
-          tc_commit(&x_empty[xst]);
-          if (ks == nks - 1 || (TWO && ks % kChunk == kChunk - 1)) tc_commit(&d_full[set]);
+          tc_commit_if(lead, &a_empty[st]);
+          tc_commit_if(lead, &x_empty[xst]);
+          if (st) a_ph ^= 1;
+          st ^= 1;
+          if (++xst == P::kStages) xst = 0, x_ph ^= 1;
+          if (!follow && (ks == nks - 1 || (DT == kF32 && ks % kChunk == kChunk - 1))) {
+            tc_commit_if(lead, &d_full[set]);
+            if (++set == P::kSets) set = 0, d_ph ^= 1;
+          }
+          if (follow)
+            sums = 1;
+          else
+            sums = 0, ++ks;
         }
-        __syncwarp();
       }
+      tc_commit_if(lead, last);
+      __syncwarp();
+      mbar_wait(last, 0, err);
     }
-    if (elect_one()) tc_commit(last);
     __syncwarp();
-    mbar_wait(last, 0, err);
   }
   tc_fence_before();
   __syncthreads();
@@ -550,30 +669,47 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <bool TWO>
-int smem_bytes(int n) { return ManyPlan<TWO>::kPre + (n + 1) * 4; }
+template <int DT>
+int smem_bytes(int n) { return ManyPlan<DT>::kPre + (n + 1) * 4; }
 
-template <bool TWO, bool GLU>
+template <int DT>
 cudaError_t launch(const ManyArgs& A, int nsm, cudaStream_t s) {
-  linear_many_kernel<TWO, GLU><<<nsm, kManyThreads, smem_bytes<TWO>(A.L.n), s>>>(A);
+  const LinArgs& L = A.L;
+  linear_rows_kernel<DT><<<(unsigned)((L.T + 7) / 8), 256, 0, s>>>(L.x, L.xs, L.T, L.in, const_cast<uint8_t*>(A.xt), A.pad,
+                                                                  const_cast<float*>(A.undo_x));
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (L.glu)
+    linear_many_kernel<DT, true><<<nsm, kManyThreads, smem_bytes<DT>(L.n), s>>>(A);
+  else
+    linear_many_kernel<DT, false><<<nsm, kManyThreads, smem_bytes<DT>(L.n), s>>>(A);
   return cudaGetLastError();
 }
 
-template <bool TWO, bool GLU>
+template <int DT, bool GLU>
 cudaError_t setup() {
-  return cudaFuncSetAttribute(linear_many_kernel<TWO, GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              smem_bytes<TWO>(kMaxMats));
+  auto* fn = linear_many_kernel<DT, GLU>;
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, fn);
+  if (e != cudaSuccess) return e;
+  // the roles' register shares are drawn from what the block is launched with
+  if ((a.numRegs + 7) / 8 * 8 < kRegs) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DT>(kMaxMats));
 }
+
+// Bytes of the workspace per row: two parts of f32 rows, the sums, the power of two.
+long long row_bytes(int in) { return (2LL * (in / 64) + sum_steps(in / 64)) * 128 + 4; }
 
 // Rows of the workspace: a tile's copies may pass a matrix's last row by less than a tile.
 long long pad_rows(int max_rows) { return (((long long)max_rows + 7) & ~7LL) + 192; }
 
 }  // namespace
 
-long long linear_many_workspace(int in, int max_rows) { return pad_rows(max_rows) * (4LL * in + 4); }
+long long linear_many_workspace(int in, int max_rows) { return pad_rows(max_rows) * row_bytes(in); }
 
 cudaError_t setup_linear_many() {
-  const cudaError_t e[4] = {setup<false, false>(), setup<false, true>(), setup<true, false>(), setup<true, true>()};
+  const cudaError_t e[6] = {setup<kF32, false>(),  setup<kF32, true>(),  setup<kF16, false>(),
+                            setup<kF16, true>(), setup<kBF16, false>(), setup<kBF16, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -583,20 +719,9 @@ cudaError_t launch_linear_many(const LinArgs& L, void* workspace, int max_rows, 
   ManyArgs A;
   A.L = L;
   A.pad = pad_rows(max_rows);
-  uint8_t* xt = static_cast<uint8_t*>(workspace);
-  float* undo = reinterpret_cast<float*>(xt + A.pad * 4 * L.in);
-  A.xt = xt, A.undo_x = undo;
-  const unsigned grid = (unsigned)((L.T + 7) / 8);
-  if (L.dtype == kF32)
-    linear_rows_kernel<kF32><<<grid, 256, 0, s>>>(L.x, L.xs, L.T, L.in, xt, A.pad, undo);
-  else if (L.dtype == kF16)
-    linear_rows_kernel<kF16><<<grid, 256, 0, s>>>(L.x, L.xs, L.T, L.in, xt, A.pad, undo);
-  else
-    linear_rows_kernel<kBF16><<<grid, 256, 0, s>>>(L.x, L.xs, L.T, L.in, xt, A.pad, undo);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (L.dtype == kF32) return L.glu ? launch<true, true>(A, nsm, s) : launch<true, false>(A, nsm, s);
-  return L.glu ? launch<false, true>(A, nsm, s) : launch<false, false>(A, nsm, s);
+  A.xt = static_cast<uint8_t*>(workspace);
+  A.undo_x = reinterpret_cast<const float*>(A.xt + A.pad * (row_bytes(L.in) - 4));
+  return L.dtype == kF32 ? launch<kF32>(A, nsm, s) : L.dtype == kF16 ? launch<kF16>(A, nsm, s) : launch<kBF16>(A, nsm, s);
 }
 
 }  // namespace strata
