@@ -9,10 +9,12 @@
 //     4i..4i+3 and column 8c+2i+1 in bits 16+4i..16+4i+3
 //   record g (16 bytes, f16): scales of row g (first block, second), of row
 //     g + 8, then the mins in the same order
-// Scales and mins carry a power of two of their row, which brings its largest
-// weight to [64, 128); the row's results are multiplied by its inverse, `undo`.
-// (A block whose scale is below 2^-20 of the row's largest weight loses low bits
-// of it: at most 2^-29 of that weight.)
+// Both carry a power of two of their row, scales 2^24 more (a masked code read as
+// f16 is the subnormal q 2^-24): the row's largest scale is in [2^14, 2^15), or its
+// largest min in [4, 8) where that is less.  A row's results are multiplied
+// by `undo`, the inverse.  (A block whose scale is below 2^-28 of the row's largest
+// loses low bits of it, a min below 2^-9 of the row's largest 15 s loses them below
+// 2^-20 of that.)
 #pragma once
 #include "kv8.cuh"
 

@@ -51,6 +51,11 @@ __device__ __forceinline__ uint32_t few_pair(uint32_t w) {
   }
 }
 
+__device__ __forceinline__ float half_of(uint32_t two, int upper) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&two);
+  return __half2float(upper ? h.y : h.x);
+}
+
 // Eight neighbouring values of a row, as kParts times four pairs.
 template <int DT>
 __device__ __forceinline__ void few_x(const void* row, int i, bool live, uint32_t (&b)[FewType<DT>::kParts][4]) {
@@ -133,11 +138,9 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(LinArgs A) {
               few_mma<DT>(d, a0, b[k][0], b[k][1]);
               few_mma<DT>(d, a1, b[k][2], b[k][3]);
             }
-            const __half2 sg = *reinterpret_cast<const __half2*>(&rec[m][t].x), s8 = *reinterpret_cast<const __half2*>(&rec[m][t].y);
-            const __half2 mg = *reinterpret_cast<const __half2*>(&rec[m][t].z), m8 = *reinterpret_cast<const __half2*>(&rec[m][t].w);
-            const float s0 = __half2float(blk ? sg.y : sg.x), s1 = __half2float(blk ? s8.y : s8.x);
-            const float o0 = fmaf(-16.f, s0, __half2float(blk ? mg.y : mg.x));
-            const float o1 = fmaf(-16.f, s1, __half2float(blk ? m8.y : m8.x));
+            const uint32_t* h = &rec[m][t].x;  // scales of rows g, g + 8 (both blocks), then mins
+            const float s0 = 0x1p-24f * half_of(h[0], blk), s1 = 0x1p-24f * half_of(h[1], blk);
+            const float o0 = fmaf(-16.f, s0, half_of(h[2], blk)), o1 = fmaf(-16.f, s1, half_of(h[3], blk));
             float(&z)[4] = acc[m][t];
             z[0] = fmaf(s0, d[0], fmaf(o0, xsum[0], z[0]));
             z[1] = fmaf(s0, d[1], fmaf(o0, xsum[1], z[1]));

@@ -23,7 +23,7 @@
 // results (each a quarter of the lanes and half of the rows of x), one of copies
 // of x, one for each half that issues its products (one warp for both spent more
 // time between a step's products and the next one's than the tensor cores have
-// work queued); one warp fills the warpgroup.  CTAs (one
+// work queued), one of copies of the codes.  CTAs (one
 // per SM) take the tiles of all matrices in turn, weight rows fastest, so that
 // concurrent CTAs share rows of x in L2.
 #include "linear.cuh"
@@ -33,7 +33,7 @@ namespace strata {
 namespace {
 
 constexpr int kConvert = 16, kResults = 8;    // warps
-constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1;
+constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1, kCodeWarp = kLoadWarp + 3;
 constexpr int kManyThreads = (kConvert + kResults + 4) * 32;
 // Registers a thread: at launch, and by role; the roles' shares are drawn from the launch's.
 constexpr int kRegs = 72, kRegConvert = 56, kRegResults = 120, kRegIssue = 40;
@@ -55,7 +55,7 @@ template <int DT> struct ManyPlan {
   static constexpr int kStage = kPart * kXParts;
   static constexpr int kFifoOff = kStages * kStage;
   static constexpr int kBars = kFifoOff + kConvert * kSlots * kSlot;
-  static constexpr int kMisc = kBars + 1024;
+  static constexpr int kMisc = kBars + 256 + 2 * 8 * kConvert * kSlots;
   static constexpr int kPre = kMisc + 64;        // [n + 1] tiles before each matrix
   static_assert(kA + 4 * 32 * kWParts <= 512, "tensor memory");
   static_assert(kPre + (kMaxMats + 1) * 4 <= 232448, "shared memory");
@@ -77,8 +77,8 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 
 // --- rows of x into the workspace --------------------------------------------------
 
-// A warp takes a row: its largest magnitude, then the values times a power of two that brings it to [2^14, 2^15), as f16
-// (f32: two of them).  A lane writes 16 bytes: pairs j of the four groups of eight columns of a block, the order in which
+// A warp takes a row: its largest magnitude, then the values times a power of two that brings it to [2^14, 2^15)
+// ([2^9, 2^10) where sums are formed), as f16 (f32: two of them).  A lane writes 16 bytes: pairs j of the four groups of eight columns of a block, the order in which
 // the conversion warps' stores put the codes; the 16-byte pieces of a row's 128 are swizzled by the row.  The blocks' sums
 // go to steps of their own, in the order of `convert_sums`; blocks past the last are zeros.
 template <int DT>
@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long lo
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  int e = 15;
+  constexpr int kTop = ManyPlan<DT>::kSums ? 10 : 15;  // (a block's sum has to be an f16 too)
+  int e = kTop;
   if (most > 0.f) frexpf(most, &e);
-  const int up = max(-126, min(126, 15 - e));
+  const int up = max(-126, min(126, kTop - e));
   const float mul = pow2i(up);
   if (lane == 0) undo[row] = pow2i(-up);
   const long long part = (long long)(in / 64) * pad * 128;
@@ -150,10 +151,9 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long lo
         *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     if constexpr (ManyPlan<DT>::kSums) {
-      // the block's sum / 32 (at most 2^15) in two parts, to the columns of its min (lane 0 of the four) and its 8 s (lane 1)
+      // the block's sum (at most 2^15) in two parts, to the columns of its min (lane 0 of the four) and its 8 s (lane 1)
       sum += __shfl_xor_sync(quad, sum, 1);
       sum += __shfl_xor_sync(quad, sum, 2);
-      sum *= 0x1p-5f;
       const int kind = i & 3, blk = (i >> 2) & 1, step = ks % kGroup, piece = (step >> 2) * 4 + blk * 2 + kind;
       const __half h = __float2half_rn(sum);
       if (kind < 2)
@@ -232,34 +232,36 @@ __device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
 }
 
 // A step of a tile, row g and row g + 8 of this lane, into the registers of a 16x128b store: the word's pair i goes to
-// column 4 i + c of its block's 16, register 2 i (row g) or 2 i + 1 (row g + 8).  A masked code is the subnormal q 2^-24
-// (or q 2^-20); times 2^15 (2^11) it is q 2^-9 exactly, and one fma with 512 s and m rounds once.
+// column 4 i + c of its block's 16, register 2 i (row g) or 2 i + 1 (row g + 8).  A masked code is the subnormal q 2^-24 (or
+// q 2^-20), the records' scales carry the 2^24, so a pair is one mask and one fma, which rounds once.
 __device__ __forceinline__ void convert(const uint4& code, const uint4& rec, uint32_t (&r)[16]) {
-  const __half2 up15 = __float2half2_rn(32768.f), up11 = __float2half2_rn(2048.f), k512 = __float2half2_rn(512.f);
+  const __half2 k16 = __float2half2_rn(0.0625f);
   const uint32_t words[4] = {code.x, code.y, code.z, code.w};
-  const __half2 s[2] = {__hmul2(as_half2(rec.x), k512), __hmul2(as_half2(rec.y), k512)};
-  const __half2 m[2] = {as_half2(rec.z), as_half2(rec.w)};
+  const __half2 s[2] = {as_half2(rec.x), as_half2(rec.y)}, m[2] = {as_half2(rec.z), as_half2(rec.w)};
+  const __half2 s16[2] = {__hmul2(s[0], k16), __hmul2(s[1], k16)};
 #pragma unroll
   for (int wi = 0; wi < 4; ++wi) {
     const int row = wi & 1, blk = wi >> 1;
     const __half2 sv = blk ? __high2half2(s[row]) : __low2half2(s[row]);
+    const __half2 tv = blk ? __high2half2(s16[row]) : __low2half2(s16[row]);
     const __half2 mv = blk ? __high2half2(m[row]) : __low2half2(m[row]);
     const uint32_t w = words[wi], v = w >> 8;
-    r[blk * 8 + 0 + row] = as_u32(__hfma2(__hmul2(as_half2(w & 0x000F000Fu), up15), sv, mv));
-    r[blk * 8 + 2 + row] = as_u32(__hfma2(__hmul2(as_half2(w & 0x00F000F0u), up11), sv, mv));
-    r[blk * 8 + 4 + row] = as_u32(__hfma2(__hmul2(as_half2(v & 0x000F000Fu), up15), sv, mv));
-    r[blk * 8 + 6 + row] = as_u32(__hfma2(__hmul2(as_half2(v & 0x00F000F0u), up11), sv, mv));
+    r[blk * 8 + 0 + row] = as_u32(__hfma2(as_half2(w & 0x000F000Fu), sv, mv));
+    r[blk * 8 + 2 + row] = as_u32(__hfma2(as_half2(w & 0x00F000F0u), tv, mv));
+    r[blk * 8 + 4 + row] = as_u32(__hfma2(as_half2(v & 0x000F000Fu), sv, mv));
+    r[blk * 8 + 6 + row] = as_u32(__hfma2(as_half2(v & 0x00F000F0u), tv, mv));
   }
 }
 
-// s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the product's
-// f16 leaves at most 5 bits.
-__device__ __forceinline__ void convert_two(const uint4& code, const uint4& rec, int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+// 2^12 s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the
+// product's f16 leaves at most 5 bits.  s: the records' scales times 2^-12 (2^24 - 12 is the factor that results lose again).
+constexpr float kTwoUndo = 0x1p-12f;
+__device__ __forceinline__ void convert_two(const uint4& code, const __half2 (&s)[2], int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
   const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f);
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
     const uint32_t word = blk ? row ? code.w : code.z : row ? code.y : code.x;
-    const __half2 s = as_half2(row ? rec.y : rec.x), sv = blk ? __high2half2(s) : __low2half2(s);
+    const __half2 sv = blk ? __high2half2(s[row]) : __low2half2(s[row]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = i < 2 ? word : word >> 8;
@@ -272,14 +274,14 @@ __device__ __forceinline__ void convert_two(const uint4& code, const uint4& rec,
   }
 }
 
-// The weights of a step of sums from the records of steps c and 4 + c of the group: the min (times 32) in column 4 i + c for
-// even i, 8 s (times 32) for odd i, i = 4 (step / 4) + 2 block + kind; a column's two f16 meet the sum's two parts.
+// The weights of a step of sums from the records of steps c and 4 + c of the group: 2^12 m in column 4 i + c for even i,
+// 2^12 8 s for odd i, i = 4 (step / 4) + 2 block + kind; a column's two f16 meet the sum's two parts.
 __device__ __forceinline__ void convert_sums(const uint4 (&rec)[2], uint32_t (&r)[16]) {
-  const __half2 k32 = __float2half2_rn(32.f), k256 = __float2half2_rn(256.f);
+  const __half2 down = __float2half2_rn(0x1p-9f), up = __float2half2_rn(0x1p12f);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const __half2 s[2] = {__hmul2(as_half2(rec[p].x), k256), __hmul2(as_half2(rec[p].y), k256)};
-    const __half2 m[2] = {__hmul2(as_half2(rec[p].z), k32), __hmul2(as_half2(rec[p].w), k32)};
+    const __half2 s[2] = {__hmul2(as_half2(rec[p].x), down), __hmul2(as_half2(rec[p].y), down)};
+    const __half2 m[2] = {__hmul2(as_half2(rec[p].z), up), __hmul2(as_half2(rec[p].w), up)};
 #pragma unroll
     for (int row = 0; row < 2; ++row) {
       r[p * 8 + 0 + row] = as_u32(__low2half2(m[row]));
@@ -299,25 +301,40 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// A lane's 16 results of one weight row f for rows r0.. of x.  16-bit types: neighbouring lanes trade, so that each
-// stores two weight rows of one row of x.
+// Two products in one instruction.
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nadd.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
+// A lane's 16 results of one weight row f for rows r0.. of x; those from begin to end are stored.  16-bit types:
+// neighbouring lanes trade, so that each stores two weight rows of every other row of x.
 template <int DT>
 __device__ __forceinline__ void store16(const LinArgs& L, const float (&v)[16], int r0, int begin, int end, int f, int lane) {
+  if (f - lane >= L.out) return;  // the warp's 32 weight rows are all past the last
+  const bool all = r0 >= begin && r0 + 16 <= end, mine = f < L.out;
   if constexpr (DT == kF32) {
-    float* y = static_cast<float*>(L.y) + f;
+    float* y = static_cast<float*>(L.y) + (long long)r0 * L.ys + f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (r0 + j >= begin && r0 + j < end && f < L.out) y[(long long)(r0 + j) * L.ys] = v[j];
+    for (int j = 0; j < 16; ++j, y += L.ys)
+      if (mine && (all || (r0 + j >= begin && r0 + j < end))) *y = v[j];
   } else {
     const int odd = lane & 1;
-    uint16_t* y = static_cast<uint16_t*>(L.y) + (f - odd);
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;  // own and got: even lanes take the lower halves, odd ones the upper
+    uint16_t* y = static_cast<uint16_t*>(L.y) + (long long)(r0 + odd) * L.ys + (f - odd);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const float give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-      const uint32_t two = odd ? pack16<DT>(got, keep) : pack16<DT>(keep, got);
+    for (int j = 0; j < 16; j += 2, y += 2 * L.ys) {
+      const uint32_t own = pack16<DT>(v[j], v[j + 1]);
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+      const uint32_t two = __byte_perm(own, got, pick);
       const int r = r0 + j + odd;
-      if (r >= begin && r < end && f < L.out) *reinterpret_cast<uint32_t*>(y + (long long)r * L.ys) = two;
+      if (mine && (all || (r >= begin && r < end))) *reinterpret_cast<uint32_t*>(y) = two;
     }
   }
 }
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
   uint64_t *x_full = bars, *x_empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 18, *d_full = bars + 20,
-           *d_empty = bars + 22, *last = bars + 24, *code_full = bars + 32;  // [kConvert][kSlots]
+           *d_empty = bars + 22, *last = bars + 24, *code_full = bars + 32, *code_empty = code_full + kConvert * kSlots;  // [kConvert][kSlots]
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
   int* pre = reinterpret_cast<int*>(smem + P::kPre);
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     for (int i = 0; i < P::kStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 2);
     for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], kConvert), mbar_init(&a_empty[i], 2);
     for (int i = 0; i < P::kSets; ++i) mbar_init(&d_full[i], 2), mbar_init(&d_empty[i], kResults);
-    for (int i = 0; i < kConvert * kSlots; ++i) mbar_init(&code_full[i], 1);
+    for (int i = 0; i < kConvert * kSlots; ++i) mbar_init(&code_full[i], 1), mbar_init(&code_empty[i], 1);
     mbar_init(last, 2);
     *dead = 0;
     fence_mbar_init();
@@ -392,102 +409,85 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     // ---- conversion: the codes of 16 weight rows of a half, a step at a time ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConvert));
     const int quarter = warp & 3, half = (warp >> 2) & 1, upper = warp >> 3;
-    uint8_t* ring = smem + P::kFifoOff + warp * (kSlots * kSlot);
-    uint64_t* full = code_full + warp * kSlots;
+    const uint8_t* ring = smem + P::kFifoOff + warp * (kSlots * kSlot);
+    uint64_t *full = code_full + warp * kSlots, *empty = code_empty + warp * kSlots;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32 + upper * 16) << 16) + P::kA + half * 32 * P::kWParts;
     const int wt0 = half * (GLU ? 0 : 8) + quarter * 2 + upper;
-    // what is copied next: steps of an item's tile (a tile past the last one is not copied; its lanes' results are not used)
-    int f_item = blockIdx.x, f_left = 0, f_slot = 0, copies = 0;
-    const uint8_t* src = nullptr;
-    auto fetch = [&]() {
-      while (f_left == 0) {
-        if (f_item >= total) return;
-        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, f_item);
-        const int wt = t.mt * (GLU ? 8 : 16) + wt0;
-        src = L.w[GLU ? half : 0].packed + ((long long)t.mat * w_tiles + wt) * nks * kLinStepBytes;
-        f_item += gridDim.x;
-        if (wt < w_tiles) f_left = nks;
-      }
-      const int steps = min(f_left, kSlotSteps);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[f_slot], steps * kLinStepBytes);
-        bulk_g2s(ring + f_slot * kSlot, src, steps * kLinStepBytes, &full[f_slot]);
-      }
-      src += kSlot, f_left -= steps, ++copies;
-      if (++f_slot == kSlots) f_slot = 0;
-    };
-#pragma unroll 1
-    for (int i = 0; i < kSlots; ++i) fetch();
     int slot = 0, st = 0;
     uint32_t slot_ph = 0, a_ph = 1;  // (a fresh barrier passes a wait for the phase before its first)
     bool ok = true;
     uint4 kept[2] = {};  // the records of steps c and 4 + c of a group
+    // the weights of a stage are in tensor memory
+    auto hand_over = [&](uint64_t* read) {
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&a_full[st]);
+        if (read) mbar_arrive(read);
+      }
+      if (st) a_ph ^= 1;
+      st ^= 1;
+    };
     for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
       const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
+      // a tile past the last one is not copied, and its lanes' results are not used
       const bool live = t.mt * (GLU ? 8 : 16) + wt0 < w_tiles;
 #pragma unroll 1
       for (int ks = 0; ks < nks; ++ks) {
-        const int in_slot = ks % kSlotSteps;
-        if (live && in_slot == 0 && !(ok = wait_warp(&full[slot], slot_ph, dead, err))) break;
-        uint32_t to = lanes + st * 64 * P::kWParts;
-        const uint8_t* step = ring + slot * kSlot + in_slot * kLinStepBytes;
-        const uint4 code = *reinterpret_cast<const uint4*>(step + lane * 16);
-        const uint4 rec = *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16);
-        if constexpr (!P::kSums) {
-          uint32_t r[16];
-          convert(code, rec, r);
-          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
-          tc_fence_after();
-          if (live) tc_st_16x128_x8(to, r);
-        } else {
-          uint32_t hi[8], lo[8];
-          convert_two(code, rec, 0, hi, lo);
-          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
-          tc_fence_after();
-          if (live) {
+        uint64_t* read = nullptr;
+        const uint32_t to = lanes + st * 64 * P::kWParts;
+        if (live) {
+          const int in_slot = ks % kSlotSteps;
+          if (in_slot == 0 && !(ok = wait_warp(&full[slot], slot_ph, dead, err))) break;
+          const uint8_t* step = ring + slot * kSlot + in_slot * kLinStepBytes;
+          const uint4 code = *reinterpret_cast<const uint4*>(step + lane * 16);
+          const uint4 rec = *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16);
+          if (in_slot == kSlotSteps - 1 || ks == nks - 1) {
+            read = &empty[slot];
+            if (++slot == kSlots) slot = 0, slot_ph ^= 1;
+          }
+          if constexpr (!P::kSums) {
+            uint32_t r[16];
+            convert(code, rec, r);
+            if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+            tc_fence_after();
+            tc_st_16x128_x8(to, r);
+          } else {
+            const __half2 down = __float2half2_rn(0x1p-12f);
+            const __half2 s[2] = {__hmul2(as_half2(rec.x), down), __hmul2(as_half2(rec.y), down)};
+            uint32_t hi[8], lo[8];
+            convert_two(code, s, 0, hi, lo);
+            if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+            tc_fence_after();
             tc_st_16x128_x4(to, hi);
             tc_st_16x128_x4(to + 32, lo);
-            convert_two(code, rec, 1, hi, lo);
+            convert_two(code, s, 1, hi, lo);
             tc_st_16x128_x4(to + 16, hi);
             tc_st_16x128_x4(to + 48, lo);
+            if ((ks & 3) == (lane & 3)) {
+              if (ks & 4)
+                kept[1] = rec;
+              else
+                kept[0] = rec;
+            }
           }
-          if ((ks & 3) == (lane & 3)) {
-            if (ks & 4)
-              kept[1] = rec;
-            else
-              kept[0] = rec;
-          }
+        } else if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) {
+          break;
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[st]);
-        if (st) a_ph ^= 1;
-        st ^= 1;
-        if (live && (in_slot == kSlotSteps - 1 || ks == nks - 1)) {  // the slot has been read
-          if (++slot == kSlots) slot = 0, slot_ph ^= 1;
-          fetch();
-        }
+        hand_over(read);
         if constexpr (P::kSums) {
           if (!sums_follow(ks, nks)) continue;
-          to = lanes + st * 64 * P::kWParts;
           uint32_t r[16];
           convert_sums(kept, r);
           if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
           tc_fence_after();
-          if (live) tc_st_16x128_x8(to, r);
+          if (live) tc_st_16x128_x8(lanes + st * 64 * P::kWParts, r);
           kept[0] = kept[1] = make_uint4(0, 0, 0, 0);
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&a_full[st]);
-          if (st) a_ph ^= 1;
-          st ^= 1;
+          hand_over(nullptr);
         }
       }
     }
-    for (int i = max(0, copies - kSlots); i < copies; ++i)  // the copies have landed before the CTA ends
-      mbar_wait(&full[i % kSlots], (i / kSlots) & 1, err);
   } else if (warp < kConvert + kResults) {
     // ---- results: 32 weight rows of each half, half of the tile's rows of x ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegResults));
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int f = GLU ? f0 : f0 + h * 128;
-        undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) : 0.f;
+        undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) * (P::kSums ? kTwoUndo : 1.f) : 0.f;
       }
       if constexpr (DT != kF32) {
         if (!(ok = wait_warp(&d_full[0], chunk & 1, dead, err))) break;
@@ -520,7 +520,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             tc_ld16(lanes + h * P::kCols + side * mine + c, r);
             tc_wait_ld(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[h][j] = __uint_as_float(r[j]) * undo[h] * ux[j];
+            for (int j = 0; j < 16; j += 2) {
+              v[h][j] = __uint_as_float(r[j]), v[h][j + 1] = __uint_as_float(r[j + 1]);
+              mul2(v[h][j], v[h][j + 1], undo[h], undo[h]);
+              mul2(v[h][j], v[h][j + 1], ux[j], ux[j + 1]);
+            }
             if constexpr (!GLU) store16<DT>(L, v[h], r0 + c, t.begin, t.end, f0 + h * 128, lane);
           }
           if constexpr (GLU) {
@@ -554,7 +558,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
                 tc_ld16(lanes + (set * 2 + h) * P::kCols + side * mine + c * 16, r);
                 tc_wait_ld(r);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[h][c][j] += __uint_as_float(r[j]);
+                for (int j = 0; j < 16; j += 2)
+                  add2(acc[h][c][j], acc[h][c][j + 1], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
               }
           tc_fence_before();
           __syncwarp();
@@ -569,7 +574,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[h][c][j] *= undo[h] * ux[j];
+            for (int j = 0; j < 16; j += 2) {
+              mul2(acc[h][c][j], acc[h][c][j + 1], undo[h], undo[h]);
+              mul2(acc[h][c][j], acc[h][c][j + 1], ux[j], ux[j + 1]);
+            }
           if constexpr (GLU) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[0][c][j] = silu_f32(acc[0][c][j]) * acc[1][c][j];
@@ -608,6 +616,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       }
       for (int i = max(0, copies - P::kStages); i < copies; ++i)  // the copies have landed before the CTA ends
         mbar_wait(&x_full[i % P::kStages], (i / P::kStages) & 1, err);
+    } else if (warp == kCodeWarp && lane < kConvert) {
+      // ---- copies of codes: a lane for each conversion warp ----
+      const int wt0 = (lane >> 2 & 1) * (GLU ? 0 : 8) + (lane & 3) * 2 + (lane >> 3);
+      const uint8_t* packed = L.w[GLU ? lane >> 2 & 1 : 0].packed;
+      uint8_t* ring = smem + P::kFifoOff + lane * (kSlots * kSlot);
+      uint64_t *full = code_full + lane * kSlots, *empty = code_empty + lane * kSlots;
+      int copies = 0, slot = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
+        const int wt = t.mt * (GLU ? 8 : 16) + wt0;
+        if (wt >= w_tiles) continue;
+        const uint8_t* src = packed + ((long long)t.mat * w_tiles + wt) * nks * kLinStepBytes;
+#pragma unroll 1
+        for (int ks = 0; ks < nks; ks += kSlotSteps, src += kSlot, ++copies) {
+          if (!(ok = wait_for(&empty[slot], ph, dead, err))) break;
+          const uint32_t bytes = min(nks - ks, kSlotSteps) * kLinStepBytes;
+          mbar_arrive_expect_tx(&full[slot], bytes);
+          bulk_g2s(ring + slot * kSlot, src, bytes, &full[slot]);
+          if (++slot == kSlots) slot = 0, ph ^= 1;
+        }
+      }
+      for (int i = max(0, copies - kSlots); i < copies; ++i)  // the copies have landed before the CTA ends
+        mbar_wait(&full[i % kSlots], (i / kSlots) & 1, err);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // ---- products: the warp stays together, so that addresses and descriptors are formed in uniform registers, and one
       // lane's predicate is on the instructions ----

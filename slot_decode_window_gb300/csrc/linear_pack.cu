@@ -10,7 +10,7 @@ __device__ __forceinline__ float half_bits(uint16_t b) { return __half2float(__u
 __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scale,
                                                           const uint16_t* __restrict__ mn, int in, int out, uint8_t* packed,
                                                           float* undo) {
-  __shared__ float most[16][8], mul[16];
+  __shared__ float most_s[16][8], most_m[16][8], mul[16];
   const int tiles = out / kLinTile, nks = in / kLinStep, nblk = in / 32;
   const long long at = blockIdx.x;  // matrix * tiles + tile
   const long long row0 = at * kLinTile;
@@ -18,23 +18,26 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
     const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
     const uint16_t* s = scale + (row0 + r) * nblk;
     const uint16_t* m = mn + (row0 + r) * nblk;
-    float b = 0.f;
-    bool finite = true;
+    float bs = 0.f, bm = 0.f;
     for (int i = part; i < nblk; i += 8) {
-      const float lo = half_bits(m[i]), hi = fmaf(15.f, half_bits(s[i]), lo);
-      finite = finite && isfinite(lo) && isfinite(hi);
-      b = fmaxf(b, fmaxf(fabsf(lo), fabsf(hi)));
+      const float a = fabsf(half_bits(s[i])), c = fabsf(half_bits(m[i]));
+      bs = a < INFINITY ? fmaxf(bs, a) : INFINITY;
+      bm = c < INFINITY ? fmaxf(bm, c) : INFINITY;
     }
-    most[r][part] = finite ? b : INFINITY;
+    most_s[r][part] = bs, most_m[r][part] = bm;
   }
   __syncthreads();
   if (threadIdx.x < 16) {
-    float b = 0.f;
-    for (int i = 0; i < 8; ++i) b = fmaxf(b, most[threadIdx.x][i]);
-    int e = 7;
-    if (b > 0.f && isfinite(b)) frexpf(b, &e);  // b in [2^(e-1), 2^e); rows of zeros or with an infinity: as they are
-    mul[threadIdx.x] = pow2i(7 - e);
-    undo[row0 + threadIdx.x] = pow2i(e - 7);
+    float bs = 0.f, bm = 0.f;
+    for (int i = 0; i < 8; ++i) bs = fmaxf(bs, most_s[threadIdx.x][i]), bm = fmaxf(bm, most_m[threadIdx.x][i]);
+    int k = 0;
+    if (bs < INFINITY && bm < INFINITY && (bs > 0.f || bm > 0.f)) {  // rows of zeros or with an infinity: as they are
+      int es, em;  // the largest is in [2^(e-1), 2^e)
+      frexpf(bs, &es), frexpf(bm, &em);
+      k = bs == 0.f ? -5 - em : bm == 0.f ? -9 - es : min(-9 - es, 3 - em);
+    }
+    mul[threadIdx.x] = pow2i(k);
+    undo[row0 + threadIdx.x] = pow2i(-k);
   }
   __syncthreads();
   uint8_t* dst = packed + at * nks * kLinStepBytes;
@@ -56,7 +59,7 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
       __half h[4];
       for (int i = 0; i < 4; ++i) {
         const int r = g + (i >> 1) * 8;
-        h[i] = __float2half_rn(half_bits(src[(row0 + r) * nblk + 2 * ks + (i & 1)]) * mul[r]);
+        h[i] = __float2half_rn(half_bits(src[(row0 + r) * nblk + 2 * ks + (i & 1)]) * (mul[r] * (c ? 1.f : 16777216.f)));
       }
       *reinterpret_cast<uint2*>(step + 512 + g * 16 + c * 8) = *reinterpret_cast<uint2*>(h);
     }
