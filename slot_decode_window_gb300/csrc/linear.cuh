@@ -1,8 +1,10 @@
 // The products' matrices in the handle's own layout, and the launches of their
 // kernels (linear_pack.cu, linear_few.cu, linear_many.cu).
 //
-// A matrix [out][in] is out/16 tiles of in/64 steps.  A step (640 bytes, 0.625 a
-// weight as in the block format) is 512 bytes of codes and 8 records:
+// A matrix [out][in] is out/16 tiles by in/64 steps.  A tile's step is 640 bytes
+// (0.625 a weight, as in the block format); the tiles of 128 rows (8, or what is
+// left) are together, step by step, so that one copy brings a step of all of them.
+// The 640 bytes are 512 of codes and 8 records:
 //   codes: lane (g = lane/4, c = lane%4) has 16 bytes, a word for row g and one
 //     for row g + 8 of the step's first block of 32 columns, then the same of its
 //     second; a word holds columns 8c..8c+7 of the block, column 8c+2i in bits
@@ -39,6 +41,13 @@ struct LinArgs {
   const int* offsets;  // [n + 1], or null (n = 1)
   unsigned* err;
 };
+
+// Where tile `tile` of matrix `mat` has step 0, and the bytes from a step of it to the next.
+__device__ __forceinline__ const uint8_t* lin_tile(const uint8_t* packed, int mat, int tile, int tiles, int nks, int& stride) {
+  const int group = tile & ~7, here = min(8, tiles - group);
+  stride = here * kLinStepBytes;
+  return packed + (((long long)mat * tiles + group) * nks + (tile - group)) * kLinStepBytes;
+}
 
 // The rows of matrix i: begin, end.  A range that is out of order or outside 0..T is empty and noted.
 __device__ __forceinline__ bool lin_rows(const LinArgs& A, int i, int& begin, int& end) {

@@ -95,11 +95,12 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(LinArgs A) {
   int begin, end;
   if (!lin_rows(A, mat, begin, end) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(A.err, kErrIndex);
   const uint8_t* src[kMats][kTiles];
+  int stride[kTiles];
 #pragma unroll
   for (int m = 0; m < kMats; ++m)
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)  // (a CTA past the last tile reads it again and writes nothing)
-      src[m][t] = A.w[m].packed + ((long long)mat * tiles + min(tile0 + t, tiles - 1)) * nks * kLinStepBytes;
+      src[m][t] = lin_tile(A.w[m].packed, mat, min(tile0 + t, tiles - 1), tiles, nks, stride[t]);
   for (int r0 = begin; r0 < end; r0 += kLinFewRows) {
     const bool live = r0 + g < end;
     const char* row = static_cast<const char*>(A.x) + (long long)(r0 + g) * A.xs * (DT == kF32 ? 4 : 2);
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(LinArgs A) {
       for (int m = 0; m < kMats; ++m)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          const uint8_t* p = src[m][t] + (long long)ks * kLinStepBytes;
+          const uint8_t* p = src[m][t] + (long long)ks * stride[t];
           code[m][t] = __ldg(reinterpret_cast<const uint4*>(p + lane * 16));
           rec[m][t] = __ldg(reinterpret_cast<const uint4*>(p + 512 + g * 16));
         }

@@ -11,21 +11,22 @@
 // bf16 rows: one product, W rounded to f16 (2^-11 of a weight against the 2^-8 of
 // the results' own rounding).  f16 and f32 rows: exact weights,
 //   W x = s (q - 8) x + (8 s + m) sum x   over a block of 32 columns:
-// s (q - 8) has 15 bits, two f16 parts (hi and what is left, both exact); after
-// every 8 steps comes a step whose "weights" are m and 8 s of its 16 blocks and
-// whose "x" are their sums, in two f16 parts.  f16 rows: hi x + lo x.  f32 rows: x
+// s (q - 8) has 15 bits, two f16 parts (hi and what is left, both exact); after the
+// last columns come steps whose "weights" are m and 8 s of 16 blocks each and
+// whose "x" are the blocks' sums, in two f16 parts.  f16 rows: hi x + lo x.  f32 rows: x
 // in two f16 parts (22 bits), lo hi + hi lo + hi hi; the accumulators' adds
 // truncate, so every two steps they are added to f32 registers, with two sets of
 // accumulators in turn.
 //
-// Roles (28 warps): 16 of conversion (16 weight rows each, a quarter of the lanes
-// of tensor memory to every four of them, codes through a ring of its own), 8 of
-// results (each a quarter of the lanes and half of the rows of x), one of copies
-// of x, one for each half that issues its products (one warp for both spent more
-// time between a step's products and the next one's than the tensor cores have
-// work queued), one of copies of the codes.  CTAs (one
-// per SM) take the tiles of all matrices in turn, weight rows fastest, so that
-// concurrent CTAs share rows of x in L2.
+// Roles (28 warps): 16 of conversion, in two groups that take the steps in turn,
+// each with a stage of weights of its own (a warp has two tiles of 16 weight rows,
+// a quarter of the lanes of one half); 8 of results (each a quarter of the lanes
+// and half of the rows of x); one of copies, codes and x of a step into one stage;
+// one for each half that issues its products (and one that fills the warpgroup).  A step has to pass in 768 clocks for the
+// tensor cores never to wait, and a warp's waits and hand-overs alone take about
+// as many: hence the two groups, and two warps that issue.  CTAs (one per SM) take
+// the tiles of all matrices in turn, weight rows fastest, so that concurrent CTAs
+// share rows of x in L2.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 
@@ -33,15 +34,14 @@ namespace strata {
 namespace {
 
 constexpr int kConvert = 16, kResults = 8;    // warps
-constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1, kCodeWarp = kLoadWarp + 3;
+constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1;
 constexpr int kManyThreads = (kConvert + kResults + 4) * 32;
 // Registers a thread: at launch, and by role; the roles' shares are drawn from the launch's.
 constexpr int kRegs = 72, kRegConvert = 56, kRegResults = 120, kRegIssue = 40;
 static_assert(kConvert * kRegConvert + kResults * kRegResults + 4 * kRegIssue <= (kConvert + kResults + 4) * kRegs, "register split");
-constexpr int kSlots = 4, kSlotSteps = 2;     // ring of codes of a conversion warp
-constexpr int kSlot = kSlotSteps * kLinStepBytes;
+constexpr int kHalfCodes = 8 * kLinStepBytes; // a step of 128 weight rows
 constexpr int kChunk = 2;                     // steps between sums of f32 rows
-constexpr int kGroup = 8;                     // steps to a step of their blocks' sums
+constexpr int kGroup = 8;                     // steps whose blocks' sums are one step
 constexpr int kMaxMats = 1024;
 
 template <int DT> struct ManyPlan {
@@ -50,20 +50,19 @@ template <int DT> struct ManyPlan {
   static constexpr int kCols = DT == kF32 ? 64 : DT == kF16 ? 128 : 192;  // most rows of x in a tile
   static constexpr int kSets = DT == kF32 ? 2 : 1;  // of accumulators
   static constexpr int kA = 2 * kSets * kCols;   // first column of the weights in tensor memory
-  static constexpr int kStages = DT == kBF16 ? 5 : 7;  // of x
-  static constexpr int kPart = kCols * 128;      // bytes of a part of a stage of x
-  static constexpr int kStage = kPart * kXParts;
-  static constexpr int kFifoOff = kStages * kStage;
-  static constexpr int kBars = kFifoOff + kConvert * kSlots * kSlot;
-  static constexpr int kMisc = kBars + 256 + 2 * 8 * kConvert * kSlots;
+  static constexpr int kStages = DT == kBF16 ? 6 : 8;  // of copies (even: a group's steps keep to its stages)
+  static constexpr int kPart = kCols * 128;      // bytes of a part of a step of x
+  static constexpr int kCodes = kPart * kXParts; // where a stage has its codes
+  static constexpr int kStage = kCodes + 2 * kHalfCodes;
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kMisc = kBars + 256;
   static constexpr int kPre = kMisc + 64;        // [n + 1] tiles before each matrix
+  static_assert(kStage % 1024 == 0 && kStages % 2 == 0, "stages");
   static_assert(kA + 4 * 32 * kWParts <= 512, "tensor memory");
   static_assert(kPre + (kMaxMats + 1) * 4 <= 232448, "shared memory");
 };
 
 __host__ __device__ inline int sum_steps(int nks) { return (nks + kGroup - 1) / kGroup; }
-// Whether a step of sums follows step ks.
-__device__ __forceinline__ bool sums_follow(int ks, int nks) { return ks % kGroup == kGroup - 1 || ks == nks - 1; }
 
 struct ManyArgs {
   LinArgs L;
@@ -356,8 +355,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   const LinArgs& L = A.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t *x_full = bars, *x_empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 18, *d_full = bars + 20,
-           *d_empty = bars + 22, *last = bars + 24, *code_full = bars + 32, *code_empty = code_full + kConvert * kSlots;  // [kConvert][kSlots]
+  uint64_t *full = bars, *empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 18, *d_full = bars + 20,
+           *d_empty = bars + 22, *last = bars + 24;
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
   int* pre = reinterpret_cast<int*>(smem + P::kPre);
@@ -367,12 +366,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     return;
   }
   const int nks = L.in / kLinStep, w_tiles = L.out / kLinTile;
+  const int steps = nks + (P::kSums ? sum_steps(nks) : 0);  // of a tile
   const int m_tiles = (L.out + (GLU ? 127 : 255)) / (GLU ? 128 : 256);
   if (tid == 0) {
-    for (int i = 0; i < P::kStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 2);
-    for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], kConvert), mbar_init(&a_empty[i], 2);
+    for (int i = 0; i < P::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kConvert / 2 + 2);
+    for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], kConvert / 2), mbar_init(&a_empty[i], 2);
     for (int i = 0; i < P::kSets; ++i) mbar_init(&d_full[i], 2), mbar_init(&d_empty[i], kResults);
-    for (int i = 0; i < kConvert * kSlots; ++i) mbar_init(&code_full[i], 1), mbar_init(&code_empty[i], 1);
     mbar_init(last, 2);
     *dead = 0;
     fence_mbar_init();
@@ -408,85 +407,109 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   if (warp < kConvert) {
     // ---- conversion: the codes of 16 weight rows of a half, a step at a time ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConvert));
-    const int quarter = warp & 3, half = (warp >> 2) & 1, upper = warp >> 3;
-    const uint8_t* ring = smem + P::kFifoOff + warp * (kSlots * kSlot);
-    uint64_t *full = code_full + warp * kSlots, *empty = code_empty + warp * kSlots;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32 + upper * 16) << 16) + P::kA + half * 32 * P::kWParts;
-    const int wt0 = half * (GLU ? 0 : 8) + quarter * 2 + upper;
-    int slot = 0, st = 0;
-    uint32_t slot_ph = 0, a_ph = 1;  // (a fresh barrier passes a wait for the phase before its first)
+    const int quarter = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
+    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + P::kA + (group * 2 + half) * 32 * P::kWParts;
+    const int wt0 = half * (GLU ? 0 : 8) + quarter * 2;
+    int st = group;
+    uint32_t ph = 0, a_ph = 1;  // (a fresh barrier passes a wait for the phase before its first)
     bool ok = true;
-    uint4 kept[2] = {};  // the records of steps c and 4 + c of a group
-    // the weights of a stage are in tensor memory
-    auto hand_over = [&](uint64_t* read) {
+    uint4 code[2], rec[2];  // a step of the two tiles (of one past the last: whatever the stage holds; its results are not used)
+    // The products wait for the weights only: who hands them over has seen the stage's copies, x among them.
+    auto copied = [&]() {
+      ok = wait_warp(&full[st], ph, dead, err);
+      const uint8_t* step = smem + st * P::kStage + P::kCodes + half * kHalfCodes + quarter * 2 * kLinStepBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        code[h] = *reinterpret_cast<const uint4*>(step + h * kLinStepBytes + lane * 16);
+        rec[h] = *reinterpret_cast<const uint4*>(step + h * kLinStepBytes + 512 + (lane >> 2) * 16);
+      }
+    };
+    auto hand_over = [&]() {
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&a_full[st]);
-        if (read) mbar_arrive(read);
+        mbar_arrive(&a_full[group]);
+        mbar_arrive(&empty[st]);
       }
-      if (st) a_ph ^= 1;
-      st ^= 1;
+      a_ph ^= 1;
+      st += 2;
+      if (st >= P::kStages) st = group, ph ^= 1;
     };
+    int first = group;  // of the tile's steps, this group's first
     for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
       const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-      // a tile past the last one is not copied, and its lanes' results are not used
-      const bool live = t.mt * (GLU ? 8 : 16) + wt0 < w_tiles;
-#pragma unroll 1
-      for (int ks = 0; ks < nks; ++ks) {
-        uint64_t* read = nullptr;
-        const uint32_t to = lanes + st * 64 * P::kWParts;
-        if (live) {
-          const int in_slot = ks % kSlotSteps;
-          if (in_slot == 0 && !(ok = wait_warp(&full[slot], slot_ph, dead, err))) break;
-          const uint8_t* step = ring + slot * kSlot + in_slot * kLinStepBytes;
-          const uint4 code = *reinterpret_cast<const uint4*>(step + lane * 16);
-          const uint4 rec = *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16);
-          if (in_slot == kSlotSteps - 1 || ks == nks - 1) {
-            read = &empty[slot];
-            if (++slot == kSlots) slot = 0, slot_ph ^= 1;
-          }
-          if constexpr (!P::kSums) {
-            uint32_t r[16];
-            convert(code, rec, r);
-            if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
-            tc_fence_after();
-            tc_st_16x128_x8(to, r);
-          } else {
-            const __half2 down = __float2half2_rn(0x1p-12f);
-            const __half2 s[2] = {__hmul2(as_half2(rec.x), down), __hmul2(as_half2(rec.y), down)};
-            uint32_t hi[8], lo[8];
-            convert_two(code, s, 0, hi, lo);
-            if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
-            tc_fence_after();
-            tc_st_16x128_x4(to, hi);
-            tc_st_16x128_x4(to + 32, lo);
-            convert_two(code, s, 1, hi, lo);
-            tc_st_16x128_x4(to + 16, hi);
-            tc_st_16x128_x4(to + 48, lo);
-            if ((ks & 3) == (lane & 3)) {
-              if (ks & 4)
-                kept[1] = rec;
-              else
-                kept[0] = rec;
-            }
-          }
-        } else if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) {
-          break;
+      int i = first;
+      if constexpr (!P::kSums) {
+        // the next step is converted in registers while the products of the one handed over run
+        uint32_t r0[16], r1[16];
+        if (i < nks) {
+          copied();
+          convert(code[0], rec[0], r0);
+          convert(code[1], rec[1], r1);
         }
-        hand_over(read);
-        if constexpr (P::kSums) {
-          if (!sums_follow(ks, nks)) continue;
-          uint32_t r[16];
-          convert_sums(kept, r);
-          if (!(ok = wait_warp(&a_empty[st], a_ph, dead, err))) break;
+#pragma unroll 1
+        for (; i < nks && ok; i += 2) {
+          if (!(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
           tc_fence_after();
-          if (live) tc_st_16x128_x8(lanes + st * 64 * P::kWParts, r);
-          kept[0] = kept[1] = make_uint4(0, 0, 0, 0);
-          hand_over(nullptr);
+          tc_st_16x128_x8(to, r0);
+          tc_st_16x128_x8(to + (16u << 16), r1);
+          hand_over();
+          if (i + 2 < nks) {
+            copied();
+            convert(code[0], rec[0], r0);
+            convert(code[1], rec[1], r1);
+          }
+        }
+      } else {
+        const __half2 down = __float2half2_rn(0x1p-12f);
+#pragma unroll 1
+        for (; i < nks && ok; i += 2) {
+          copied();
+          uint32_t hi[8], lo[8];
+          __half2 s[2] = {__hmul2(as_half2(rec[0].x), down), __hmul2(as_half2(rec[0].y), down)};
+          convert_two(code[0], s, 0, hi, lo);
+          if (!ok || !(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
+          tc_fence_after();
+          tc_st_16x128_x4(to, hi);
+          tc_st_16x128_x4(to + 32, lo);
+          convert_two(code[0], s, 1, hi, lo);
+          tc_st_16x128_x4(to + 16, hi);
+          tc_st_16x128_x4(to + 48, lo);
+          s[0] = __hmul2(as_half2(rec[1].x), down), s[1] = __hmul2(as_half2(rec[1].y), down);
+          convert_two(code[1], s, 0, hi, lo);
+          tc_st_16x128_x4(to + (16u << 16), hi);
+          tc_st_16x128_x4(to + (16u << 16) + 32, lo);
+          convert_two(code[1], s, 1, hi, lo);
+          tc_st_16x128_x4(to + (16u << 16) + 16, hi);
+          tc_st_16x128_x4(to + (16u << 16) + 48, lo);
+          hand_over();
+        }
+        const int wt = t.mt * (GLU ? 8 : 16) + wt0;
+        int stride;
+        const uint8_t* recs = lin_tile(L.w[GLU ? half : 0].packed, t.mat, wt, w_tiles, nks, stride) + 512 + (lane >> 2) * 16;
+#pragma unroll 1
+        for (; i < steps && ok; i += 2) {
+          const int ks = (i - nks) * kGroup + (lane & 3);  // this lane's steps of the group: c and 4 + c
+          uint32_t r[2][16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 two[2] = {};
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              if (wt + h < w_tiles && ks + 4 * p < nks)
+                two[p] = __ldg(reinterpret_cast<const uint4*>(recs + (long long)(ks + 4 * p) * stride + h * kLinStepBytes));
+            convert_sums(two, r[h]);
+          }
+          if (!(ok = wait_warp(&full[st], ph, dead, err))) break;
+          if (!(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
+          tc_fence_after();
+          tc_st_16x128_x8(to, r[0]);
+          tc_st_16x128_x8(to + (16u << 16), r[1]);
+          hand_over();
         }
       }
+      first = i - steps;
     }
   } else if (warp < kConvert + kResults) {
     // ---- results: 32 weight rows of each half, half of the tile's rows of x ----
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.f;
-        for (int ks = 0; ks < nks; ks += kChunk, ++chunk) {
+        for (int i = 0; i < steps; i += kChunk, ++chunk) {
           const int set = chunk & 1;
           if (!(ok = wait_warp(&d_full[set], (chunk >> 1) & 1, dead, err))) break;
           tc_fence_after();
@@ -591,81 +614,67 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegIssue));
     if (warp == kLoadWarp && lane == 0) {
-      // ---- copies of x ----
+      // ---- copies ----
       int copies = 0, st = 0;
       uint32_t ph = 1;
       bool ok = true;
       for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
         const uint32_t bytes = (uint32_t)t.cols * 128;
+        const uint8_t* x = A.xt + (long long)t.row0 * 128;
+        // the tiles of a half that there are (of the second half possibly none)
+        const int wt = t.mt * (GLU ? 8 : 16), here0 = min(8, w_tiles - wt), here1 = GLU ? here0 : max(0, min(8, w_tiles - wt - 8));
+        int s0, s1;
+        const uint8_t* w0 = lin_tile(L.w[0].packed, t.mat, wt, w_tiles, nks, s0);
+        const uint8_t* w1 = here1 == 0 ? nullptr : lin_tile(L.w[GLU].packed, t.mat, GLU ? wt : wt + 8, w_tiles, nks, s1);
+        const uint32_t codes = (here0 + here1) * kLinStepBytes;
 #pragma unroll 1
-        for (int ks = 0, sums = 0; ks < nks; ++copies) {
-          if (!(ok = wait_for(&x_empty[st], ph, dead, err))) break;
-          const int parts = sums ? 1 : P::kXParts;
-          mbar_arrive_expect_tx(&x_full[st], bytes * parts);
-          for (int p = 0; p < parts; ++p)
-            bulk_g2s(smem + st * P::kStage + p * P::kPart,
-                     A.xt + ((sums ? (long long)P::kXParts * nks + ks / kGroup : (long long)p * nks + ks) * A.pad + t.row0) * 128,
-                     bytes, &x_full[st]);
+        for (int i = 0; i < steps; ++i, ++copies, x += A.pad * 128) {
+          if (!(ok = wait_for(&empty[st], ph, dead, err))) break;
+          uint8_t* to = smem + st * P::kStage;
+          if (i < nks) {
+            mbar_arrive_expect_tx(&full[st], bytes * P::kXParts + codes);
+            bulk_g2s(to + P::kCodes, w0, here0 * kLinStepBytes, &full[st]);
+            w0 += s0;
+            if (here1 > 0) {
+              bulk_g2s(to + P::kCodes + kHalfCodes, w1, here1 * kLinStepBytes, &full[st]);
+              w1 += s1;
+            }
+            bulk_g2s(to, x, bytes, &full[st]);
+            if constexpr (P::kXParts == 2) bulk_g2s(to + P::kPart, x + nks * A.pad * 128, bytes, &full[st]);
+          } else {  // (the sums are behind the last part's steps)
+            mbar_arrive_expect_tx(&full[st], bytes);
+            bulk_g2s(to, x + (P::kXParts - 1) * nks * A.pad * 128, bytes, &full[st]);
+          }
           if (++st == P::kStages) st = 0, ph ^= 1;
-          if (P::kSums && !sums && sums_follow(ks, nks))
-            sums = 1;
-          else
-            sums = 0, ++ks;
         }
       }
       for (int i = max(0, copies - P::kStages); i < copies; ++i)  // the copies have landed before the CTA ends
-        mbar_wait(&x_full[i % P::kStages], (i / P::kStages) & 1, err);
-    } else if (warp == kCodeWarp && lane < kConvert) {
-      // ---- copies of codes: a lane for each conversion warp ----
-      const int wt0 = (lane >> 2 & 1) * (GLU ? 0 : 8) + (lane & 3) * 2 + (lane >> 3);
-      const uint8_t* packed = L.w[GLU ? lane >> 2 & 1 : 0].packed;
-      uint8_t* ring = smem + P::kFifoOff + lane * (kSlots * kSlot);
-      uint64_t *full = code_full + lane * kSlots, *empty = code_empty + lane * kSlots;
-      int copies = 0, slot = 0;
-      uint32_t ph = 1;
-      bool ok = true;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-        const int wt = t.mt * (GLU ? 8 : 16) + wt0;
-        if (wt >= w_tiles) continue;
-        const uint8_t* src = packed + ((long long)t.mat * w_tiles + wt) * nks * kLinStepBytes;
-#pragma unroll 1
-        for (int ks = 0; ks < nks; ks += kSlotSteps, src += kSlot, ++copies) {
-          if (!(ok = wait_for(&empty[slot], ph, dead, err))) break;
-          const uint32_t bytes = min(nks - ks, kSlotSteps) * kLinStepBytes;
-          mbar_arrive_expect_tx(&full[slot], bytes);
-          bulk_g2s(ring + slot * kSlot, src, bytes, &full[slot]);
-          if (++slot == kSlots) slot = 0, ph ^= 1;
-        }
-      }
-      for (int i = max(0, copies - kSlots); i < copies; ++i)  // the copies have landed before the CTA ends
-        mbar_wait(&full[i % kSlots], (i / kSlots) & 1, err);
+        mbar_wait(&full[i % P::kStages], (i / P::kStages) & 1, err);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // ---- products: the warp stays together, so that addresses and descriptors are formed in uniform registers, and one
       // lane's predicate is on the instructions ----
       const uint32_t lead = elect_one();
       const int half = warp - kMmaWarp;
       int st = 0, xst = 0, set = 0;
-      uint32_t a_ph = 0, x_ph = 0, d_ph = 1;
+      uint32_t a_ph = 0, d_ph = 1;
       bool ok = true;
       for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-        const int halves = GLU || t.mt * 256 + 128 < L.out ? 2 : 1;
+        const bool mine = half == 0 || GLU || t.mt * 256 + 128 < L.out;
         const uint32_t id = 1u << 4 | (uint32_t)(t.cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // f16, f32, M = 128
 #pragma unroll 1
-        for (int ks = 0, sums = 0; ks < nks;) {
-          const bool first = !sums && (DT == kF32 ? ks % kChunk == 0 : ks == 0);
+        for (int i = 0; i < steps; ++i) {
+          const bool first = DT == kF32 ? i % kChunk == 0 : i == 0;
           if (first && !(ok = wait_warp(&d_empty[set], d_ph, dead, err))) break;
-          if (!(ok = wait_warp(&x_full[xst], x_ph, dead, err))) break;
           if (!(ok = wait_warp(&a_full[st], a_ph, dead, err))) break;
           tc_fence_after();
-          const bool follow = P::kSums && !sums && sums_follow(ks, nks);
           const uint64_t b = tc_desc(smem + xst * P::kStage, 1024, 0);
           const uint32_t d = (set * 2 + half) * P::kCols, a = P::kA + (st * 2 + half) * 32 * P::kWParts;
-          if (half < halves) {
+          if (mine) {
+            const bool two = P::kSums && i < nks;
             // the small parts first: an add truncates by the accumulator's size
-            if (P::kSums && !sums) {
+            if (two) {
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 tc_mma_ts_if(lead, d, a + 32 + y * 8, b + y * 2, id, !first || y > 0);
@@ -673,21 +682,17 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
               }
             }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, P::kSums || !first || y > 0);
+            for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, two || !first || y > 0);
           }
           tc_commit_if(lead, &a_empty[st]);
-          tc_commit_if(lead, &x_empty[xst]);
+          tc_commit_if(lead, &empty[xst]);
           if (st) a_ph ^= 1;
           st ^= 1;
-          if (++xst == P::kStages) xst = 0, x_ph ^= 1;
-          if (!follow && (ks == nks - 1 || (DT == kF32 && ks % kChunk == kChunk - 1))) {
+          if (++xst == P::kStages) xst = 0;
+          if (i == steps - 1 || (DT == kF32 && i % kChunk == kChunk - 1)) {
             tc_commit_if(lead, &d_full[set]);
             if (++set == P::kSets) set = 0, d_ph ^= 1;
           }
-          if (follow)
-            sums = 1;
-          else
-            sums = 0, ++ks;
         }
       }
       tc_commit_if(lead, last);

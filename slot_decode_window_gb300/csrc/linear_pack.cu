@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
     undo[row0 + threadIdx.x] = pow2i(-k);
   }
   __syncthreads();
-  uint8_t* dst = packed + at * nks * kLinStepBytes;
+  const int mat = (int)(at / tiles);
+  int stride;
+  uint8_t* dst = const_cast<uint8_t*>(lin_tile(packed, mat, (int)(at - (long long)mat * tiles), tiles, nks, stride));
   for (int item = threadIdx.x; item < nks * 32; item += 128) {
     const int ks = item >> 5, lane = item & 31, g = lane >> 2, c = lane & 3;
     uint32_t words[4];
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
       for (int u = 0; u < 8; ++u) w |= ((cw >> (4 * u)) & 15u) << ((u & 1 ? 16 : 0) + 4 * (u >> 1));
       words[wi] = w;
     }
-    uint8_t* step = dst + (long long)ks * kLinStepBytes;
+    uint8_t* step = dst + (long long)ks * stride;
     *reinterpret_cast<uint4*>(step + lane * 16) = make_uint4(words[0], words[1], words[2], words[3]);
     if (c < 2) {  // c = 0: the scales, 1: the mins
       const uint16_t* src = c ? mn : scale;
