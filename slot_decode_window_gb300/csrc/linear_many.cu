@@ -18,9 +18,10 @@
 // truncate, so every two steps they are added to f32 registers, with two sets of
 // accumulators in turn.
 //
-// Roles (28 warps): 16 of conversion, in two groups that take the steps in turn,
-// each with a stage of weights of its own (a warp has two tiles of 16 weight rows,
-// a quarter of the lanes of one half); 8 of results (each a quarter of the lanes
+// Roles (28 warps): 16 of conversion, in two groups that take the steps in turn
+// (exact weights: one block of 32 columns each of every step), with stages of
+// weights of their own (a warp has two tiles of 16 weight rows, a quarter of the
+// lanes of one half); 8 of results (each a quarter of the lanes
 // and half of the rows of x); one of copies, codes and x of a step into one stage;
 // one for each half that issues its products (and one that fills the warpgroup).  A step has to pass in 768 clocks for the
 // tensor cores never to wait, and a warp's waits and hand-overs alone take about
@@ -36,9 +37,7 @@ namespace {
 constexpr int kConvert = 16, kResults = 8;    // warps
 constexpr int kLoadWarp = kConvert + kResults, kMmaWarp = kLoadWarp + 1;
 constexpr int kManyThreads = (kConvert + kResults + 4) * 32;
-// Registers a thread: at launch, and by role; the roles' shares are drawn from the launch's.
-constexpr int kRegs = 72, kRegConvert = 56, kRegResults = 120, kRegIssue = 40;
-static_assert(kConvert * kRegConvert + kResults * kRegResults + 4 * kRegIssue <= (kConvert + kResults + 4) * kRegs, "register split");
+constexpr int kRegs = 72;  // registers a thread at launch; the roles' shares below are drawn from them
 constexpr int kHalfCodes = 8 * kLinStepBytes; // a step of 128 weight rows
 constexpr int kChunk = 2;                     // steps between sums of f32 rows
 constexpr int kGroup = 8;                     // steps whose blocks' sums are one step
@@ -57,6 +56,9 @@ template <int DT> struct ManyPlan {
   static constexpr int kBars = kStages * kStage;
   static constexpr int kMisc = kBars + 256;
   static constexpr int kPre = kMisc + 64;        // [n + 1] tiles before each matrix
+  static constexpr int kUnits = kSums ? 4 : 2;   // stages of weights: 32 columns each, or 64
+  static constexpr int kRegConvert = 56, kRegResults = 120, kRegIssue = 40;
+  static_assert(kConvert * kRegConvert + kResults * kRegResults + 4 * kRegIssue <= (kConvert + kResults + 4) * kRegs, "register split");
   static_assert(kStage % 1024 == 0 && kStages % 2 == 0, "stages");
   static_assert(kA + 4 * 32 * kWParts <= 512, "tensor memory");
   static_assert(kPre + (kMaxMats + 1) * 4 <= 232448, "shared memory");
@@ -76,89 +78,128 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 
 // --- rows of x into the workspace --------------------------------------------------
 
-// A warp takes a row: its largest magnitude, then the values times a power of two that brings it to [2^14, 2^15)
-// ([2^9, 2^10) where sums are formed), as f16 (f32: two of them).  A lane writes 16 bytes: pairs j of the four groups of eight columns of a block, the order in which
-// the conversion warps' stores put the codes; the 16-byte pieces of a row's 128 are swizzled by the row.  The blocks' sums
-// go to steps of their own, in the order of `convert_sums`; blocks past the last are zeros.
+// `warps` warps of a CTA take a row: its largest magnitude, then the values times a power of two that brings it to
+// [2^14, 2^15) ([2^9, 2^10) where sums are formed), as f16 (f32: two of them).  A lane has eight columns of a block of 32 at
+// a time, kOct of them in registers between the two passes (longer rows are read again).  The four lanes of a block trade
+// pairs, so that lane j stores pairs j of all four: 16 bytes, in the order in which the conversion warps' stores put the
+// codes; the 16-byte pieces of a row's 128 are swizzled by the row.  The blocks' sums go to steps of their own, in the order of
+// `convert_sums`; blocks past the last are zeros.
+template <int DT> struct RowsPlan {
+  static constexpr int kOct = DT == kF32 ? 4 : 8;
+};
 template <int DT>
-__global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long long xs, int T, int in, uint8_t* xt, long long pad,
-                                                          float* undo) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= T) return;
-  constexpr int kPer = DT == kF32 ? 4 : 8;
-  const char* src = static_cast<const char*>(x) + (long long)row * xs * (DT == kF32 ? 4 : 2);
+__global__ void __launch_bounds__(256) linear_rows_kernel(const void* x, long long xs, int T, int in, int warps, uint8_t* xt,
+                                                          long long pad, float* undo) {
+  constexpr int kOct = RowsPlan<DT>::kOct, kWords = DT == kF32 ? 2 : 1;  // 16-byte words of eight columns
+  constexpr bool kSums = ManyPlan<DT>::kSums;
+  __shared__ float part[8];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * (8 / warps) + warp / warps, mine = (warp % warps) * 32 + lane, step = warps * 32;
+  const bool live = row < T;  // (the CTA meets at a barrier)
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + (long long)(live ? row : 0) * xs * (DT == kF32 ? 4 : 2));
+  const int octets = in / 8, all = kSums ? sum_steps(in / 64) * kGroup * 8 : octets;
+  auto values = [](const uint4 (&u)[kWords], float (&f)[8]) {
+    if constexpr (DT == kF32) {
+      Val<float>::unpack(u[0], f);
+      Val<float>::unpack(u[1], f + 4);
+    } else if constexpr (DT == kF16) {
+      Val<__half>::unpack(u[0], f);
+    } else {
+      Val<__nv_bfloat16>::unpack(u[0], f);
+    }
+  };
+  uint4 held[kOct][kWords];
   float most = 0.f;
-  for (int i = lane; i < in / kPer; i += 32) {
-    const uint4 u = reinterpret_cast<const uint4*>(src)[i];
-    float f[kPer];
-    if constexpr (DT == kF32)
-      Val<float>::unpack(u, f);
-    else if constexpr (DT == kF16)
-      Val<__half>::unpack(u, f);
-    else
-      Val<__nv_bfloat16>::unpack(u, f);
+  auto look = [&](const uint4 (&u)[kWords]) {
+    float f[8];
+    values(u, f);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float a = fabsf(f[j]);
       most = fmaxf(most, a < INFINITY ? a : 0.f);
     }
+  };
+#pragma unroll
+  for (int k = 0; k < kOct; ++k) {
+    const int i = mine + k * step;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) held[k][w] = live && i < octets ? src[i * kWords + w] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < kOct; ++k) look(held[k]);
+  for (int i = mine + kOct * step; live && i < octets; i += step) {
+    uint4 u[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) u[w] = src[i * kWords + w];
+    look(u);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  constexpr int kTop = ManyPlan<DT>::kSums ? 10 : 15;  // (a block's sum has to be an f16 too)
+  if (warps > 1) {
+    if (lane == 0) part[warp] = most;
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) most = fmaxf(most, part[warp / warps * warps + w]);
+  }
+  if (!live) return;
+  constexpr int kTop = kSums ? 10 : 15;  // (a block's sum has to be an f16 too)
   int e = kTop;
   if (most > 0.f) frexpf(most, &e);
   const int up = max(-126, min(126, kTop - e));
   const float mul = pow2i(up);
-  if (lane == 0) undo[row] = pow2i(-up);
-  const long long part = (long long)(in / 64) * pad * 128;
-  uint8_t* sums = xt + part * ManyPlan<DT>::kXParts;
-  const int pieces = in / 8, all = ManyPlan<DT>::kSums ? sum_steps(in / 64) * kGroup * 8 : pieces;
-  for (int i = lane; i < all; i += 32) {  // (`all` is a multiple of 8: the four lanes of a block stay together)
-    const int first = (i >> 2) * 32 + (i & 3) * 2, ks = i >> 3, at = (i & 7) ^ (row & 7);
-    const unsigned quad = 0xFu << (lane & 28);
-    float sum = 0.f;
-    if (i < pieces) {
-      uint32_t hi[4], lo[4];
+  if (mine == 0) undo[row] = pow2i(-up);
+  const long long next = (long long)(in / 64) * pad * 128;  // from a part to the other
+  uint8_t* sums = xt + next * ManyPlan<DT>::kXParts;
+  auto put = [&](int i, const uint4 (&u)[kWords]) {
+    const int ks = i >> 3, j = i & 3, odd = lane & 1, two = lane & 2;
+    float f[8], sum = 0.f;
+    values(u, f);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float a, b;
-        if constexpr (DT == kF32) {
-          const float2 t = *reinterpret_cast<const float2*>(src + (first + 8 * c) * 4);
-          a = t.x, b = t.y;
-        } else {
-          const uint32_t t = *reinterpret_cast<const uint32_t*>(src + (first + 8 * c) * 2);
-          if constexpr (DT == kF16) {
-            const float2 h = __half22float2(as_half2(t));
-            a = h.x, b = h.y;
-          } else {
-            a = __uint_as_float(t << 16), b = __uint_as_float(t & 0xFFFF0000u);
-          }
-        }
-        a *= mul, b *= mul;
-        sum += a + b;
-        const __half2 h = __floats2half2_rn(a, b);
-        hi[c] = as_u32(h);
-        if constexpr (DT == kF32) {
-          const float2 back = __half22float2(h);
-          lo[c] = pack_half2(a - back.x, b - back.y);
-        }
+    for (int c = 0; c < 4; ++c) {
+      const float a = f[2 * c] * mul, b = f[2 * c + 1] * mul;
+      sum += a + b;
+      const __half2 h = __floats2half2_rn(a, b);
+      hi[c] = as_u32(h);
+      if constexpr (DT == kF32) {
+        const float2 back = __half22float2(h);
+        lo[c] = pack_half2(a - back.x, b - back.y);
       }
-      uint4* dst = reinterpret_cast<uint4*>(xt + ((long long)ks * pad + row) * 128 + at * 16);
-      *dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if constexpr (DT == kF32)
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if constexpr (ManyPlan<DT>::kSums) {
+    auto trade = [&](uint32_t (&r)[4]) {  // r[c] of lane l becomes r[l] of lane c, within the four lanes
+      const uint32_t s0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[0] : r[1], 1), s1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[2] : r[3], 1);
+      if (odd) r[0] = s0, r[2] = s1;
+      else r[1] = s0, r[3] = s1;
+      const uint32_t t0 = __shfl_xor_sync(0xFFFFFFFFu, two ? r[0] : r[2], 2), t1 = __shfl_xor_sync(0xFFFFFFFFu, two ? r[1] : r[3], 2);
+      if (two) r[0] = t0, r[1] = t1;
+      else r[2] = t0, r[3] = t1;
+    };
+    trade(hi);
+    if constexpr (DT == kF32) trade(lo);
+    if (i < octets) {
+      uint8_t* dst = xt + ((long long)ks * pad + row) * 128 + ((i & 7) ^ (row & 7)) * 16;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (DT == kF32) *reinterpret_cast<uint4*>(dst + next) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if constexpr (kSums) {
       // the block's sum (at most 2^15) in two parts, to the columns of its min (lane 0 of the four) and its 8 s (lane 1)
-      sum += __shfl_xor_sync(quad, sum, 1);
-      sum += __shfl_xor_sync(quad, sum, 2);
-      const int kind = i & 3, blk = (i >> 2) & 1, step = ks % kGroup, piece = (step >> 2) * 4 + blk * 2 + kind;
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      const int blk = (i >> 2) & 1, at = ks % kGroup, piece = (at >> 2) * 4 + blk * 2 + j;
       const __half h = __float2half_rn(sum);
-      if (kind < 2)
-        *reinterpret_cast<uint32_t*>(sums + ((long long)(ks / kGroup) * pad + row) * 128 + (piece ^ (row & 7)) * 16 + (step & 3) * 4) =
+      if (j < 2 && i < all)
+        *reinterpret_cast<uint32_t*>(sums + ((long long)(ks / kGroup) * pad + row) * 128 + (piece ^ (row & 7)) * 16 + (at & 3) * 4) =
             pack_half2(__half2float(h), sum - __half2float(h));
     }
+  };
+#pragma unroll
+  for (int k = 0; k < kOct; ++k)
+    if (k * step < all) put(mine + k * step, held[k]);
+  for (int i = kOct * step; i < all; i += step) {  // (whole warps: lanes past the end trade zeros)
+    uint4 u[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) u[w] = i + mine < octets ? src[(i + mine) * kWords + w] : make_uint4(0, 0, 0, 0);
+    put(i + mine, u);
   }
 }
 
@@ -255,12 +296,12 @@ __device__ __forceinline__ void convert(const uint4& code, const uint4& rec, uin
 // 2^12 s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the
 // product's f16 leaves at most 5 bits.  s: the records' scales times 2^-12 (2^24 - 12 is the factor that results lose again).
 constexpr float kTwoUndo = 0x1p-12f;
-__device__ __forceinline__ void convert_two(const uint4& code, const __half2 (&s)[2], int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
-  const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f);
+__device__ __forceinline__ void convert_two(const uint2& code, const uint2& scale, int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f), down = __float2half2_rn(0x1p-12f);
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
-    const uint32_t word = blk ? row ? code.w : code.z : row ? code.y : code.x;
-    const __half2 sv = blk ? __high2half2(s[row]) : __low2half2(s[row]);
+    const uint32_t word = row ? code.y : code.x;
+    const __half2 s = __hmul2(as_half2(row ? scale.y : scale.x), down), sv = blk ? __high2half2(s) : __low2half2(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = i < 2 ? word : word >> 8;
@@ -273,21 +314,18 @@ __device__ __forceinline__ void convert_two(const uint4& code, const __half2 (&s
   }
 }
 
-// The weights of a step of sums from the records of steps c and 4 + c of the group: 2^12 m in column 4 i + c for even i,
-// 2^12 8 s for odd i, i = 4 (step / 4) + 2 block + kind; a column's two f16 meet the sum's two parts.
-__device__ __forceinline__ void convert_sums(const uint4 (&rec)[2], uint32_t (&r)[16]) {
+// The weights of half a step of sums (16 columns) from the record of step c (first half) or 4 + c of the group: 2^12 m in column
+// 4 i + c for even i, 2^12 8 s for odd i, i / 2 the block; a column's two f16 meet the sum's two parts.
+__device__ __forceinline__ void convert_sums(const uint4& rec, uint32_t (&r)[8]) {
   const __half2 down = __float2half2_rn(0x1p-9f), up = __float2half2_rn(0x1p12f);
+  const __half2 s[2] = {__hmul2(as_half2(rec.x), down), __hmul2(as_half2(rec.y), down)};
+  const __half2 m[2] = {__hmul2(as_half2(rec.z), up), __hmul2(as_half2(rec.w), up)};
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const __half2 s[2] = {__hmul2(as_half2(rec[p].x), down), __hmul2(as_half2(rec[p].y), down)};
-    const __half2 m[2] = {__hmul2(as_half2(rec[p].z), up), __hmul2(as_half2(rec[p].w), up)};
-#pragma unroll
-    for (int row = 0; row < 2; ++row) {
-      r[p * 8 + 0 + row] = as_u32(__low2half2(m[row]));
-      r[p * 8 + 2 + row] = as_u32(__low2half2(s[row]));
-      r[p * 8 + 4 + row] = as_u32(__high2half2(m[row]));
-      r[p * 8 + 6 + row] = as_u32(__high2half2(s[row]));
-    }
+  for (int row = 0; row < 2; ++row) {
+    r[0 + row] = as_u32(__low2half2(m[row]));
+    r[2 + row] = as_u32(__low2half2(s[row]));
+    r[4 + row] = as_u32(__high2half2(m[row]));
+    r[6 + row] = as_u32(__high2half2(s[row]));
   }
 }
 
@@ -355,8 +393,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   const LinArgs& L = A.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBars);
-  uint64_t *full = bars, *empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 18, *d_full = bars + 20,
-           *d_empty = bars + 22, *last = bars + 24;
+  uint64_t *full = bars, *empty = bars + 8, *a_full = bars + 16, *a_empty = bars + 20, *d_full = bars + 24,
+           *d_empty = bars + 26, *last = bars + 28;
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + P::kMisc);
   volatile int* dead = reinterpret_cast<volatile int*>(smem + P::kMisc + 8);
   int* pre = reinterpret_cast<int*>(smem + P::kPre);
@@ -369,8 +407,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
   const int steps = nks + (P::kSums ? sum_steps(nks) : 0);  // of a tile
   const int m_tiles = (L.out + (GLU ? 127 : 255)) / (GLU ? 128 : 256);
   if (tid == 0) {
-    for (int i = 0; i < P::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], kConvert / 2 + 2);
-    for (int i = 0; i < 2; ++i) mbar_init(&a_full[i], kConvert / 2), mbar_init(&a_empty[i], 2);
+    for (int i = 0; i < P::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], (P::kSums ? kConvert : kConvert / 2) + 2);
+    for (int i = 0; i < P::kUnits; ++i) mbar_init(&a_full[i], kConvert / 2), mbar_init(&a_empty[i], 2);
     for (int i = 0; i < P::kSets; ++i) mbar_init(&d_full[i], 2), mbar_init(&d_empty[i], kResults);
     mbar_init(last, 2);
     *dead = 0;
@@ -406,114 +444,114 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
 
   if (warp < kConvert) {
     // ---- conversion: the codes of 16 weight rows of a half, a step at a time ----
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegConvert));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegConvert));
     const int quarter = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
-    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + P::kA + (group * 2 + half) * 32 * P::kWParts;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + P::kA + half * 32;  // (a stage is 64 columns)
     const int wt0 = half * (GLU ? 0 : 8) + quarter * 2;
-    int st = group;
-    uint32_t ph = 0, a_ph = 1;  // (a fresh barrier passes a wait for the phase before its first)
     bool ok = true;
-    uint4 code[2], rec[2];  // a step of the two tiles (of one past the last: whatever the stage holds; its results are not used)
-    // The products wait for the weights only: who hands them over has seen the stage's copies, x among them.
-    auto copied = [&]() {
-      ok = wait_warp(&full[st], ph, dead, err);
-      const uint8_t* step = smem + st * P::kStage + P::kCodes + half * kHalfCodes + quarter * 2 * kLinStepBytes;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        code[h] = *reinterpret_cast<const uint4*>(step + h * kLinStepBytes + lane * 16);
-        rec[h] = *reinterpret_cast<const uint4*>(step + h * kLinStepBytes + 512 + (lane >> 2) * 16);
-      }
-    };
-    auto hand_over = [&]() {
+    // The products wait for the weights only: who hands them over has seen the step's copies, x among them.
+    auto hand_over = [&](uint64_t* weights, uint64_t* step) {
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&a_full[group]);
-        mbar_arrive(&empty[st]);
+        mbar_arrive(weights);
+        mbar_arrive(step);
       }
-      a_ph ^= 1;
-      st += 2;
-      if (st >= P::kStages) st = group, ph ^= 1;
     };
-    int first = group;  // of the tile's steps, this group's first
-    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-      const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-      int i = first;
-      if constexpr (!P::kSums) {
-        // the next step is converted in registers while the products of the one handed over run
-        uint32_t r0[16], r1[16];
-        if (i < nks) {
-          copied();
-          convert(code[0], rec[0], r0);
-          convert(code[1], rec[1], r1);
-        }
+    // (of a tile past the last, the stage holds whatever it held; its lanes' results are not used)
+    const int from = P::kCodes + half * kHalfCodes + quarter * 2 * kLinStepBytes;
+    if constexpr (!P::kSums) {
+      // The group's steps, 64 columns: the next one is converted in registers while the products of the one handed over run.
+      const uint32_t to = lanes + group * 64;
+      int st = group, first = group;  // first: of the tile's steps, this group's first
+      uint32_t ph = 0, a_ph = 1;      // (a fresh barrier passes a wait for the phase before its first)
+      uint32_t r0[16], r1[16];
+      auto next = [&]() {
+        ok = wait_warp(&full[st], ph, dead, err);
+        const uint8_t* step = smem + st * P::kStage + from;
+        convert(*reinterpret_cast<const uint4*>(step + lane * 16), *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16), r0);
+        step += kLinStepBytes;
+        convert(*reinterpret_cast<const uint4*>(step + lane * 16), *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16), r1);
+      };
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        int i = first;
+        if (i < nks) next();
 #pragma unroll 1
         for (; i < nks && ok; i += 2) {
           if (!(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
           tc_fence_after();
           tc_st_16x128_x8(to, r0);
           tc_st_16x128_x8(to + (16u << 16), r1);
-          hand_over();
-          if (i + 2 < nks) {
-            copied();
-            convert(code[0], rec[0], r0);
-            convert(code[1], rec[1], r1);
-          }
+          hand_over(&a_full[group], &empty[st]);
+          a_ph ^= 1;
+          if ((st += 2) >= P::kStages) st = group, ph ^= 1;
+          if (i + 2 < nks) next();
         }
-      } else {
-        const __half2 down = __float2half2_rn(0x1p-12f);
+        first = i - steps;
+      }
+    } else {
+      // The group's block of every step, 32 columns, in two stages in turn; the next one in registers as above.
+      int st = 0, turn = 0;
+      uint32_t ph = 0, a_ph = 1;
+      uint32_t hi[2][8], lo[2][8];
+      auto next = [&]() {
+        ok = wait_warp(&full[st], ph, dead, err);
+        const uint8_t* step = smem + st * P::kStage + from;
+#pragma unroll
+        for (int h = 0; h < 2; ++h, step += kLinStepBytes)
+          convert_two(*reinterpret_cast<const uint2*>(step + lane * 16 + group * 8),
+                      *reinterpret_cast<const uint2*>(step + 512 + (lane >> 2) * 16), group, hi[h], lo[h]);
+      };
+      auto handed = [&]() {
+        hand_over(&a_full[turn * 2 + group], &empty[st]);
+        if (turn) a_ph ^= 1;
+        turn ^= 1;
+        if (++st == P::kStages) st = 0, ph ^= 1;
+      };
+      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        next();
 #pragma unroll 1
-        for (; i < nks && ok; i += 2) {
-          copied();
-          uint32_t hi[8], lo[8];
-          __half2 s[2] = {__hmul2(as_half2(rec[0].x), down), __hmul2(as_half2(rec[0].y), down)};
-          convert_two(code[0], s, 0, hi, lo);
-          if (!ok || !(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
+        for (int i = 0; i < nks && ok; ++i) {
+          if (!(ok = wait_warp(&a_empty[turn * 2 + group], a_ph, dead, err))) break;
           tc_fence_after();
-          tc_st_16x128_x4(to, hi);
-          tc_st_16x128_x4(to + 32, lo);
-          convert_two(code[0], s, 1, hi, lo);
-          tc_st_16x128_x4(to + 16, hi);
-          tc_st_16x128_x4(to + 48, lo);
-          s[0] = __hmul2(as_half2(rec[1].x), down), s[1] = __hmul2(as_half2(rec[1].y), down);
-          convert_two(code[1], s, 0, hi, lo);
-          tc_st_16x128_x4(to + (16u << 16), hi);
-          tc_st_16x128_x4(to + (16u << 16) + 32, lo);
-          convert_two(code[1], s, 1, hi, lo);
-          tc_st_16x128_x4(to + (16u << 16) + 16, hi);
-          tc_st_16x128_x4(to + (16u << 16) + 48, lo);
-          hand_over();
+          const uint32_t to = lanes + (turn * 2 + group) * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tc_st_16x128_x4(to + ((uint32_t)(16 * h) << 16), hi[h]);
+            tc_st_16x128_x4(to + ((uint32_t)(16 * h) << 16) + 16, lo[h]);
+          }
+          handed();
+          if (i + 1 < nks) next();
         }
+        const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
         const int wt = t.mt * (GLU ? 8 : 16) + wt0;
         int stride;
         const uint8_t* recs = lin_tile(L.w[GLU ? half : 0].packed, t.mat, wt, w_tiles, nks, stride) + 512 + (lane >> 2) * 16;
 #pragma unroll 1
-        for (; i < steps && ok; i += 2) {
-          const int ks = (i - nks) * kGroup + (lane & 3);  // this lane's steps of the group: c and 4 + c
-          uint32_t r[2][16];
+        for (int i = nks; i < steps && ok; ++i) {
+          const int ks = (i - nks) * kGroup + group * 4 + (lane & 3);  // this lane's step of the sums' group
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint4 two[2] = {};
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              if (wt + h < w_tiles && ks + 4 * p < nks)
-                two[p] = __ldg(reinterpret_cast<const uint4*>(recs + (long long)(ks + 4 * p) * stride + h * kLinStepBytes));
-            convert_sums(two, r[h]);
+            uint4 rec = {};
+            if (wt + h < w_tiles && ks < nks)
+              rec = __ldg(reinterpret_cast<const uint4*>(recs + (long long)ks * stride + h * kLinStepBytes));
+            convert_sums(rec, hi[h]);
           }
           if (!(ok = wait_warp(&full[st], ph, dead, err))) break;
-          if (!(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
+          if (!(ok = wait_warp(&a_empty[turn * 2 + group], a_ph, dead, err))) break;
           tc_fence_after();
-          tc_st_16x128_x8(to, r[0]);
-          tc_st_16x128_x8(to + (16u << 16), r[1]);
-          hand_over();
+          const uint32_t to = lanes + (turn * 2 + group) * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) tc_st_16x128_x4(to + ((uint32_t)(16 * h) << 16), hi[h]);
+          handed();
         }
       }
-      first = i - steps;
     }
   } else if (warp < kConvert + kResults) {
     // ---- results: 32 weight rows of each half, half of the tile's rows of x ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegResults));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::kRegResults));
+    griddep_wait();  // the rows' powers of two
     const int quarter = warp & 3, side = (warp - kConvert) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     int chunk = 0;
@@ -552,7 +590,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           }
           if constexpr (GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[0][j] = silu_f32(v[0][j]) * v[1][j];
+            for (int j = 0; j < 16; ++j) v[0][j] = __fdividef(v[0][j], 1.f + __expf(-v[0][j])) * v[1][j];
             store16<DT>(L, v[0], r0 + c, t.begin, t.end, f0, lane);
           }
         }
@@ -612,9 +650,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegIssue));
     if (warp == kLoadWarp && lane == 0) {
       // ---- copies ----
+      griddep_wait();  // the rows of x in the workspace
       int copies = 0, st = 0;
       uint32_t ph = 1;
       bool ok = true;
@@ -667,24 +706,35 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         for (int i = 0; i < steps; ++i) {
           const bool first = DT == kF32 ? i % kChunk == 0 : i == 0;
           if (first && !(ok = wait_warp(&d_empty[set], d_ph, dead, err))) break;
-          if (!(ok = wait_warp(&a_full[st], a_ph, dead, err))) break;
-          tc_fence_after();
           const uint64_t b = tc_desc(smem + xst * P::kStage, 1024, 0);
-          const uint32_t d = (set * 2 + half) * P::kCols, a = P::kA + (st * 2 + half) * 32 * P::kWParts;
-          if (mine) {
-            const bool two = P::kSums && i < nks;
-            // the small parts first: an add truncates by the accumulator's size
-            if (two) {
+          const uint32_t d = (set * 2 + half) * P::kCols;
+          constexpr int kParts = P::kUnits / 2;  // stages of weights to a step
+          const bool two = P::kSums && i < nks;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                tc_mma_ts_if(lead, d, a + 32 + y * 8, b + y * 2, id, !first || y > 0);
-                if constexpr (P::kXParts == 2) tc_mma_ts_if(lead, d, a + y * 8, b + (P::kPart >> 4) + y * 2, id, 1);
+          for (int u = 0; u < kParts && ok; ++u) {
+            const int at = st * kParts + u;
+            if (!(ok = wait_warp(&a_full[at], a_ph, dead, err))) break;
+            tc_fence_after();
+            const uint32_t a = P::kA + at * 64 + half * 32;
+            if (mine) {
+              if constexpr (P::kSums) {
+                // the small parts first: an add truncates by the accumulator's size
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint64_t by = b + (u * 2 + y) * 2;
+                  if (two) tc_mma_ts_if(lead, d, a + 16 + y * 8, by, id, !first || u > 0 || y > 0);
+                  if (two && P::kXParts == 2) tc_mma_ts_if(lead, d, a + y * 8, by + (P::kPart >> 4), id, 1);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + (u * 2 + y) * 2, id, two || !first || u > 0 || y > 0);
+              } else {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, !first || y > 0);
               }
             }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, two || !first || y > 0);
+            tc_commit_if(lead, &a_empty[at]);
           }
-          tc_commit_if(lead, &a_empty[st]);
+          if (!ok) break;
           tc_commit_if(lead, &empty[xst]);
           if (st) a_ph ^= 1;
           st ^= 1;
@@ -713,15 +763,22 @@ int smem_bytes(int n) { return ManyPlan<DT>::kPre + (n + 1) * 4; }
 template <int DT>
 cudaError_t launch(const ManyArgs& A, int nsm, cudaStream_t s) {
   const LinArgs& L = A.L;
-  linear_rows_kernel<DT><<<(unsigned)((L.T + 7) / 8), 256, 0, s>>>(L.x, L.xs, L.T, L.in, const_cast<uint8_t*>(A.xt), A.pad,
-                                                                  const_cast<float*>(A.undo_x));
+  // warps per row: as many as keep it in registers, at most a CTA's
+  int warps = 1;
+  while (warps < 8 && L.in / 8 > warps * 32 * RowsPlan<DT>::kOct) warps *= 2;
+  const int per = 8 / warps;
+  linear_rows_kernel<DT><<<(unsigned)((L.T + per - 1) / per), 256, 0, s>>>(L.x, L.xs, L.T, L.in, warps, const_cast<uint8_t*>(A.xt),
+                                                                          A.pad, const_cast<float*>(A.undo_x));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (L.glu)
-    linear_many_kernel<DT, true><<<nsm, kManyThreads, smem_bytes<DT>(L.n), s>>>(A);
-  else
-    linear_many_kernel<DT, false><<<nsm, kManyThreads, smem_bytes<DT>(L.n), s>>>(A);
-  return cudaGetLastError();
+  // launched while the rows are prepared: its start (barriers, tensor memory, the list of tiles, the first codes) needs none
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(nsm), cfg.blockDim = dim3(kManyThreads), cfg.dynamicSmemBytes = smem_bytes<DT>(L.n), cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at, cfg.numAttrs = 1;
+  return L.glu ? cudaLaunchKernelEx(&cfg, linear_many_kernel<DT, true>, A) : cudaLaunchKernelEx(&cfg, linear_many_kernel<DT, false>, A);
 }
 
 template <int DT, bool GLU>
