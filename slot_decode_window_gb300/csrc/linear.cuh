@@ -64,9 +64,10 @@ cudaError_t launch_linear_pack(const void* codes, const uint16_t* scale, const u
                                uint8_t* packed, float* undo, cudaStream_t s);
 cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s);
 
-// The many-row path: its workspace's bytes, its shared memory limit (once per handle, on the current device).
+// The many-row path: its workspace's bytes; its shared memory limit and how many clusters of 2, 4 and 8 CTAs run at once
+// (once per handle, on the current device).
 long long linear_many_workspace(int in, int max_rows);
-cudaError_t setup_linear_many();
-cudaError_t launch_linear_many(const LinArgs& A, void* workspace, int max_rows, int nsm, cudaStream_t s);
+cudaError_t setup_linear_many(int (&clusters)[3]);
+cudaError_t launch_linear_many(const LinArgs& A, void* workspace, int max_rows, int nsm, const int (&clusters)[3], cudaStream_t s);
 
 }  // namespace strata

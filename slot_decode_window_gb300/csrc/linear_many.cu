@@ -27,7 +27,10 @@
 // tensor cores never to wait, and a warp's waits and hand-overs alone take about
 // as many: hence the two groups, and two warps that issue.  CTAs (one per SM) take
 // the tiles of all matrices in turn, weight rows fastest, so that concurrent CTAs
-// share rows of x in L2.
+// share rows of x in L2.  Where there are fewer tiles than SMs, a cluster of 2, 4 or
+// 8 CTAs takes a tile, each a part of its columns; a CTA sends its part of the
+// results to those that add them up (each a share of the rows of x, in the cluster's
+// order) through distributed shared memory.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 
@@ -71,6 +74,7 @@ struct ManyArgs {
   const uint8_t* xt;     // [parts][in / 64][pad][128 bytes], swizzled, then [groups][pad][128 bytes] of sums (f16, f32)
   const float* undo_x;   // [pad]
   long long pad;         // rows of the workspace
+  int split;             // CTAs of a cluster that share a tile's columns
 };
 
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
@@ -384,6 +388,44 @@ __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
   }
 }
 
+// The same for two rows of x (all lanes of a warp call it).
+template <int DT>
+__device__ __forceinline__ void store2(const LinArgs& L, const float (&v)[2], int r0, int begin, int end, int f, int lane) {
+  if (f - lane >= L.out) return;
+  const bool mine = f < L.out;
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (mine && r0 + j >= begin && r0 + j < end) static_cast<float*>(L.y)[(long long)(r0 + j) * L.ys + f] = v[j];
+  } else {
+    const int odd = lane & 1, r = r0 + odd;
+    const uint32_t own = pack16<DT>(v[0], v[1]);
+    const uint32_t two = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), odd ? 0x3276u : 0x5410u);
+    if (mine && r >= begin && r < end)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(L.y) + (long long)r * L.ys + (f - odd)) = two;
+  }
+}
+
+// A cluster's parts of a tile, in the shared memory of the CTA that adds them up (where the stages of copies were):
+// [part][half][row of x of its share][128 weight rows] f32.
+__device__ __forceinline__ uint32_t part_at(uint32_t smem, int part, int h, int share, int c, int row) {
+  return smem + (((part * 2 + h) * share + c) * 128 + row) * 4;
+}
+// 16 rows of x from row c of the tile on.
+__device__ __forceinline__ void give_part(uint32_t smem, int part, int h, int share, int c, int row, const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 4) {  // (a share is a multiple of 4 rows)
+    const int to = (c + j) / share;
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(part_at(smem, part, h, share, c + j - to * share, row)), "r"(to));
+#pragma unroll
+    for (int y = 0; y < 4; ++y) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + y * 512), "f"(v[j + y]) : "memory");
+  }
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // --- the kernel ---------------------------------------------------------------------
 
 template <int DT, bool GLU>
@@ -404,7 +446,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     return;
   }
   const int nks = L.in / kLinStep, w_tiles = L.out / kLinTile;
-  const int steps = nks + (P::kSums ? sum_steps(nks) : 0);  // of a tile
+  // this CTA's part of a tile's columns: steps k0 to k0 + mine, steps of sums from j0 on
+  uint32_t rank = 0;
+  if (A.split > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int k0 = nks * rank / A.split, mine = nks * (rank + 1) / A.split - k0;
+  const int j0 = sum_steps(nks) * rank / A.split;
+  const int steps = mine + (P::kSums ? sum_steps(nks) * (rank + 1) / A.split - j0 : 0);
+  const int item0 = blockIdx.x / A.split, items = gridDim.x / A.split;
   const int m_tiles = (L.out + (GLU ? 127 : 255)) / (GLU ? 128 : 256);
   if (tid == 0) {
     for (int i = 0; i < P::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], (P::kSums ? kConvert : kConvert / 2) + 2);
@@ -474,11 +522,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         step += kLinStepBytes;
         convert(*reinterpret_cast<const uint4*>(step + lane * 16), *reinterpret_cast<const uint4*>(step + 512 + (lane >> 2) * 16), r1);
       };
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      for (int item = item0; item < total && ok; item += items) {
         int i = first;
-        if (i < nks) next();
+        if (i < mine) next();
 #pragma unroll 1
-        for (; i < nks && ok; i += 2) {
+        for (; i < mine && ok; i += 2) {
           if (!(ok = wait_warp(&a_empty[group], a_ph, dead, err))) break;
           tc_fence_after();
           tc_st_16x128_x8(to, r0);
@@ -486,7 +534,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           hand_over(&a_full[group], &empty[st]);
           a_ph ^= 1;
           if ((st += 2) >= P::kStages) st = group, ph ^= 1;
-          if (i + 2 < nks) next();
+          if (i + 2 < mine) next();
         }
         first = i - steps;
       }
@@ -509,10 +557,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         turn ^= 1;
         if (++st == P::kStages) st = 0, ph ^= 1;
       };
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      for (int item = item0; item < total && ok; item += items) {
         next();
 #pragma unroll 1
-        for (int i = 0; i < nks && ok; ++i) {
+        for (int i = 0; i < mine && ok; ++i) {
           if (!(ok = wait_warp(&a_empty[turn * 2 + group], a_ph, dead, err))) break;
           tc_fence_after();
           const uint32_t to = lanes + (turn * 2 + group) * 64;
@@ -522,15 +570,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             tc_st_16x128_x4(to + ((uint32_t)(16 * h) << 16) + 16, lo[h]);
           }
           handed();
-          if (i + 1 < nks) next();
+          if (i + 1 < mine) next();
         }
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
         const int wt = t.mt * (GLU ? 8 : 16) + wt0;
         int stride;
         const uint8_t* recs = lin_tile(L.w[GLU ? half : 0].packed, t.mat, wt, w_tiles, nks, stride) + 512 + (lane >> 2) * 16;
 #pragma unroll 1
-        for (int i = nks; i < steps && ok; ++i) {
-          const int ks = (i - nks) * kGroup + group * 4 + (lane & 3);  // this lane's step of the sums' group
+        for (int i = mine; i < steps && ok; ++i) {
+          const int ks = (j0 + i - mine) * kGroup + group * 4 + (lane & 3);  // this lane's step of the sums' group
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint4 rec = {};
@@ -556,11 +604,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     int chunk = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+    for (int item = item0; item < total && ok; item += items) {
       const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
       const int f0 = (GLU ? t.mt * 128 : t.mt * 256) + quarter * 32 + lane;
       const int halves = GLU || t.mt * 256 + 128 < L.out ? 2 : 1;
-      const int r0 = t.row0 + side * (t.cols >> 1), mine = t.cols >> 1;
+      const int r0 = t.row0 + side * (t.cols >> 1), cols = t.cols >> 1;
       float undo[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -570,7 +618,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       if constexpr (DT != kF32) {
         if (!(ok = wait_warp(&d_full[0], chunk & 1, dead, err))) break;
         tc_fence_after();
-        for (int c = 0; c < mine; c += 16) {
+        if (A.split > 1) cluster_meet();  // the cluster's stages of copies are free
+        for (int c = 0; c < cols; c += 16) {
+          if (A.split > 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h >= halves) break;
+              uint32_t r[16];
+              tc_ld16(lanes + h * P::kCols + side * cols + c, r);
+              tc_wait_ld(r);
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+              give_part(smem_u32(smem), rank, h, t.cols / A.split, side * cols + c, quarter * 32 + lane, v);
+            }
+            continue;
+          }
           float ux[16];
           load16(A.undo_x + r0 + c, ux);
           float v[2][16];
@@ -578,7 +641,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           for (int h = 0; h < 2; ++h) {
             if (h >= halves) break;
             uint32_t r[16];
-            tc_ld16(lanes + h * P::kCols + side * mine + c, r);
+            tc_ld16(lanes + h * P::kCols + side * cols + c, r);
             tc_wait_ld(r);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -614,9 +677,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (h < halves && c * 16 < mine) {
+              if (h < halves && c * 16 < cols) {
                 uint32_t r[16];
-                tc_ld16(lanes + (set * 2 + h) * P::kCols + side * mine + c * 16, r);
+                tc_ld16(lanes + (set * 2 + h) * P::kCols + side * cols + c * 16, r);
                 tc_wait_ld(r);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2)
@@ -627,9 +690,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           if (lane == 0) mbar_arrive(&d_empty[set]);
         }
         if (!ok) break;
+        if (A.split > 1) cluster_meet();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if (c * 16 >= mine) break;
+          if (c * 16 >= cols) break;
+          if (A.split > 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (h < halves) give_part(smem_u32(smem), rank, h, t.cols / A.split, side * cols + c * 16, quarter * 32 + lane, acc[h][c]);
+            continue;
+          }
           float ux[16];
           load16(A.undo_x + r0 + c * 16, ux);
 #pragma unroll
@@ -649,6 +719,40 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         }
       }
     }
+    if (A.split > 1) {
+      // this CTA's share of the tile's rows of x, added up in the cluster's order
+      if (!ok) cluster_meet();  // (the others count on it)
+      cluster_meet();
+      const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item0);
+      const int f0 = (GLU ? t.mt * 128 : t.mt * 256) + quarter * 32 + lane;
+      const int halves = GLU || t.mt * 256 + 128 < L.out ? 2 : 1, share = t.cols / A.split;
+      float undo[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int f = GLU ? f0 : f0 + h * 128;
+        undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) * (P::kSums ? kTwoUndo : 1.f) : 0.f;
+      }
+      for (int c = side * 2; c < share && ok; c += 4) {
+        const int r = t.row0 + (int)rank * share + c;
+        float v[2][2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves) break;
+          for (int q = 0; q < A.split; ++q) {
+            const float* part = reinterpret_cast<const float*>(smem) + part_at(0, q, h, share, c, quarter * 32 + lane) / 4;
+            v[h][0] += part[0], v[h][1] += part[128];
+          }
+          v[h][0] *= undo[h] * __ldg(A.undo_x + r), v[h][1] *= undo[h] * __ldg(A.undo_x + r + 1);
+        }
+        if constexpr (GLU) {
+          v[0][0] = silu_f32(v[0][0]) * v[1][0], v[0][1] = silu_f32(v[0][1]) * v[1][1];
+          store2<DT>(L, v[0], r, t.begin, t.end, f0, lane);
+        } else {
+          store2<DT>(L, v[0], r, t.begin, t.end, f0, lane);
+          if (halves > 1) store2<DT>(L, v[1], r, t.begin, t.end, f0 + 128, lane);
+        }
+      }
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::kRegIssue));
     if (warp == kLoadWarp && lane == 0) {
@@ -657,21 +761,24 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       int copies = 0, st = 0;
       uint32_t ph = 1;
       bool ok = true;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      for (int item = item0; item < total && ok; item += items) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
         const uint32_t bytes = (uint32_t)t.cols * 128;
-        const uint8_t* x = A.xt + (long long)t.row0 * 128;
+        const uint8_t* x = A.xt + ((long long)k0 * A.pad + t.row0) * 128;
+        const uint8_t* sums = A.xt + (((long long)P::kXParts * nks + j0) * A.pad + t.row0) * 128;  // (behind the last part's steps)
         // the tiles of a half that there are (of the second half possibly none)
         const int wt = t.mt * (GLU ? 8 : 16), here0 = min(8, w_tiles - wt), here1 = GLU ? here0 : max(0, min(8, w_tiles - wt - 8));
         int s0, s1;
         const uint8_t* w0 = lin_tile(L.w[0].packed, t.mat, wt, w_tiles, nks, s0);
         const uint8_t* w1 = here1 == 0 ? nullptr : lin_tile(L.w[GLU].packed, t.mat, GLU ? wt : wt + 8, w_tiles, nks, s1);
         const uint32_t codes = (here0 + here1) * kLinStepBytes;
+        w0 += (long long)k0 * s0;
+        if (here1 > 0) w1 += (long long)k0 * s1;
 #pragma unroll 1
-        for (int i = 0; i < steps; ++i, ++copies, x += A.pad * 128) {
+        for (int i = 0; i < steps; ++i, ++copies) {
           if (!(ok = wait_for(&empty[st], ph, dead, err))) break;
           uint8_t* to = smem + st * P::kStage;
-          if (i < nks) {
+          if (i < mine) {
             mbar_arrive_expect_tx(&full[st], bytes * P::kXParts + codes);
             bulk_g2s(to + P::kCodes, w0, here0 * kLinStepBytes, &full[st]);
             w0 += s0;
@@ -681,9 +788,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             }
             bulk_g2s(to, x, bytes, &full[st]);
             if constexpr (P::kXParts == 2) bulk_g2s(to + P::kPart, x + nks * A.pad * 128, bytes, &full[st]);
-          } else {  // (the sums are behind the last part's steps)
+            x += A.pad * 128;
+          } else {
             mbar_arrive_expect_tx(&full[st], bytes);
-            bulk_g2s(to, x + (P::kXParts - 1) * nks * A.pad * 128, bytes, &full[st]);
+            bulk_g2s(to, sums, bytes, &full[st]);
+            sums += A.pad * 128;
           }
           if (++st == P::kStages) st = 0, ph ^= 1;
         }
@@ -698,9 +807,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       int st = 0, xst = 0, set = 0;
       uint32_t a_ph = 0, d_ph = 1;
       bool ok = true;
-      for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+      for (int item = item0; item < total && ok; item += items) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
-        const bool mine = half == 0 || GLU || t.mt * 256 + 128 < L.out;
+        const bool live = half == 0 || GLU || t.mt * 256 + 128 < L.out;
         const uint32_t id = 1u << 4 | (uint32_t)(t.cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // f16, f32, M = 128
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
@@ -709,14 +818,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           const uint64_t b = tc_desc(smem + xst * P::kStage, 1024, 0);
           const uint32_t d = (set * 2 + half) * P::kCols;
           constexpr int kParts = P::kUnits / 2;  // stages of weights to a step
-          const bool two = P::kSums && i < nks;
+          const bool two = P::kSums && i < mine;
 #pragma unroll
           for (int u = 0; u < kParts && ok; ++u) {
             const int at = st * kParts + u;
             if (!(ok = wait_warp(&a_full[at], a_ph, dead, err))) break;
             tc_fence_after();
             const uint32_t a = P::kA + at * 64 + half * 32;
-            if (mine) {
+            if (live) {
               if constexpr (P::kSums) {
                 // the small parts first: an add truncates by the accumulator's size
 #pragma unroll
@@ -751,6 +860,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
     }
     __syncwarp();
   }
+  if (A.split > 1 && (warp < kConvert || warp >= kConvert + kResults)) {
+    cluster_meet();
+    cluster_meet();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -760,9 +873,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
 template <int DT>
 int smem_bytes(int n) { return ManyPlan<DT>::kPre + (n + 1) * 4; }
 
+// CTAs to a tile: as many as leave every tile a cluster of its own at once and every CTA two steps.
+int split_of(int tiles, int nks, const int (&clusters)[3]) {
+  for (int i = 2; i >= 0; --i)
+    if (tiles <= clusters[i] && nks >= 4 << i) return 2 << i;
+  return 1;
+}
+
 template <int DT>
-cudaError_t launch(const ManyArgs& A, int nsm, cudaStream_t s) {
+cudaError_t launch(ManyArgs A, int nsm, const int (&clusters)[3], cudaStream_t s) {
   const LinArgs& L = A.L;
+  int tiles = nsm;
+  A.split = 1;
+  if (!L.offsets) {  // (with offsets the number of tiles is the device's)
+    const long long all = ((long long)L.out + (L.glu ? 127 : 255)) / (L.glu ? 128 : 256) * ((L.T + ManyPlan<DT>::kCols - 1) / ManyPlan<DT>::kCols);
+    if (all < nsm) tiles = (int)all, A.split = split_of(tiles, L.in / kLinStep, clusters);
+  }
   // warps per row: as many as keep it in registers, at most a CTA's
   int warps = 1;
   while (warps < 8 && L.in / 8 > warps * 32 * RowsPlan<DT>::kOct) warps *= 2;
@@ -774,10 +900,13 @@ cudaError_t launch(const ManyArgs& A, int nsm, cudaStream_t s) {
   // launched while the rows are prepared: its start (barriers, tensor memory, the list of tiles, the first codes) needs none
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(nsm), cfg.blockDim = dim3(kManyThreads), cfg.dynamicSmemBytes = smem_bytes<DT>(L.n), cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at, cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = A.split, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at, cfg.numAttrs = A.split > 1 ? 2 : 1;
+  if (A.split > 1) cfg.gridDim = dim3(tiles * A.split);
   return L.glu ? cudaLaunchKernelEx(&cfg, linear_many_kernel<DT, true>, A) : cudaLaunchKernelEx(&cfg, linear_many_kernel<DT, false>, A);
 }
 
@@ -802,21 +931,34 @@ long long pad_rows(int max_rows) { return (((long long)max_rows + 7) & ~7LL) + 1
 
 long long linear_many_workspace(int in, int max_rows) { return pad_rows(max_rows) * row_bytes(in); }
 
-cudaError_t setup_linear_many() {
+// clusters: how many clusters of 2, 4 and 8 CTAs run at once.
+cudaError_t setup_linear_many(int (&clusters)[3]) {
   const cudaError_t e[6] = {setup<kF32, false>(),  setup<kF32, true>(),  setup<kF16, false>(),
                             setup<kF16, true>(), setup<kBF16, false>(), setup<kBF16, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
+  for (int i = 0; i < 3; ++i) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(64 << i), cfg.blockDim = dim3(kManyThreads), cfg.dynamicSmemBytes = smem_bytes<kF16>(kMaxMats);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2 << i, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at, cfg.numAttrs = 1;
+    const cudaError_t x = cudaOccupancyMaxActiveClusters(&clusters[i], linear_many_kernel<kF16, false>, &cfg);
+    if (x != cudaSuccess) return x;
+  }
   return cudaSuccess;
 }
 
-cudaError_t launch_linear_many(const LinArgs& L, void* workspace, int max_rows, int nsm, cudaStream_t s) {
+cudaError_t launch_linear_many(const LinArgs& L, void* workspace, int max_rows, int nsm, const int (&clusters)[3], cudaStream_t s) {
   ManyArgs A;
   A.L = L;
   A.pad = pad_rows(max_rows);
   A.xt = static_cast<uint8_t*>(workspace);
   A.undo_x = reinterpret_cast<const float*>(A.xt + A.pad * (row_bytes(L.in) - 4));
-  return L.dtype == kF32 ? launch<kF32>(A, nsm, s) : L.dtype == kF16 ? launch<kF16>(A, nsm, s) : launch<kBF16>(A, nsm, s);
+  return L.dtype == kF32   ? launch<kF32>(A, nsm, clusters, s)
+         : L.dtype == kF16 ? launch<kF16>(A, nsm, clusters, s)
+                           : launch<kBF16>(A, nsm, clusters, s);
 }
 
 }  // namespace strata

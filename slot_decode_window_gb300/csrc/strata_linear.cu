@@ -12,6 +12,7 @@ using namespace strata;
 struct strata_linear {
   strata_linear_desc desc;
   int device = 0, nsm = 0, mats = 1;
+  int clusters[3] = {};  // of 2, 4 and 8 CTAs that run at once
   uint8_t* mem = nullptr;  // error word, then the matrices and their rows' powers of two
   unsigned* err = nullptr;
   LinMat w[2] = {};
@@ -88,7 +89,7 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
       free_linear(h);
       return STRATA_ENOMEM;
     }
-    if (setup_linear_many() != cudaSuccess) {
+    if (setup_linear_many(h->clusters) != cudaSuccess) {
       cudaGetLastError();
       free_linear(h);
       return STRATA_ECUDA;
@@ -133,7 +134,7 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
   A.x = x, A.y = y, A.xs = x_stride, A.ys = y_stride, A.dtype = dtype, A.T = T, A.offsets = offsets, A.err = h->err;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool few = d.n == 1 && T <= kLinFewRows;
-  if ((few ? launch_linear_few(A, h->nsm, s) : launch_linear_many(A, h->ws, d.max_rows, h->nsm, s)) != cudaSuccess) {
+  if ((few ? launch_linear_few(A, h->nsm, s) : launch_linear_many(A, h->ws, d.max_rows, h->nsm, h->clusters, s)) != cudaSuccess) {
     cudaGetLastError();
     return STRATA_ECUDA;
   }
