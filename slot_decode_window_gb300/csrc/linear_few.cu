@@ -14,8 +14,6 @@
 namespace strata {
 namespace {
 
-constexpr int kFewWarps = 16, kFewThreads = kFewWarps * 32;
-
 template <int DT> struct FewType;
 template <> struct FewType<kF32> {
   static constexpr int kParts = 3;
@@ -58,13 +56,8 @@ __device__ __forceinline__ float half_of(uint32_t two, int upper) {
 
 // Eight neighbouring values of a row, as kParts times four pairs.
 template <int DT>
-__device__ __forceinline__ void few_x(const void* row, int i, bool live, uint32_t (&b)[FewType<DT>::kParts][4]) {
+__device__ __forceinline__ void few_x(const uint4 (&u)[DT == kF32 ? 2 : 1], uint32_t (&b)[FewType<DT>::kParts][4]) {
   if constexpr (DT == kF32) {
-    uint4 u[2] = {};
-    if (live) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + i);
-      u[0] = p[0], u[1] = p[1];
-    }
     const uint32_t v[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -77,133 +70,150 @@ __device__ __forceinline__ void few_x(const void* row, int i, bool live, uint32_
       }
     }
   } else {
-    uint4 u = {};
-    if (live) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
-    b[0][0] = u.x, b[0][1] = u.y, b[0][2] = u.z, b[0][3] = u.w;
+    b[0][0] = u[0].x, b[0][1] = u[0].y, b[0][2] = u[0].z, b[0][3] = u[0].w;
   }
 }
 
-// A CTA takes kTiles tiles of each stack; its warps take the steps in turn.
-template <int DT, int kTiles, bool kGlu>
-__global__ void __launch_bounds__(kFewThreads) few_kernel(LinArgs A) {
-  constexpr int kMats = kGlu ? 2 : 1, kParts = FewType<DT>::kParts;
+// A CTA takes kTiles neighbouring tiles of each stack, whose step is one piece of memory; its kWarps warps take the steps in
+// turn, and their sums meet in shared memory in the warps' order.  A step's columns of x are split into parts once for
+// all of its tiles.
+template <int DT, int kTiles, int kWarps, bool kGlu>
+__global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : DT == kF32 || kGlu ? 1 : 2) few_kernel(LinArgs A) {
+  constexpr int kMats = kGlu ? 2 : 1, kParts = FewType<DT>::kParts, kAll = kMats * kTiles;
   constexpr uint32_t kOnes = DT == kF16 ? 0x3C003C00u : 0x3F803F80u;
-  __shared__ float red[kFewWarps][kMats][kTiles * 128];
+  __shared__ float red[kWarps][kAll * 128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int tiles = A.out / kLinTile, nks = A.in / kLinStep;
-  const int tile0 = blockIdx.x * kTiles, mat = blockIdx.y;
+  const int tile0 = blockIdx.x * kTiles;
   int begin, end;
-  if (!lin_rows(A, mat, begin, end) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(A.err, kErrIndex);
-  const uint8_t* src[kMats][kTiles];
-  int stride[kTiles];
+  if (!lin_rows(A, 0, begin, end) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(A.err, kErrIndex);
+  if (begin >= end) return;
+  int stride;  // (the tiles of a CTA are of one group of 8; those past the last read it again and write nothing)
+  const uint8_t* src[kMats];
 #pragma unroll
-  for (int m = 0; m < kMats; ++m)
+  for (int m = 0; m < kMats; ++m) src[m] = lin_tile(A.w[m].packed, 0, tile0, tiles, nks, stride);
+  const bool live = begin + g < end;
+  const char* row = static_cast<const char*>(A.x) + (long long)(begin + g) * A.xs * (DT == kF32 ? 4 : 2);
+  float acc[kAll][4] = {};
+  uint4 code[kAll], rec[kAll];
+  auto load = [&](int ks, int y) {
+    const uint8_t* p = src[y / kTiles] + (long long)ks * stride + min(y % kTiles, tiles - 1 - tile0) * kLinStepBytes;
+    code[y] = __ldg(reinterpret_cast<const uint4*>(p + lane * 16));
+    rec[y] = __ldg(reinterpret_cast<const uint4*>(p + 512 + g * 16));
+  };
+  uint4 xr[2][DT == kF32 ? 2 : 1];  // this lane's eight columns of the step's two blocks
+  auto load_x = [&](int ks) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)  // (a CTA past the last tile reads it again and writes nothing)
-      src[m][t] = lin_tile(A.w[m].packed, mat, min(tile0 + t, tiles - 1), tiles, nks, stride[t]);
-  for (int r0 = begin; r0 < end; r0 += kLinFewRows) {
-    const bool live = r0 + g < end;
-    const char* row = static_cast<const char*>(A.x) + (long long)(r0 + g) * A.xs * (DT == kF32 ? 4 : 2);
-    float acc[kMats][kTiles][4] = {};
-    for (int ks = warp; ks < nks; ks += kFewWarps) {
-      uint4 code[kMats][kTiles], rec[kMats][kTiles];
+    for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-      for (int m = 0; m < kMats; ++m)
+      for (int w = 0; w < (DT == kF32 ? 2 : 1); ++w)
+        xr[blk][w] = live ? reinterpret_cast<const uint4*>(row + (ks * kLinStep + blk * 32 + c * 8) * (DT == kF32 ? 4 : 2))[w]
+                          : make_uint4(0, 0, 0, 0);
+  };
+  if (warp < nks) {
+    load_x(warp);
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const uint8_t* p = src[m][t] + (long long)ks * stride[t];
-          code[m][t] = __ldg(reinterpret_cast<const uint4*>(p + lane * 16));
-          rec[m][t] = __ldg(reinterpret_cast<const uint4*>(p + 512 + g * 16));
-        }
+    for (int y = 0; y < kAll; ++y) load(warp, y);
+  }
+  for (int ks = warp; ks < nks; ks += kWarps) {
+    const int next = ks + kWarps;
+    uint32_t b[2][kParts][4];
+    float xsum[2][4] = {};
+    const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+      few_x<DT>(xr[blk], b[blk]);
+#pragma unroll
+      for (int k = kParts - 1; k >= 0; --k) {
+        few_mma<DT>(xsum[blk], ones, b[blk][k][0], b[blk][k][1]);
+        few_mma<DT>(xsum[blk], ones, b[blk][k][2], b[blk][k][3]);
+      }
+    }
+    if (next < nks) load_x(next);
+#pragma unroll
+    for (int y = 0; y < kAll; ++y) {
+      // a tile's next step is on its way from here on
+      const uint4 now = code[y], scales = rec[y];
+      if (next < nks) load(next, y);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
-        uint32_t b[kParts][4];
-        few_x<DT>(row, ks * kLinStep + blk * 32 + c * 8, live, b);
-        float xsum[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+        const uint32_t w0 = blk ? now.z : now.x, w1 = blk ? now.w : now.y;
+        const uint32_t a0[4] = {few_pair<DT, 0>(w0), few_pair<DT, 0>(w1), few_pair<DT, 1>(w0), few_pair<DT, 1>(w1)};
+        const uint32_t a1[4] = {few_pair<DT, 2>(w0), few_pair<DT, 2>(w1), few_pair<DT, 3>(w0), few_pair<DT, 3>(w1)};
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = kParts - 1; k >= 0; --k) {
-          few_mma<DT>(xsum, ones, b[k][0], b[k][1]);
-          few_mma<DT>(xsum, ones, b[k][2], b[k][3]);
+          few_mma<DT>(d, a0, b[blk][k][0], b[blk][k][1]);
+          few_mma<DT>(d, a1, b[blk][k][2], b[blk][k][3]);
         }
-#pragma unroll
-        for (int m = 0; m < kMats; ++m)
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            const uint32_t w0 = blk ? code[m][t].z : code[m][t].x, w1 = blk ? code[m][t].w : code[m][t].y;
-            const uint32_t a0[4] = {few_pair<DT, 0>(w0), few_pair<DT, 0>(w1), few_pair<DT, 1>(w0), few_pair<DT, 1>(w1)};
-            const uint32_t a1[4] = {few_pair<DT, 2>(w0), few_pair<DT, 2>(w1), few_pair<DT, 3>(w0), few_pair<DT, 3>(w1)};
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = kParts - 1; k >= 0; --k) {
-              few_mma<DT>(d, a0, b[k][0], b[k][1]);
-              few_mma<DT>(d, a1, b[k][2], b[k][3]);
-            }
-            const uint32_t* h = &rec[m][t].x;  // scales of rows g, g + 8 (both blocks), then mins
-            const float s0 = 0x1p-24f * half_of(h[0], blk), s1 = 0x1p-24f * half_of(h[1], blk);
-            const float o0 = fmaf(-16.f, s0, half_of(h[2], blk)), o1 = fmaf(-16.f, s1, half_of(h[3], blk));
-            float(&z)[4] = acc[m][t];
-            z[0] = fmaf(s0, d[0], fmaf(o0, xsum[0], z[0]));
-            z[1] = fmaf(s0, d[1], fmaf(o0, xsum[1], z[1]));
-            z[2] = fmaf(s1, d[2], fmaf(o1, xsum[0], z[2]));
-            z[3] = fmaf(s1, d[3], fmaf(o1, xsum[1], z[3]));
-          }
+        const float s0 = 0x1p-24f * half_of(scales.x, blk), s1 = 0x1p-24f * half_of(scales.y, blk);
+        const float o0 = fmaf(-16.f, s0, half_of(scales.z, blk)), o1 = fmaf(-16.f, s1, half_of(scales.w, blk));
+        float(&z)[4] = acc[y];
+        z[0] = fmaf(s0, d[0], fmaf(o0, xsum[blk][0], z[0]));
+        z[1] = fmaf(s0, d[1], fmaf(o0, xsum[blk][1], z[1]));
+        z[2] = fmaf(s1, d[2], fmaf(o1, xsum[blk][0], z[2]));
+        z[3] = fmaf(s1, d[3], fmaf(o1, xsum[blk][1], z[3]));
       }
     }
+  }
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
+  for (int y = 0; y < kAll; ++y)
+    *reinterpret_cast<float4*>(&red[warp][y * 128 + lane * 4]) = make_float4(acc[y][0], acc[y][1], acc[y][2], acc[y][3]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kTiles * 128; i += kWarps * 32) {
+    // consecutive threads take consecutive weight rows of one row of x
+    const int col = i / (kTiles * 16), t = i / 16 % kTiles, r = i & 15;
+    const int from = t * 128 + ((r & 7) * 4 + (col >> 1)) * 4 + (r >> 3) * 2 + (col & 1);
+    const int o = (tile0 + t) * kLinTile + r;
+    if (tile0 + t >= tiles || begin + col >= end) continue;
+    float v[kMats];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-        *reinterpret_cast<float4*>(&red[warp][m][t * 128 + lane * 4]) =
-            make_float4(acc[m][t][0], acc[m][t][1], acc[m][t][2], acc[m][t][3]);
-    __syncthreads();
-    if (threadIdx.x < kTiles * 128) {
-      // consecutive threads take consecutive weight rows of one row of x
-      const int t = threadIdx.x >> 7, col = (threadIdx.x >> 4) & 7, r = threadIdx.x & 15;
-      const int from = t * 128 + ((r & 7) * 4 + (col >> 1)) * 4 + (r >> 3) * 2 + (col & 1);
-      const int o = (tile0 + t) * kLinTile + r;
-      if (tile0 + t < tiles && r0 + col < end) {
-        float v[kMats];
+    for (int m = 0; m < kMats; ++m) {
+      float s = 0.f;
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          float s = 0.f;
-#pragma unroll
-          for (int w = 0; w < kFewWarps; ++w) s += red[w][m][from];
-          v[m] = s * A.w[m].undo[(long long)mat * A.out + o];
-        }
-        const float y = kGlu ? silu_f32(v[0]) * v[kMats - 1] : v[0];
-        const long long at = (long long)(r0 + col) * A.ys + o;
-        if constexpr (DT == kF32)
-          static_cast<float*>(A.y)[at] = y;
-        else if constexpr (DT == kF16)
-          static_cast<__half*>(A.y)[at] = __float2half_rn(y);
-        else
-          static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(y);
-      }
+      for (int w = 0; w < kWarps; ++w) s += red[w][m * kTiles * 128 + from];
+      v[m] = s * A.w[m].undo[o];
     }
-    __syncthreads();
+    const float y = kGlu ? silu_f32(v[0]) * v[kMats - 1] : v[0];
+    const long long at = (long long)(begin + col) * A.ys + o;
+    if constexpr (DT == kF32)
+      static_cast<float*>(A.y)[at] = y;
+    else if constexpr (DT == kF16)
+      static_cast<__half*>(A.y)[at] = __float2half_rn(y);
+    else
+      static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(y);
   }
 }
 
-template <int DT, int kTiles>
-void launch_t(const LinArgs& A, cudaStream_t s) {
-  const dim3 grid((A.out / kLinTile + kTiles - 1) / kTiles, A.n);
-  if (A.glu)
-    few_kernel<DT, kTiles, true><<<grid, kFewThreads, 0, s>>>(A);
+template <int DT, int kTiles, int kWarps, bool kGlu>
+void launch_k(const LinArgs& A, cudaStream_t s) {
+  few_kernel<DT, kTiles, kWarps, kGlu><<<(A.out / kLinTile + kTiles - 1) / kTiles, kWarps * 32, 0, s>>>(A);
+}
+
+// One tile and 16 warps a CTA while all tiles' CTAs run at once (two an SM), so that a small matrix is spread over the SMs; 4
+// tiles (of a pair, 2 of each) for larger ones, which are bound by memory and by x's parts, with 8 warps and, where an SM
+// gets CTAs enough, 4: the fewer warps share the steps, the less of a CTA's time is its start and its join.  One row of 4096
+// columns: 8192 weight rows 10.5 us with 8 warps, 12.8 us with 4; 2048 columns, 151936 weight rows 60.5 and 55.6 us.
+template <int DT, bool kGlu>
+void launch_t(const LinArgs& A, int nsm, cudaStream_t s) {
+  const int tiles = A.out / kLinTile;
+  if (tiles <= 2 * nsm)
+    launch_k<DT, 1, 16, kGlu>(A, s);
+  else if (tiles <= 16 * nsm)
+    launch_k<DT, kGlu ? 2 : 4, 8, kGlu>(A, s);
   else
-    few_kernel<DT, kTiles, false><<<grid, kFewThreads, 0, s>>>(A);
+    launch_k<DT, kGlu ? 2 : 4, 4, kGlu>(A, s);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s) {
-  (void)nsm;
   if (A.dtype == kF32)
-    launch_t<kF32, 1>(A, s);
+    A.glu ? launch_t<kF32, true>(A, nsm, s) : launch_t<kF32, false>(A, nsm, s);
   else if (A.dtype == kF16)
-    launch_t<kF16, 1>(A, s);
+    A.glu ? launch_t<kF16, true>(A, nsm, s) : launch_t<kF16, false>(A, nsm, s);
   else
-    launch_t<kBF16, 1>(A, s);
+    A.glu ? launch_t<kBF16, true>(A, nsm, s) : launch_t<kBF16, false>(A, nsm, s);
   return cudaGetLastError();
 }
 

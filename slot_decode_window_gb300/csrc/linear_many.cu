@@ -342,6 +342,13 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// z / (1 + e^-z); for 16-bit results with the fast exponential and quotient (a few 2^-22 of it against their 2^-12).
+template <int DT>
+__device__ __forceinline__ float silu(float z) {
+  if constexpr (DT == kF32) return silu_f32(z);
+  return __fdividef(z, 1.f + __expf(-z));
+}
+
 // Two products in one instruction.
 __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
   asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
@@ -390,7 +397,7 @@ __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
 
 // The same for two rows of x (all lanes of a warp call it).
 template <int DT>
-__device__ __forceinline__ void store2(const LinArgs& L, const float (&v)[2], int r0, int begin, int end, int f, int lane) {
+__device__ __forceinline__ void store2(const LinArgs& L, const float* v, int r0, int begin, int end, int f, int lane) {
   if (f - lane >= L.out) return;
   const bool mine = f < L.out;
   if constexpr (DT == kF32) {
@@ -653,7 +660,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           }
           if constexpr (GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[0][j] = __fdividef(v[0][j], 1.f + __expf(-v[0][j])) * v[1][j];
+            for (int j = 0; j < 16; ++j) v[0][j] = silu<DT>(v[0][j]) * v[1][j];
             store16<DT>(L, v[0], r0 + c, t.begin, t.end, f0, lane);
           }
         }
@@ -711,7 +718,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             }
           if constexpr (GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[0][c][j] = silu_f32(acc[0][c][j]) * acc[1][c][j];
+            for (int j = 0; j < 16; ++j) acc[0][c][j] = silu<DT>(acc[0][c][j]) * acc[1][c][j];
           }
 #pragma unroll
           for (int h = 0; h < (GLU ? 1 : 2); ++h)
@@ -732,24 +739,38 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         const int f = GLU ? f0 : f0 + h * 128;
         undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) * (P::kSums ? kTwoUndo : 1.f) : 0.f;
       }
-      for (int c = side * 2; c < share && ok; c += 4) {
-        const int r = t.row0 + (int)rank * share + c;
-        float v[2][2] = {};
+      // 8 rows of x at a time, whose chains of sums, results and stores overlap (a share is 4, 8 or a multiple of 4 rows)
+#pragma unroll 1
+      for (int c0 = 0; c0 < share && ok; c0 += 16) {
+        const int c = c0 + side * 8, r = t.row0 + (int)rank * share + c, n = min(8, share - c);
+        float v[2][8] = {};
+        float4 ux[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          if (j < n) ux[j / 4] = __ldg(reinterpret_cast<const float4*>(A.undo_x + r + j));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h >= halves) break;
           for (int q = 0; q < A.split; ++q) {
             const float* part = reinterpret_cast<const float*>(smem) + part_at(0, q, h, share, c, quarter * 32 + lane) / 4;
-            v[h][0] += part[0], v[h][1] += part[128];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < n) v[h][j] += part[j * 128];
           }
-          v[h][0] *= undo[h] * __ldg(A.undo_x + r), v[h][1] *= undo[h] * __ldg(A.undo_x + r + 1);
+          const float* u = &ux[0].x;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[h][j] *= undo[h] * u[j];
         }
         if constexpr (GLU) {
-          v[0][0] = silu_f32(v[0][0]) * v[1][0], v[0][1] = silu_f32(v[0][1]) * v[1][1];
-          store2<DT>(L, v[0], r, t.begin, t.end, f0, lane);
-        } else {
-          store2<DT>(L, v[0], r, t.begin, t.end, f0, lane);
-          if (halves > 1) store2<DT>(L, v[1], r, t.begin, t.end, f0 + 128, lane);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[0][j] = silu<DT>(v[0][j]) * v[1][j];
+        }
+#pragma unroll
+        for (int h = 0; h < (GLU ? 1 : 2); ++h) {
+          if (h >= halves) break;
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            if (j < n) store2<DT>(L, v[h] + j, r + j, t.begin, t.end, f0 + h * 128, lane);
         }
       }
     }
