@@ -725,17 +725,20 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * the same address).  offsets: device int32 [n + 1], matrix i takes the rows
  * offsets[i] to offsets[i + 1] - 1 (strata_sort_plan's); NULL for n = 1: all
  * rows.  Rows of no matrix are left as they were.  A matrix whose range is out
- * of order or outside 0..T is left out, and the next strata_linear_sync reports
- * EDEVICE.  T = 0 does nothing.
- * Sums are f32.  Up to 8 rows of n = 1 (offsets NULL) are one launch on the exact weights
- * and the exact f16, bf16 or (24 bits) f32 rows, and a row's bits do not depend
- * on the others.  More take 16-bit parts: f16 and bf16 rows exactly, with
- * weights rounded to f16; f32 rows and their weights in two parts (22 bits).
- * Rows are scaled by a power of two of their own, so values of any size keep
- * this.  A row with infinities or NaN gives numbers of no meaning in that row
- * only.  Calls of more rows use the workspace: on one handle they, and replays of
- * captured ones, must not overlap on the GPU.  The same call gives the same
- * bits.  Returns EINVAL (T above max_rows among it), ECUDA. */
+ * of order or outside 0..T is left out (rows that two others then both name have
+ * no defined output), and the next strata_linear_sync reports EDEVICE.  T = 0 does
+ * nothing.
+ * Sums are f32.  Up to 8 rows of n = 1 are one launch on the exact weights and the
+ * exact rows (24 bits of f32), and a row's bits do not depend on the others.
+ * More take f16 products: f16 rows exactly and f32 rows in two parts (22 bits),
+ * with exact weights; bf16 rows exactly with weights rounded to f16.  Rows are
+ * scaled by a power of two of their own and weights by one of their row of W, so
+ * values of any size keep this (exact: but for bits below 2^-34 of a row's largest
+ * value, and scales below 2^-24 of the largest of their row of W).  A row with
+ * infinities or NaN gives numbers of no meaning in that row only.  Calls of more
+ * rows use the workspace: on one handle they, and replays of captured ones, must
+ * not overlap on the GPU.  The same call gives the same bits.  Returns EINVAL (T
+ * above max_rows among it), ECUDA. */
 strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_stride, void* y, int64_t y_stride,
                                     int32_t dtype, int32_t T, const int32_t* offsets, void* cuda_stream);
 
