@@ -1233,10 +1233,28 @@ class Linear:
 
 class SortPlan:
     """The order of T*k entries: counts [E], offsets [E + 1], entries [T*k] by expert, place [T*k] of each entry (-1: no
-    expert's), CUDA int32 tensors."""
+    expert's), CUDA int32 tensors (views of one, formed when they are asked for)."""
 
-    def __init__(self, counts, offsets, entries, place, T: int):
-        self.counts, self.offsets, self.entries, self.place, self.T = counts, offsets, entries, place, T
+    def __init__(self, mem, n_experts: int, n: int, T: int):
+        self.mem, self.T, self._E, self._n = mem, T, n_experts, n
+        at = mem.data_ptr()
+        self.c = strata_sort_order(at, at + 4 * n_experts, at + 4 * (2 * n_experts + 1), at + 4 * (2 * n_experts + 1 + n))
+
+    @property
+    def counts(self):
+        return self.mem[:self._E]
+
+    @property
+    def offsets(self):
+        return self.mem[self._E:2 * self._E + 1]
+
+    @property
+    def entries(self):
+        return self.mem[2 * self._E + 1:2 * self._E + 1 + self._n]
+
+    @property
+    def place(self):
+        return self.mem[2 * self._E + 1 + self._n:]
 
 
 class ExpertSort:
@@ -1278,14 +1296,11 @@ class ExpertSort:
         T = topk_idx.shape[0]
         p = _words(topk_idx, (T, k), _torch.int32, dev, "topk_idx")
         n = T * k
-        mem = _empty((2 * E + 1 + 2 * n,), _torch.int32, topk_idx.device, stream)
-        counts, offsets, entries, place = mem[:E], mem[E:2 * E + 1], mem[2 * E + 1:2 * E + 1 + n], mem[2 * E + 1 + n:]
-        at = mem.data_ptr()
-        st = self._plan(self.handle, p, T, strata_sort_order(at, at + 4 * E, at + 4 * (2 * E + 1), at + 4 * (2 * E + 1 + n)),
-                        _raw_stream(dev, stream))
+        plan = SortPlan(_empty((2 * E + 1 + 2 * n,), _torch.int32, topk_idx.device, stream), E, n, T)
+        st = self._plan(self.handle, p, T, plan.c, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_plan")
-        return SortPlan(counts, offsets, entries, place, T)
+        return plan
 
     def _weights(self, w, T: int):
         return _words(w, (T, self.top_k), _torch.float32, self.device, "w") if w is not None else None
@@ -1302,7 +1317,7 @@ class ExpertSort:
         else:
             os_ = _rows(out, (T * self.top_k, width), "out")
             _same(out, x, "out")
-        st = self._gather(self.handle, plan.place.data_ptr(), x.data_ptr(), xs, out.data_ptr(), os_, _DTYPE[x.dtype], T,
+        st = self._gather(self.handle, plan.c.place, x.data_ptr(), xs, out.data_ptr(), os_, _DTYPE[x.dtype], T,
                           width, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_gather")
@@ -1323,7 +1338,7 @@ class ExpertSort:
         else:
             os_ = _rows(out, (T, width), "out")
             _same(out, z, "out")
-        st = self._combine(self.handle, plan.place.data_ptr(), z.data_ptr(), zs, self._weights(w, T),
+        st = self._combine(self.handle, plan.c.place, z.data_ptr(), zs, self._weights(w, T),
                            base.data_ptr() if base is not None else None, bs, out.data_ptr(), os_, _DTYPE[z.dtype], T,
                            width, _raw_stream(dev, stream))
         if st != STRATA_OK:
@@ -1345,7 +1360,7 @@ class ExpertSort:
             os_ = _rows(dz, (T * self.top_k, width), "dz")
             _same(dz, z, "dz")
         dw = _empty((T, self.top_k), _torch.float32, z.device, stream)
-        st = self._backward(self.handle, plan.place.data_ptr(), dy.data_ptr(), ds, z.data_ptr(), zs, self._weights(w, T),
+        st = self._backward(self.handle, plan.c.place, dy.data_ptr(), ds, z.data_ptr(), zs, self._weights(w, T),
                             dz.data_ptr(), os_, dw.data_ptr(), _DTYPE[z.dtype], T, width, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_combine_backward")

@@ -12,7 +12,7 @@ using namespace strata;
 struct strata_blocknorm {
   strata_blocknorm_desc desc;
   int device = 0;
-  float* mem = nullptr;  // [3][hidden]: after gain, before gain, channel gate (ones where there is none)
+  float* mem = nullptr;  // [2][hidden]: after gain times channel gate, before gain (ones where there is none)
 };
 
 namespace {
@@ -21,7 +21,7 @@ struct BnArgs {
   const void *x, *y, *gate;
   void *h, *n;
   long long xs, ys, gs, hs, ns;
-  const float* par;  // [3][hidden]
+  const float* par;  // [2][hidden]
   int hidden, after, before, gate_kind, sigmoid;
   float eps, rscale, bscale, inv;
 };
@@ -40,8 +40,11 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int warps) {
 
 // A CTA owns a row: kVec 16-byte pieces of it in each thread's registers from the first load to the last store, so that
 // x, y and an element gate are read once and h and n written once, with two sums over the CTA between.
+// HBM bound in a prompt (8191 bf16 rows of 4096): with the before norm alone 43.5 us (91% of the measured rate); the after norm's
+// gains, twice a row's bytes from L1, and its sum cost the rest.  Two rows to a CTA (57 registers and more) 58.8 us, two or four
+// pieces a thread of smaller CTAs 54.5 and 59.5 us against 55.2 us for one, 40 registers with spills 58.6 us.
 template <typename T, int kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads) blocknorm_kernel(BnArgs A) {
+__global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blocknorm_kernel(BnArgs A) {
   constexpr int E = Val<T>::kPer;
   __shared__ float part[2][32];
   const long long row = blockIdx.x;
@@ -77,7 +80,6 @@ __global__ void __launch_bounds__(kThreads) blocknorm_kernel(BnArgs A) {
   }
   const float* after = A.par;
   const float* before = A.par + A.hidden;
-  const float* channel = A.par + 2 * A.hidden;
   float r = 1.f;
   if (A.after) r = rsqrtf(cta_sum(sum, part[0], warps) * A.inv + A.eps);
   sum = 0.f;
@@ -89,20 +91,14 @@ __global__ void __launch_bounds__(kThreads) blocknorm_kernel(BnArgs A) {
       for (int j = 0; j < E; ++j) h[i][j] = 0.f;
       continue;
     }
-    if (A.after) {
+    if (A.after || A.gate_kind == STRATA_GATE_CHANNEL) {  // (one vector: its reads are L1's, for every row)
 #pragma unroll
       for (int j = 0; j < E; j += 4) {
         const float4 w = reinterpret_cast<const float4*>(after + p * E)[j / 4];
         h[i][j] *= r * w.x, h[i][j + 1] *= r * w.y, h[i][j + 2] *= r * w.z, h[i][j + 3] *= r * w.w;
       }
     }
-    if (A.gate_kind == STRATA_GATE_CHANNEL) {  // (a sigmoid is the handle's already)
-#pragma unroll
-      for (int j = 0; j < E; j += 4) {
-        const float4 w = reinterpret_cast<const float4*>(channel + p * E)[j / 4];
-        h[i][j] *= w.x, h[i][j + 1] *= w.y, h[i][j + 2] *= w.z, h[i][j + 3] *= w.w;
-      }
-    } else if (ge) {
+    if (ge) {
       float f[E];
       Val<T>::unpack(gr[i], f);
 #pragma unroll
@@ -132,9 +128,10 @@ __global__ void __launch_bounds__(kThreads) blocknorm_kernel(BnArgs A) {
   }
 }
 
-__global__ void sigmoid_kernel(float* v, int n) {
+// gain *= gate (through the sigmoid)
+__global__ void fold_kernel(float* gain, const float* gate, int sigmoid, int n) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) v[i] = 1.f / (1.f + expf(-v[i]));
+  if (i < n) gain[i] *= sigmoid ? 1.f / (1.f + expf(-gate[i])) : gate[i];
 }
 
 // One piece a thread where a row has at most 512 of them (a row's loads are all in flight at once either way).
@@ -197,18 +194,18 @@ strata_status strata_blocknorm_create(const strata_blocknorm_desc* d, const floa
   const size_t row = (size_t)d->hidden * 4;
   if (cudaGetDevice(&h->device) != cudaSuccess)
     st = STRATA_ECUDA;
-  else if (cudaMalloc(&h->mem, 3 * row) != cudaSuccess)
+  else if (cudaMalloc(&h->mem, 2 * row) != cudaSuccess)
     st = STRATA_ENOMEM;
   if (st == STRATA_OK) {
     for (int i = 0; i < d->hidden; ++i) ones[i] = 1.f;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const float* from[3] = {after_gain, before_gain, d->gate == STRATA_GATE_CHANNEL ? channel_gate : nullptr};
+    const float* from[2] = {after_gain, before_gain};
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i)
       e = cudaMemcpyAsync(h->mem + (size_t)i * d->hidden, from[i] ? from[i] : ones, row,
                           from[i] ? cudaMemcpyDeviceToDevice : cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess && from[2] && d->sigmoid) {
-      sigmoid_kernel<<<(d->hidden + 255) / 256, 256, 0, s>>>(h->mem + 2 * (size_t)d->hidden, d->hidden);
+    if (e == cudaSuccess && d->gate == STRATA_GATE_CHANNEL) {
+      fold_kernel<<<(d->hidden + 255) / 256, 256, 0, s>>>(h->mem, channel_gate, d->sigmoid, d->hidden);
       e = cudaGetLastError();
     }
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);

@@ -95,10 +95,21 @@ __global__ void __launch_bounds__(128) route_kernel(const float* logits, long lo
 
 // A stable counting sort in one launch of one cluster.  The entries are cut into equal stretches, one for each warp of
 // the cluster in turn, so that an expert's entries of an earlier warp come first: a warp counts its stretch (lanes with
-// the same expert find each other with match, the first of them adds), the CTAs exchange their totals through
+// the same expert find each other by a ballot for each bit of it, the first of them adds), the CTAs exchange their totals through
 // distributed shared memory, and each warp walks its stretch again with running positions.  No atomics: the same order
 // always.  Latency bound (a prompt's 65528 entries are 256 a warp).
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kPlanCluster = 8;
+constexpr int kHeld = 8;  // entries of a lane loaded at once
+
+// The lanes that have this lane's value, of `bits` bits.
+__device__ __forceinline__ unsigned same_lanes(int v, int bits) {
+  unsigned same = kAll;
+  for (int b = 0; b < bits; ++b) {
+    const unsigned set = __ballot_sync(kAll, v >> b & 1);
+    same &= v >> b & 1 ? set : ~set;
+  }
+  return same;
+}
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int* __restrict__ idx, int n, int E, int* counts, int* offsets,
                                                                int* entries, int* place) {
@@ -116,13 +127,27 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int* __rest
   const int begin = (int)(lo < n ? lo : n), end = (int)(lo + stretch < n ? lo + stretch : n);
   int* mine = run + warp * E;
   __syncthreads();
-  for (int base = begin; base < end; base += 32) {
-    const int i = base + lane;
-    const int e = i < end ? idx[i] : -1;
-    const bool ok = e >= 0 && e < E;
-    const unsigned same = __match_any_sync(kAll, ok ? e : -1);
-    if (ok && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  // kHeld loads at a time; of a stretch of at most that many the values stay for the second walk
+  int held[kHeld];
+  unsigned same[kHeld];
+  const int bits = 32 - __clz(E);
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int y = 0; y < kHeld; ++y) {
+      const int i = base + y * 32 + lane;
+      held[y] = i < end ? idx[i] : -1;
+      if (held[y] < 0 || held[y] >= E) held[y] = E;
+    }
+  };
+  for (int base = begin; base < end; base += 32 * kHeld) {
+    fetch(base);
+#pragma unroll
+    for (int y = 0; y < kHeld; ++y) {
+      if (base + y * 32 >= end) break;
+      same[y] = same_lanes(held[y], bits);
+      if (held[y] < E && lane == __ffs(same[y]) - 1) mine[held[y]] += __popc(same[y]);
+      __syncwarp();
+    }
   }
   __syncthreads();
   const int e = threadIdx.x;  // E <= 1024
@@ -167,19 +192,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const int* __rest
   int live = 0;  // entries that are an expert's
   for (int w = 0; w < kPlanWarps; ++w) live += scan[w];
   cl.sync();  // the runs are written, and no CTA leaves while its totals are read
-  for (int base = begin; base < end; base += 32) {
-    const int i = base + lane;
-    const int x = i < end ? idx[i] : -1;
-    const bool ok = x >= 0 && x < E;
-    const unsigned same = __match_any_sync(kAll, ok ? x : -1);
-    int at = -1;
-    if (ok) at = mine[x] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (ok && lane == __ffs(same) - 1) mine[x] += __popc(same);
-    __syncwarp();
-    if (i < end) {
-      place[i] = at;
-      if (ok) entries[at] = i;
+  for (int base = begin; base < end; base += 32 * kHeld) {
+    const bool again = end - begin > 32 * kHeld;
+    if (again) fetch(base);
+#pragma unroll
+    for (int y = 0; y < kHeld; ++y) {
+      if (base + y * 32 >= end) break;
+      const int i = base + y * 32 + lane, x = held[y];
+      const unsigned us = again ? same_lanes(x, bits) : same[y];
+      int at = -1;
+      if (x < E) at = mine[x] + __popc(us & ((1u << lane) - 1));
+      __syncwarp();
+      if (x < E && lane == __ffs(us) - 1) mine[x] += __popc(us);
+      __syncwarp();
+      if (i < end) {
+        place[i] = at;
+        if (x < E) entries[at] = i;
+      }
     }
   }
   for (long long i = (long long)live + rank * kPlanThreads + threadIdx.x; i < n; i += (long long)ctas * kPlanThreads)
@@ -406,15 +435,18 @@ strata_status strata_sort_plan(strata_sort* h, const int32_t* topk_idx, int32_t 
     cudaGetLastError();
     return STRATA_ECUDA;
   }
-  cudaLaunchConfig_t cfg{};
   // one CTA up to 64 entries a warp, where a cluster's exchange costs more than it saves
-  const unsigned ctas = n <= kPlanWarps * 64 ? 1 : kPlanCluster;
-  cfg.gridDim = dim3(ctas), cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = (size_t)(kPlanWarps + 1) * E * 4;
-  cfg.stream = static_cast<cudaStream_t>(cuda_stream);
+  const size_t smem = (size_t)(kPlanWarps + 1) * E * 4;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (n <= kPlanWarps * 64) {
+    plan_kernel<<<1, kPlanThreads, smem, s>>>(topk_idx, (int)n, E, o->counts, o->offsets, o->entries, o->place);
+    return launched();
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kPlanCluster), cfg.blockDim = dim3(kPlanThreads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = kPlanCluster, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, plan_kernel, topk_idx, (int)n, E, o->counts, o->offsets, o->entries, o->place) != cudaSuccess) {
     cudaGetLastError();

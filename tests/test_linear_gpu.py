@@ -50,8 +50,9 @@ def test_one_matrix_any_number_of_rows(B, d, out, dtype, glu):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_many_tiles_and_long_columns(B, dtype):
-    """More tiles than SMs (every CTA takes several), and 12288 columns."""
-    for T, d, out, glu in ((2003, 128, 5136, False), (1500, 256, 2576, True), (40, 12288, 160, False), (6, 12288, 160, False)):
+    """More tiles than SMs (every CTA takes several), and up to 65536 columns (rows of x that do not fit a CTA's registers)."""
+    for T, d, out, glu in ((2003, 128, 5136, False), (1500, 256, 2576, True), (40, 12288, 160, False), (6, 12288, 160, False),
+                           (11, 65536, 16, False), (3, 65536, 16, False), (70, 20544, 48, True)):
         w, up = _qmat(1, out, d, 3), _qmat(1, out, d, 4) if glu else None
         h = B.Linear(w, up=up, max_rows=T)
         x = _rows(T, d, dtype, 5)
