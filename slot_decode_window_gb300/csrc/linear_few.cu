@@ -11,8 +11,8 @@
 // the f16 instruction, f32 as three bf16 parts by truncation (24 bits).
 //
 // Measured: one bf16 row of 2048 -> 4096 6.1 us, eight f32 rows of 4096 -> 2048 8.2 us (latency: launch, one or two rounds of
-// loads a warp, the join); one bf16 row of 2048 -> 151936 56 us (3.5 TB/s, 52% of the measured HBM rate: loads wait for
-// arithmetic, some 75 instructions for 640 bytes), eight f32 rows 85 us.
+// loads a warp, the join); one bf16 row of 2048 -> 151936 52 us (3.8 TB/s, 55% of the measured HBM rate: 61% of the issue slots,
+// some 110 instructions for a tile's 640 bytes), eight f32 rows 76 us.
 #include "linear.cuh"
 
 namespace strata {
@@ -29,16 +29,18 @@ template <> struct FewType<kBF16> {
   static constexpr int kParts = 1;
 };
 
-template <int DT>
+// D = A B + C; C is D, or zeros (kStart).
+template <int DT, bool kStart>
 __device__ __forceinline__ void few_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  const float c[4] = {kStart ? 0.f : d[0], kStart ? 0.f : d[1], kStart ? 0.f : d[2], kStart ? 0.f : d[3]};
   if constexpr (DT == kF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // Pair i of a word of codes as two numbers 16 + q: the code in the top mantissa bits of 16.
@@ -92,18 +94,21 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : DT ==
   int begin, end;
   if (!lin_rows(A, 0, begin, end) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(A.err, kErrIndex);
   if (begin >= end) return;
-  int stride;  // (the tiles of a CTA are of one group of 8; those past the last read it again and write nothing)
+  int stride;  // (the tiles of a CTA are of one group of 8; one past the last reads what is behind it and writes nothing)
   const uint8_t* src[kMats];
 #pragma unroll
-  for (int m = 0; m < kMats; ++m) src[m] = lin_tile(A.w[m].packed, 0, tile0, tiles, nks, stride);
+  for (int m = 0; m < kMats; ++m)
+    src[m] = lin_tile(A.w[m].packed, 0, tile0, tiles, nks, stride) + (long long)warp * stride + lane * 16;
+  const int to_rec = 512 + g * 16 - lane * 16;
+  const long long ahead = (long long)kWarps * stride;
   const bool live = begin + g < end;
   const char* row = static_cast<const char*>(A.x) + (long long)(begin + g) * A.xs * (DT == kF32 ? 4 : 2);
   float acc[kAll][4] = {};
   uint4 code[kAll], rec[kAll];
-  auto load = [&](int ks, int y) {
-    const uint8_t* p = src[y / kTiles] + (long long)ks * stride + min(y % kTiles, tiles - 1 - tile0) * kLinStepBytes;
-    code[y] = __ldg(reinterpret_cast<const uint4*>(p + lane * 16));
-    rec[y] = __ldg(reinterpret_cast<const uint4*>(p + 512 + g * 16));
+  auto load = [&](int y) {  // from the step that src is at
+    const uint8_t* p = src[y / kTiles] + y % kTiles * kLinStepBytes;
+    code[y] = __ldg(reinterpret_cast<const uint4*>(p));
+    rec[y] = __ldg(reinterpret_cast<const uint4*>(p + to_rec));
   };
   uint4 xr[2][DT == kF32 ? 2 : 1];  // this lane's eight columns of the step's two blocks
   auto load_x = [&](int ks) {
@@ -117,38 +122,46 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : DT ==
   if (warp < nks) {
     load_x(warp);
 #pragma unroll
-    for (int y = 0; y < kAll; ++y) load(warp, y);
+    for (int y = 0; y < kAll; ++y) load(y);
   }
   for (int ks = warp; ks < nks; ks += kWarps) {
     const int next = ks + kWarps;
     uint32_t b[2][kParts][4];
-    float xsum[2][4] = {};
+    float xsum[2][4];
     const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
       few_x<DT>(xr[blk], b[blk]);
 #pragma unroll
       for (int k = kParts - 1; k >= 0; --k) {
-        few_mma<DT>(xsum[blk], ones, b[blk][k][0], b[blk][k][1]);
-        few_mma<DT>(xsum[blk], ones, b[blk][k][2], b[blk][k][3]);
+        if (k == kParts - 1)
+          few_mma<DT, true>(xsum[blk], ones, b[blk][k][0], b[blk][k][1]);
+        else
+          few_mma<DT, false>(xsum[blk], ones, b[blk][k][0], b[blk][k][1]);
+        few_mma<DT, false>(xsum[blk], ones, b[blk][k][2], b[blk][k][3]);
       }
     }
     if (next < nks) load_x(next);
 #pragma unroll
+    for (int m = 0; m < kMats; ++m) src[m] += ahead;
+#pragma unroll
     for (int y = 0; y < kAll; ++y) {
       // a tile's next step is on its way from here on
       const uint4 now = code[y], scales = rec[y];
-      if (next < nks) load(next, y);
+      if (next < nks) load(y);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         const uint32_t w0 = blk ? now.z : now.x, w1 = blk ? now.w : now.y;
         const uint32_t a0[4] = {few_pair<DT, 0>(w0), few_pair<DT, 0>(w1), few_pair<DT, 1>(w0), few_pair<DT, 1>(w1)};
         const uint32_t a1[4] = {few_pair<DT, 2>(w0), few_pair<DT, 2>(w1), few_pair<DT, 3>(w0), few_pair<DT, 3>(w1)};
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[4];
 #pragma unroll
         for (int k = kParts - 1; k >= 0; --k) {
-          few_mma<DT>(d, a0, b[blk][k][0], b[blk][k][1]);
-          few_mma<DT>(d, a1, b[blk][k][2], b[blk][k][3]);
+          if (k == kParts - 1)
+            few_mma<DT, true>(d, a0, b[blk][k][0], b[blk][k][1]);
+          else
+            few_mma<DT, false>(d, a0, b[blk][k][0], b[blk][k][1]);
+          few_mma<DT, false>(d, a1, b[blk][k][2], b[blk][k][3]);
         }
         const float s0 = 0x1p-24f * half_of(scales.x, blk), s1 = 0x1p-24f * half_of(scales.y, blk);
         const float o0 = fmaf(-16.f, s0, half_of(scales.z, blk)), o1 = fmaf(-16.f, s1, half_of(scales.w, blk));
@@ -197,7 +210,8 @@ void launch_k(const LinArgs& A, cudaStream_t s) {
 // One tile and 16 warps a CTA while all tiles' CTAs run at once (two an SM), so that a small matrix is spread over the SMs; 4
 // tiles (of a pair, 2 of each) for larger ones, which are bound by memory and by x's parts, with 8 warps and, where an SM
 // gets CTAs enough, 4: the fewer warps share the steps, the less of a CTA's time is its start and its join.  One row of 4096
-// columns: 8192 weight rows 10.5 us with 8 warps, 12.8 us with 4; 2048 columns, 151936 weight rows 60.5 and 55.6 us.
+// columns: 8192 weight rows 10.5 us with 8 warps, 12.8 us with 4; 2048 columns, 151936 weight rows 60.5 and
+// 55.6 us (then).
 template <int DT, bool kGlu>
 void launch_t(const LinArgs& A, int nsm, cudaStream_t s) {
   const int tiles = A.out / kLinTile;

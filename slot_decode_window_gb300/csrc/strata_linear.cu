@@ -76,7 +76,8 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
   const long long packed = linear_packed_bytes(desc->n, desc->in, desc->out);
   const long long rows = ((long long)desc->n * desc->out * 4 + 255) / 256 * 256;
   h->weight_bytes = h->mats * packed;
-  if (cudaMalloc(&h->mem, (size_t)(256 + h->mats * (packed + rows))) != cudaSuccess) {
+  // (2 KB behind: the few-row kernel reads up to three tiles' steps past the last tile)
+  if (cudaMalloc(&h->mem, (size_t)(256 + h->mats * (packed + rows) + 2048)) != cudaSuccess) {
     cudaGetLastError();
     free_linear(h);
     return STRATA_ENOMEM;
