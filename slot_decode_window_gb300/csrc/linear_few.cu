@@ -84,7 +84,7 @@ __device__ __forceinline__ void few_x(const uint4 (&u)[DT == kF32 ? 2 : 1], uint
 // turn, and their sums meet in shared memory in the warps' order.  A step's columns of x are split into parts once for
 // all of its tiles.
 template <int DT, int kTiles, int kWarps, bool kGlu>
-__global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : DT == kF32 || kGlu ? 1 : 2) few_kernel(LinArgs A) {
+__global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) few_kernel(LinArgs A) {
   constexpr int kMats = kGlu ? 2 : 1, kParts = FewType<DT>::kParts, kAll = kMats * kTiles;
   constexpr uint32_t kOnes = DT == kF16 ? 0x3C003C00u : 0x3F803F80u;
   __shared__ float red[kWarps][kAll * 128];
@@ -207,16 +207,17 @@ void launch_k(const LinArgs& A, cudaStream_t s) {
   few_kernel<DT, kTiles, kWarps, kGlu><<<(A.out / kLinTile + kTiles - 1) / kTiles, kWarps * 32, 0, s>>>(A);
 }
 
-// One tile and 16 warps a CTA while all tiles' CTAs run at once (two an SM), so that a small matrix is spread over the SMs; 4
-// tiles (of a pair, 2 of each) for larger ones, which are bound by memory and by x's parts, with 8 warps and, where an SM
-// gets CTAs enough, 4: the fewer warps share the steps, the less of a CTA's time is its start and its join.  One row of 4096
-// columns: 8192 weight rows 10.5 us with 8 warps, 12.8 us with 4; 2048 columns, 151936 weight rows 60.5 and
-// 55.6 us (then).
+// One tile a CTA while all tiles' CTAs run at once (two an SM), so that a small matrix is spread over the SMs: 16 warps for f32 rows,
+// whose parts cost most (eight rows of 4096 -> 2048 in a graph 5.2 us, with 8 warps 5.5 us), else 8 (one bf16 row of 2048 -> 4096
+// 3.5 us, with 16 warps 3.9 us; with gate 5.2 and 6.4 us: two of the larger CTAs do not fit an SM).  4 tiles (of a pair, 2 of each)
+// for larger matrices, which are bound by memory and by x's parts, with 8 warps and, where an SM gets CTAs enough, 4: the fewer warps
+// share the steps, the less of a CTA's time is its start and its join.  One row of 4096 columns: 8192 weight rows 10.5 us with
+// 8 warps, 12.8 us with 4; 2048 columns, 151936 weight rows 60.5 and 55.6 us (51.7 us since).
 template <int DT, bool kGlu>
 void launch_t(const LinArgs& A, int nsm, cudaStream_t s) {
   const int tiles = A.out / kLinTile;
   if (tiles <= 2 * nsm)
-    launch_k<DT, 1, 16, kGlu>(A, s);
+    launch_k<DT, 1, DT == kF32 && !kGlu ? 16 : 8, kGlu>(A, s);
   else if (tiles <= 16 * nsm)
     launch_k<DT, kGlu ? 2 : 4, 8, kGlu>(A, s);
   else
