@@ -728,9 +728,9 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * of order or outside 0..T is left out (rows that two others then both name have
  * no defined output), and the next strata_linear_sync reports EDEVICE.  T = 0 does
  * nothing.
- * Sums are f32.  Up to 8 rows of n = 1 are one launch on the exact weights and the
- * exact rows (24 bits of f32), and a row's bits do not depend on the others.
- * More take f16 products: f16 rows exactly and f32 rows in two parts (22 bits),
+ * Sums are f32.  Up to 8 rows of n = 1 (up to 64 of a small matrix) are one launch
+ * on the exact weights and the exact rows (24 bits of f32), and a row's bits do not
+ * depend on the others of such a call.  More take f16 products: f16 rows exactly and f32 rows in two parts (22 bits),
  * with exact weights; bf16 rows exactly with weights rounded to f16.  Rows are
  * scaled by a power of two of their own and weights by one of their row of W, so
  * values of any size keep this (exact: but for bits below 2^-34 of a row's largest

@@ -62,6 +62,8 @@ __device__ __forceinline__ bool lin_rows(const LinArgs& A, int i, int& begin, in
 long long linear_packed_bytes(int n, int in, int out);
 cudaError_t launch_linear_pack(const void* codes, const uint16_t* scale, const uint16_t* mn, int n, int in, int out,
                                uint8_t* packed, float* undo, cudaStream_t s);
+// Whether a call is the few-row path's.
+bool linear_few_rows(const LinArgs& A, int nsm);
 cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s);
 
 // The many-row path: its workspace's bytes; its shared memory limit and how many clusters of 2, 4 and 8 CTAs run at once

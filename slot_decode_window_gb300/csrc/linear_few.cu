@@ -1,4 +1,4 @@
-// Products of few rows with 4-bit matrices.
+// Products of few rows with 4-bit matrices (8 to a CTA).
 //
 // y = W x with W = s q + m per block of 32 columns.  A tile of 16 weight rows is
 // the A operand of mma.sync.m16n8k16, up to 8 rows of x the B operand; the order
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) fe
   const int tiles = A.out / kLinTile, nks = A.in / kLinStep;
   const int tile0 = blockIdx.x * kTiles;
   int begin, end;
-  if (!lin_rows(A, 0, begin, end) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(A.err, kErrIndex);
+  if (!lin_rows(A, 0, begin, end) && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(A.err, kErrIndex);
+  begin += blockIdx.y * kLinFewRows;  // 8 rows to a CTA
   if (begin >= end) return;
   int stride;  // (the tiles of a CTA are of one group of 8; one past the last reads what is behind it and writes nothing)
   const uint8_t* src[kMats];
@@ -204,7 +205,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) fe
 
 template <int DT, int kTiles, int kWarps, bool kGlu>
 void launch_k(const LinArgs& A, cudaStream_t s) {
-  few_kernel<DT, kTiles, kWarps, kGlu><<<(A.out / kLinTile + kTiles - 1) / kTiles, kWarps * 32, 0, s>>>(A);
+  const dim3 grid((A.out / kLinTile + kTiles - 1) / kTiles, (A.T + kLinFewRows - 1) / kLinFewRows);
+  few_kernel<DT, kTiles, kWarps, kGlu><<<grid, kWarps * 32, 0, s>>>(A);
 }
 
 // One tile a CTA while all tiles' CTAs run at once (two an SM), so that a small matrix is spread over the SMs: 16 warps for f32 rows,
@@ -225,6 +227,16 @@ void launch_t(const LinArgs& A, int nsm, cudaStream_t s) {
 }
 
 }  // namespace
+
+// At most 8 rows; and more, 8 to a CTA, where the steps of all tiles and groups of 8 rows are few: then one launch without a
+// workspace is faster than two with (in a graph: 16 bf16 rows of 4096 -> 4096 9.1 us against 12.5 us, 24 rows 12.4 and 12.6 us, 32 rows
+// 14.5 and 12.7 us; f32 rows of 4096 -> 2048 16: 9.9 and 14.1 us, 24: 14.2 and 14.1 us; 64 bf16 rows of 2048 -> 512 4.1 and 10.3 us).
+bool linear_few_rows(const LinArgs& A, int nsm) {
+  if (A.n != 1) return false;
+  if (A.T <= kLinFewRows) return true;
+  const long long tiles = A.out / kLinTile, groups = (A.T + kLinFewRows - 1) / kLinFewRows;
+  return A.T <= 64 && tiles <= 2 * nsm && (A.glu ? 2 : 1) * tiles * groups * (A.in / kLinStep) <= (A.dtype == kF32 ? 130LL : 320LL) * nsm;
+}
 
 cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s) {
   if (A.dtype == kF32)

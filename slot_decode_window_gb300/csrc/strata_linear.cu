@@ -134,7 +134,7 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
   A.n = d.n, A.in = d.in, A.out = d.out, A.glu = h->mats == 2;
   A.x = x, A.y = y, A.xs = x_stride, A.ys = y_stride, A.dtype = dtype, A.T = T, A.offsets = offsets, A.err = h->err;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  const bool few = d.n == 1 && T <= kLinFewRows;
+  const bool few = linear_few_rows(A, h->nsm);
   if ((few ? launch_linear_few(A, h->nsm, s) : launch_linear_many(A, h->ws, d.max_rows, h->nsm, h->clusters, s)) != cudaSuccess) {
     cudaGetLastError();
     return STRATA_ECUDA;

@@ -3,7 +3,7 @@
 u(t) = finfo(t).eps / 2 is half a step relative to the value; a matrix unit's f32 add may truncate: 2^-23 of the larger operand.
 
 Products.  For a row and a weight row with weights W = s q + m, block by block:
-* few rows (at most 8 of one matrix, no other part): weights and x exact.  A block's products are of (16 + q) x and 16 s - m
+* few rows (at most 8 of one matrix; of a small one, up to 64: few = None takes either path's bound): weights and x exact.  A block's products are of (16 + q) x and 16 s - m
   times its sum: B = sum over blocks of (31 |s| + |m - 16 s|) sum |x| bounds every partial sum's terms.  A term passes at most 6
   adds in its block, one per step of a warp, 16 of the join and 4 scalings: (nks + 32) 2^-23 B.
 * bf16 rows: weights are one f16 of the row's scale: 2^-11 |W|, or half of f16's least step, 2^-25, where a weight is below
@@ -59,6 +59,9 @@ def product_bound(x, q, i, few):
 
 def linear_bound(x, w, up, i=0, few=False):
     """(y, bound) of the call's rows with matrix i."""
+    if few is None:
+        y, a = linear_bound(x, w, up, i, False)
+        return y, torch.maximum(a, linear_bound(x, w, up, i, True)[1])
     g, eg = product_bound(x, w, i, few)
     if up is not None:
         v, ev = product_bound(x, up, i, few)

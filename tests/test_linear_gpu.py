@@ -41,7 +41,7 @@ def test_one_matrix_any_number_of_rows(B, d, out, dtype, glu):
         whole = torch.full((T + 2, out + 16), 7.0, dtype=x.dtype, device="cuda")
         y = whole[1:T + 1, :out]
         assert h.forward(x, y=y) is y
-        want, bound = linear_bound(x, w, up, few=T <= 8)
+        want, bound = linear_bound(x, w, up, few=True if T <= 8 else None)
         check_rows(y, want, bound)
         assert (whole[0] == 7).all() and (whole[-1] == 7).all() and (whole[:, out:] == 7).all()
     h.sync()
@@ -58,7 +58,7 @@ def test_many_tiles_and_long_columns(B, dtype):
         x = _rows(T, d, dtype, 5)
         y = h.forward(x)
         h.sync()
-        check_rows(y, *linear_bound(x, w, up, few=T <= 8))
+        check_rows(y, *linear_bound(x, w, up, few=True if T <= 8 else None))
         h.close()
 
 
@@ -154,7 +154,7 @@ def test_rows_and_weights_of_any_size(B, dtype, T):
     x = (x.float() * scale).to(x.dtype)
     h = B.Linear(w, max_rows=100)
     y = h.forward(x)
-    check_rows(y, *linear_bound(x, w, None, few=T <= 8))
+    check_rows(y, *linear_bound(x, w, None, few=True if T <= 8 else None))
     assert (y[3] == 0).all()
     h.close()
 
