@@ -1162,7 +1162,7 @@ class Linear:
     [n][rows][cols / 32], on one CUDA device), as ``workloads.QMat``; with ``up`` (the same shape) silu(W x) * (U x).
     The handle keeps its own copy.  max_rows: most rows of a call.
 
-    Calls of more than 8 rows, or with offsets, use the handle's workspace: they, and replays of captured ones, must not
+    Calls of more than 8 rows, or with offsets, may use the handle's workspace: they, and replays of captured ones, must not
     run at the same time.  On one stream they do not; across streams, order them with events.
     """
 

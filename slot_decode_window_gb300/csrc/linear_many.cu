@@ -32,9 +32,9 @@
 // results to those that add them up (each a share of the rows of x, in the cluster's
 // order) through distributed shared memory.
 // Measured: 8191 bf16 rows of 2048 -> 5120 125 to 131 us, of which 14 us prepare the rows (the products alone 1.5 PFLOP/s, 78%
-// of the measured cuBLAS rate; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 111 us (three products: 1.0 PFLOP/s with
+// of the measured cuBLAS rate; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 108 us (three products: 1.0 PFLOP/s with
 // the preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 205 us, 46 us of it the rows
-// (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 16 bf16 rows of 4096 -> 4096 15 us.  Tiles of fewer than some 170 rows of x are
+// (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 64 bf16 rows of 4096 -> 4096 17 us.  Tiles of fewer than some 170 rows of x are
 // bound by the roles' instructions and hand-overs, some 650 clocks a step.
 #include "linear.cuh"
 #include "tcgen05.cuh"
@@ -272,6 +272,23 @@ __device__ __forceinline__ void tc_mma_ts_if(uint32_t lead, uint32_t d, uint32_t
       "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
+}
+// Two products, 16 columns on, and a look at a barrier: whether its phase is complete.  The look is issued first and its answer
+// read last, so that the products do not wait for it.
+__device__ __forceinline__ uint32_t tc_mma_pair_look(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                                     uint64_t* bar, uint32_t parity) {
+  uint32_t seen;
+  asm volatile(
+      "{\n.reg .pred p, q, t, s;\n.reg .b32 a1;\n.reg .b64 b1;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%7], %8;\n"
+      "setp.ne.u32 p, %5, 0;\nsetp.ne.u32 q, %6, 0;\nsetp.eq.u32 t, 0, 0;\nadd.u32 a1, %2, 8;\nadd.u64 b1, %3, 2;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [a1], b1, %4, t;\n"
+      "selp.u32 %0, 1, 0, s;\n}"
+      : "=r"(seen)
+      : "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead), "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return seen;
 }
 __device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
   asm volatile(
@@ -831,7 +848,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
       const uint32_t lead = elect_one();
       const int half = warp - kMmaWarp;
       int st = 0, xst = 0, set = 0;
-      uint32_t a_ph = 0, d_ph = 1;
+      uint32_t a_ph = 0, d_ph = 1, seen = 0;  // seen: the next stage of weights is there
       bool ok = true;
       for (int item = item0; item < total && ok; item += items) {
         const Tile t = tile_at<P::kCols>(L, pre, m_tiles, item);
@@ -846,26 +863,32 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           constexpr int kParts = P::kUnits / 2;  // stages of weights to a step
           const bool two = P::kSums && i < mine;
 #pragma unroll
-          for (int u = 0; u < kParts && ok; ++u) {
+          for (int u = 0; u < kParts; ++u) {
             const int at = st * kParts + u;
-            if (!(ok = wait_warp(&a_full[at], a_ph, dead, err))) break;
+            if (!__all_sync(0xFFFFFFFFu, seen) && !(ok = wait_warp(&a_full[at], a_ph, dead, err))) break;
             tc_fence_after();
             const uint32_t a = P::kA + at * 64 + half * 32;
-            if (live) {
-              if constexpr (P::kSums) {
-                // the small parts first: an add truncates by the accumulator's size
+            // The next stage's barrier is looked at beside the last products: the tensor cores queue some four of them, less time
+            // than a wait takes (f32 rows of 4096 -> 2048 112 -> 108 us, bf16 and f16 rows as before).
+            uint64_t* next = &a_full[u + 1 < kParts ? at + 1 : (st ^ 1) * kParts];
+            const uint32_t next_ph = u + 1 < kParts || st == 0 ? a_ph : a_ph ^ 1;
+            if (!live) {
+              seen = 0;
+            } else if constexpr (P::kSums) {
+              // the small parts first: an add truncates by the accumulator's size
+              if (two) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const uint64_t by = b + (u * 2 + y) * 2;
-                  if (two) tc_mma_ts_if(lead, d, a + 16 + y * 8, by, id, !first || u > 0 || y > 0);
-                  if (two && P::kXParts == 2) tc_mma_ts_if(lead, d, a + y * 8, by + (P::kPart >> 4), id, 1);
+                  tc_mma_ts_if(lead, d, a + 16 + y * 8, by, id, !first || u > 0 || y > 0);
+                  if constexpr (P::kXParts == 2) tc_mma_ts_if(lead, d, a + y * 8, by + (P::kPart >> 4), id, 1);
                 }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + (u * 2 + y) * 2, id, two || !first || u > 0 || y > 0);
-              } else {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) tc_mma_ts_if(lead, d, a + y * 8, b + y * 2, id, !first || y > 0);
               }
+              seen = tc_mma_pair_look(lead, d, a, b + u * 4, id, two || !first || u > 0, next, next_ph);
+            } else {
+              tc_mma_ts_if(lead, d, a, b, id, !first);
+              tc_mma_ts_if(lead, d, a + 8, b + 2, id, 1);
+              seen = tc_mma_pair_look(lead, d, a + 16, b + 4, id, 1, next, next_ph);
             }
             tc_commit_if(lead, &a_empty[at]);
           }
