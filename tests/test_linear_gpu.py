@@ -77,6 +77,23 @@ def test_few_rows_of_large_matrices(B, dtype, glu):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("d,out", [(512, 4880), (5184, 4864), (4096, 4096), (16384, 1024)])
+def test_nine_to_sixty_four_rows_of_matrices_of_middling_size(B, d, out, dtype, glu):
+    """Both sides of the rule that gives small matrices' rows to the few-row kernel; narrow tiles of x whose columns a cluster
+    shares."""
+    w, up = _qmat(1, out, d, 26), _qmat(1, out, d, 27) if glu else None
+    h = B.Linear(w, up=up, max_rows=64)
+    for T in (9, 16, 17, 24, 33, 40, 57, 64):
+        x = _rows(T, d, dtype, T)
+        y = h.forward(x)
+        check_rows(y, *linear_bound(x, w, up, few=None))
+        assert torch.equal(y, h.forward(x))
+    h.sync()
+    h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("glu", [False, True])
 def test_rows_sorted_by_matrix(B, dtype, glu):
     """Matrices with no rows, one row and many; rows before the first and behind the last stay as they were."""
     w, up = _qmat(6, 208, 320, 8), _qmat(6, 208, 320, 9) if glu else None
