@@ -1235,8 +1235,9 @@ class SortPlan:
     """The order of T*k entries: counts [E], offsets [E + 1], entries [T*k] by expert, place [T*k] of each entry (-1: no
     expert's), CUDA int32 tensors (views of one, formed when they are asked for)."""
 
-    def __init__(self, mem, n_experts: int, n: int, T: int):
-        self.mem, self.T, self._E, self._n = mem, T, n_experts, n
+    def __init__(self, mem, n_experts: int, top_k: int, T: int):
+        n = T * top_k
+        self.mem, self.T, self.top_k, self._E, self._n = mem, T, top_k, n_experts, n
         at = mem.data_ptr()
         self.c = strata_sort_order(at, at + 4 * n_experts, at + 4 * (2 * n_experts + 1), at + 4 * (2 * n_experts + 1 + n))
 
@@ -1295,12 +1296,16 @@ class ExpertSort:
         E, k, dev = self.n_experts, self.top_k, self.device
         T = topk_idx.shape[0]
         p = _words(topk_idx, (T, k), _torch.int32, dev, "topk_idx")
-        n = T * k
-        plan = SortPlan(_empty((2 * E + 1 + 2 * n,), _torch.int32, topk_idx.device, stream), E, n, T)
+        plan = SortPlan(_empty((2 * E + 1 + 2 * T * k,), _torch.int32, topk_idx.device, stream), E, k, T)
         st = self._plan(self.handle, p, T, plan.c, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_plan")
         return plan
+
+    def _place(self, plan: SortPlan) -> int:
+        if plan.top_k != self.top_k or plan.mem.get_device() != self.device:
+            raise StrataError(STRATA_EINVAL, "plan: want one of a sort with as many choices, on the handle's device")
+        return plan.c.place
 
     def _weights(self, w, T: int):
         return _words(w, (T, self.top_k), _torch.float32, self.device, "w") if w is not None else None
@@ -1317,7 +1322,7 @@ class ExpertSort:
         else:
             os_ = _rows(out, (T * self.top_k, width), "out")
             _same(out, x, "out")
-        st = self._gather(self.handle, plan.c.place, x.data_ptr(), xs, out.data_ptr(), os_, _DTYPE[x.dtype], T,
+        st = self._gather(self.handle, self._place(plan), x.data_ptr(), xs, out.data_ptr(), os_, _DTYPE[x.dtype], T,
                           width, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_gather")
@@ -1338,7 +1343,7 @@ class ExpertSort:
         else:
             os_ = _rows(out, (T, width), "out")
             _same(out, z, "out")
-        st = self._combine(self.handle, plan.c.place, z.data_ptr(), zs, self._weights(w, T),
+        st = self._combine(self.handle, self._place(plan), z.data_ptr(), zs, self._weights(w, T),
                            base.data_ptr() if base is not None else None, bs, out.data_ptr(), os_, _DTYPE[z.dtype], T,
                            width, _raw_stream(dev, stream))
         if st != STRATA_OK:
@@ -1360,7 +1365,7 @@ class ExpertSort:
             os_ = _rows(dz, (T * self.top_k, width), "dz")
             _same(dz, z, "dz")
         dw = _empty((T, self.top_k), _torch.float32, z.device, stream)
-        st = self._backward(self.handle, plan.c.place, dy.data_ptr(), ds, z.data_ptr(), zs, self._weights(w, T),
+        st = self._backward(self.handle, self._place(plan), dy.data_ptr(), ds, z.data_ptr(), zs, self._weights(w, T),
                             dz.data_ptr(), os_, dw.data_ptr(), _DTYPE[z.dtype], T, width, _raw_stream(dev, stream))
         if st != STRATA_OK:
             check(st, "strata_sort_combine_backward")

@@ -236,3 +236,17 @@ def test_refusals(B):
     assert B.strata_sort_plan(h.handle, idx.data_ptr(), 1 << 28, B.strata_sort_order(pl, pl, pl, q)) == B.STRATA_EUNSUPPORTED
     assert h.route(l[:0])[0].shape == (0, 2)
     h.close()
+
+
+def test_a_plan_of_another_number_of_choices_is_refused(B):
+    """Its places are fewer (or more) than the call would read."""
+    h, other = B.ExpertSort(8, 4), B.ExpertSort(8, 2)
+    plan = other.plan(other.route(torch.randn(4, 8, device="cuda"))[0])
+    x, z = torch.randn(4, 16, device="cuda"), torch.randn(16, 16, device="cuda")
+    for call in (lambda: h.gather(plan, x), lambda: h.combine(plan, z), lambda: h.combine_backward(plan, x, z)):
+        with pytest.raises(B.StrataError) as e:
+            call()
+        assert e.value.status == B.STRATA_EINVAL
+    again = B.ExpertSort(16, 2)  # the experts of a plan are in its places alone
+    assert torch.equal(again.gather(plan, x), other.gather(plan, x))
+    h.close(), other.close(), again.close()
