@@ -38,18 +38,18 @@ __device__ __forceinline__ float cta_sum(float v, float* part, int warps) {
   return s;
 }
 
-// A CTA owns a row: kVec 16-byte pieces of it in each thread's registers from the first load to the last store, so that
+// A CTA of at most kMax threads owns a row: kVec 16-byte pieces of it in each thread's registers from the first load to the last store, so that
 // x, y and an element gate are read once and h and n written once, with two sums over the CTA between.
 // HBM bound in a prompt: 8191 bf16 rows of 4096 with the before norm alone 44 us (90% of the measured rate), with the after norm and a
 // channel gate 51 us: the gains, twice a row's bytes, come from L1, and there is a second sum.  The bounds ask for 2048 threads an SM
 // (32 registers; at 40, three CTAs of 512, 57.5 us).  Two rows to a CTA 58.8 us, two or four pieces a thread of smaller CTAs no
-// better.
-template <typename T, int kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blocknorm_kernel(BnArgs A) {
+// better; CTAs that keep the gains in registers and take rows in turn from copies in shared memory 58 us (half the warps).
+template <typename T, int kVec, int kMax>
+__global__ void __launch_bounds__(kMax, kVec == 1 ? 2048 / kMax : 1) blocknorm_kernel(BnArgs A) {
   constexpr int E = Val<T>::kPer;
   __shared__ float part[2][32];
   const long long row = blockIdx.x;
-  const int pieces = A.hidden / E, warps = kThreads / 32;
+  const int pieces = A.hidden / E, threads = blockDim.x, warps = threads / 32;
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(A.x) + row * A.xs);
   const uint4* y = A.y ? reinterpret_cast<const uint4*>(static_cast<const T*>(A.y) + row * A.ys) : nullptr;
   const uint4* ge = A.gate_kind == STRATA_GATE_ELEMENT
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blo
   uint4 xr[kVec], yr[kVec], gr[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int p = i * kThreads + threadIdx.x;
+    const int p = i * threads + threadIdx.x;
     xr[i] = yr[i] = gr[i] = make_uint4(0, 0, 0, 0);
     if (p < pieces) {
       xr[i] = x[p];
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blo
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int p = i * kThreads + threadIdx.x;
+    const int p = i * threads + threadIdx.x;
     if (p >= pieces) {  // (its registers are zeros)
 #pragma unroll
       for (int j = 0; j < E; ++j) h[i][j] = 0.f;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 1 ? 2048 / kThreads : 1) blo
   r = rsqrtf(cta_sum(sum, part[1], warps) * A.inv + A.eps);
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int p = i * kThreads + threadIdx.x;
+    const int p = i * threads + threadIdx.x;
     if (p >= pieces) break;
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
@@ -135,22 +135,27 @@ __global__ void fold_kernel(float* gain, const float* gate, int sigmoid, int n) 
   if (i < n) gain[i] *= sigmoid ? 1.f / (1.f + expf(-gate[i])) : gate[i];
 }
 
-// One piece a thread where a row has at most 512 of them (a row's loads are all in flight at once either way).
+template <typename T, int kVec, int kMax>
+void launch_vec(const BnArgs& A, unsigned rows, cudaStream_t s) {
+  const int pieces = A.hidden / Val<T>::kPer, threads = (pieces + kVec - 1) / kVec;
+  blocknorm_kernel<T, kVec, kMax><<<rows, (threads + 31) / 32 * 32, 0, s>>>(A);
+}
+
+// One piece a thread where a row has at most 512 of them (a row's loads are all in flight at once either way), and no more warps
+// than the pieces fill: their places are other rows' (8191 bf16 rows of 2304 28.3 us, with 512 threads to a row 38.2 us; of 5120
+// 62.5 and 82 us; 16384 rows of 512 12.3 us, with 128 threads 16.3 us).  Larger rows take two or four pieces: one piece of up to 1024
+// threads is no better (rows of 8192 103 us against 100 us).
 template <typename T>
 void launch_t(const BnArgs& A, unsigned rows, cudaStream_t s) {
   const int pieces = A.hidden / Val<T>::kPer;
-  if (pieces <= 128)
-    blocknorm_kernel<T, 1, 128><<<rows, 128, 0, s>>>(A);
-  else if (pieces <= 256)
-    blocknorm_kernel<T, 1, 256><<<rows, 256, 0, s>>>(A);
-  else if (pieces <= 512)
-    blocknorm_kernel<T, 1, 512><<<rows, 512, 0, s>>>(A);
+  if (pieces <= 512)
+    launch_vec<T, 1, 512>(A, rows, s);
   else if (pieces <= 1024)
-    blocknorm_kernel<T, 2, 512><<<rows, 512, 0, s>>>(A);
+    launch_vec<T, 2, 512>(A, rows, s);
   else if (pieces <= 2048)
-    blocknorm_kernel<T, 4, 512><<<rows, 512, 0, s>>>(A);
+    launch_vec<T, 4, 512>(A, rows, s);
   else
-    blocknorm_kernel<T, 4, 1024><<<rows, 1024, 0, s>>>(A);
+    launch_vec<T, 4, 1024>(A, rows, s);
 }
 
 void free_blocknorm(strata_blocknorm* h) {
