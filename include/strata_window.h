@@ -734,7 +734,8 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * with exact weights; bf16 rows exactly with weights rounded to f16.  Rows are
  * scaled by a power of two of their own and weights by one of their row of W, so
  * values of any size keep this (exact: but for bits below 2^-34 of a row's largest
- * value, and scales below 2^-24 of the largest of their row of W).  A row with
+ * value, and scales below 2^-24 of the largest of their row of W; up to 8 rows are
+ * not scaled: their values from 2^-100 to 2^100).  A row with
  * infinities or NaN gives numbers of no meaning in that row only.  Calls of more
  * rows use the workspace: on one handle they, and replays of captured ones, must
  * not overlap on the GPU.  The same call gives the same bits.  Returns EINVAL (T

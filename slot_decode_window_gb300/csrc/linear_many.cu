@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           }
           const float* u = &ux[0].x;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[h][j] *= undo[h] * u[j];
+          for (int j = 0; j < 8; ++j) v[h][j] = v[h][j] * undo[h] * u[j];  // (undo u may not be finite)
         }
         if constexpr (GLU) {
 #pragma unroll

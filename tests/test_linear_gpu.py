@@ -176,6 +176,23 @@ def test_rows_and_weights_of_any_size(B, dtype, T):
     h.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_largest_rows_with_weights_of_the_largest_scale(B, dtype):
+    """A row's and a weight row's powers of two together pass f32's range, their product with a result does not: x of 2^126 meets
+    weights of zeros, beside a block of scale 2^15 that meets zeros."""
+    d, out, T = 128, 32, 70
+    w = _qmat(1, out, d, 28)
+    s, m = w.scale.view(torch.float16), w.min.view(torch.float16)
+    s[0, :, 1], m[0, :, 1] = 2.0 ** 15, 0
+    s[0, :, 0], m[0, :, 0] = 0, 0
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x[:, :32] = 2.0 ** 126
+    h = B.Linear(w, max_rows=T)
+    assert (h.forward(x) == 0).all()
+    h.sync()
+    h.close()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T", [8, 70])
 def test_a_row_without_meaning_stays_alone(B, dtype, T):
