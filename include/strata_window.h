@@ -730,8 +730,8 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * nothing.
  * Sums are f32.  Up to 8 rows of n = 1 (up to 64 of a small matrix) are one launch
  * on the exact weights and the exact rows (24 bits of f32), and a row's bits do not
- * depend on the others of such a call.  More take f16 products: f16 rows exactly and f32 rows in two parts (22 bits),
- * with exact weights; bf16 rows exactly with weights rounded to f16.  Rows are
+ * depend on the others of such a call.  More take f16 products, on the exact weights
+ * (strata_linear_round_weights apart): 16-bit rows exactly, f32 rows in two parts (22 bits).  Rows are
  * scaled by a power of two of their own and weights by one of their row of W, so
  * values of any size keep this (exact: but for bits below 2^-34 of a row's largest
  * value, and scales below 2^-24 of the largest of their row of W; up to 8 rows are
@@ -742,6 +742,12 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * above max_rows among it), ECUDA. */
 strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_stride, void* y, int64_t y_stride,
                                     int32_t dtype, int32_t T, const int32_t* offsets, void* cuda_stream);
+
+/* on = 1: later calls that take f16 products (above) round the weights to f16 for
+ * bf16 rows, one product in place of two: 2^-11 of a weight (2^-14 of its row's
+ * largest scale where that is more), in about 0.55 of the time of a prompt.  0, as
+ * create leaves it: exact weights.  Captured calls keep what they were captured with. */
+strata_status strata_linear_round_weights(strata_linear* h, int32_t on);
 
 /* Wait for the handle's device; report (and clear) any error the GPU recorded:
  * EDEVICE in that case.  Not during a capture. */

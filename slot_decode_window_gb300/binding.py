@@ -30,8 +30,8 @@ EXPORTED = ("strata_window_create", "strata_moe_window_forward", "strata_window_
             "strata_window_slots", "strata_stack_set_kv", "strata_stack_forward_kv", "strata_qknorm_create",
             "strata_qknorm_forward", "strata_qknorm_destroy", "strata_kv8_create", "strata_kv8_append",
             "strata_kv8_read", "strata_kv8_attend", "strata_kv8_sync", "strata_kv8_query", "strata_kv8_destroy",
-            "strata_linear_create", "strata_linear_forward", "strata_linear_sync", "strata_linear_query",
-            "strata_linear_destroy", "strata_sort_create", "strata_sort_route", "strata_sort_plan",
+            "strata_linear_create", "strata_linear_forward", "strata_linear_round_weights", "strata_linear_sync",
+            "strata_linear_query", "strata_linear_destroy", "strata_sort_create", "strata_sort_route", "strata_sort_plan",
             "strata_sort_gather", "strata_sort_combine", "strata_sort_combine_backward", "strata_sort_destroy",
             "strata_blocknorm_create", "strata_blocknorm_forward", "strata_blocknorm_destroy")
 STRATA_F32, STRATA_F16, STRATA_BF16 = range(3)
@@ -261,6 +261,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.strata_kv8_destroy.restype = ctypes.c_int
     lib.strata_linear_create.argtypes = [P(strata_linear_desc), P(strata_qmat), P(strata_qmat), vp, P(vp)]
     lib.strata_linear_forward.argtypes = [vp, vp, i64, vp, i64, i32, i32, vp, vp]
+    lib.strata_linear_round_weights.argtypes = [vp, i32]
     lib.strata_linear_sync.argtypes = [vp]
     lib.strata_linear_query.argtypes = [vp, P(i64), P(i64)]
     lib.strata_linear_destroy.argtypes = [vp]
@@ -274,7 +275,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.strata_blocknorm_create.argtypes = [P(strata_blocknorm_desc), vp, vp, vp, vp, P(vp)]
     lib.strata_blocknorm_forward.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp]
     lib.strata_blocknorm_destroy.argtypes = [vp]
-    for name in ("linear_create", "linear_forward", "linear_sync", "linear_query", "linear_destroy", "sort_create",
+    for name in ("linear_create", "linear_forward", "linear_round_weights", "linear_sync", "linear_query", "linear_destroy", "sort_create",
                  "sort_route", "sort_plan", "sort_gather", "sort_combine", "sort_combine_backward", "sort_destroy",
                  "blocknorm_create", "blocknorm_forward", "blocknorm_destroy"):
         getattr(lib, "strata_" + name).restype = ctypes.c_int
@@ -542,6 +543,10 @@ def strata_linear_create(desc: strata_linear_desc, weight: strata_qmat, up: Opti
 def strata_linear_forward(handle, x_ptr, x_stride: int, y_ptr, y_stride: int, dtype: int, T: int, offsets_ptr=None,
                           stream: int = 0) -> int:
     return load().strata_linear_forward(handle, x_ptr, x_stride, y_ptr, y_stride, dtype, T, offsets_ptr, stream)
+
+
+def strata_linear_round_weights(handle, on: int) -> int:
+    return load().strata_linear_round_weights(handle, on)
 
 
 def strata_linear_sync(handle) -> int:
@@ -1160,13 +1165,14 @@ def _words(t, shape, dtype, device: int, what: str):
 class Linear:
     """Products with a stack of 4-bit matrices (block format: codes uint8 [n][rows][cols / 2], scale and min 16-bit
     [n][rows][cols / 32], on one CUDA device), as ``workloads.QMat``; with ``up`` (the same shape) silu(W x) * (U x).
-    The handle keeps its own copy.  max_rows: most rows of a call.
+    The handle keeps its own copy.  max_rows: most rows of a call.  rounded: calls of many bf16 rows take weights rounded to
+    f16, faster (exact weights otherwise).
 
     Calls of more than 8 rows, or with offsets, may use the handle's workspace: they, and replays of captured ones, must not
     run at the same time.  On one stream they do not; across streams, order them with events.
     """
 
-    def __init__(self, weight, up=None, max_rows: int = 8, stream=None):
+    def __init__(self, weight, up=None, max_rows: int = 8, stream=None, rounded: bool = False):
         torch = _with_torch()
         n, rows, cols = weight.codes.shape[0], weight.rows, weight.cols
         device = weight.codes.get_device()
@@ -1188,6 +1194,7 @@ class Linear:
                                          _qmat(weight), _qmat(up) if up is not None else None, s)
         check(st, "strata_linear_create")
         self.handle = h
+        check(strata_linear_round_weights(h, int(rounded)), "strata_linear_round_weights")
         self._forward = load().strata_linear_forward
 
     def forward(self, x, y=None, offsets=None, stream=None):

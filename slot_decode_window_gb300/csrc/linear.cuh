@@ -34,6 +34,7 @@ struct LinMat {
 struct LinArgs {
   LinMat w[2];        // the stack, and the one behind the gate (glu)
   int n, in, out, glu;
+  int rounded;        // many bf16 rows take weights rounded to f16
   const void* x;
   void* y;
   long long xs, ys;

@@ -1,8 +1,8 @@
 // Products of many rows with 4-bit matrices on the 5th-generation tensor cores.
 //
 // D = W X^T for 256 weight rows (two halves of 128: the second half, or the
-// stack behind the gate) and up to 192 rows of x (64 of f32 rows): weights are the
-// A operand, in tensor memory, where the conversion warps write them as f16 from
+// stack behind the gate) and up to 128 rows of x (64 of f32 rows, 192 with rounded
+// weights): weights are the A operand, in tensor memory, where the conversion warps write them as f16 from
 // the 4-bit codes, 64 columns at a time; x is the B operand, f16 in the order of
 // the codes, swizzled, brought by bulk copies from the workspace that
 // linear_rows_kernel fills.  Weight rows on the M side leave the rows of x free
@@ -13,13 +13,15 @@
 //   W x = s (q - 8) x + (8 s + m) sum x   over a block of 32 columns:
 // s (q - 8) has 15 bits, two f16 parts (hi and what is left, both exact); after the
 // last columns come steps whose "weights" are m and 8 s of 16 blocks each and
-// whose "x" are the blocks' sums, in two f16 parts.  f16 rows: hi x + lo x.  f32 rows: x
+// whose "x" are the blocks' sums, in two f16 parts.  16-bit rows: hi x + lo x.  f32 rows: x
 // in two f16 parts (22 bits), lo hi + hi lo + hi hi; the accumulators' adds
 // truncate, so every two steps they are added to f32 registers, with two sets of
 // accumulators in turn.
+// Rounded weights (bf16 rows, where the caller asks for them): one product, W
+// rounded to f16, 2^-11 of a weight.
 //
-// Roles (28 warps): 16 of conversion, in two groups that take the steps in turn
-// (exact weights: one block of 32 columns each of every step), with stages of
+// Roles (28 warps): 16 of conversion, in two groups that take a block of 32 columns
+// each of every step (rounded weights: the steps in turn), with stages of
 // weights of their own (a warp has two tiles of 16 weight rows, a quarter of the
 // lanes of one half); 8 of results (each a quarter of the lanes
 // and half of the rows of x); one of copies, codes and x of a step into one stage;
@@ -31,10 +33,10 @@
 // 8 CTAs takes a tile, each a part of its columns; a CTA sends its part of the
 // results to those that add them up (each a share of the rows of x, in the cluster's
 // order) through distributed shared memory.
-// Measured: 8191 bf16 rows of 2048 -> 5120 125 to 131 us, of which 14 us prepare the rows (the products alone 1.5 PFLOP/s, 78%
-// of the measured cuBLAS rate; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 108 us (three products: 1.0 PFLOP/s with
-// the preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 205 us, 46 us of it the rows
-// (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 64 bf16 rows of 4096 -> 4096 17 us.  Tiles of fewer than some 170 rows of x are
+// Measured: 8191 bf16 rows of 2048 -> 5120 236 us (1.46 PFLOP/s of its two products, 77% of the measured cuBLAS rate), with rounded
+// weights 130 us, of which 14 us prepare the rows (the product alone 1.5 PFLOP/s; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 108 us (three products: 1.0 PFLOP/s with
+// the preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 386 us, rounded 213 us, 46 us of it the
+// rows (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 64 bf16 rows of 4096 -> 4096 17 us.  Tiles of fewer than some 170 rows of x are
 // bound by the roles' instructions and hand-overs, some 650 clocks a step.
 #include "linear.cuh"
 #include "tcgen05.cuh"
@@ -50,11 +52,12 @@ constexpr int kHalfCodes = 8 * kLinStepBytes; // a step of 128 weight rows
 constexpr int kChunk = 2;                     // steps between sums of f32 rows
 constexpr int kGroup = 8;                     // steps whose blocks' sums are one step
 constexpr int kMaxMats = 1024;
+constexpr int kBF16X = 3;  // bf16 rows with exact weights (kBF16: with weights rounded to f16)
 
 template <int DT> struct ManyPlan {
   static constexpr bool kSums = DT != kBF16;     // exact weights
   static constexpr int kXParts = DT == kF32 ? 2 : 1, kWParts = kSums ? 2 : 1;
-  static constexpr int kCols = DT == kF32 ? 64 : DT == kF16 ? 128 : 192;  // most rows of x in a tile
+  static constexpr int kCols = DT == kF32 ? 64 : DT == kBF16 ? 192 : 128;  // most rows of x in a tile
   static constexpr int kSets = DT == kF32 ? 2 : 1;  // of accumulators
   static constexpr int kA = 2 * kSets * kCols;   // first column of the weights in tensor memory
   static constexpr int kStages = DT == kBF16 ? 6 : 8;  // of copies (even: a group's steps keep to its stages)
@@ -982,8 +985,8 @@ long long linear_many_workspace(int in, int max_rows) { return pad_rows(max_rows
 
 // clusters: how many clusters of 2, 4 and 8 CTAs run at once.
 cudaError_t setup_linear_many(int (&clusters)[3]) {
-  const cudaError_t e[6] = {setup<kF32, false>(),  setup<kF32, true>(),  setup<kF16, false>(),
-                            setup<kF16, true>(), setup<kBF16, false>(), setup<kBF16, true>()};
+  const cudaError_t e[8] = {setup<kF32, false>(),  setup<kF32, true>(),  setup<kF16, false>(),   setup<kF16, true>(),
+                            setup<kBF16, false>(), setup<kBF16, true>(), setup<kBF16X, false>(), setup<kBF16X, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   for (int i = 0; i < 3; ++i) {
@@ -1007,7 +1010,8 @@ cudaError_t launch_linear_many(const LinArgs& L, void* workspace, int max_rows, 
   A.undo_x = reinterpret_cast<const float*>(A.xt + A.pad * (row_bytes(L.in) - 4));
   return L.dtype == kF32   ? launch<kF32>(A, nsm, clusters, s)
          : L.dtype == kF16 ? launch<kF16>(A, nsm, clusters, s)
-                           : launch<kBF16>(A, nsm, clusters, s);
+         : L.rounded       ? launch<kBF16>(A, nsm, clusters, s)
+                           : launch<kBF16X>(A, nsm, clusters, s);
 }
 
 }  // namespace strata

@@ -11,7 +11,7 @@ using namespace strata;
 
 struct strata_linear {
   strata_linear_desc desc;
-  int device = 0, nsm = 0, mats = 1;
+  int device = 0, nsm = 0, mats = 1, rounded = 0;
   int clusters[3] = {};  // of 2, 4 and 8 CTAs that run at once
   uint8_t* mem = nullptr;  // error word, then the matrices and their rows' powers of two
   unsigned* err = nullptr;
@@ -131,7 +131,7 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
   }
   LinArgs A{};
   A.w[0] = h->w[0], A.w[1] = h->w[1];
-  A.n = d.n, A.in = d.in, A.out = d.out, A.glu = h->mats == 2;
+  A.n = d.n, A.in = d.in, A.out = d.out, A.glu = h->mats == 2, A.rounded = h->rounded;
   A.x = x, A.y = y, A.xs = x_stride, A.ys = y_stride, A.dtype = dtype, A.T = T, A.offsets = offsets, A.err = h->err;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool few = linear_few_rows(A, h->nsm);
@@ -139,6 +139,12 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
     cudaGetLastError();
     return STRATA_ECUDA;
   }
+  return STRATA_OK;
+}
+
+strata_status strata_linear_round_weights(strata_linear* h, int32_t on) {
+  if (!h || (on != 0 && on != 1)) return STRATA_EINVAL;
+  h->rounded = on;
   return STRATA_OK;
 }
 

@@ -108,3 +108,7 @@ def test_binding_refuses_what_it_can_see():
         with pytest.raises(B.StrataError) as e:
             call()
         assert e.value.status == B.STRATA_EINVAL
+
+
+def test_round_weights_on_a_null_handle(lib):
+    assert B.strata_linear_round_weights(None, 0) == B.STRATA_EINVAL

@@ -1,0 +1,91 @@
+"""How exactly the products hold weights and rows, beyond the general bounds of tests/layer_helpers.py: rows that cancel, that meet
+one block only, of the largest values, of many columns, and gates far below zero.
+
+Bounds: h = half a step of the result's type; a matrix unit's add may be off by 2^-23 of the larger operand, and only adds of
+something other than zero are.  C as in tests/layer_helpers.py: the size of the terms s (q - 8), 8 s and m times x.
+"""
+import pytest
+import torch
+
+from slot_decode_window_gb300 import workloads as wlm
+from tests.layer_helpers import DTYPES, check_rows, half_step, i32, linear_bound, parts64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from slot_decode_window_gb300 import binding, build
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    binding.load()
+    return binding
+
+
+def _qmat(n, rows, cols, seed):
+    return wlm.make_qmat(n, rows, cols, 4, 32, [seed * 100 + i for i in range(n)], "cuda")
+
+
+def _terms(x, q, i=0):
+    """(y, C) in 64 bits."""
+    s, m, c = (t[i] for t in parts64(q))
+    xd = x.double()
+    return xd @ (s * c + m).T, xd.abs() @ ((s * (c - 8)).abs() + 8 * s.abs() + m.abs()).T
+
+
+def _close(got, y, size):
+    """size: the bound before the result's own rounding."""
+    h = half_step(got.dtype)
+    check_rows(got, y, size * (1 + h) + h * y.abs() + (2.0 ** -25 if got.dtype == torch.float16 else 2.0 ** -130))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [8, 33, 70, 300])
+def test_rows_that_cancel_meet_the_exact_weights(B, dtype, T):
+    """Rows of one 1 and one -1: two weights' difference, where a weight rounded to f16 would show.  At most two instructions with
+    products other than zero for each of the two columns, two of their blocks' sums, 4 scalings and sums: 16 2^-23 C."""
+    d, out = 512, 208
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = _qmat(3, out, d, 40)
+    at = torch.randint(0, d - 1, (T, 2), generator=g, device="cuda")
+    at[:, 1] += at[:, 1] >= at[:, 0]
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x.scatter_(1, at, torch.tensor([1.0, -1.0], device="cuda", dtype=x.dtype).expand(T, 2))
+    one = wlm.QMat(w.codes[:1], w.scale[:1], w.min[:1], out, d, 4, 32)
+    h, hs = B.Linear(one, max_rows=T), B.Linear(w, max_rows=T)
+    y, C = _terms(x, w)
+    _close(h.forward(x), y, 16 * 2.0 ** -23 * C)
+    off = [0, T // 3, T // 2, T]
+    got = hs.forward(x, offsets=i32(off))
+    for i in range(3):
+        y, C = _terms(x[off[i]:off[i + 1]], w, i)
+        _close(got[off[i]:off[i + 1]], y, 16 * 2.0 ** -23 * C)
+    hs.sync()
+    h.close(), hs.close()
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_rounded_weights_are_the_callers_choice(B, glu):
+    """With rounded = True many bf16 rows keep to the bound of weights rounded to f16 (one matrix, and a stack's rows); few rows and
+    other types have the bits that they have without."""
+    d, out, T = 1088, 400, 200
+    w, up = _qmat(2, out, d, 55), _qmat(2, out, d, 56) if glu else None
+    first = lambda q: wlm.QMat(q.codes[:1], q.scale[:1], q.min[:1], out, d, 4, 32) if q else None
+    exact, rounded = (B.Linear(first(w), up=first(up), max_rows=T, rounded=r) for r in (False, True))
+    stack = B.Linear(w, up=up, max_rows=T, rounded=True)
+    x = torch.randn(T, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    for dtype in DTYPES.values():
+        for t in (5, T):
+            a, b = exact.forward(x[:t].to(dtype)), rounded.forward(x[:t].to(dtype))
+            assert torch.equal(a, b) == (dtype != torch.bfloat16 or t == 5)
+    xb = x.bfloat16()
+    check_rows(rounded.forward(xb), *linear_bound(xb, w, up, few=False))
+    y = stack.forward(xb, offsets=i32([0, 70, T]))
+    check_rows(y[:70], *linear_bound(xb[:70], w, up, 0, few=False))
+    check_rows(y[70:], *linear_bound(xb[70:], w, up, 1, few=False))
+    assert B.strata_linear_round_weights(rounded.handle, 2) == B.STRATA_EINVAL
+    assert B.strata_linear_round_weights(rounded.handle, 0) == B.STRATA_OK
+    assert torch.equal(rounded.forward(xb), exact.forward(xb))
+    for h in (exact, rounded, stack):
+        h.sync()
+        h.close()
