@@ -733,8 +733,9 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * depend on the others of such a call.  More take f16 products, on the exact weights
  * (strata_linear_round_weights apart): 16-bit rows exactly, f32 rows in two parts (22 bits).  Rows are
  * scaled by a power of two of their own and weights by one of their row of W, so
- * values of any size keep this (exact: but for bits below 2^-34 of a row's largest
- * value, and scales below 2^-24 of the largest of their row of W; up to 8 rows are
+ * values of any size keep this (exact: but for bits of x below 2^-34 of a row's
+ * largest value, and bits of scales and mins below 2^-33 of the largest scale, or
+ * 2^-39 of the largest min, of their row of W, whichever is more; up to 8 rows are
  * not scaled: their values from 2^-100 to 2^100).  A row with
  * infinities or NaN gives numbers of no meaning in that row only.  Calls of more
  * rows use the workspace: on one handle they, and replays of captured ones, must
@@ -745,7 +746,7 @@ strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_s
 
 /* on = 1: later calls that take f16 products (above) round the weights to f16 for
  * bf16 rows, one product in place of two: 2^-11 of a weight (2^-14 of its row's
- * largest scale where that is more), in about 0.55 of the time of a prompt.  0, as
+ * largest scale or 2^-20 of its largest min where that is more), in about 0.55 of the time of a prompt.  0, as
  * create leaves it: exact weights.  Captured calls keep what they were captured with. */
 strata_status strata_linear_round_weights(strata_linear* h, int32_t on);
 

@@ -12,11 +12,10 @@
 //   record g (16 bytes, f16): scales of row g (first block, second), of row
 //     g + 8, then the mins in the same order
 // Both carry a power of two of their row, scales 2^24 more (a masked code read as
-// f16 is the subnormal q 2^-24): the row's largest scale is in [2^14, 2^15), or its
-// largest min in [4, 8) where that is less.  A row's results are multiplied
-// by `undo`, the inverse.  (A block whose scale is below 2^-28 of the row's largest
-// loses low bits of it, a min below 2^-9 of the row's largest 15 s loses them below
-// 2^-20 of that.)
+// f16 is the subnormal q 2^-24) and mins 2^18 more: the row's largest scale is in
+// [2^14, 2^15), or its largest min where that is less.  A row's results are multiplied
+// by `undo`, the inverse.  (f16's least step, 2^-24, is 2^-38 of the row's largest
+// scale for scales and 2^-32 of it for mins, or 2^-44 and 2^-38 of its largest min.)
 #pragma once
 #include "kv8.cuh"
 
@@ -24,6 +23,7 @@ namespace strata {
 
 constexpr int kLinStep = 64, kLinStepBytes = 640, kLinTile = 16;
 constexpr int kLinFewRows = 8;
+constexpr float kLinScale = 0x1p24f, kLinMin = 0x1p18f;  // what the records' scales and mins carry
 constexpr int kF32 = 0, kF16 = 1, kBF16 = 2;  // strata_dtype
 
 struct LinMat {

@@ -7,7 +7,7 @@
 // pair, and a block's products t = sum (16 + q) x start from zero, so
 //   y += s t + (m - 16 s) sum x
 // in f32 keeps the weights exact; sum x comes out of the same instruction with
-// ones for A, in the lanes that need it.  x is exact too: bf16 as it is, f16 on
+// ones for A (2^-18: the records' mins are 2^18 m), in the lanes that need it.  x is exact too: bf16 as it is, f16 on
 // the f16 instruction, f32 as three bf16 parts by truncation (24 bits).
 //
 // Measured: one bf16 row of 2048 -> 4096 6.1 us (3.5 us in a graph), eight f32 rows of 4096 -> 2048 8.2 us (5.2; latency: launch,
@@ -86,7 +86,7 @@ __device__ __forceinline__ void few_x(const uint4 (&u)[DT == kF32 ? 2 : 1], uint
 template <int DT, int kTiles, int kWarps, bool kGlu>
 __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) few_kernel(LinArgs A) {
   constexpr int kMats = kGlu ? 2 : 1, kParts = FewType<DT>::kParts, kAll = kMats * kTiles;
-  constexpr uint32_t kOnes = DT == kF16 ? 0x3C003C00u : 0x3F803F80u;
+  constexpr uint32_t kOnes = DT == kF16 ? 0x00400040u : 0x36803680u;  // 1 / kLinMin, which the mins carry
   __shared__ float red[kWarps][kAll * 128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int tiles = A.out / kLinTile, nks = A.in / kLinStep;
@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) fe
             few_mma<DT, false>(d, a0, b[blk][k][0], b[blk][k][1]);
           few_mma<DT, false>(d, a1, b[blk][k][2], b[blk][k][3]);
         }
-        const float s0 = 0x1p-24f * half_of(scales.x, blk), s1 = 0x1p-24f * half_of(scales.y, blk);
-        const float o0 = fmaf(-16.f, s0, half_of(scales.z, blk)), o1 = fmaf(-16.f, s1, half_of(scales.w, blk));
+        const float s0 = 1.f / kLinScale * half_of(scales.x, blk), s1 = 1.f / kLinScale * half_of(scales.y, blk);
+        const float o0 = fmaf(-16.f * kLinMin, s0, half_of(scales.z, blk)), o1 = fmaf(-16.f * kLinMin, s1, half_of(scales.w, blk));
         float(&z)[4] = acc[y];
         z[0] = fmaf(s0, d[0], fmaf(o0, xsum[blk][0], z[0]));
         z[1] = fmaf(s0, d[1], fmaf(o0, xsum[blk][1], z[1]));

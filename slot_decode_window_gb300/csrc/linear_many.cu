@@ -302,11 +302,13 @@ __device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
 
 // A step of a tile, row g and row g + 8 of this lane, into the registers of a 16x128b store: the word's pair i goes to
 // column 4 i + c of its block's 16, register 2 i (row g) or 2 i + 1 (row g + 8).  A masked code is the subnormal q 2^-24 (or
-// q 2^-20), the records' scales carry the 2^24, so a pair is one mask and one fma, which rounds once.
+// q 2^-20), the records' scales carry the 2^24, so a pair is one mask and one fma, which rounds once (a min that is then below
+// f16's least normal number is rounded before).
 __device__ __forceinline__ void convert(const uint4& code, const uint4& rec, uint32_t (&r)[16]) {
   const __half2 k16 = __float2half2_rn(0.0625f);
   const uint32_t words[4] = {code.x, code.y, code.z, code.w};
-  const __half2 s[2] = {as_half2(rec.x), as_half2(rec.y)}, m[2] = {as_half2(rec.z), as_half2(rec.w)};
+  const __half2 s[2] = {as_half2(rec.x), as_half2(rec.y)}, down = __float2half2_rn(1.f / kLinMin);
+  const __half2 m[2] = {__hmul2(as_half2(rec.z), down), __hmul2(as_half2(rec.w), down)};
   const __half2 s16[2] = {__hmul2(s[0], k16), __hmul2(s[1], k16)};
 #pragma unroll
   for (int wi = 0; wi < 4; ++wi) {
@@ -322,11 +324,12 @@ __device__ __forceinline__ void convert(const uint4& code, const uint4& rec, uin
   }
 }
 
-// 2^12 s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the
-// product's f16 leaves at most 5 bits.  s: the records' scales times 2^-12 (2^24 - 12 is the factor that results lose again).
-constexpr float kTwoUndo = 0x1p-12f;
+// 2^18 s (q - 8) in two parts, both exact: the code in the mantissa of 1024 (or of 64) less 1032 (72) is q - 8, and the
+// product's f16 leaves at most 5 bits.  2^18 is the mins' factor, which results lose again.  s is the records' scale times 2^-6,
+// [2^8, 2^9) for the row's largest: down to 2^-22 of that it keeps all of its bits.
+constexpr float kTwoUndo = 1.f / kLinMin;
 __device__ __forceinline__ void convert_two(const uint2& code, const uint2& scale, int blk, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
-  const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f), down = __float2half2_rn(0x1p-12f);
+  const __half2 low = __float2half2_rn(-1032.f), high = __float2half2_rn(-72.f), down = __float2half2_rn(kLinMin / kLinScale);
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
     const uint32_t word = row ? code.y : code.x;
@@ -343,12 +346,12 @@ __device__ __forceinline__ void convert_two(const uint2& code, const uint2& scal
   }
 }
 
-// The weights of half a step of sums (16 columns) from the record of step c (first half) or 4 + c of the group: 2^12 m in column
-// 4 i + c for even i, 2^12 8 s for odd i, i / 2 the block; a column's two f16 meet the sum's two parts.
+// The weights of half a step of sums (16 columns) from the record of step c (first half) or 4 + c of the group: 2^18 m in column
+// 4 i + c for even i, 2^18 8 s for odd i, i / 2 the block; a column's two f16 meet the sum's two parts.
 __device__ __forceinline__ void convert_sums(const uint4& rec, uint32_t (&r)[8]) {
-  const __half2 down = __float2half2_rn(0x1p-9f), up = __float2half2_rn(0x1p12f);
+  const __half2 down = __float2half2_rn(8.f * kLinMin / kLinScale);
   const __half2 s[2] = {__hmul2(as_half2(rec.x), down), __hmul2(as_half2(rec.y), down)};
-  const __half2 m[2] = {__hmul2(as_half2(rec.z), up), __hmul2(as_half2(rec.w), up)};
+  const __half2 m[2] = {as_half2(rec.z), as_half2(rec.w)};
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
     r[0 + row] = as_u32(__low2half2(m[row]));

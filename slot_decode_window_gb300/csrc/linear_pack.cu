@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
     if (bs < INFINITY && bm < INFINITY && (bs > 0.f || bm > 0.f)) {  // rows of zeros or with an infinity: as they are
       int es, em;  // the largest is in [2^(e-1), 2^e)
       frexpf(bs, &es), frexpf(bm, &em);
-      k = bs == 0.f ? -5 - em : bm == 0.f ? -9 - es : min(-9 - es, 3 - em);
+      k = bs == 0.f ? -3 - em : bm == 0.f ? -9 - es : min(-9 - es, -3 - em);
     }
     mul[threadIdx.x] = pow2i(k);
     undo[row0 + threadIdx.x] = pow2i(-k);
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(128) linear_pack_kernel(const uint8_t* __restr
       __half h[4];
       for (int i = 0; i < 4; ++i) {
         const int r = g + (i >> 1) * 8;
-        h[i] = __float2half_rn(half_bits(src[(row0 + r) * nblk + 2 * ks + (i & 1)]) * (mul[r] * (c ? 1.f : 16777216.f)));
+        h[i] = __float2half_rn(half_bits(src[(row0 + r) * nblk + 2 * ks + (i & 1)]) * (mul[r] * (c ? kLinMin : kLinScale)));
       }
       *reinterpret_cast<uint2*>(step + 512 + g * 16 + c * 8) = *reinterpret_cast<uint2*>(h);
     }

@@ -89,3 +89,43 @@ def test_rounded_weights_are_the_callers_choice(B, glu):
     for h in (exact, rounded, stack):
         h.sync()
         h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("T", [3, 70])
+def test_small_mins_beside_large_scales(B, dtype, T):
+    """Mins of 1 / 130 of the scale, codes of zeros, rows of one 1: the result is the min.  Two instructions with products other than
+    zero (-8 s; 8 s and m), or two fma of a difference: 4 2^-23 C."""
+    d, out = 128, 64
+    w = _qmat(1, out, d, 41)
+    w.codes.zero_()
+    s, m = w.scale.view(torch.float16), w.min.view(torch.float16)
+    s.fill_(0.0133)
+    m.copy_(1.003e-4 * (1 + torch.rand(m.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))))
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x[torch.arange(T), torch.arange(T) * 37 % d] = 1
+    h = B.Linear(w, max_rows=T)
+    y, C = _terms(x, w)
+    _close(h.forward(x), y, 4 * 2.0 ** -23 * C)
+    h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [7, 70])
+def test_rows_that_meet_only_a_block_of_small_scale(B, dtype, T):
+    """A block's scale is 2^-16 to 2^-22 of its row's largest; rows of x have values in one such block only.  Its columns are two
+    instructions of two parts each, six for f32 rows, and one of the sums, with 6 scalings and sums: 16 2^-23 C; a sum of x in two
+    parts 2^-21, f32 rows' x in two parts 2^-21: 2^-20 C."""
+    d, out = 256, 96
+    w = _qmat(1, out, d, 42)
+    s, m = w.scale.view(torch.float16), w.min.view(torch.float16)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    s.copy_((1 + torch.rand(s.shape, generator=g, device="cuda")) * 2.0 ** 10)
+    s[..., 1:] *= 2.0 ** -torch.arange(16, 23, device="cuda").half()
+    m.copy_(-7.5 * s.float())
+    x = torch.randn(T, 8, 32, generator=g, device="cuda")
+    x = (x * torch.nn.functional.one_hot(torch.arange(T, device="cuda") % 7 + 1, 8)[..., None]).flatten(1).to(DTYPES[dtype])
+    h = B.Linear(w, max_rows=T)
+    y, C = _terms(x, w)
+    _close(h.forward(x), y, (16 * 2.0 ** -23 + 2.0 ** -20) * C)
+    h.close()
