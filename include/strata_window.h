@@ -728,26 +728,31 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * of order or outside 0..T is left out (rows that two others then both name have
  * no defined output), and the next strata_linear_sync reports EDEVICE.  T = 0 does
  * nothing.
- * Sums are f32.  Up to 8 rows of n = 1 (up to 64 of a small matrix) are one launch
- * on the exact weights and the exact rows (24 bits of f32), and a row's bits do not
- * depend on the others of such a call.  More take f16 products, on the exact weights
- * (strata_linear_round_weights apart): 16-bit rows exactly, f32 rows in two parts (22 bits).  Rows are
- * scaled by a power of two of their own and weights by one of their row of W, so
- * values of any size keep this (exact: but for bits of x below 2^-34 of a row's
- * largest value, and bits of scales and mins below 2^-33 of the largest scale, or
- * 2^-39 of the largest min, of their row of W, whichever is more; up to 8 rows are
- * not scaled: their values from 2^-100 to 2^100).  A row with
- * infinities or NaN gives numbers of no meaning in that row only.  Calls of more
- * rows use the workspace: on one handle they, and replays of captured ones, must
- * not overlap on the GPU.  The same call gives the same bits.  Returns EINVAL (T
- * above max_rows among it), ECUDA. */
+ * Sums are f32.  Calls of few rows are one launch on the exact weights and the
+ * exact rows (24 bits of f32), and a row's bits do not depend on the others of such
+ * a call.  Few are, of n = 1, 8 rows; and up to 64 rows of a small matrix:
+ * out <= 32 S and (2 with up, else 1) * out/16 * ceil(T/8) * in/64 <= 440 S (130 S
+ * of f32 rows, 320 S of bf16 rows with rounded weights), S the device's
+ * multiprocessors.  Their rows are not scaled: values from 2^-100 to 2^100, and
+ * zeros.
+ * Other calls, of many rows, take f16 products, on the exact weights
+ * (strata_linear_round_weights apart): 16-bit rows exactly, f32 rows in two parts
+ * (22 bits).  Their rows are scaled by a power of two of their own, so values of
+ * any size keep this, but for bits of x below 2^-34 of a row's largest value.
+ * Weights are scaled by a power of two of their row of W; bits of scales and mins
+ * below 2^-33 of the row's largest scale, or 2^-39 of its largest min, whichever is
+ * more, are lost.  Calls of many rows use the workspace: on one handle they, and
+ * replays of captured ones, must not overlap on the GPU.
+ * A row with infinities or NaN gives numbers of no meaning in that row only.  The
+ * same call gives the same bits.  Returns EINVAL (T above max_rows among it), ECUDA. */
 strata_status strata_linear_forward(strata_linear* h, const void* x, int64_t x_stride, void* y, int64_t y_stride,
                                     int32_t dtype, int32_t T, const int32_t* offsets, void* cuda_stream);
 
-/* on = 1: later calls that take f16 products (above) round the weights to f16 for
- * bf16 rows, one product in place of two: 2^-11 of a weight (2^-14 of its row's
- * largest scale or 2^-20 of its largest min where that is more), in about 0.55 of the time of a prompt.  0, as
- * create leaves it: exact weights.  Captured calls keep what they were captured with. */
+/* on = 1: later calls of many rows (above) round the weights to f16 for bf16 rows,
+ * one product in place of two: 2^-11 of a weight (2^-14 of its row's largest scale
+ * or 2^-20 of its largest min where that is more), in about 0.55 of the time of a
+ * prompt.  0, as create leaves it: exact weights.  Captured calls keep what they
+ * were captured with. */
 strata_status strata_linear_round_weights(strata_linear* h, int32_t on);
 
 /* Wait for the handle's device; report (and clear) any error the GPU recorded:

@@ -8,7 +8,11 @@
 //   y += s t + (m - 16 s) sum x
 // in f32 keeps the weights exact; sum x comes out of the same instruction with
 // ones for A (2^-18: the records' mins are 2^18 m), in the lanes that need it.  x is exact too: bf16 as it is, f16 on
-// the f16 instruction, f32 as three bf16 parts by truncation (24 bits).
+// the f16 instruction, f32 as three bf16 parts by truncation (24 bits).  Rows are not
+// scaled: nothing here passes f32's range, and no bit falls out of it, while they are
+// between 2^-100 and 2^100 (a row's largest, found by a first read, and its power of
+// two would cost 20 to 45% of 9 to 64 rows' time: 16 bf16 rows of 4096 -> 4096 12.8 us
+// against 9.1 us).
 //
 // Measured: one bf16 row of 2048 -> 4096 6.1 us (3.5 us in a graph), eight f32 rows of 4096 -> 2048 8.2 us (5.2; latency: launch,
 // one or two rounds of loads a warp, the join); 16 bf16 rows of 4096 -> 4096 9.1 us; one bf16 row of 2048 -> 151936 52 us (3.8 TB/s, 55% of the measured HBM rate: 61% of the issue slots,
@@ -229,13 +233,16 @@ void launch_t(const LinArgs& A, int nsm, cudaStream_t s) {
 }  // namespace
 
 // At most 8 rows; and more, 8 to a CTA, where the steps of all tiles and groups of 8 rows are few: then one launch without a
-// workspace is faster than two with (in a graph: 16 bf16 rows of 4096 -> 4096 9.1 us against 12.5 us, 24 rows 12.4 and 12.6 us, 32 rows
-// 14.5 and 12.7 us; f32 rows of 4096 -> 2048 16: 9.9 and 14.1 us, 24: 14.2 and 14.1 us; 64 bf16 rows of 2048 -> 512 4.1 and 10.3 us).
+// workspace is faster than two with (in a graph, 16-bit rows against exact weights: 16 rows of 4096 -> 4096 9.2 us against 19.1 us, 32 rows
+// 14.5 and 19.2 us, 48 rows 21.5 and 20.1 us; 64 rows of 2048 -> 4096 16.0 and 14.8 us, of 4096 -> 2048 14.7 and 15.9 us, of 2048 -> 512 3.9 and
+// 12.8 us.  Against rounded weights: 24 rows of 4096 -> 4096 12.6 and 12.6 us, 32 rows 14.5 and 12.6 us.  f32 rows of 4096 -> 2048: 16 9.8
+// and 14.0 us, 24 14.2 and 14.1 us).
 bool linear_few_rows(const LinArgs& A, int nsm) {
   if (A.n != 1) return false;
   if (A.T <= kLinFewRows) return true;
   const long long tiles = A.out / kLinTile, groups = (A.T + kLinFewRows - 1) / kLinFewRows;
-  return A.T <= 64 && tiles <= 2 * nsm && (A.glu ? 2 : 1) * tiles * groups * (A.in / kLinStep) <= (A.dtype == kF32 ? 130LL : 320LL) * nsm;
+  const long long most = A.dtype == kF32 ? 130 : A.dtype == kBF16 && A.rounded ? 320 : 440;
+  return A.T <= 64 && tiles <= 2 * nsm && (A.glu ? 2 : 1) * tiles * groups * (A.in / kLinStep) <= most * nsm;
 }
 
 cudaError_t launch_linear_few(const LinArgs& A, int nsm, cudaStream_t s) {

@@ -301,3 +301,37 @@ def test_refusals(B):
     assert h.forward(x[:0], offsets=off).shape == (0, 64)
     h.sync()
     h.close()
+
+
+@pytest.mark.parametrize("dtype,rounded", [("f32", False), ("f16", False), ("f16", True), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("d,out", [(2048, 512), (4096, 2048), (4096, 4096), (1024, 4864), (1024, 4880)])
+def test_which_kernel_takes_nine_to_sixty_four_rows(B, d, out, dtype, rounded, glu):
+    """The rule that the header gives: the few-row kernel's rows have the bits that they have in calls of 8, the others keep to the
+    many-row kernel's own bound (and f32 rows, of 22 bits there, do not have those bits)."""
+    w, up = _qmat(1, out, d, 51), _qmat(1, out, d, 52) if glu else None
+    h = B.Linear(w, up=up, max_rows=64, rounded=rounded)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    most = {"f32": 130, "f16": 440, "bf16": 320 if rounded else 440}[dtype]
+    for T in (9, 16, 17, 24, 33, 48, 64):
+        x = _rows(T, d, dtype, T)
+        y = h.forward(x)
+        few = out <= 32 * sms and (2 if glu else 1) * (out // 16) * (-(-T // 8)) * (d // 64) <= most * sms
+        eights = torch.cat([h.forward(x[t:t + 8]) for t in range(0, T, 8)])
+        assert not few or torch.equal(y, eights)
+        if not few:
+            check_rows(y, *linear_bound(x, w, up, few=False))
+            assert dtype != "f32" or not torch.equal(y, eights)
+    h.close()
+
+
+@pytest.mark.parametrize("d,out", [(64, 272), (192, 400), (2048, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("glu", [False, True])
+def test_many_rows_keep_to_their_own_bound(B, d, out, dtype, glu):
+    w, up = _qmat(1, out, d, 53), _qmat(1, out, d, 54) if glu else None
+    h = B.Linear(w, up=up, max_rows=700)
+    for T in (65, 129, 193, 200, 385, 700):
+        x = _rows(T, d, dtype, T)
+        check_rows(h.forward(x), *linear_bound(x, w, up, few=False))
+    h.close()

@@ -129,3 +129,37 @@ def test_rows_that_meet_only_a_block_of_small_scale(B, dtype, T):
     y, C = _terms(x, w)
     _close(h.forward(x), y, (16 * 2.0 ** -23 + 2.0 ** -20) * C)
     h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [5, 9, 16, 64])
+def test_rows_of_the_few_row_kernel_over_the_range_that_the_header_gives(B, dtype, T):
+    """Values from 2^-100 to 2^100, rows of zeros, weights of 2^-9 of the usual; rows of 2^100 that meet weights of zeros beside a
+    block of scale 2^15; infinities and NaN stay in their rows."""
+    d, out = 128, 32
+    w = _qmat(1, out, d, 43)
+    s, m = w.scale.view(torch.float16), w.min.view(torch.float16)
+    s[0, :, 1], m[0, :, 1] = 2.0 ** 15, 0
+    s[0, :, 0], m[0, :, 0] = 0, 0
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x[:, :32] = 2.0 ** 100
+    h = B.Linear(w, max_rows=T)
+    assert (h.forward(x) == 0).all()
+    h.close()
+    w = _qmat(1, out, d, 44)
+    w.scale.view(torch.float16)[0, :16] *= 2.0 ** -9
+    w.min.view(torch.float16)[0, :16] *= 2.0 ** -9
+    g = torch.Generator(device="cuda").manual_seed(T)
+    scale = torch.tensor([2.0 ** -100, 2.0 ** 99, 1.0, 0.0, 2.0 ** -20], device="cuda").repeat(T)[:T, None]
+    x = (1 + torch.rand(T, d, generator=g, device="cuda")) * torch.where(torch.rand(T, d, generator=g, device="cuda") < 0.5, -1, 1)
+    x = (x * scale).to(DTYPES[dtype])
+    h = B.Linear(w, max_rows=T)
+    y = h.forward(x)
+    check_rows(y, *linear_bound(x, w, None, few=True))
+    assert (y[3] == 0).all()
+    bad = x.clone()
+    bad[2, 5], bad[4, 7] = float("nan"), float("inf")
+    z = h.forward(bad)
+    keep = [t for t in range(T) if t not in (2, 4)]
+    assert torch.equal(z[keep], y[keep]) and not torch.isfinite(z[[2, 4]]).any()
+    h.close()
