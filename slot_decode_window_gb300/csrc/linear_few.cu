@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps < 16 ? 16 / kWarps : 1) fe
       for (int w = 0; w < kWarps; ++w) s += red[w][m * kTiles * 128 + from];
       v[m] = s * A.w[m].undo[o];
     }
-    const float y = kGlu ? silu_f32(v[0]) * v[kMats - 1] : v[0];
+    const float y = kGlu ? lin_silu<false>(v[0]) * v[kMats - 1] : v[0];
     const long long at = (long long)(begin + col) * A.ys + o;
     if constexpr (DT == kF32)
       static_cast<float*>(A.y)[at] = y;

@@ -370,13 +370,6 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// z / (1 + e^-z); for 16-bit results with the fast exponential and quotient (a few 2^-22 of it against their 2^-12).
-template <int DT>
-__device__ __forceinline__ float silu(float z) {
-  if constexpr (DT == kF32) return silu_f32(z);
-  return __fdividef(z, 1.f + __expf(-z));
-}
-
 // Two products in one instruction.
 __device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
   asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
@@ -688,7 +681,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           }
           if constexpr (GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[0][j] = silu<DT>(v[0][j]) * v[1][j];
+            for (int j = 0; j < 16; ++j) v[0][j] = lin_silu<DT != kF32>(v[0][j]) * v[1][j];
             store16<DT>(L, v[0], r0 + c, t.begin, t.end, f0, lane);
           }
         }
@@ -746,7 +739,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
             }
           if constexpr (GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[0][c][j] = silu<DT>(acc[0][c][j]) * acc[1][c][j];
+            for (int j = 0; j < 16; ++j) acc[0][c][j] = lin_silu<DT != kF32>(acc[0][c][j]) * acc[1][c][j];
           }
 #pragma unroll
           for (int h = 0; h < (GLU ? 1 : 2); ++h)
@@ -791,7 +784,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         }
         if constexpr (GLU) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[0][j] = silu<DT>(v[0][j]) * v[1][j];
+          for (int j = 0; j < 8; ++j) v[0][j] = lin_silu<DT != kF32>(v[0][j]) * v[1][j];
         }
 #pragma unroll
         for (int h = 0; h < (GLU ? 1 : 2); ++h) {

@@ -163,3 +163,43 @@ def test_rows_of_the_few_row_kernel_over_the_range_that_the_header_gives(B, dtyp
     keep = [t for t in range(T) if t not in (2, 4)]
     assert torch.equal(z[keep], y[keep]) and not torch.isfinite(z[[2, 4]]).any()
     h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [4, 70])
+def test_gates_far_below_zero(B, dtype, T):
+    """silu(z) for z from -80 to -97, where e^-z leaves f32 or its quotient does, times 2^10: e^z is down to 2^-140, 9 bits of a
+    subnormal, so the result is within 2^-9 and its own rounding."""
+    d, out = 64, 32
+    w, up = _qmat(1, out, d, 45), _qmat(1, out, d, 46)
+    z = -torch.linspace(80, 97, out, device="cuda").half()
+    for q, v in ((w, z), (up, torch.full_like(z, 1024.0))):
+        q.scale.zero_(), q.min.zero_()
+        q.min.view(torch.float16)[0, :, 0] = v
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x[torch.arange(T), torch.arange(T) % 32] = 1
+    h = B.Linear(w, up=up, max_rows=T)
+    y = h.forward(x)
+    zd = z.double()
+    want = (zd * torch.exp(zd) / (1 + torch.exp(zd)) * 1024).expand(T, out)
+    check_rows(y, want, (2.0 ** -9 + half_step(x.dtype)) * want.abs())
+    h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T", [4, 70])
+def test_the_largest_gates(B, dtype, T):
+    """silu is z or 0 at the far ends, and not a number of neither."""
+    d, out = 64, 16
+    w, up = _qmat(1, out, d, 47), _qmat(1, out, d, 48)
+    z = torch.tensor([-6e4, -1e3, -200, -104, 89, 200, 1e3, 6e4] * 2, device="cuda").half()
+    for q, v in ((w, z), (up, torch.full_like(z, 1.0))):
+        q.scale.zero_(), q.min.zero_()
+        q.min.view(torch.float16)[0, :, 0] = v
+    x = torch.zeros(T, d, device="cuda", dtype=DTYPES[dtype])
+    x[:, 3] = 1
+    h = B.Linear(w, up=up, max_rows=T)
+    want = z.clamp(min=0).to(x.dtype).expand(T, out)
+    y = h.forward(x)
+    assert torch.isfinite(y).all() and ((y - want).abs() <= 2 * half_step(x.dtype) * want + 2.0 ** -100).all()
+    h.close()
