@@ -853,8 +853,8 @@ typedef struct {
 } strata_blocknorm_desc;
 
 /* Create on the current device.  after_gain, before_gain, channel_gate: device
- * fp32 [hidden] (copied on cuda_stream; create waits), NULL for ones;
- * channel_gate is wanted by STRATA_GATE_CHANNEL.  Returns EINVAL, EUNSUPPORTED,
+ * fp32 [hidden] (copied on cuda_stream; create waits), NULL for ones; a gain
+ * without its norm is not read.  channel_gate is wanted by STRATA_GATE_CHANNEL.  Returns EINVAL, EUNSUPPORTED,
  * ENOMEM, ECUDA. */
 strata_status strata_blocknorm_create(const strata_blocknorm_desc* desc, const float* after_gain,
                                       const float* before_gain, const float* channel_gate, void* cuda_stream,

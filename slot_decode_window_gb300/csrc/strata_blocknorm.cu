@@ -205,7 +205,7 @@ strata_status strata_blocknorm_create(const strata_blocknorm_desc* d, const floa
   if (st == STRATA_OK) {
     for (int i = 0; i < d->hidden; ++i) ones[i] = 1.f;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const float* from[2] = {after_gain, before_gain};
+    const float* from[2] = {d->after ? after_gain : nullptr, d->before ? before_gain : nullptr};
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 2 && e == cudaSuccess; ++i)
       e = cudaMemcpyAsync(h->mem + (size_t)i * d->hidden, from[i] ? from[i] : ones, row,

@@ -139,3 +139,17 @@ def test_refusals(B):
                  (p, d, q, d, r, 0, h.data_ptr(), d, n.data_ptr(), d, 5, 4), (p, d, q, d, r + 2, 0, h.data_ptr(), d, n.data_ptr(), d, 0, 4)):
         assert f(bn.handle, *args) == B.STRATA_EINVAL
     assert f(bn.handle, p, d, q, d, r, 0, h.data_ptr(), d, n.data_ptr(), d, 0, 0) == B.STRATA_OK
+
+
+def test_a_gain_without_its_norm_is_not_applied(B):
+    """after = 0: u = y whatever after_gain is, with a channel gate (which is folded into the same vector) as without."""
+    d, T = 64, 3
+    x, y, gain, gate = (torch.randn(*s, device="cuda") for s in ((T, d), (T, d), (d,), (d,)))
+    for kind, p, g in ((B.STRATA_GATE_CHANNEL, gate.data_ptr(), gate), (B.STRATA_GATE_NONE, None, None)):
+        st, h = B.strata_blocknorm_create(B.strata_blocknorm_desc(d, 0, 0, kind, 0, 1e-6, 1.0, 1.0), gain.data_ptr(), None, p)
+        assert st == B.STRATA_OK
+        out = torch.empty_like(x)
+        assert B.strata_blocknorm_forward(h, x.data_ptr(), d, y.data_ptr(), d, None, 0, out.data_ptr(), d, None, 0, 0, T) == B.STRATA_OK
+        torch.cuda.synchronize()
+        _check((out, None), x, y, None, None, g, False, 1.0, 1.0, 1e-6)
+        B.strata_blocknorm_destroy(h)
