@@ -154,7 +154,7 @@ void launch_t(const BnArgs& A, unsigned rows, cudaStream_t s) {
     launch_vec<T, 2, 512>(A, rows, s);
   else if (pieces <= 2048)
     launch_vec<T, 4, 512>(A, rows, s);
-  else
+  else if constexpr (Val<T>::kPer == 4)  // (only f32 rows have more)
     launch_vec<T, 4, 1024>(A, rows, s);
 }
 
