@@ -408,10 +408,13 @@ __device__ __forceinline__ void store16(const LinArgs& L, const float (&v)[16], 
   }
 }
 
+// Powers of two of rows of x.  Ordinary loads: the kernel that writes them runs beside this one's start, and the read-only path
+// is for what does not change while a kernel lives.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 t = __ldg(reinterpret_cast<const float4*>(p) + i);
+    const float4 t = load4(p + 4 * i);
     v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
   }
 }
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         float4 ux[2] = {};
 #pragma unroll
         for (int j = 0; j < 8; j += 4)
-          if (j < n) ux[j / 4] = __ldg(reinterpret_cast<const float4*>(A.undo_x + r + j));
+          if (j < n) ux[j / 4] = load4(A.undo_x + r + j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h >= halves) break;
