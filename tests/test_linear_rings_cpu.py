@@ -1,7 +1,64 @@
-"""How the many-row product kernel (csrc/linear_many.cu) reads what its overlapped preparation writes."""
+"""Two things of the many-row product kernel (csrc/linear_many.cu) that its barrier protocol's play (tests/test_linear_protocol_cpu.py)
+leaves out: the conversion groups' own way around the ring of copies, and how it reads what its overlapped preparation writes."""
 import re
 
-from tests.test_linear_protocol_cpu import SOURCE
+import pytest
+
+from tests.test_kv8_protocol_cpu import Bar, Machine
+from tests.test_linear_protocol_cpu import SOURCE, constants
+
+
+def play(tiles, stages, seed):
+    """Rounded weights: copies and products go around the ring stage by stage, a conversion group by two, from its own first stage,
+    with a phase that turns where its index does, as the kernel's `(st += 2) >= P::kStages` has it."""
+    m, total = Machine(seed), sum(tiles)
+    for i in range(stages):
+        m.bars["full", i], m.bars["empty", i] = Bar(1), Bar(2)
+
+    def copies():
+        for use in range(total):
+            if use >= stages:
+                yield "wait", ("empty", use % stages), use // stages - 1
+            m.mem["stage", use % stages] = None
+
+            def landed(use=use):
+                m.mem["stage", use % stages] = use
+                m.arrive(("full", use % stages))
+            yield "async", "copies", 1.0, landed
+
+    def convert(group):
+        st, turn = group, 0
+        for use in range(group, total, 2):
+            yield "wait", ("full", st), turn
+            m.expect(("stage", st), use)
+            yield "work", 1.0
+            m.expect(("stage", st), use)
+            yield "arrive", ("empty", st)
+            st += 2
+            if st >= stages:
+                st, turn = group, turn + 1
+
+    def products():
+        for use in range(total):
+            yield "wait", ("full", use % stages), use // stages
+            yield "work", 1.0
+            yield "arrive", ("empty", use % stages)
+
+    m.run([copies(), convert(0), convert(1), products()])
+
+
+def test_groups_that_keep_to_their_stages():
+    assert "if ((st += 2) >= P::kStages) st = group, ph ^= 1;" in open(SOURCE).read()  # what is played here
+    for tiles in ([1], [3, 1, 1, 4], [7, 9, 12], [33, 2, 18]):
+        for seed in range(25):
+            play(tiles, constants("bf16")["stages"], seed)
+
+
+@pytest.mark.parametrize("stages", [3, 5, 7])
+def test_an_odd_ring_is_found(stages):
+    for seed in range(10):
+        with pytest.raises(AssertionError):
+            play([9, 12, 5], stages, seed)
 
 
 def test_what_the_overlapped_preparation_writes_is_not_read_through_the_read_only_path():

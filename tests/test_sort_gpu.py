@@ -250,3 +250,31 @@ def test_a_plan_of_another_number_of_choices_is_refused(B):
     again = B.ExpertSort(16, 2)  # the experts of a plan are in its places alone
     assert torch.equal(again.gather(plan, x), other.gather(plan, x))
     h.close(), other.close(), again.close()
+
+
+def test_gradient_against_differences_within_the_sums_own_rounding(B):
+    """As above, with the bound formed entry by entry: a shifted z and w are rounded once each and a row's k products in f32 take k
+    roundings, (k + 2) 2^-24 of |w| |z| each, over 2 t; a product of the gradient's rounds once, a sum of `width` of them in at
+    most width / 32 + 16 adds."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    T, k, E, width, u = 40, 3, 6, 64, 2.0 ** -24
+    h = B.ExpertSort(E, k)
+    plan = h.plan(torch.randint(-1, E, (T, k), generator=g, device="cuda").to(torch.int32))
+    z, a = (torch.randn(T * k, width, generator=g, device="cuda") for _ in range(2))
+    w, b = (torch.randn(T, k, generator=g, device="cuda") for _ in range(2))
+    dy = torch.randn(T, width, generator=g, device="cuda")
+    dz, dw = h.combine_backward(plan, dy, z, w=w, dz=torch.zeros_like(z))
+    live = (plan.place >= 0).view(T, k, 1).double()
+    at = plan.place.clamp(min=0).long()
+    rows = lambda v: v.double()[at].view(T, k, width) * live
+    t, size = 0.125, 0.0
+    for s in (1, -1):
+        size = size + ((w + s * t * b).double().abs()[..., None] * rows((z + s * t * a).abs())).sum(1)
+    bound = (size * (k + 2) * u * dy.double().abs()).sum() / (2 * t)
+    bound += (u * rows(dz).abs() * rows(a).abs()).sum()
+    bound += ((width / 32 + 16) * u * (dy.double().abs()[:, None] * rows(z).abs()).sum(-1) * b.double().abs()).sum()
+    up, down = (h.combine(plan, z + s * t * a, w=w + s * t * b) for s in (1, -1))
+    num = ((up.double() - down.double()) * dy.double()).sum() / (2 * t)
+    ana = (rows(dz) * rows(a)).sum() + (dw.double() * b.double()).sum()
+    assert abs(num - ana) <= bound
+    h.close()
