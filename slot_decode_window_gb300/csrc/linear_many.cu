@@ -16,7 +16,7 @@
 // whose "x" are the blocks' sums, in two f16 parts.  16-bit rows: hi x + lo x.  f32 rows: x
 // in two f16 parts (22 bits), lo hi + hi lo + hi hi; the accumulators' adds
 // truncate, so every two steps they are added to f32 registers, with two sets of
-// accumulators in turn.
+// accumulators in turn; so are f16 rows of more than 29120 columns.
 // Rounded weights (bf16 rows, where the caller asks for them): one product, W
 // rounded to f16, 2^-11 of a weight.
 //
@@ -52,7 +52,9 @@ constexpr int kHalfCodes = 8 * kLinStepBytes; // a step of 128 weight rows
 constexpr int kChunk = 2;                     // steps between sums of f32 rows
 constexpr int kGroup = 8;                     // steps whose blocks' sums are one step
 constexpr int kMaxMats = 1024;
-constexpr int kBF16X = 3;  // bf16 rows with exact weights (kBF16: with weights rounded to f16)
+// Kinds of rows besides strata_dtype's: bf16 rows with exact weights (kBF16: with weights rounded to f16), f16 rows of many columns.
+constexpr int kBF16X = 3, kF16Long = 4;
+constexpr int value_type(int kind) { return kind == kBF16X ? kBF16 : kind == kF16Long ? kF16 : kind; }
 
 template <int DT> struct ManyPlan {
   static constexpr bool kSums = DT != kBF16;     // exact weights
@@ -73,6 +75,11 @@ template <int DT> struct ManyPlan {
   static_assert(kStage % 1024 == 0 && kStages % 2 == 0, "stages");
   static_assert(kA + 4 * 32 * kWParts <= 512, "tensor memory");
   static_assert(kPre + (kMaxMats + 1) * 4 <= 232448, "shared memory");
+};
+
+// As f32 rows, with one part of x (the place of the other is not used).
+template <> struct ManyPlan<kF16Long> : ManyPlan<kF32> {
+  static constexpr int kXParts = 1;
 };
 
 __host__ __device__ inline int sum_steps(int nks) { return (nks + kGroup - 1) / kGroup; }
@@ -365,7 +372,7 @@ __device__ __forceinline__ void convert_sums(const uint4& rec, uint32_t (&r)[8])
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
-  if constexpr (DT == kF16) return pack_half2(a, b);
+  if constexpr (value_type(DT) == kF16) return pack_half2(a, b);
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         const int f = GLU ? f0 : f0 + h * 128;
         undo[h] = f < L.out ? __ldg(L.w[GLU ? h : 0].undo + (long long)t.mat * L.out + f) * (P::kSums ? kTwoUndo : 1.f) : 0.f;
       }
-      if constexpr (DT != kF32) {
+      if constexpr (P::kSets == 1) {
         if (!(ok = wait_warp(&d_full[0], chunk & 1, dead, err))) break;
         tc_fence_after();
         if (A.split > 1) cluster_meet();  // the cluster's stages of copies are free
@@ -858,7 +865,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
         const uint32_t id = 1u << 4 | (uint32_t)(t.cols >> 3) << 17 | (uint32_t)(128 >> 4) << 24;  // f16, f32, M = 128
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
-          const bool first = DT == kF32 ? i % kChunk == 0 : i == 0;
+          const bool first = P::kSets == 2 ? i % kChunk == 0 : i == 0;
           if (first && !(ok = wait_warp(&d_empty[set], d_ph, dead, err))) break;
           const uint64_t b = tc_desc(smem + xst * P::kStage, 1024, 0);
           const uint32_t d = (set * 2 + half) * P::kCols;
@@ -899,7 +906,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) linear_many_kernel(const __gr
           if (st) a_ph ^= 1;
           st ^= 1;
           if (++xst == P::kStages) xst = 0;
-          if (i == steps - 1 || (DT == kF32 && i % kChunk == kChunk - 1)) {
+          if (i == steps - 1 || (P::kSets == 2 && i % kChunk == kChunk - 1)) {
             tc_commit_if(lead, &d_full[set]);
             if (++set == P::kSets) set = 0, d_ph ^= 1;
           }
@@ -942,10 +949,11 @@ cudaError_t launch(ManyArgs A, int nsm, const int (&clusters)[3], cudaStream_t s
   }
   // warps per row: as many as keep it in registers, at most a CTA's
   int warps = 1;
-  while (warps < 8 && L.in / 8 > warps * 32 * RowsPlan<DT>::kOct) warps *= 2;
+  constexpr int kRows = DT == kF16Long ? kF16 : DT;
+  while (warps < 8 && L.in / 8 > warps * 32 * RowsPlan<kRows>::kOct) warps *= 2;
   const int per = 8 / warps;
-  linear_rows_kernel<DT><<<(unsigned)((L.T + per - 1) / per), 256, 0, s>>>(L.x, L.xs, L.T, L.in, warps, const_cast<uint8_t*>(A.xt),
-                                                                          A.pad, const_cast<float*>(A.undo_x));
+  linear_rows_kernel<kRows><<<(unsigned)((L.T + per - 1) / per), 256, 0, s>>>(L.x, L.xs, L.T, L.in, warps, const_cast<uint8_t*>(A.xt),
+                                                                             A.pad, const_cast<float*>(A.undo_x));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // launched while the rows are prepared: its start (barriers, tensor memory, the list of tiles, the first codes) needs none
@@ -984,8 +992,9 @@ long long linear_many_workspace(int in, int max_rows) { return pad_rows(max_rows
 
 // clusters: how many clusters of 2, 4 and 8 CTAs run at once.
 cudaError_t setup_linear_many(int (&clusters)[3]) {
-  const cudaError_t e[8] = {setup<kF32, false>(),  setup<kF32, true>(),  setup<kF16, false>(),   setup<kF16, true>(),
-                            setup<kBF16, false>(), setup<kBF16, true>(), setup<kBF16X, false>(), setup<kBF16X, true>()};
+  const cudaError_t e[10] = {setup<kF32, false>(),   setup<kF32, true>(),   setup<kF16, false>(),    setup<kF16, true>(),
+                             setup<kBF16, false>(),  setup<kBF16, true>(),  setup<kBF16X, false>(),  setup<kBF16X, true>(),
+                             setup<kF16Long, false>(), setup<kF16Long, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   for (int i = 0; i < 3; ++i) {
@@ -1007,10 +1016,12 @@ cudaError_t launch_linear_many(const LinArgs& L, void* workspace, int max_rows, 
   A.pad = pad_rows(max_rows);
   A.xt = static_cast<uint8_t*>(workspace);
   A.undo_x = reinterpret_cast<const float*>(A.xt + A.pad * (row_bytes(L.in) - 4));
-  return L.dtype == kF32   ? launch<kF32>(A, nsm, clusters, s)
-         : L.dtype == kF16 ? launch<kF16>(A, nsm, clusters, s)
-         : L.rounded       ? launch<kBF16>(A, nsm, clusters, s)
-                           : launch<kBF16X>(A, nsm, clusters, s);
+  if (L.dtype == kF32) return launch<kF32>(A, nsm, clusters, s);
+  // An accumulator's adds truncate, some 9 of them a step of 64 columns, by 2^-23 of it at most: while that is below half a step
+  // of an f16 result the sum stays in it.  (65536 columns of one sign in one accumulator drifted by 2.3e-4, half of that half step;
+  // the registers' sums cost 1280 rows of 32768 -> 4096 1163 us against 735 us.)
+  if (L.dtype == kF16) return 9 * (L.in / kLinStep) > 1 << 12 ? launch<kF16Long>(A, nsm, clusters, s) : launch<kF16>(A, nsm, clusters, s);
+  return L.rounded ? launch<kBF16>(A, nsm, clusters, s) : launch<kBF16X>(A, nsm, clusters, s);
 }
 
 }  // namespace strata

@@ -203,3 +203,51 @@ def test_the_largest_gates(B, dtype, T):
     y = h.forward(x)
     assert torch.isfinite(y).all() and ((y - want).abs() <= 2 * half_step(x.dtype) * want + 2.0 ** -100).all()
     h.close()
+
+
+@pytest.mark.parametrize("dtype,d", [("f16", 65536), ("f16", 29184), ("f16", 29120), ("bf16", 65536)])
+@pytest.mark.parametrize("glu", [False, True])
+def test_long_sums_of_one_sign(B, dtype, d, glu):
+    """All products positive, so that adds that truncate drift one way, in tiles enough that no cluster shares their columns.  f16
+    rows of more than 29120 columns are added up in f32 registers every two steps of 64 columns: 32 2^-23 within them and one
+    rounding each, d / 128 2^-24 in all.  Others take at most 9 adds a step: 9 d / 64 2^-23.  A pair in 16 bits: 2^-18 of its silu."""
+    T, out = 1283, 2048 if glu else 4096
+    g = torch.Generator(device="cuda").manual_seed(d)
+
+    def mat():  # codes of 8 and more, mins as the scales: C is y
+        codes = (torch.randint(0, 256, (1, out, d // 2), generator=g, device="cuda", dtype=torch.int32) | 0x88).to(torch.uint8)
+        s = (1.0 / d * (1 + torch.rand(1, out, d // 32, generator=g, device="cuda"))).half()
+        return wlm.QMat(codes, s.view(torch.int16), s.clone().view(torch.int16), out, d, 4, 32)
+
+    w, up = mat(), mat() if glu else None
+    x = (0.5 + 0.5 * torch.rand(T, d, generator=g, device="cuda")).to(DTYPES[dtype])
+    h = B.Linear(w, up=up, max_rows=T)
+    got = h.forward(x)[::20, ::64]
+    some = lambda q: wlm.QMat(q.codes[:, ::64], q.scale[:, ::64], q.min[:, ::64], q.codes[:, ::64].shape[1], d, 4, 32)
+    y, C = _terms(x[::20], some(w))
+    rel = 32 * 2.0 ** -23 + d / 128 * 2.0 ** -24 if dtype == "f16" and d > 29120 else 9 * d / 64 * 2.0 ** -23
+    size = rel * C
+    if glu:
+        v, Cv = _terms(x[::20], some(up))
+        sg = y * torch.sigmoid(y)
+        y, size = sg * v, 1.1 * size * (v + rel * Cv) + sg * rel * Cv + 2.0 ** -18 * sg * v
+    _close(got, y, size)
+    h.sync()
+    h.close()
+
+
+def test_long_f16_rows_of_stacks_and_clusters(B):
+    """f16 rows of more than 29120 columns with offsets, and few tiles (clusters share their columns)."""
+    d, out = 29184, 48
+    w, up = _qmat(2, out, d, 57), _qmat(2, out, d, 58)
+    one = wlm.QMat(w.codes[:1], w.scale[:1], w.min[:1], out, d, 4, 32)
+    x = torch.randn(150, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).half()
+    h, hs = B.Linear(one, max_rows=150), B.Linear(w, up=up, max_rows=150)
+    check_rows(h.forward(x), *linear_bound(x, w, None, few=False))
+    y = torch.full((150, out), 7.0, dtype=x.dtype, device="cuda")
+    hs.forward(x, y=y, offsets=i32([3, 70, 149]))
+    for i, (a, b) in enumerate(((3, 70), (70, 149))):
+        check_rows(y[a:b], *linear_bound(x[a:b], w, up, i, few=False))
+    assert (y[:3] == 7).all() and (y[149:] == 7).all()
+    hs.sync()
+    h.close(), hs.close()
