@@ -1,9 +1,12 @@
 """Two things of the many-row product kernel (csrc/linear_many.cu) that its barrier protocol's play (tests/test_linear_protocol_cpu.py)
 leaves out: the conversion groups' own way around the ring of copies, and how it reads what its overlapped preparation writes."""
+import os
 import re
+import subprocess
 
 import pytest
 
+from slot_decode_window_gb300 import build
 from tests.test_kv8_protocol_cpu import Bar, Machine
 from tests.test_linear_protocol_cpu import SOURCE, constants
 
@@ -68,3 +71,16 @@ def test_what_the_overlapped_preparation_writes_is_not_read_through_the_read_onl
         assert "__ldg" not in body
     uses = [line for line in text.split("\n") if re.search(r"A\.undo_x \+ ", line)]
     assert len(uses) == 3 and all(re.search(r"load(4|16)\(A\.undo_x", line) for line in uses)
+
+
+def test_registers_at_launch():
+    """The roles' register shares are drawn from what a block is launched with: every variant has to be compiled with kRegs a thread
+    (create refuses one that is not, as its waits for registers would never end)."""
+    text = open(SOURCE).read()
+    regs = int(re.search(r"kRegs = (\d+);", text)[1])
+    cmd = [build.nvcc(), "-c", SOURCE, "-o", os.devnull, build.ARCH, "-O3", "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC,
+           "--expt-relaxed-constexpr", "-Xptxas", "-v"]
+    out = subprocess.run(cmd, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    used = re.findall(r"entry function '\w*linear_many_kernel\w*'.*?Used (\d+) registers", out.stderr, re.S)
+    assert len(used) == 2 * len(re.findall(r"setup<\w+, true>\(\)", text)) and set(used) == {str(regs)}
