@@ -834,7 +834,9 @@ strata_status strata_sort_destroy(strata_sort* h);
  *   h = residual_scale * x + block_scale * g * u
  *   n = h / sqrt(mean(h^2) + eps) * before_gain         (before = 1)
  * x is the residual stream, y the block's output, h the new stream and n the
- * next block's input, from the unrounded h.  fp32 arithmetic. */
+ * next block's input, from the unrounded h.  fp32 arithmetic: the squares' sum has
+ * to be an fp32, so what is normed is at most 2^56 (and, with eps = 0, its root
+ * mean square at least 2^-60). */
 typedef struct strata_blocknorm strata_blocknorm;
 
 typedef enum {

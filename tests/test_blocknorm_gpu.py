@@ -153,3 +153,19 @@ def test_a_gain_without_its_norm_is_not_applied(B):
         torch.cuda.synchronize()
         _check((out, None), x, y, None, None, g, False, 1.0, 1.0, 1e-6)
         B.strata_blocknorm_destroy(h)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_over_the_range_that_the_header_gives(B, dtype):
+    """Rows of 2^56 in the widest hidden size, and of 2^-60 without eps."""
+    d = 16384
+    g = torch.Generator(device="cuda").manual_seed(9)
+    sign = torch.where(torch.rand(4, d, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    scale = torch.tensor([2.0 ** 56, 2.0 ** -60, 1.0, 2.0 ** 30], device="cuda")[:, None]
+    y = (sign * scale).to(DTYPES[dtype])
+    x = torch.zeros_like(y)
+    one = torch.ones(d, device="cuda")
+    for after in (None, one):
+        h = B.BlockNorm(d, after=after, before=True, eps=0.0)
+        _check(h.forward(x, y), x, y, after, one, None, False, 1.0, 1.0, 0.0)
+        h.close()
