@@ -15,7 +15,7 @@
 // against 9.1 us).
 //
 // Measured: one bf16 row of 2048 -> 4096 6.1 us (3.5 us in a graph), eight f32 rows of 4096 -> 2048 8.2 us (5.2; latency: launch,
-// one or two rounds of loads a warp, the join); 16 bf16 rows of 4096 -> 4096 9.1 us; one bf16 row of 2048 -> 151936 52 us (3.8 TB/s, 55% of the measured HBM rate: 61% of the issue slots,
+// one or two rounds of loads a warp, the join); 16 bf16 rows of 4096 -> 4096 9.1 us; one bf16 row of 2048 -> 151936 53 us (3.7 TB/s, 54% of the measured HBM rate: 60% of the issue slots,
 // some 110 instructions for a tile's 640 bytes), eight f32 rows 76 us.
 #include "linear.cuh"
 

@@ -25,19 +25,20 @@
 // weights of their own (a warp has two tiles of 16 weight rows, a quarter of the
 // lanes of one half); 8 of results (each a quarter of the lanes
 // and half of the rows of x); one of copies, codes and x of a step into one stage;
-// one for each half that issues its products (and one that fills the warpgroup).  A step has to pass in 768 clocks for the
-// tensor cores never to wait, and a warp's waits and hand-overs alone take about
+// one for each half that issues its products (and one that fills the warpgroup).  A step has to pass in 768 clocks (1024 of
+// 16-bit rows with exact weights) for the tensor cores never to wait, and a warp's waits and hand-overs alone take about
 // as many: hence the two groups, and two warps that issue.  CTAs (one per SM) take
 // the tiles of all matrices in turn, weight rows fastest, so that concurrent CTAs
 // share rows of x in L2.  Where there are fewer tiles than SMs, a cluster of 2, 4 or
 // 8 CTAs takes a tile, each a part of its columns; a CTA sends its part of the
 // results to those that add them up (each a share of the rows of x, in the cluster's
 // order) through distributed shared memory.
-// Measured: 8191 bf16 rows of 2048 -> 5120 236 us (1.46 PFLOP/s of its two products, 77% of the measured cuBLAS rate), with rounded
-// weights 130 us, of which 14 us prepare the rows (the product alone 1.5 PFLOP/s; 885 clocks a step of 768); 2041 f32 rows of 4096 -> 2048 108 us (three products: 1.0 PFLOP/s with
-// the preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 386 us, rounded 213 us, 46 us of it the
-// rows (HBM); 203 f16 rows with gate 2048 -> 4096 27 us; 64 bf16 rows of 4096 -> 4096 17 us.  Tiles of fewer than some 170 rows of x are
-// bound by the roles' instructions and hand-overs, some 650 clocks a step.
+// Measured: 8191 bf16 or f16 rows of 2048 -> 5120 234 to 239 us (1.45 PFLOP/s of the two products, 76% of the measured cuBLAS rate;
+// rounded weights 130 us), of which 14 us prepare the rows; 2041 f32 rows of 4096 -> 2048 108 us (three products: 0.95 PFLOP/s with the
+// preparation, 1.7 waves of tiles); 128 experts' gate and up of 2048 -> 768 for 32104 bf16 rows 386 us (rounded 213 us), 46 us of it the
+// rows (HBM), down 227 us (rounded 142 us); 512 rows over those experts, gate and up, 143 us, 152 us of f32; 203 f16 rows with gate
+// 2048 -> 4096 27 us; 64 bf16 rows of 4096 -> 4096 20 us in a graph.  Tiles of fewer than some 170 rows of x are bound by the roles'
+// instructions and hand-overs, some 650 clocks a step with rounded weights.
 #include "linear.cuh"
 #include "tcgen05.cuh"
 
