@@ -1,5 +1,6 @@
-"""Two things of the many-row product kernel (csrc/linear_many.cu) that its barrier protocol's play (tests/test_linear_protocol_cpu.py)
-leaves out: the conversion groups' own way around the ring of copies, and how it reads what its overlapped preparation writes."""
+"""What the play of the many-row product kernel's barrier protocol (tests/test_linear_protocol_cpu.py) leaves out of
+csrc/linear_many.cu: the conversion groups' own way around the ring of copies, how it reads what its overlapped preparation writes, and
+the registers that its roles share."""
 import os
 import re
 import subprocess
