@@ -729,9 +729,10 @@ strata_status strata_linear_create(const strata_linear_desc* desc, const strata_
  * no defined output), and the next strata_linear_sync reports EDEVICE.  T = 0 does
  * nothing.
  * Sums are f32; a tensor core's adds, which truncate, stay below half a step of 16-bit
- * results and are summed again by 128 columns for f32 rows.  Calls of few rows are one launch on the exact weights and the
- * exact rows (24 bits of f32), and a row's bits do not depend on the others of such
- * a call.  Few are, of n = 1, 8 rows; and up to 64 rows of a small matrix:
+ * results and are summed again by 128 columns for f32 rows.
+ * Calls of few rows are one launch on the exact weights and the exact rows (24 bits
+ * of f32), and a row's bits do not depend on the others of such a call.  Few are,
+ * of n = 1, 8 rows; and up to 64 rows of a small matrix:
  * out <= 32 S and (2 with up, else 1) * out/16 * ceil(T/8) * in/64 <= 440 S (130 S
  * of f32 rows, 320 S of bf16 rows with rounded weights), S the device's
  * multiprocessors.  Their rows are not scaled: values from 2^-100 to 2^100, and
